@@ -129,14 +129,15 @@ __device__ __attribute__((always_inline)) inline void quantize_cols_body(int64_t
 // (t % 16, t / 16) owns rows k0 + 8kg .. +7 of columns n0 + 8g .. +7: the 8
 // codes of one column are one 32-bit word of its packed row, and lanes
 // 4q .. 4q+3 share block q. Block scales go to the step-major array Ws (the
-// byte of block b of column n at (b / 4) * 4N + 4n + b % 4).
+// byte of block b of column n at (b / 4) * 4ns + 4n + b % 4, ns the rows of that
+// array: N, or those of all matrices whose scales share it).
 constexpr int kMxTK = 128;  // codes along K per column tile
 constexpr int kMxTN = 128;  // columns per tile
 
 template <class In, bool kAligned>
 __device__ __attribute__((always_inline)) inline void quantize_cols_mx_body(
     int64_t bx, int64_t by, const typename In::T* __restrict__ W, int64_t K, int64_t N,
-    int64_t ldw, uint8_t* __restrict__ Wq, int64_t ldq, uint8_t* __restrict__ Ws) {
+    int64_t ldw, uint8_t* __restrict__ Wq, int64_t ldq, uint8_t* __restrict__ Ws, int64_t ns) {
   const int t = threadIdx.x;
   const int kg = t & 15, g = t >> 4;
   const int64_t n0 = bx * kMxTN;
@@ -173,7 +174,7 @@ __device__ __attribute__((always_inline)) inline void quantize_cols_mx_body(
               << (4 * u);
     *reinterpret_cast<uint32_t*>(Wq + (c + j) * ldq + kr / 2) = word;
     // rows kr .. kr+7: block kr / 32 of K step kr / 128 (the tile's step by)
-    if ((kg & 3) == 0) Ws[(kr / 128) * 4 * N + 4 * (c + j) + ((kr / 32) & 3)] = uint8_t(e[j] + 127);
+    if ((kg & 3) == 0) Ws[(kr / 128) * 4 * ns + 4 * (c + j) + ((kr / 32) & 3)] = uint8_t(e[j] + 127);
   }
 }
 

@@ -85,7 +85,7 @@ template <class In, bool kAligned>
 __global__ __launch_bounds__(kMxThreads) void quantize_cols_mx_kernel(
     const typename In::T* __restrict__ W, int64_t K, int64_t N, int64_t ldw,
     uint8_t* __restrict__ Wq, int64_t ldq, uint8_t* __restrict__ Ws) {
-  quantize_cols_mx_body<In, kAligned>(blockIdx.x, blockIdx.y, W, K, N, ldw, Wq, ldq, Ws);
+  quantize_cols_mx_body<In, kAligned>(blockIdx.x, blockIdx.y, W, K, N, ldw, Wq, ldq, Ws, N);
 }
 
 // chunks of a row across x (at most 64 workgroups), rows across y (at most 65535)
