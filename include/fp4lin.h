@@ -368,6 +368,93 @@ fp4lin_status fp4lin_forward(const void* A, const void* W, fp4lin_dtype dt, int6
                              float* Y, int64_t ldy, void* ws, size_t ws_bytes,
                              hipStream_t stream);
 
+/* ---- Products grouped by expert (micro-scaled FP4) -------------------------
+ * A layer of E experts: the rows of the activations are sorted by expert, and
+ * expert e owns the rows [row_end[e-1], row_end[e]) (from 0 for e = 0).
+ *   row_end  device, E int32, ascending, each in [0, M]. The values are not
+ *            known to the host; the kernels read them as a running maximum
+ *            clamped to [0, M], so no value leads out of an operand.
+ * Experts may have no rows. Rows from row_end[E-1] up to M belong to no
+ * expert: their output rows are zeros. M = 0 is a valid batch (nothing is
+ * written, and a weight gradient is all zeros; the pointers of M-row arrays may
+ * then be NULL).
+ * Quantization is that of the micro-scaled variant (32 codes along the
+ * product's reduction, one E8M0 byte each), without a clamp and without
+ * compensation. Every product accumulates in fp32 and is rounded once where
+ * the output is bfloat16.
+ * Weights of all experts are one array: expert e's K x N matrix starts at row
+ * e * K (E * K rows, leading dimension ldw).
+ * Limits: E <= 65534; packed operands of one expert and the scales of all
+ * experts are addressed with 32-bit byte offsets (else FP4LIN_ERR_SHAPE). */
+typedef enum {
+  FP4LIN_EXPERTS_FORWARD = 0,  /* fp4lin_experts_forward_mx */
+  FP4LIN_EXPERTS_DGRAD = 1,    /* fp4lin_experts_dgrad_mx   */
+  FP4LIN_EXPERTS_WGRAD = 2,    /* fp4lin_experts_wgrad_mx   */
+  FP4LIN_EXPERTS_APPLY = 3     /* fp4lin_experts_apply_mx   */
+} fp4lin_experts_pass;
+
+/* Bytes of workspace of a pass (at least 256); 0 for invalid arguments. The
+ * answer depends on the sizes alone, so it covers every row_end. */
+size_t fp4lin_experts_workspace_bytes(fp4lin_experts_pass pass, int64_t E, int64_t M, int64_t K,
+                                      int64_t N);
+
+/* Weights of all experts, quantized along K as fp4lin_quantize_weight_mx does
+ * for one.
+ *   Wq       device, E * N rows of fp4lin_packed_ld(K) bytes (output)
+ *   Ws       device, E * N * fp4lin_mx_scales_ld(K) bytes: step-major over the
+ *            E * N rows (the byte of block b of column n of expert e is at
+ *            (b / 4) * 4EN + 4(eN + n) + b % 4) (output)
+ * Wq and Ws must be 16-byte aligned.
+ * Errors: NULL, SHAPE, DTYPE, ALIGN, LAUNCH. */
+fp4lin_status fp4lin_experts_quantize_weight_mx(const void* W, fp4lin_dtype dt, int64_t E,
+                                                int64_t K, int64_t N, int64_t ldw, uint8_t* Wq,
+                                                uint8_t* Ws, hipStream_t stream);
+
+/* Y[r, :] = Q(A)[r, :] . Q(W[e])  for the rows r of expert e (reduction K).
+ *   A        device, M x K, dtype dt, leading dimension lda
+ *   W        device, E * K x N, dtype dt, leading dimension ldw
+ *   Y        device, M x N, dtype ydt, leading dimension ldy (output)
+ *   ws       device, >= fp4lin_experts_workspace_bytes(FORWARD, E, M, K, N)
+ * Errors: NULL, SHAPE, DTYPE, ALIGN, WORKSPACE, LAUNCH. */
+fp4lin_status fp4lin_experts_forward_mx(const void* A, const void* W, fp4lin_dtype dt,
+                                        const int32_t* row_end, int64_t E, int64_t M, int64_t K,
+                                        int64_t N, int64_t lda, int64_t ldw, void* Y,
+                                        fp4lin_dtype ydt, int64_t ldy, void* ws, size_t ws_bytes,
+                                        hipStream_t stream);
+
+/* The same with weights that fp4lin_experts_quantize_weight_mx has quantized
+ * before (serving): with few rows an expert it reads each weight's code once.
+ *   Wq, Ws   device, as written by that call (16-byte aligned)
+ *   ws       device, >= fp4lin_experts_workspace_bytes(APPLY, E, M, K, N)
+ * Errors: NULL, SHAPE, DTYPE, ALIGN, WORKSPACE, LAUNCH. */
+fp4lin_status fp4lin_experts_apply_mx(const void* A, fp4lin_dtype dt, const uint8_t* Wq,
+                                      const uint8_t* Ws, const int32_t* row_end, int64_t E,
+                                      int64_t M, int64_t K, int64_t N, int64_t lda, void* Y,
+                                      fp4lin_dtype ydt, int64_t ldy, void* ws, size_t ws_bytes,
+                                      hipStream_t stream);
+
+/* dX[r, :] = Q(dY)[r, :] . Q(W[e])^T  for the rows r of expert e (reduction N).
+ *   dY       device, M x N, dtype dt, leading dimension lddy
+ *   dX       device, M x K, dtype xdt, leading dimension lddx (output)
+ *   ws       device, >= fp4lin_experts_workspace_bytes(DGRAD, E, M, K, N)
+ * Errors: NULL, SHAPE, DTYPE, ALIGN, WORKSPACE, LAUNCH. */
+fp4lin_status fp4lin_experts_dgrad_mx(const void* dY, const void* W, fp4lin_dtype dt,
+                                      const int32_t* row_end, int64_t E, int64_t M, int64_t K,
+                                      int64_t N, int64_t lddy, int64_t ldw, void* dX,
+                                      fp4lin_dtype xdt, int64_t lddx, void* ws, size_t ws_bytes,
+                                      hipStream_t stream);
+
+/* dW[e] = Q(A_e)^T . Q(dY_e) over the rows of expert e, whose blocks of 32
+ * rows count from its first row; zeros for an expert without rows.
+ *   dW       device, E * K x N, dtype wdt, leading dimension lddw (output)
+ *   ws       device, >= fp4lin_experts_workspace_bytes(WGRAD, E, M, K, N)
+ * Errors: NULL, SHAPE, DTYPE, ALIGN, WORKSPACE, LAUNCH. */
+fp4lin_status fp4lin_experts_wgrad_mx(const void* A, const void* dY, fp4lin_dtype dt,
+                                      const int32_t* row_end, int64_t E, int64_t M, int64_t K,
+                                      int64_t N, int64_t lda, int64_t lddy, void* dW,
+                                      fp4lin_dtype wdt, int64_t lddw, void* ws, size_t ws_bytes,
+                                      hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

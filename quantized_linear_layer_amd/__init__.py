@@ -9,6 +9,7 @@ is no CPU path.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 
 from . import _lib
@@ -22,6 +23,10 @@ __all__ = [
     "CooBuffers", "mx_scales_ld", "fp4lin_quantize_act_mx", "fp4lin_quantize_weight_mx",
     "fp4lin_gemm_mx", "quantize_act_mx", "quantize_weight_mx", "gemm_mx",
     "fp4lin_forward_mx", "forward_mx", "forward_layout_mx",
+    "experts_workspace_bytes", "fp4lin_experts_quantize_weight_mx", "fp4lin_experts_forward_mx",
+    "fp4lin_experts_apply_mx", "fp4lin_experts_dgrad_mx", "fp4lin_experts_wgrad_mx",
+    "experts_quantize_weight_mx", "experts_forward_mx", "experts_apply_mx", "experts_dgrad_mx",
+    "experts_wgrad_mx",
 ]
 
 
@@ -356,3 +361,217 @@ def forward_mx(A, W, q, stream=None, return_workspace=False):
     Y = _empty((M, N), torch.float32, A.device)
     fp4lin_forward_mx(A, W, q, Y, ws, stream)
     return (Y, ws) if return_workspace else Y
+
+
+# ---- products grouped by expert ------------------------------------------------------
+def _experts_weight(W, name):
+    """(E, K, N, ldw) of a stack of row-major matrices with one row stride throughout."""
+    if W.dim() != 3 or W.stride(2) != 1 or (W.shape[0] > 1 and W.stride(0) != W.shape[1] * W.stride(1)):
+        raise ValueError(f"{name} must be a 3-D tensor (experts, rows, columns) with unit column "
+                         "stride and experts that follow one another at the row stride")
+    return W.shape[0], W.shape[1], W.shape[2], _row_stride(W.stride(1), W.shape[2])
+
+
+def _row_stride(ld, cols):
+    """A stride that a tensor of at most one row need not carry is the row length."""
+    return max(int(ld), int(cols))
+
+
+def _rows(t, name):
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be a 2-D row-major tensor with unit column stride")
+    if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+        raise ValueError(f"{name} must not have overlapping rows")
+    return t.shape[0], t.shape[1], _row_stride(t.stride(0), t.shape[1])
+
+
+def _row_end(row_end, E):
+    torch = _torch()
+    if row_end.dtype != torch.int32 or row_end.dim() != 1 or not row_end.is_contiguous():
+        raise TypeError("row_end must be a contiguous int32 vector")
+    if row_end.numel() != E:
+        raise ValueError(f"row_end has {row_end.numel()} entries for {E} experts")
+    return _dev(row_end, "row_end")
+
+
+def _same(what, **tensors):
+    """All on one GPU, and of one dtype where `what` says so."""
+    first = None
+    for name, t in tensors.items():
+        _dev(t, name)
+        if first is None:
+            first = (name, t)
+        elif t.device != first[1].device:
+            raise ValueError(f"{name} is on {t.device}, {first[0]} on {first[1].device}")
+        elif what == "dtype" and t.dtype != first[1].dtype:
+            raise TypeError(f"{first[0]} and {name} must have the same dtype")
+
+
+def _need(ok, message):
+    if not ok:
+        raise ValueError(message)
+
+
+@contextlib.contextmanager
+def _on(t, stream):
+    """The device of t and the stream the call runs on, so that what is
+    allocated inside belongs to that stream."""
+    torch = _torch()
+    with torch.cuda.device(t.device):
+        if stream is None:
+            yield
+        else:
+            with torch.cuda.stream(stream):
+                yield
+
+
+def experts_workspace_bytes(which: int, E: int, M: int, K: int, N: int) -> int:
+    return int(lib().fp4lin_experts_workspace_bytes(which, E, M, K, N))
+
+
+def _experts_ws(which, E, M, K, N, device, where):
+    n = experts_workspace_bytes(which, E, M, K, N)
+    if n == 0:
+        raise Fp4linError(_lib.ERR_SHAPE, where)
+    return _empty((n,), _torch().uint8, device)
+
+
+def _nbytes(ws):
+    return ws.numel() * ws.element_size()
+
+
+def fp4lin_experts_quantize_weight_mx(W, Wq, Ws, stream=None):
+    E, K, N, ldw = _experts_weight(W, "W")
+    _check(lib().fp4lin_experts_quantize_weight_mx(
+        _dev(W, "W"), _dtype_code(W), E, K, N, ldw, _dev(Wq, "Wq"), _dev(Ws, "Ws"),
+        _stream(stream)), "fp4lin_experts_quantize_weight_mx")
+
+
+def fp4lin_experts_forward_mx(A, W, row_end, Y, ws, stream=None):
+    M, K, lda = _rows(A, "A")
+    E, K2, N, ldw = _experts_weight(W, "W")
+    My, Ny, ldy = _rows(Y, "Y")
+    _same("dtype", A=A, W=W)
+    _same("", A=A, row_end=row_end, Y=Y, ws=ws)
+    _need(K2 == K, f"A is {M}x{K} but the weights are {K2}x{N}")
+    _need((My, Ny) == (M, N), f"Y is {My}x{Ny}, not {M}x{N}")
+    _check(lib().fp4lin_experts_forward_mx(
+        _dev(A, "A"), _dev(W, "W"), _dtype_code(A), _row_end(row_end, E), E, M, K, N, lda, ldw,
+        _dev(Y, "Y"), _dtype_code(Y), ldy, _dev(ws, "ws"), _nbytes(ws), _stream(stream)),
+        "fp4lin_experts_forward_mx")
+
+
+def fp4lin_experts_apply_mx(A, Wq, Ws, row_end, Y, ws, stream=None):
+    torch = _torch()
+    M, K, lda = _rows(A, "A")
+    My, N, ldy = _rows(Y, "Y")
+    E = row_end.numel()
+    _same("", A=A, Wq=Wq, Ws=Ws, row_end=row_end, Y=Y, ws=ws)
+    _need(My == M, f"Y has {My} rows, A {M}")
+    for name, t, want in (("Wq", Wq, E * N * packed_ld(K)), ("Ws", Ws, E * N * mx_scales_ld(K))):
+        if t.dtype != torch.uint8 or not t.is_contiguous():
+            raise TypeError(f"{name} must be a contiguous uint8 tensor")
+        _need(t.numel() == want, f"{name} holds {t.numel()} bytes, not {want}")
+    _check(lib().fp4lin_experts_apply_mx(
+        _dev(A, "A"), _dtype_code(A), _dev(Wq, "Wq"), _dev(Ws, "Ws"), _row_end(row_end, E), E, M, K,
+        N, lda, _dev(Y, "Y"), _dtype_code(Y), ldy, _dev(ws, "ws"), _nbytes(ws), _stream(stream)),
+        "fp4lin_experts_apply_mx")
+
+
+def fp4lin_experts_dgrad_mx(dY, W, row_end, dX, ws, stream=None):
+    M, N, lddy = _rows(dY, "dY")
+    E, K, N2, ldw = _experts_weight(W, "W")
+    Mx, Kx, lddx = _rows(dX, "dX")
+    _same("dtype", dY=dY, W=W)
+    _same("", dY=dY, row_end=row_end, dX=dX, ws=ws)
+    _need(N2 == N, f"dY is {M}x{N} but the weights are {K}x{N2}")
+    _need((Mx, Kx) == (M, K), f"dX is {Mx}x{Kx}, not {M}x{K}")
+    _check(lib().fp4lin_experts_dgrad_mx(
+        _dev(dY, "dY"), _dev(W, "W"), _dtype_code(dY), _row_end(row_end, E), E, M, K, N, lddy, ldw,
+        _dev(dX, "dX"), _dtype_code(dX), lddx, _dev(ws, "ws"), _nbytes(ws), _stream(stream)),
+        "fp4lin_experts_dgrad_mx")
+
+
+def fp4lin_experts_wgrad_mx(A, dY, row_end, dW, ws, stream=None):
+    M, K, lda = _rows(A, "A")
+    My, N, lddy = _rows(dY, "dY")
+    E, Kw, Nw, lddw = _experts_weight(dW, "dW")
+    _same("dtype", A=A, dY=dY)
+    _same("", A=A, row_end=row_end, dW=dW, ws=ws)
+    _need(My == M, f"dY has {My} rows, A {M}")
+    _need((Kw, Nw) == (K, N), f"dW holds {Kw}x{Nw} matrices, not {K}x{N}")
+    _check(lib().fp4lin_experts_wgrad_mx(
+        _dev(A, "A"), _dev(dY, "dY"), _dtype_code(A), _row_end(row_end, E), E, M, K, N, lda, lddy,
+        _dev(dW, "dW"), _dtype_code(dW), lddw, _dev(ws, "ws"), _nbytes(ws), _stream(stream)),
+        "fp4lin_experts_wgrad_mx")
+
+
+def experts_quantize_weight_mx(W, stream=None):
+    """Weights (E, K, N) for experts_apply_mx. Returns (Wq uint8 (E, N,
+    packed_ld(K)), Ws uint8 (steps, E, N, 4)), the scales step-major."""
+    torch = _torch()
+    E, K, N, _ = _experts_weight(W, "W")
+    _dev(W, "W")
+    with _on(W, stream):
+        Wq = _empty((E, N, packed_ld(K)), torch.uint8, W.device)
+        Ws = _empty((mx_scales_ld(K) // 4, E, N, 4), torch.uint8, W.device)
+        fp4lin_experts_quantize_weight_mx(W, Wq, Ws)
+    return Wq, Ws
+
+
+def experts_forward_mx(A, W, row_end, out_dtype=None, stream=None):
+    """Y (M, N) = the rows of A (M, K), sorted by expert, times their expert's
+    weight of W (E, K, N), both quantized to micro-scaled FP4. Expert e owns
+    the rows row_end[e-1] .. row_end[e] - 1 (int32, on the GPU); rows past
+    row_end[-1] give zeros. out_dtype: float32 (default) or bfloat16."""
+    torch = _torch()
+    M, K, _ = _rows(A, "A")
+    E, _, N, _ = _experts_weight(W, "W")
+    _dev(A, "A")
+    with _on(A, stream):
+        Y = _empty((M, N), out_dtype or torch.float32, A.device)
+        ws = _experts_ws(_lib.EXPERTS_FORWARD, E, M, K, N, A.device, "experts_forward_mx")
+        fp4lin_experts_forward_mx(A, W, row_end, Y, ws)
+    return Y
+
+
+def experts_apply_mx(A, Wq, Ws, row_end, out_dtype=None, stream=None):
+    """experts_forward_mx with weights from experts_quantize_weight_mx."""
+    torch = _torch()
+    M, K, _ = _rows(A, "A")
+    _need(Wq.dim() == 3, "Wq must be (experts, columns, packed bytes)")
+    E, N, _ = Wq.shape
+    _dev(A, "A")
+    with _on(A, stream):
+        Y = _empty((M, N), out_dtype or torch.float32, A.device)
+        ws = _experts_ws(_lib.EXPERTS_APPLY, E, M, K, N, A.device, "experts_apply_mx")
+        fp4lin_experts_apply_mx(A, Wq, Ws, row_end, Y, ws)
+    return Y
+
+
+def experts_dgrad_mx(dY, W, row_end, out_dtype=None, stream=None):
+    """dX (M, K) = the rows of dY (M, N) times their expert's weight transposed."""
+    torch = _torch()
+    M, N, _ = _rows(dY, "dY")
+    E, K, _, _ = _experts_weight(W, "W")
+    _dev(dY, "dY")
+    with _on(dY, stream):
+        dX = _empty((M, K), out_dtype or torch.float32, dY.device)
+        ws = _experts_ws(_lib.EXPERTS_DGRAD, E, M, K, N, dY.device, "experts_dgrad_mx")
+        fp4lin_experts_dgrad_mx(dY, W, row_end, dX, ws)
+    return dX
+
+
+def experts_wgrad_mx(A, dY, row_end, out_dtype=None, stream=None):
+    """dW (E, K, N): each expert's rows of A (M, K) transposed times its rows of
+    dY (M, N); zeros for an expert without rows."""
+    torch = _torch()
+    M, K, _ = _rows(A, "A")
+    N = dY.shape[1]
+    E = row_end.numel()
+    _dev(A, "A")
+    with _on(A, stream):
+        dW = _empty((E, K, N), out_dtype or torch.float32, A.device)
+        ws = _experts_ws(_lib.EXPERTS_WGRAD, E, M, K, N, A.device, "experts_wgrad_mx")
+        fp4lin_experts_wgrad_mx(A, dY, row_end, dW, ws)
+    return dW

@@ -16,6 +16,8 @@ c_int = ctypes.c_int
 OK, ERR_NULL, ERR_SHAPE, ERR_DTYPE, ERR_QUANTILE, ERR_CAPACITY, ERR_ALIGN, ERR_WORKSPACE, \
     ERR_LAUNCH, ERR_SCRATCH = range(10)
 F32, BF16 = 0, 1
+# fp4lin_experts_pass
+EXPERTS_FORWARD, EXPERTS_DGRAD, EXPERTS_WGRAD, EXPERTS_APPLY = range(4)
 
 
 class Coo(ctypes.Structure):
@@ -67,6 +69,18 @@ SIGNATURES = {
                                          ctypes.POINTER(ForwardOffsets)]),
     "fp4lin_forward_mx": (c_int, [c_ptr, c_ptr, c_int, c_i64, c_i64, c_i64, c_i64, c_i64, c_dbl,
                                   c_ptr, c_i64, c_ptr, c_size, c_ptr]),
+    "fp4lin_experts_workspace_bytes": (c_size, [c_int, c_i64, c_i64, c_i64, c_i64]),
+    "fp4lin_experts_quantize_weight_mx": (c_int, [c_ptr, c_int, c_i64, c_i64, c_i64, c_i64, c_ptr,
+                                                  c_ptr, c_ptr]),
+    "fp4lin_experts_forward_mx": (c_int, [c_ptr, c_ptr, c_int, c_ptr, c_i64, c_i64, c_i64, c_i64,
+                                          c_i64, c_i64, c_ptr, c_int, c_i64, c_ptr, c_size,
+                                          c_ptr]),
+    "fp4lin_experts_apply_mx": (c_int, [c_ptr, c_int, c_ptr, c_ptr, c_ptr, c_i64, c_i64, c_i64,
+                                        c_i64, c_i64, c_ptr, c_int, c_i64, c_ptr, c_size, c_ptr]),
+    "fp4lin_experts_dgrad_mx": (c_int, [c_ptr, c_ptr, c_int, c_ptr, c_i64, c_i64, c_i64, c_i64,
+                                        c_i64, c_i64, c_ptr, c_int, c_i64, c_ptr, c_size, c_ptr]),
+    "fp4lin_experts_wgrad_mx": (c_int, [c_ptr, c_ptr, c_int, c_ptr, c_i64, c_i64, c_i64, c_i64,
+                                        c_i64, c_i64, c_ptr, c_int, c_i64, c_ptr, c_size, c_ptr]),
 }
 
 _lib = None

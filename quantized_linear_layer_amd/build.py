@@ -21,7 +21,8 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libfp4lin.so")
 ARCH = "gfx950"
 
-SOURCES = ["api.hip", "select.hip", "quantize.hip", "mx.hip", "gemm.hip", "spmm.hip"]
+SOURCES = ["api.hip", "select.hip", "quantize.hip", "mx.hip", "gemm.hip", "spmm.hip",
+           "experts.hip"]
 
 # Packed fp32 VALU ops are switched off for all device code; fp32 denormals are
 # kept (inputs may be subnormal and the encoder must see them); no FMA
@@ -51,7 +52,7 @@ def _run(cmd):
     return err
 
 
-def build(verbose: bool = False, jobs: int = 4) -> str:
+def build(verbose: bool = False, jobs: int = 8) -> str:
     os.makedirs(BUILD, exist_ok=True)
     cc = hipcc()
     objs = []

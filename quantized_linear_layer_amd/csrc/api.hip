@@ -508,3 +508,229 @@ fp4lin_status fp4lin_forward_mx(const void* A, const void* W, fp4lin_dtype dt, i
 }
 
 }  // extern "C"
+
+// ---- products grouped by expert -------------------------------------------------
+namespace {
+
+constexpr int64_t kMaxExperts = 65534;  // experts index a grid dimension, one group more
+
+bool ok_rows(int64_t M) { return M >= 0 && M < kMaxDim; }
+
+// Sizes that every pass checks; the offsets of a pass's operands besides.
+fp4lin_status experts_sizes(int64_t E, int64_t M, int64_t K, int64_t N) {
+  if (E < 1 || E > kMaxExperts || !ok_rows(M) || !ok_dim(K) || !ok_dim(N)) return FP4LIN_ERR_SHAPE;
+  return FP4LIN_OK;
+}
+
+// Packed rows of ldq bytes that one resource covers, and the scales of `all`
+// packed rows of L codes.
+bool packed_fits(int64_t rows, int64_t ldq) { return (rows + 1) * ldq < kMaxDim; }
+bool scales_fit(int64_t all, int64_t L) {
+  return double(all) * double(fp4lin_mx_scales_ld(L)) < double(kMaxDim);
+}
+
+// Workgroups of the tiled products (at the finest 128 x 256 tiles) and of the
+// quantizers fit a grid.
+bool tiles_fit(double rows, double groups, double cols) {
+  return (rows / 128 + groups + 1) * (cols / 256 + 1) < double(kMaxDim);
+}
+
+// Reduction along L of M rows against E * n rows of weights (forward: L = K,
+// n = N; dgrad: L = N, n = K).
+fp4lin_status experts_rows_fit(int64_t E, int64_t M, int64_t L, int64_t n) {
+  const int64_t ldq = fp4lin_packed_ld(L);
+  if (!packed_fits(M, ldq) || !packed_fits(n, ldq) || !scales_fit(E * n, L) || !scales_fit(M, L) ||
+      L > kMaxColK || !tiles_fit(double(M), double(E), double(n)))
+    return FP4LIN_ERR_SHAPE;
+  return FP4LIN_OK;
+}
+
+fp4lin_status experts_cols_fit(int64_t E, int64_t M, int64_t K, int64_t N) {
+  const int64_t steps = fp4lin::experts_steps(E, M);
+  const int64_t most = K > N ? K : N;
+  if (steps > 65535 || double(most) * double(steps + 1) * 64 >= double(kMaxDim) ||
+      double(E) * (double(K) / 128 + 1) * (double(N) / 256 + 1) >= double(kMaxDim))
+    return FP4LIN_ERR_SHAPE;
+  return FP4LIN_OK;
+}
+
+// Where a pass keeps its two quantized operands in the workspace.
+struct ExpertsLayout {
+  size_t Aq, As, Bq, Bs, total;
+};
+
+fp4lin_status experts_layout(fp4lin_experts_pass pass, int64_t E, int64_t M, int64_t K, int64_t N,
+                             ExpertsLayout* out) {
+  fp4lin_status s = experts_sizes(E, M, K, N);
+  if (s != FP4LIN_OK) return s;
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off = round_up(off + bytes, 256);
+    return at;
+  };
+  ExpertsLayout o{};
+  if (pass == FP4LIN_EXPERTS_WGRAD) {
+    s = experts_cols_fit(E, M, K, N);
+    if (s != FP4LIN_OK) return s;
+    const size_t steps = size_t(fp4lin::experts_steps(E, M));
+    o.Aq = take(size_t(K) * steps * 64);
+    o.As = take(size_t(K) * steps * 4);
+    o.Bq = take(size_t(N) * steps * 64);
+    o.Bs = take(size_t(N) * steps * 4);
+  } else if (pass == FP4LIN_EXPERTS_FORWARD || pass == FP4LIN_EXPERTS_DGRAD ||
+             pass == FP4LIN_EXPERTS_APPLY) {
+    const int64_t L = pass == FP4LIN_EXPERTS_DGRAD ? N : K;
+    const int64_t n = pass == FP4LIN_EXPERTS_DGRAD ? K : N;
+    s = experts_rows_fit(E, M, L, n);
+    if (s != FP4LIN_OK) return s;
+    const size_t ldq = size_t(fp4lin_packed_ld(L)), lds = size_t(fp4lin_mx_scales_ld(L));
+    o.Aq = take(size_t(M) * ldq);
+    o.As = take(size_t(M) * lds);
+    if (pass != FP4LIN_EXPERTS_APPLY) {
+      o.Bq = take(size_t(E) * size_t(n) * ldq);
+      o.Bs = take(size_t(E) * size_t(n) * lds);
+    }
+  } else {
+    return FP4LIN_ERR_SHAPE;
+  }
+  o.total = off > 256 ? off : 256;
+  *out = o;
+  return FP4LIN_OK;
+}
+
+fp4lin_status experts_workspace(fp4lin_experts_pass pass, int64_t E, int64_t M, int64_t K,
+                                int64_t N, const void* ws, size_t ws_bytes, ExpertsLayout* out) {
+  const fp4lin_status s = experts_layout(pass, E, M, K, N, out);
+  if (s != FP4LIN_OK) return s;
+  if (ws == nullptr) return FP4LIN_ERR_NULL;
+  if (!aligned16(ws)) return FP4LIN_ERR_ALIGN;
+  return ws_bytes < out->total ? FP4LIN_ERR_WORKSPACE : FP4LIN_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t fp4lin_experts_workspace_bytes(fp4lin_experts_pass pass, int64_t E, int64_t M, int64_t K,
+                                      int64_t N) {
+  ExpertsLayout o;
+  return experts_layout(pass, E, M, K, N, &o) == FP4LIN_OK ? o.total : 0;
+}
+
+fp4lin_status fp4lin_experts_quantize_weight_mx(const void* W, fp4lin_dtype dt, int64_t E,
+                                                int64_t K, int64_t N, int64_t ldw, uint8_t* Wq,
+                                                uint8_t* Ws, hipStream_t stream) {
+  if (W == nullptr || Wq == nullptr || Ws == nullptr) return FP4LIN_ERR_NULL;
+  if (bad_dtype(dt)) return FP4LIN_ERR_DTYPE;
+  fp4lin_status s = experts_sizes(E, 0, K, N);
+  if (s == FP4LIN_OK) s = experts_rows_fit(E, 0, K, N);
+  if (s != FP4LIN_OK) return s;
+  if (ldw < N) return FP4LIN_ERR_SHAPE;
+  if (!aligned16(Wq) || !aligned16(Ws)) return FP4LIN_ERR_ALIGN;
+  return launch_status(fp4lin::launch_experts_quantize_cols_mx(
+      W, dt == FP4LIN_BF16, E, K, N, ldw, Wq, fp4lin_packed_ld(K), Ws, stream));
+}
+
+fp4lin_status fp4lin_experts_forward_mx(const void* A, const void* W, fp4lin_dtype dt,
+                                        const int32_t* row_end, int64_t E, int64_t M, int64_t K,
+                                        int64_t N, int64_t lda, int64_t ldw, void* Y,
+                                        fp4lin_dtype ydt, int64_t ldy, void* ws, size_t ws_bytes,
+                                        hipStream_t stream) {
+  if (W == nullptr || row_end == nullptr || (M != 0 && (A == nullptr || Y == nullptr)))
+    return FP4LIN_ERR_NULL;
+  if (bad_dtype(dt) || bad_dtype(ydt)) return FP4LIN_ERR_DTYPE;
+  ExpertsLayout o;
+  fp4lin_status s = experts_workspace(FP4LIN_EXPERTS_FORWARD, E, M, K, N, ws, ws_bytes, &o);
+  if (s != FP4LIN_OK) return s;
+  if (lda < K || ldw < N || ldy < N) return FP4LIN_ERR_SHAPE;
+  if (M == 0) return FP4LIN_OK;
+  uint8_t* const base = static_cast<uint8_t*>(ws);
+  const int64_t ldq = fp4lin_packed_ld(K);
+  s = launch_status(fp4lin::launch_quantize_rows_mx(A, dt == FP4LIN_BF16, M, K, lda, nullptr,
+                                                    base + o.Aq, ldq, base + o.As, stream));
+  if (s != FP4LIN_OK) return s;
+  s = launch_status(fp4lin::launch_experts_quantize_cols_mx(W, dt == FP4LIN_BF16, E, K, N, ldw,
+                                                            base + o.Bq, ldq, base + o.Bs, stream));
+  if (s != FP4LIN_OK) return s;
+  return launch_status(fp4lin::launch_experts_rows(base + o.Aq, base + o.As, base + o.Bq,
+                                                   base + o.Bs, row_end, E, M, N, ldq, Y,
+                                                   ydt == FP4LIN_BF16, ldy, stream));
+}
+
+fp4lin_status fp4lin_experts_apply_mx(const void* A, fp4lin_dtype dt, const uint8_t* Wq,
+                                      const uint8_t* Ws, const int32_t* row_end, int64_t E,
+                                      int64_t M, int64_t K, int64_t N, int64_t lda, void* Y,
+                                      fp4lin_dtype ydt, int64_t ldy, void* ws, size_t ws_bytes,
+                                      hipStream_t stream) {
+  if (Wq == nullptr || Ws == nullptr || row_end == nullptr ||
+      (M != 0 && (A == nullptr || Y == nullptr)))
+    return FP4LIN_ERR_NULL;
+  if (bad_dtype(dt) || bad_dtype(ydt)) return FP4LIN_ERR_DTYPE;
+  ExpertsLayout o;
+  fp4lin_status s = experts_workspace(FP4LIN_EXPERTS_APPLY, E, M, K, N, ws, ws_bytes, &o);
+  if (s != FP4LIN_OK) return s;
+  if (lda < K || ldy < N) return FP4LIN_ERR_SHAPE;
+  if (!aligned16(Wq) || !aligned16(Ws)) return FP4LIN_ERR_ALIGN;
+  if (M == 0) return FP4LIN_OK;
+  uint8_t* const base = static_cast<uint8_t*>(ws);
+  const int64_t ldq = fp4lin_packed_ld(K);
+  s = launch_status(fp4lin::launch_quantize_rows_mx(A, dt == FP4LIN_BF16, M, K, lda, nullptr,
+                                                    base + o.Aq, ldq, base + o.As, stream));
+  if (s != FP4LIN_OK) return s;
+  return launch_status(fp4lin::launch_experts_rows(base + o.Aq, base + o.As, Wq, Ws, row_end, E, M,
+                                                   N, ldq, Y, ydt == FP4LIN_BF16, ldy, stream));
+}
+
+fp4lin_status fp4lin_experts_dgrad_mx(const void* dY, const void* W, fp4lin_dtype dt,
+                                      const int32_t* row_end, int64_t E, int64_t M, int64_t K,
+                                      int64_t N, int64_t lddy, int64_t ldw, void* dX,
+                                      fp4lin_dtype xdt, int64_t lddx, void* ws, size_t ws_bytes,
+                                      hipStream_t stream) {
+  if (W == nullptr || row_end == nullptr || (M != 0 && (dY == nullptr || dX == nullptr)))
+    return FP4LIN_ERR_NULL;
+  if (bad_dtype(dt) || bad_dtype(xdt)) return FP4LIN_ERR_DTYPE;
+  ExpertsLayout o;
+  fp4lin_status s = experts_workspace(FP4LIN_EXPERTS_DGRAD, E, M, K, N, ws, ws_bytes, &o);
+  if (s != FP4LIN_OK) return s;
+  if (lddy < N || ldw < N || lddx < K) return FP4LIN_ERR_SHAPE;
+  if (M == 0) return FP4LIN_OK;
+  uint8_t* const base = static_cast<uint8_t*>(ws);
+  const int64_t ldq = fp4lin_packed_ld(N);
+  s = launch_status(fp4lin::launch_quantize_rows_mx(dY, dt == FP4LIN_BF16, M, N, lddy, nullptr,
+                                                    base + o.Aq, ldq, base + o.As, stream));
+  if (s != FP4LIN_OK) return s;
+  // the E * K rows of all weights are the packed rows the product reads
+  s = launch_status(fp4lin::launch_quantize_rows_mx(W, dt == FP4LIN_BF16, E * K, N, ldw, nullptr,
+                                                    base + o.Bq, ldq, base + o.Bs, stream));
+  if (s != FP4LIN_OK) return s;
+  return launch_status(fp4lin::launch_experts_rows(base + o.Aq, base + o.As, base + o.Bq,
+                                                   base + o.Bs, row_end, E, M, K, ldq, dX,
+                                                   xdt == FP4LIN_BF16, lddx, stream));
+}
+
+fp4lin_status fp4lin_experts_wgrad_mx(const void* A, const void* dY, fp4lin_dtype dt,
+                                      const int32_t* row_end, int64_t E, int64_t M, int64_t K,
+                                      int64_t N, int64_t lda, int64_t lddy, void* dW,
+                                      fp4lin_dtype wdt, int64_t lddw, void* ws, size_t ws_bytes,
+                                      hipStream_t stream) {
+  if (dW == nullptr || row_end == nullptr || (M != 0 && (A == nullptr || dY == nullptr)))
+    return FP4LIN_ERR_NULL;
+  if (bad_dtype(dt) || bad_dtype(wdt)) return FP4LIN_ERR_DTYPE;
+  ExpertsLayout o;
+  fp4lin_status s = experts_workspace(FP4LIN_EXPERTS_WGRAD, E, M, K, N, ws, ws_bytes, &o);
+  if (s != FP4LIN_OK) return s;
+  if (lda < K || lddy < N || lddw < N) return FP4LIN_ERR_SHAPE;
+  uint8_t* const base = static_cast<uint8_t*>(ws);
+  s = launch_status(fp4lin::launch_experts_quantize_ragged_mx(
+      A, dt == FP4LIN_BF16, row_end, E, M, K, lda, base + o.Aq, base + o.As, stream));
+  if (s != FP4LIN_OK) return s;
+  s = launch_status(fp4lin::launch_experts_quantize_ragged_mx(
+      dY, dt == FP4LIN_BF16, row_end, E, M, N, lddy, base + o.Bq, base + o.Bs, stream));
+  if (s != FP4LIN_OK) return s;
+  return launch_status(fp4lin::launch_experts_wgrad(base + o.Aq, base + o.As, base + o.Bq,
+                                                    base + o.Bs, row_end, E, M, K, N, dW,
+                                                    wdt == FP4LIN_BF16, lddw, stream));
+}
+
+}  // extern "C"

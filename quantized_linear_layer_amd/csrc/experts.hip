@@ -1,0 +1,453 @@
+// Products grouped by expert on micro-scaled FP4 operands.
+//
+// The rows of the activations are sorted by expert: expert e owns the rows
+// [b_e, n_e), n_e = row_end[e] and b_e = n_(e-1) (b_0 = 0), in numbers that only
+// the device knows. With Q the block quantization of mx.hip along the product's
+// reduction,
+//   forward  Y[r, :]  = Q(A)[r, :] . Q(W[e])        over K, for the rows r of e
+//   dgrad    dX[r, :] = Q(dY)[r, :] . Q(W[e])^T     over N
+//   wgrad    dW[e]    = Q(A_e)^T . Q(dY_e)          over e's rows; blocks of 32
+//                                                   rows count from its first row
+// Each is a sum over blocks of 2^(eA + eB) * (FP4 dot product), accumulated in
+// fp32 by the matrix core and written once, in fp32 or rounded to bfloat16.
+//
+// Ragged groups without a host copy of row_end: a launch covers the most tiles
+// that any split of the rows over the experts can need, every wave finds its
+// tile's expert by a scan over row_end (64 experts a round: one load, a running
+// maximum and a prefix sum across lanes), and workgroups past the last tile
+// end at once. The scan also gives the number of tiles, which the mapping of
+// workgroups to XCDs needs. row_end is read as a running maximum clamped to
+// [0, M], so no content of it can lead outside the operands.
+//
+// Rows at and past the last expert's end belong to nobody: their output rows
+// are written as zeros by the workgroups of one more group.
+#include <type_traits>
+
+#include "colquant.hpp"
+#include "device_common.hpp"
+#include "gemm_core.hpp"
+#include "internal.hpp"
+
+namespace fp4lin {
+
+namespace {
+
+constexpr int kThreads = 256;
+
+// ---------------------------------------------------------------------------
+// Groups.
+// ---------------------------------------------------------------------------
+// Running maximum and sum across the wave (inclusive).
+__device__ inline int wave_scan_max(int v) {
+  const int lane = threadIdx.x & (kWave - 1);
+#pragma unroll
+  for (int off = 1; off < kWave; off <<= 1) {
+    const int o = __shfl_up(v, off, kWave);
+    if (lane >= off) v = v > o ? v : o;
+  }
+  return v;
+}
+
+__device__ inline int wave_scan_sum(int v) {
+  const int lane = threadIdx.x & (kWave - 1);
+#pragma unroll
+  for (int off = 1; off < kWave; off <<= 1) {
+    const int o = __shfl_up(v, off, kWave);
+    if (lane >= off) v += o;
+  }
+  return v;
+}
+
+// A group of rows: expert e's, or with e == E the rows past the last expert's
+// end. first: the units (of R rows, the last one of a group part full) of all
+// groups before it.
+struct Group {
+  int e, begin, rows, first;
+};
+
+// 64 experts of the scan, one per lane: [begin, end) and the units up to and
+// with the lane's own. Lanes past E hold empty groups.
+template <int R>
+struct GroupScan {
+  int begin, end, upto;
+
+  __device__ inline void read(const int32_t* row_end, int base, int E, int M, int end0,
+                              int units0) {
+    const int lane = threadIdx.x & (kWave - 1);
+    int n = base + lane < E ? row_end[base + lane] : 0;
+    n = n < 0 ? 0 : (n > M ? M : n);
+    n = wave_scan_max(n > end0 ? n : end0);
+    const int p = __shfl_up(n, 1, kWave);
+    begin = lane == 0 ? end0 : p;
+    end = n;
+    upto = units0 + wave_scan_sum((end - begin + R - 1) / R);
+  }
+  __device__ inline Group group(int base, int lane) const {
+    const int b = __builtin_amdgcn_readlane(begin, lane);
+    const int n = __builtin_amdgcn_readlane(end, lane);
+    const int u = __builtin_amdgcn_readlane(upto, lane);
+    return Group{base + lane, b, n - b, u - (n - b + R - 1) / R};
+  }
+};
+
+// Number of units of all groups, the one past the last expert among them.
+template <int R>
+__device__ inline int total_units(const int32_t* row_end, int E, int M) {
+  int end0 = 0, units0 = 0;
+  for (int base = 0; base < E; base += kWave) {
+    GroupScan<R> s;
+    s.read(row_end, base, E, M, end0, units0);
+    end0 = __builtin_amdgcn_readlane(s.end, kWave - 1);
+    units0 = __builtin_amdgcn_readlane(s.upto, kWave - 1);
+  }
+  return units0 + (M - end0 + R - 1) / R;
+}
+
+// The group of unit u (0 <= u < total_units).
+template <int R>
+__device__ inline Group group_of_unit(const int32_t* row_end, int E, int M, int u) {
+  int end0 = 0, units0 = 0;
+  for (int base = 0; base < E; base += kWave) {
+    GroupScan<R> s;
+    s.read(row_end, base, E, M, end0, units0);
+    const uint64_t past = __ballot(u < s.upto);
+    if (past != 0) return s.group(base, __builtin_ctzll(past));
+    end0 = __builtin_amdgcn_readlane(s.end, kWave - 1);
+    units0 = __builtin_amdgcn_readlane(s.upto, kWave - 1);
+  }
+  return Group{E, end0, M - end0, units0};
+}
+
+// Group e (0 <= e <= E).
+template <int R>
+__device__ inline Group group_of_expert(const int32_t* row_end, int E, int M, int e) {
+  int end0 = 0, units0 = 0;
+  for (int base = 0; base < E; base += kWave) {
+    GroupScan<R> s;
+    s.read(row_end, base, E, M, end0, units0);
+    if (e < base + kWave && e < E) return s.group(base, e - base);
+    end0 = __builtin_amdgcn_readlane(s.end, kWave - 1);
+    units0 = __builtin_amdgcn_readlane(s.upto, kWave - 1);
+  }
+  return Group{E, end0, M - end0, units0};
+}
+
+// ---------------------------------------------------------------------------
+// Quantizers.
+// ---------------------------------------------------------------------------
+// Weights, reduction along K (rows of W[e]): tile (blockIdx.x, blockIdx.y) of
+// expert blockIdx.z. Codes go to the N packed rows of expert e, scales to one
+// step-major array over the E * N columns of all experts.
+template <class In, bool kAligned>
+__global__ __launch_bounds__(kThreads) void experts_cols_mx_kernel(
+    const typename In::T* __restrict__ W, int64_t K, int64_t N, int64_t ldw, int64_t ns,
+    uint8_t* __restrict__ Wq, int64_t ldq, uint8_t* __restrict__ Ws) {
+  const int64_t e = blockIdx.z;
+  quantize_cols_mx_body<In, kAligned>(blockIdx.x, blockIdx.y, W + e * K * ldw, K, N, ldw,
+                                      Wq + e * N * ldq, ldq, Ws + 4 * e * N, ns);
+}
+
+// Activations or gradients, reduction along each expert's own rows: K step
+// blockIdx.y of all experts' steps (128 rows each, the last one of an expert
+// filled with zeros) and 128 columns. Codes of global step s go to bytes
+// 64s .. 64s+63 of each column's packed row of ldq bytes.
+template <class In, bool kAligned>
+__global__ __launch_bounds__(kThreads) void experts_ragged_mx_kernel(
+    const typename In::T* __restrict__ X, const int32_t* __restrict__ row_end, int E, int M,
+    int64_t N, int64_t ldx, uint8_t* __restrict__ Xq, int64_t ldq, uint8_t* __restrict__ Xs) {
+  const int s = blockIdx.y;
+  const Group g = group_of_unit<128>(row_end, E, M, s);
+  if (g.e == E) return;
+  quantize_cols_mx_body<In, kAligned>(blockIdx.x, s - g.first, X + int64_t(g.begin) * ldx, g.rows,
+                                      N, ldx, Xq + int64_t(g.first) * 64, ldq,
+                                      Xs + int64_t(g.first) * 4 * N, N);
+}
+
+// ---------------------------------------------------------------------------
+// Products over tiles.
+// ---------------------------------------------------------------------------
+struct TileArgs {
+  const uint8_t *Aq, *As, *Bq, *Bs;
+  const int32_t* row_end;
+  int E, M;        // M: rows of the activations
+  int rows, cols;  // of an expert's output (rows: wgrad only)
+  int ldq;         // bytes of a packed row
+  void* Y;
+  int64_t ldy;
+};
+
+// kWgrad false: forward and dgrad, A the packed rows of the activations, B
+// the packed weights of all experts (cols rows each). kWgrad true: A and B
+// the column-packed activations and gradients, row stride ldq, expert e's
+// reduction steps a range of columns of both.
+template <class C, class Out, bool kWgrad>
+__global__ __launch_bounds__(C::kThreads, C::kMinBlocks) void experts_gemm_kernel(TileArgs p) {
+  constexpr int SB = C::kStageBytes;
+  __shared__ __attribute__((aligned(16))) uint8_t st0[SB];
+  __shared__ __attribute__((aligned(16))) uint8_t st1[SB];
+  __shared__ __attribute__((aligned(16))) uint8_t st2[SB];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int tiles_n = (p.cols + C::BN - 1) / C::BN;
+  int m0, n0, rows, nkt;
+  Fp4Operand A, B;
+  Out* Y = static_cast<Out*>(p.Y);
+  if constexpr (kWgrad) {
+    const int tiles_m = (p.rows + C::BM - 1) / C::BM;
+    const int t = xcd_run(blockIdx.x, p.E * tiles_m * tiles_n);
+    if (t < 0) return;
+    const int e = t / (tiles_m * tiles_n);
+    int tm, tn;
+    tile_of(t - e * tiles_m * tiles_n, tiles_m, tiles_n, tm, tn);
+    const Group g = group_of_expert<128>(p.row_end, p.E, p.M, e);
+    nkt = (g.rows + 127) / 128;
+    m0 = tm * C::BM;
+    n0 = tn * C::BN;
+    rows = p.rows;
+    const int64_t at = int64_t(g.first) * 64;
+    A = Fp4Operand{p.Aq + at, p.ldq, p.rows, nkt * 64, p.As + int64_t(g.first) * 4 * p.rows,
+                   4 * p.rows, nkt * 4 * p.rows};
+    B = Fp4Operand{p.Bq + at, p.ldq, p.cols, nkt * 64, p.Bs + int64_t(g.first) * 4 * p.cols,
+                   4 * p.cols, nkt * 4 * p.cols};
+    Y += int64_t(e) * p.rows * p.ldy;
+  } else {
+    const int t = xcd_run(blockIdx.x, total_units<C::BM>(p.row_end, p.E, p.M) * tiles_n);
+    if (t < 0) return;
+    const Group g = group_of_unit<C::BM>(p.row_end, p.E, p.M, t / tiles_n);
+    int tm, tn;
+    tile_of(t - g.first * tiles_n, (g.rows + C::BM - 1) / C::BM, tiles_n, tm, tn);
+    // the rows past the last expert's end: no steps, zeros
+    nkt = g.e == p.E ? 0 : p.ldq / 64;
+    m0 = tm * C::BM;
+    n0 = tn * C::BN;
+    rows = g.rows;
+    const int nblk = p.ldq / 16, all = p.E * p.cols, e = g.e == p.E ? 0 : g.e;
+    A = Fp4Operand{p.Aq + int64_t(g.begin) * p.ldq, p.ldq, g.rows, p.ldq,
+                   p.As + 4 * int64_t(g.begin), 4 * p.M, p.M * nblk - 4 * g.begin};
+    B = Fp4Operand{p.Bq + int64_t(e) * p.cols * p.ldq, p.ldq, p.cols, p.ldq,
+                   p.Bs + 4 * int64_t(e) * p.cols, 4 * all, all * nblk - 4 * e * p.cols};
+    Y += int64_t(g.begin) * p.ldy;
+  }
+  Fp4Feed<C, true> f(A, B, m0, n0, wave, lane);
+  if (nkt > 0) gemm_pipeline(f, nkt, st0, st1, st2);
+  store_tile<C>(st0, st1, st2, wave, lane, m0, n0, rows, p.cols, Y, p.ldy,
+                [&](int fm, int fn, int r) { return f.acc[fm][fn][r]; });
+}
+
+// ---------------------------------------------------------------------------
+// Few rows an expert (serving): bound by reading the weights' codes once.
+// ---------------------------------------------------------------------------
+// A workgroup of four waves owns 16 columns of one expert and walks its rows in
+// chunks of 16 * MF. The waves split K: wave w takes the K steps w, w + 4, ...,
+// so that the four read 256 contiguous bytes of each column's packed row. Codes
+// go from memory straight to the matrix core's registers (the 16x16x128 shape:
+// lane l holds the 32 codes of block l / 16 of the step for column l % 16, one
+// 16-byte load, and the block's scale byte); kAhead steps of loads are in
+// flight. The four partial sums are added in wave order through LDS.
+constexpr int kFewWaves = 4;
+
+typedef float v4f __attribute__((ext_vector_type(4)));
+
+struct FewArgs {
+  const uint8_t *Aq, *As, *Bq, *Bs;
+  const int32_t* row_end;
+  int E, M, N, ldq;
+  void* Y;
+  int64_t ldy;
+};
+
+__device__ inline void store_out(float* p, float v) { *p = v; }
+__device__ inline void store_out(uint16_t* p, float v) { *p = uint16_t(bf16_pair(v, v)); }
+
+template <int MF, class Out>
+__global__ __launch_bounds__(kFewWaves * 64) void experts_few_kernel(FewArgs p) {
+  __shared__ v4f part[kFewWaves][MF][64];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const Group g = group_of_expert<16>(p.row_end, p.E, p.M, blockIdx.y);
+  if (g.rows == 0) return;
+  Out* const Y = static_cast<Out*>(p.Y);
+  const int n = blockIdx.x * 16 + (lane & 15);
+  const int q = lane >> 4;
+  const int nkt = g.e == p.E ? 0 : p.ldq / 64;
+  const int64_t bcol = int64_t(g.e == p.E ? 0 : g.e) * p.N + (n < p.N ? n : p.N - 1);
+  const uint8_t* const brow = p.Bq + bcol * p.ldq + q * 16;
+  const uint8_t* const bsc = p.Bs + 4 * bcol + q;
+  const int64_t bstep = 4 * int64_t(p.E) * p.N, astep = 4 * int64_t(p.M);
+  constexpr int kAhead = MF == 1 ? 8 : 4;
+  for (int r0 = 0; r0 < g.rows; r0 += 16 * MF) {
+    v4f acc[MF];
+    const uint8_t *arow[MF], *asc[MF];
+#pragma unroll
+    for (int i = 0; i < MF; ++i) {
+      acc[i] = v4f{};
+      // rows past the group's end repeat its last row; they are not stored
+      const int r = r0 + 16 * i + (lane & 15);
+      const int64_t row = g.begin + (r < g.rows ? r : g.rows - 1);
+      arow[i] = p.Aq + row * p.ldq + q * 16;
+      asc[i] = p.As + 4 * row + q;
+    }
+    for (int s0 = wave; s0 < nkt; s0 += kFewWaves * kAhead) {
+      uint4 b[kAhead], a[kAhead][MF];
+      int sb[kAhead], sa[kAhead][MF];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        // steps past the end repeat the last one and are not multiplied
+        const int s = s0 + u * kFewWaves < nkt ? s0 + u * kFewWaves : nkt - 1;
+        b[u] = *reinterpret_cast<const uint4*>(brow + s * 64);
+        sb[u] = bsc[s * bstep];
+#pragma unroll
+        for (int i = 0; i < MF; ++i) {
+          a[u][i] = *reinterpret_cast<const uint4*>(arow[i] + s * 64);
+          sa[u][i] = asc[i][s * astep];
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        if (s0 + u * kFewWaves < nkt) {
+          const v8i bf{int(b[u].x), int(b[u].y), int(b[u].z), int(b[u].w), 0, 0, 0, 0};
+#pragma unroll
+          for (int i = 0; i < MF; ++i) {
+            const v8i af{int(a[u][i].x), int(a[u][i].y), int(a[u][i].z), int(a[u][i].w), 0, 0, 0, 0};
+            acc[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(af, bf, acc[i], 4, 4, 0,
+                                                                      sa[u][i], 0, sb[u]);
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < MF; ++i) part[wave][i][lane] = acc[i];
+    __syncthreads();
+    // wave w finishes the fragments w, w + 4, ...
+#pragma unroll
+    for (int i = 0; i < MF; ++i) {
+      if (i % kFewWaves != wave) continue;
+      v4f sum = part[0][i][lane];
+#pragma unroll
+      for (int w = 1; w < kFewWaves; ++w) sum += part[w][i][lane];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int r = r0 + 16 * i + 4 * q + c;
+        if (r < g.rows && n < p.N) store_out(Y + (g.begin + r) * p.ldy + n, sum[c]);
+      }
+    }
+    __syncthreads();
+  }
+}
+
+using LargeTile = GemmCfg<256, 256, 4, 2, 64, 1>;
+using SmallTile = GemmCfg<128, 256, 2, 2, 64, 2>;
+constexpr int kLargeTilesMin = 512;
+constexpr int64_t kFewRows = 32;  // rows an expert on average
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+template <class C, class Out, bool kWgrad>
+hipError_t run_tiles(const TileArgs& p, int64_t tiles, hipStream_t stream) {
+  if (tiles >= (int64_t(1) << 31)) return hipErrorInvalidValue;
+  experts_gemm_kernel<C, Out, kWgrad><<<dim3(unsigned(tiles)), C::kThreads, 0, stream>>>(p);
+  return hipGetLastError();
+}
+
+// Row tiles of BM rows that M rows in at most E + 1 groups can need.
+int64_t most_units(int64_t M, int64_t E, int64_t R) {
+  const int64_t groups = E + 1 < M ? E + 1 : M;
+  return (M + groups * (R - 1)) / R;
+}
+
+template <class Out>
+hipError_t run_rows(const TileArgs& p, hipStream_t stream) {
+  const int64_t tiles_n = ceil_div(p.cols, 256);
+  if (p.M <= kFewRows * p.E && p.E < 65535) {
+    const FewArgs a{p.Aq, p.As, p.Bq, p.Bs, p.row_end, p.E, p.M, p.cols, p.ldq, p.Y, p.ldy};
+    const dim3 grid(unsigned(ceil_div(p.cols, 16)), unsigned(p.E + 1));
+    if (p.M <= 16 * p.E)
+      experts_few_kernel<1, Out><<<grid, kFewWaves * 64, 0, stream>>>(a);
+    else
+      experts_few_kernel<2, Out><<<grid, kFewWaves * 64, 0, stream>>>(a);
+    return hipGetLastError();
+  }
+  if (ceil_div(p.M, LargeTile::BM) * tiles_n >= kLargeTilesMin)
+    return run_tiles<LargeTile, Out, false>(p, most_units(p.M, p.E, LargeTile::BM) * tiles_n,
+                                            stream);
+  return run_tiles<SmallTile, Out, false>(p, most_units(p.M, p.E, SmallTile::BM) * tiles_n, stream);
+}
+
+template <class Out>
+hipError_t run_wgrad(const TileArgs& p, hipStream_t stream) {
+  const int64_t tiles_n = ceil_div(p.cols, 256);
+  const int64_t large = p.E * ceil_div(p.rows, LargeTile::BM) * tiles_n;
+  if (large >= kLargeTilesMin) return run_tiles<LargeTile, Out, true>(p, large, stream);
+  return run_tiles<SmallTile, Out, true>(p, p.E * ceil_div(p.rows, SmallTile::BM) * tiles_n,
+                                         stream);
+}
+
+template <class In>
+hipError_t run_cols(const void* Wp, int64_t E, int64_t K, int64_t N, int64_t ldw, uint8_t* Wq,
+                    int64_t ldq, uint8_t* Ws, hipStream_t stream) {
+  const auto* W = static_cast<const typename In::T*>(Wp);
+  const bool aligned = (reinterpret_cast<uintptr_t>(Wp) % 16 == 0) && ((ldw * In::kBytes) % 16 == 0);
+  const dim3 grid(unsigned(ceil_div(N, kMxTN)), unsigned((ldq * 2) / kMxTK), unsigned(E));
+  if (aligned)
+    experts_cols_mx_kernel<In, true><<<grid, kThreads, 0, stream>>>(W, K, N, ldw, E * N, Wq, ldq, Ws);
+  else
+    experts_cols_mx_kernel<In, false><<<grid, kThreads, 0, stream>>>(W, K, N, ldw, E * N, Wq, ldq, Ws);
+  return hipGetLastError();
+}
+
+template <class In>
+hipError_t run_ragged(const void* Xp, const int32_t* row_end, int64_t E, int64_t M, int64_t N,
+                      int64_t ldx, uint8_t* Xq, int64_t steps, uint8_t* Xs, hipStream_t stream) {
+  const auto* X = static_cast<const typename In::T*>(Xp);
+  const bool aligned = (reinterpret_cast<uintptr_t>(Xp) % 16 == 0) && ((ldx * In::kBytes) % 16 == 0);
+  const dim3 grid(unsigned(ceil_div(N, kMxTN)), unsigned(steps));
+  if (aligned)
+    experts_ragged_mx_kernel<In, true><<<grid, kThreads, 0, stream>>>(X, row_end, int(E), int(M), N,
+                                                                      ldx, Xq, steps * 64, Xs);
+  else
+    experts_ragged_mx_kernel<In, false><<<grid, kThreads, 0, stream>>>(X, row_end, int(E), int(M),
+                                                                       N, ldx, Xq, steps * 64, Xs);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+int64_t experts_steps(int64_t E, int64_t M) {
+  const int64_t groups = E < M ? E : M;
+  return (M + groups * 127) / 128;
+}
+
+hipError_t launch_experts_quantize_cols_mx(const void* W, bool bf16, int64_t E, int64_t K,
+                                           int64_t N, int64_t ldw, uint8_t* Wq, int64_t ldq,
+                                           uint8_t* Ws, hipStream_t stream) {
+  return bf16 ? run_cols<BF16In>(W, E, K, N, ldw, Wq, ldq, Ws, stream)
+              : run_cols<F32In>(W, E, K, N, ldw, Wq, ldq, Ws, stream);
+}
+
+hipError_t launch_experts_quantize_ragged_mx(const void* X, bool bf16, const int32_t* row_end,
+                                             int64_t E, int64_t M, int64_t N, int64_t ldx,
+                                             uint8_t* Xq, uint8_t* Xs, hipStream_t stream) {
+  const int64_t steps = experts_steps(E, M);
+  if (steps == 0) return hipSuccess;
+  return bf16 ? run_ragged<BF16In>(X, row_end, E, M, N, ldx, Xq, steps, Xs, stream)
+              : run_ragged<F32In>(X, row_end, E, M, N, ldx, Xq, steps, Xs, stream);
+}
+
+hipError_t launch_experts_rows(const uint8_t* Aq, const uint8_t* As, const uint8_t* Bq,
+                               const uint8_t* Bs, const int32_t* row_end, int64_t E, int64_t M,
+                               int64_t N, int64_t ldq, void* Y, bool y_bf16, int64_t ldy,
+                               hipStream_t stream) {
+  const TileArgs p{Aq, As, Bq, Bs, row_end, int(E), int(M), 0, int(N), int(ldq), Y, ldy};
+  return y_bf16 ? run_rows<uint16_t>(p, stream) : run_rows<float>(p, stream);
+}
+
+hipError_t launch_experts_wgrad(const uint8_t* Aq, const uint8_t* As, const uint8_t* Bq,
+                                const uint8_t* Bs, const int32_t* row_end, int64_t E, int64_t M,
+                                int64_t K, int64_t N, void* dW, bool w_bf16, int64_t ldw,
+                                hipStream_t stream) {
+  const TileArgs p{Aq, As, Bq, Bs, row_end, int(E), int(M), int(K), int(N),
+                   int(experts_steps(E, M) * 64), dW, ldw};
+  return w_bf16 ? run_wgrad<uint16_t>(p, stream) : run_wgrad<float>(p, stream);
+}
+
+}  // namespace fp4lin

@@ -81,4 +81,25 @@ hipError_t launch_fp4_gemm_mx(const uint8_t* Aq, const uint8_t* As, const uint8_
                               const uint8_t* Bs, int64_t M, int64_t N, int64_t ldq,
                               const SparseArgs& sp, float* Y, int64_t ldy, hipStream_t stream);
 
+// Products grouped by expert (experts.hip). experts_steps: the K steps (128
+// rows) of a reduction over each expert's own rows, for any split of M rows.
+int64_t experts_steps(int64_t E, int64_t M);
+hipError_t launch_experts_quantize_cols_mx(const void* W, bool bf16, int64_t E, int64_t K,
+                                           int64_t N, int64_t ldw, uint8_t* Wq, int64_t ldq,
+                                           uint8_t* Ws, hipStream_t stream);
+// Columns of X packed along each expert's rows: N rows of experts_steps * 64
+// bytes, scales step-major.
+hipError_t launch_experts_quantize_ragged_mx(const void* X, bool bf16, const int32_t* row_end,
+                                             int64_t E, int64_t M, int64_t N, int64_t ldx,
+                                             uint8_t* Xq, uint8_t* Xs, hipStream_t stream);
+// M rows against N packed columns of each expert (forward, dgrad, apply).
+hipError_t launch_experts_rows(const uint8_t* Aq, const uint8_t* As, const uint8_t* Bq,
+                               const uint8_t* Bs, const int32_t* row_end, int64_t E, int64_t M,
+                               int64_t N, int64_t ldq, void* Y, bool y_bf16, int64_t ldy,
+                               hipStream_t stream);
+hipError_t launch_experts_wgrad(const uint8_t* Aq, const uint8_t* As, const uint8_t* Bq,
+                                const uint8_t* Bs, const int32_t* row_end, int64_t E, int64_t M,
+                                int64_t K, int64_t N, void* dW, bool w_bf16, int64_t ldw,
+                                hipStream_t stream);
+
 }  // namespace fp4lin
