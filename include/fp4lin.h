@@ -80,7 +80,8 @@ typedef enum {
   FP4LIN_ERR_ALIGN = 6,      /* a pointer that must be 16-byte aligned is not   */
   FP4LIN_ERR_WORKSPACE = 7,  /* workspace smaller than the *_workspace_bytes   */
   FP4LIN_ERR_LAUNCH = 8,     /* the HIP runtime rejected a kernel launch        */
-  FP4LIN_ERR_SCRATCH = 9     /* beyond the allocation-free call's static scratch */
+  FP4LIN_ERR_SCRATCH = 9,    /* beyond the allocation-free call's static scratch */
+  FP4LIN_ERR_VALUE = 10      /* a number argument is NaN or outside its range   */
 } fp4lin_status;
 
 typedef enum { FP4LIN_F32 = 0, FP4LIN_BF16 = 1 } fp4lin_dtype;
@@ -454,6 +455,87 @@ fp4lin_status fp4lin_experts_wgrad_mx(const void* A, const void* dY, fp4lin_dtyp
                                       int64_t N, int64_t lda, int64_t lddy, void* dW,
                                       fp4lin_dtype wdt, int64_t lddw, void* ws, size_t ws_bytes,
                                       hipStream_t stream);
+
+/* ---- Head loss: softmax cross entropy of a large vocabulary ----------------
+ *   l = X W,  lse_t = log sum_v exp l_tv,  loss_t = lse_t - l_(t, target_t)
+ *   G_tv = (exp(l_tv - lse_t) - [v = target_t]) * dloss_t
+ *   dX = G W^T,  dW = X^T G
+ * without the T x V logits in memory: the forward keeps a maximum and a sum
+ * per row and group of columns, the backward forms the logits again in pieces
+ * of the vocabulary.
+ *   X        device, T x H, dtype dt, leading dimension ldx
+ *   W        device, dtype dt, leading dimension ldw: H x V (layout
+ *            FP4LIN_HEAD_HIDDEN_MAJOR, in-features x out-features) or V x H
+ *            (FP4LIN_HEAD_VOCAB_MAJOR, as an embedding shares it)
+ *   target   device, T int32. A target outside [0, V) leaves its row out: loss
+ *            0, no gradient. (lse is that of the row's logits all the same.)
+ * X, W and the workspace must be 16-byte aligned; any sizes and leading
+ * dimensions (where a row of X or W is not a multiple of 8 elements or its
+ * stride not one of 16 bytes, a padded copy is kept in the workspace).
+ * T = 0 is a valid batch (a weight gradient is all zeros). Sums are fp32; in
+ * the backward G is rounded to dt before the two products that take it.
+ * Limits: 256 * ld * element size < 2^31 for every leading dimension. */
+typedef enum { FP4LIN_HEAD_HIDDEN_MAJOR = 0, FP4LIN_HEAD_VOCAB_MAJOR = 1 } fp4lin_head_layout;
+
+/* Bytes of workspace of the two calls (at least 256); 0 for invalid
+ * arguments. */
+size_t fp4lin_head_loss_workspace_bytes(fp4lin_dtype dt, fp4lin_head_layout layout, int64_t T,
+                                        int64_t H, int64_t V, int64_t ldx, int64_t ldw);
+size_t fp4lin_head_loss_backward_workspace_bytes(fp4lin_dtype dt, fp4lin_head_layout layout,
+                                                 int64_t T, int64_t H, int64_t V, int64_t ldx,
+                                                 int64_t ldw);
+
+/*   loss, lse  device, T floats each (outputs)
+ * Errors: NULL, SHAPE, DTYPE, ALIGN, WORKSPACE, LAUNCH. */
+fp4lin_status fp4lin_head_loss(const void* X, const void* W, fp4lin_dtype dt,
+                               fp4lin_head_layout layout, const int32_t* target, int64_t T,
+                               int64_t H, int64_t V, int64_t ldx, int64_t ldw, float* loss,
+                               float* lse, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/*   lse      device, T floats, from fp4lin_head_loss on the same X and W
+ *   dloss    device, T floats: the gradient of each row's loss
+ *   dX       device, T x H, dtype dt, leading dimension lddx (output)
+ *   dW       device, dtype dt, leading dimension lddw, laid out as W (output)
+ * Errors: NULL, SHAPE, DTYPE, ALIGN, WORKSPACE, LAUNCH. */
+fp4lin_status fp4lin_head_loss_backward(const void* X, const void* W, fp4lin_dtype dt,
+                                        fp4lin_head_layout layout, const int32_t* target,
+                                        const float* lse, const float* dloss, int64_t T, int64_t H,
+                                        int64_t V, int64_t ldx, int64_t ldw, void* dX, int64_t lddx,
+                                        void* dW, int64_t lddw, void* ws, size_t ws_bytes,
+                                        hipStream_t stream);
+
+/* ---- Global gradient norm and clipping -------------------------------------
+ * Over the elements of all tensors together,
+ *   norm = sqrt(sum g^2)     (summed in double, in an order that the sizes fix)
+ *   out  = g * c,  c = min(1, max_norm / (norm + 1e-6))    (fp32, rounded once)
+ * A NaN in any tensor makes norm and every output NaN; an infinity makes norm
+ * infinite, c zero and the infinite elements NaN. */
+typedef struct {
+  const void* g;    /* device, n elements of dtype dt, contiguous (NULL if n = 0) */
+  void* out;        /* device, n elements of dtype dt; may be g, else no overlap  */
+  int64_t n;
+  fp4lin_dtype dt;
+} fp4lin_grad;
+
+/* Bytes of workspace for `count` tensors of `elements` elements in all; 0 for
+ * invalid arguments. */
+size_t fp4lin_clip_workspace_bytes(int64_t count, int64_t elements);
+
+/* The norm alone (out is not used).
+ *   grads    host, count entries, read before the call returns
+ *   norm     device, 1 float (output)
+ *   ws       device, 16-byte aligned, >= fp4lin_clip_workspace_bytes
+ * Errors: NULL, SHAPE, DTYPE, ALIGN, WORKSPACE, LAUNCH. */
+fp4lin_status fp4lin_grad_norm(const fp4lin_grad* grads /* host */, int64_t count, float* norm,
+                               void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* The norm and the clipped gradients. With out = g nothing is written where
+ * c = 1. max_norm must be a number >= 0, else FP4LIN_ERR_VALUE. A tensor must
+ * not be listed twice.
+ * Errors: NULL, SHAPE, DTYPE, VALUE, ALIGN, WORKSPACE, LAUNCH. */
+fp4lin_status fp4lin_clip_grads(const fp4lin_grad* grads /* host */, int64_t count,
+                                double max_norm, float* norm, void* ws, size_t ws_bytes,
+                                hipStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -27,6 +27,9 @@ __all__ = [
     "fp4lin_experts_apply_mx", "fp4lin_experts_dgrad_mx", "fp4lin_experts_wgrad_mx",
     "experts_quantize_weight_mx", "experts_forward_mx", "experts_apply_mx", "experts_dgrad_mx",
     "experts_wgrad_mx",
+    "head_loss_workspace_bytes", "fp4lin_head_loss", "fp4lin_head_loss_backward", "head_loss",
+    "head_loss_backward", "clip_workspace_bytes", "fp4lin_grad_norm", "fp4lin_clip_grads",
+    "grad_norm", "clip_grads",
 ]
 
 
@@ -575,3 +578,184 @@ def experts_wgrad_mx(A, dY, row_end, out_dtype=None, stream=None):
         ws = _experts_ws(_lib.EXPERTS_WGRAD, E, M, K, N, A.device, "experts_wgrad_mx")
         fp4lin_experts_wgrad_mx(A, dY, row_end, dW, ws)
     return dW
+
+
+# ---- head loss -------------------------------------------------------------------------
+def head_loss_workspace_bytes(dtype_code, by_vocab, T, H, V, ldx, ldw, backward=False) -> int:
+    f = lib().fp4lin_head_loss_backward_workspace_bytes if backward else \
+        lib().fp4lin_head_loss_workspace_bytes
+    return int(f(dtype_code, int(bool(by_vocab)), T, H, V, ldx, ldw))
+
+
+def _head_sizes(X, W, target, by_vocab):
+    """(T, H, V, ldx, ldw) of matching X, W and targets."""
+    torch = _torch()
+    T, H, ldx = _rows(X, "X")
+    r, c, ldw = _rows(W, "W")
+    _same("dtype", X=X, W=W)
+    _same("", X=X, target=target)
+    _need((c if by_vocab else r) == H, f"X is {T}x{H} but W is {r}x{c}" +
+          (" (vocabulary first)" if by_vocab else ""))
+    if target.dtype != torch.int32 or target.dim() != 1 or not target.is_contiguous():
+        raise TypeError("target must be a contiguous int32 vector")
+    _need(target.numel() == T, f"{target.numel()} targets for {T} rows")
+    return T, H, r if by_vocab else c, ldx, ldw
+
+
+def _row_floats(t, T, name):
+    torch = _torch()
+    if t.dtype != torch.float32 or t.dim() != 1 or not t.is_contiguous():
+        raise TypeError(f"{name} must be a contiguous float32 vector")
+    _need(t.numel() == T, f"{name} has {t.numel()} entries for {T} rows")
+    return _dev(t, name)
+
+
+def fp4lin_head_loss(X, W, target, loss, lse, ws, by_vocab=False, stream=None):
+    T, H, V, ldx, ldw = _head_sizes(X, W, target, by_vocab)
+    _same("", X=X, loss=loss, lse=lse, ws=ws)
+    _check(lib().fp4lin_head_loss(
+        _dev(X, "X"), _dev(W, "W"), _dtype_code(X), int(bool(by_vocab)), _dev(target, "target"), T,
+        H, V, ldx, ldw, _row_floats(loss, T, "loss"), _row_floats(lse, T, "lse"), _dev(ws, "ws"),
+        _nbytes(ws), _stream(stream)), "fp4lin_head_loss")
+
+
+def fp4lin_head_loss_backward(X, W, target, lse, dloss, dX, dW, ws, by_vocab=False, stream=None):
+    T, H, V, ldx, ldw = _head_sizes(X, W, target, by_vocab)
+    _same("dtype", X=X, dX=dX, dW=dW)
+    _same("", X=X, lse=lse, dloss=dloss, ws=ws)
+    Tx, Hx, lddx = _rows(dX, "dX")
+    r, c, lddw = _rows(dW, "dW")
+    _need((Tx, Hx) == (T, H), f"dX is {Tx}x{Hx}, not {T}x{H}")
+    _need((r, c) == tuple(W.shape), f"dW is {r}x{c}, W {W.shape[0]}x{W.shape[1]}")
+    _check(lib().fp4lin_head_loss_backward(
+        _dev(X, "X"), _dev(W, "W"), _dtype_code(X), int(bool(by_vocab)), _dev(target, "target"),
+        _row_floats(lse, T, "lse"), _row_floats(dloss, T, "dloss"), T, H, V, ldx, ldw,
+        _dev(dX, "dX"), lddx, _dev(dW, "dW"), lddw, _dev(ws, "ws"), _nbytes(ws), _stream(stream)),
+        "fp4lin_head_loss_backward")
+
+
+def _aligned(t):
+    """t, or a copy of it where its first element is not 16-byte aligned."""
+    return t if t.data_ptr() % 16 == 0 else t.clone(memory_format=_torch().contiguous_format)
+
+
+def _head_ws(X, W, T, H, V, ldx, ldw, by_vocab, backward, where):
+    n = head_loss_workspace_bytes(_dtype_code(X), by_vocab, T, H, V, ldx, ldw, backward)
+    if n == 0:
+        raise Fp4linError(_lib.ERR_SHAPE, where)
+    return _empty((n,), _torch().uint8, X.device)
+
+
+def head_loss(X, W, target, by_vocab=False, stream=None):
+    """Cross entropy of the rows' logits X W against target (int32), without
+    keeping the logits. X is (T, H), W (H, V) or with by_vocab (V, H); float32 or
+    bfloat16. Returns (loss, lse), float32 of T entries; a row whose target
+    lies outside [0, V) has loss 0."""
+    torch = _torch()
+    _head_sizes(X, W, target, by_vocab)
+    with _on(X, stream):
+        X, W = _aligned(X), _aligned(W)
+        T, H, V, ldx, ldw = _head_sizes(X, W, target, by_vocab)
+        ws = _head_ws(X, W, T, H, V, ldx, ldw, by_vocab, False, "head_loss")
+        loss = _empty((T,), torch.float32, X.device)
+        lse = _empty((T,), torch.float32, X.device)
+        fp4lin_head_loss(X, W, target, loss, lse, ws, by_vocab)
+    return loss, lse
+
+
+def head_loss_backward(X, W, target, lse, dloss, by_vocab=False, stream=None):
+    """Gradients of sum(dloss * loss) of head_loss: (dX, dW), of X's and W's
+    shape and dtype. lse is head_loss's, dloss float32 of T entries."""
+    _head_sizes(X, W, target, by_vocab)
+    with _on(X, stream):
+        X, W = _aligned(X), _aligned(W)
+        T, H, V, ldx, ldw = _head_sizes(X, W, target, by_vocab)
+        ws = _head_ws(X, W, T, H, V, ldx, ldw, by_vocab, True, "head_loss_backward")
+        dX = _empty((T, H), X.dtype, X.device)
+        dW = _empty(tuple(W.shape), W.dtype, W.device)
+        fp4lin_head_loss_backward(X, W, target, lse, dloss, dX, dW, ws, by_vocab)
+    return dX, dW
+
+
+# ---- gradient norm and clipping ----------------------------------------------------------
+def clip_workspace_bytes(count: int, elements: int) -> int:
+    return int(lib().fp4lin_clip_workspace_bytes(count, elements))
+
+
+def _dense(t, name):
+    """A tensor whose elements fill its memory without gaps or overlaps."""
+    if t.is_contiguous() or t.numel() == 0:
+        return
+    at = 1
+    for stride, size in sorted((t.stride(d), t.shape[d]) for d in range(t.dim()) if t.shape[d] > 1):
+        if stride != at:
+            raise ValueError(f"{name} must be dense in memory")
+        at *= size
+
+
+def _grads(tensors, out):
+    """The C array of a list of gradients and its outputs, and its elements."""
+    tensors = list(tensors)
+    out = tensors if out is None else list(out)
+    _need(len(out) == len(tensors), f"{len(out)} outputs for {len(tensors)} gradients")
+    array = (_lib.Grad * max(len(tensors), 1))()
+    elements, device = 0, None
+    for i, (g, o) in enumerate(zip(tensors, out)):
+        _dev(g, "gradient")
+        if device is None:
+            device = g.device
+        _need(g.device == device, f"gradient {i} is on {g.device}, the first on {device}")
+        _dense(g, f"gradient {i}")
+        if o is not g:
+            _dev(o, "output")
+            if o.dtype != g.dtype:
+                raise TypeError(f"output {i} is {o.dtype}, gradient {i} {g.dtype}")
+            _need(o.device == device and o.shape == g.shape and
+                  (o.stride() == g.stride() or (o.is_contiguous() and g.is_contiguous())),
+                  f"output {i} must have the shape, strides and device of gradient {i}")
+        array[i] = _lib.Grad(g.data_ptr(), o.data_ptr(), g.numel(), _dtype_code(g))
+        elements += g.numel()
+    return array, len(tensors), elements
+
+
+def fp4lin_grad_norm(tensors, norm, ws, stream=None):
+    array, count, _ = _grads(tensors, None)
+    _check(lib().fp4lin_grad_norm(array, count, _dev(norm, "norm"), _dev(ws, "ws"), _nbytes(ws),
+                                  _stream(stream)), "fp4lin_grad_norm")
+
+
+def fp4lin_clip_grads(tensors, max_norm, norm, ws, out=None, stream=None):
+    array, count, _ = _grads(tensors, out)
+    _check(lib().fp4lin_clip_grads(array, count, float(max_norm), _dev(norm, "norm"),
+                                   _dev(ws, "ws"), _nbytes(ws), _stream(stream)),
+           "fp4lin_clip_grads")
+
+
+def _clip(tensors, max_norm, out, stream):
+    torch = _torch()
+    tensors = list(tensors)
+    _need(len(tensors) > 0, "no gradients")
+    array, count, elements = _grads(tensors, out)
+    _dev(tensors[0], "gradient")
+    with _on(tensors[0], stream):
+        device = tensors[0].device
+        ws = _empty((clip_workspace_bytes(count, elements),), torch.uint8, device)
+        norm = _empty((), torch.float32, device)
+        args = (_dev(norm, "norm"), _dev(ws, "ws"), _nbytes(ws), _stream(None))
+        if max_norm is None:
+            _check(lib().fp4lin_grad_norm(array, count, *args), "grad_norm")
+        else:
+            _check(lib().fp4lin_clip_grads(array, count, float(max_norm), *args), "clip_grads")
+    return norm
+
+
+def grad_norm(tensors, stream=None):
+    """2-norm of all elements of a list of float32 or bfloat16 tensors (a
+    float32 scalar on the GPU)."""
+    return _clip(tensors, None, None, stream)
+
+
+def clip_grads(tensors, max_norm, out=None, stream=None):
+    """Scales the tensors by min(1, max_norm / (norm + 1e-6)), norm their global
+    2-norm, in place or into the list `out`; returns norm (on the GPU)."""
+    return _clip(tensors, max_norm, out, stream)

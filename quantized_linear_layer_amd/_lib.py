@@ -14,8 +14,10 @@ c_int = ctypes.c_int
 
 # enum values of fp4lin_status / fp4lin_dtype
 OK, ERR_NULL, ERR_SHAPE, ERR_DTYPE, ERR_QUANTILE, ERR_CAPACITY, ERR_ALIGN, ERR_WORKSPACE, \
-    ERR_LAUNCH, ERR_SCRATCH = range(10)
+    ERR_LAUNCH, ERR_SCRATCH, ERR_VALUE = range(11)
 F32, BF16 = 0, 1
+# fp4lin_head_layout
+HEAD_HIDDEN_MAJOR, HEAD_VOCAB_MAJOR = 0, 1
 # fp4lin_experts_pass
 EXPERTS_FORWARD, EXPERTS_DGRAD, EXPERTS_WGRAD, EXPERTS_APPLY = range(4)
 
@@ -29,6 +31,10 @@ class ForwardOffsets(ctypes.Structure):
     _fields_ = [("tau", c_size), ("coo_row", c_size), ("coo_col", c_size), ("coo_val", c_size),
                 ("row_ptr", c_size), ("Aq", c_size), ("sA", c_size), ("Wq", c_size),
                 ("sW", c_size), ("scratch", c_size), ("capacity", c_i64), ("total", c_size)]
+
+
+class Grad(ctypes.Structure):
+    _fields_ = [("g", c_ptr), ("out", c_ptr), ("n", c_i64), ("dt", c_int)]
 
 
 # name -> (restype, argtypes); every symbol declared in include/fp4lin.h
@@ -81,6 +87,17 @@ SIGNATURES = {
                                         c_i64, c_i64, c_ptr, c_int, c_i64, c_ptr, c_size, c_ptr]),
     "fp4lin_experts_wgrad_mx": (c_int, [c_ptr, c_ptr, c_int, c_ptr, c_i64, c_i64, c_i64, c_i64,
                                         c_i64, c_i64, c_ptr, c_int, c_i64, c_ptr, c_size, c_ptr]),
+    "fp4lin_head_loss_workspace_bytes": (c_size, [c_int, c_int, c_i64, c_i64, c_i64, c_i64, c_i64]),
+    "fp4lin_head_loss_backward_workspace_bytes": (c_size, [c_int, c_int, c_i64, c_i64, c_i64, c_i64,
+                                                           c_i64]),
+    "fp4lin_head_loss": (c_int, [c_ptr, c_ptr, c_int, c_int, c_ptr, c_i64, c_i64, c_i64, c_i64,
+                                 c_i64, c_ptr, c_ptr, c_ptr, c_size, c_ptr]),
+    "fp4lin_head_loss_backward": (c_int, [c_ptr, c_ptr, c_int, c_int, c_ptr, c_ptr, c_ptr, c_i64,
+                                          c_i64, c_i64, c_i64, c_i64, c_ptr, c_i64, c_ptr, c_i64,
+                                          c_ptr, c_size, c_ptr]),
+    "fp4lin_clip_workspace_bytes": (c_size, [c_i64, c_i64]),
+    "fp4lin_grad_norm": (c_int, [ctypes.POINTER(Grad), c_i64, c_ptr, c_ptr, c_size, c_ptr]),
+    "fp4lin_clip_grads": (c_int, [ctypes.POINTER(Grad), c_i64, c_dbl, c_ptr, c_ptr, c_size, c_ptr]),
 }
 
 _lib = None

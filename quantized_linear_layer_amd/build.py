@@ -22,7 +22,7 @@ LIB = os.path.join(PKG, "libfp4lin.so")
 ARCH = "gfx950"
 
 SOURCES = ["api.hip", "select.hip", "quantize.hip", "mx.hip", "gemm.hip", "spmm.hip",
-           "experts.hip"]
+           "experts.hip", "head.hip", "clip.hip"]
 
 # Packed fp32 VALU ops are switched off for all device code; fp32 denormals are
 # kept (inputs may be subnormal and the encoder must see them); no FMA

@@ -170,6 +170,7 @@ const char* fp4lin_status_str(fp4lin_status s) {
     case FP4LIN_ERR_WORKSPACE: return "workspace too small";
     case FP4LIN_ERR_LAUNCH: return "kernel launch failed";
     case FP4LIN_ERR_SCRATCH: return "input needs more than the static scratch of the allocation-free call";
+    case FP4LIN_ERR_VALUE: return "a number argument is NaN or out of range";
   }
   return "unknown status";
 }
@@ -731,6 +732,194 @@ fp4lin_status fp4lin_experts_wgrad_mx(const void* A, const void* dY, fp4lin_dtyp
   return launch_status(fp4lin::launch_experts_wgrad(base + o.Aq, base + o.As, base + o.Bq,
                                                     base + o.Bs, row_end, E, M, K, N, dW,
                                                     wdt == FP4LIN_BF16, lddw, stream));
+}
+
+}  // extern "C"
+
+// ---- head loss ------------------------------------------------------------------
+namespace {
+
+struct HeadLayout {
+  fp4lin::HeadPlan plan;
+  size_t x, w, part, tlogit, G, acc, total;
+};
+
+// Sizes and strides that both calls check, and where they keep what they keep.
+fp4lin_status head_layout(fp4lin_dtype dt, fp4lin_head_layout layout, int64_t T, int64_t H,
+                          int64_t V, int64_t ldx, int64_t ldw, bool backward, HeadLayout* out) {
+  if (bad_dtype(dt)) return FP4LIN_ERR_DTYPE;
+  const bool by_vocab = layout == FP4LIN_HEAD_VOCAB_MAJOR;
+  if (!by_vocab && layout != FP4LIN_HEAD_HIDDEN_MAJOR) return FP4LIN_ERR_SHAPE;
+  const int64_t esz = dt == FP4LIN_BF16 ? 2 : 4;
+  const int64_t most = kMaxDim / 256 / esz - 16;  // of a leading dimension
+  if (!ok_rows(T) || !ok_dim(H) || !ok_dim(V) || ldx < H || ldw < (by_vocab ? H : V))
+    return FP4LIN_ERR_SHAPE;
+  if (ldx > most || ldw > most || H > most || V > most) return FP4LIN_ERR_SHAPE;
+  // tiles index a grid of at most 2^31 - 1 workgroups
+  if ((double(T) / 64 + 1) * (double(V) / 128 + 1) >= double(kMaxDim)) return FP4LIN_ERR_SHAPE;
+  HeadLayout o{};
+  o.plan = fp4lin::head_plan(dt == FP4LIN_BF16, T, H, V, by_vocab, ldx, ldw);
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off = round_up(off + bytes, 256);
+    return at;
+  };
+  o.x = take(size_t(o.plan.x_bytes));
+  o.w = take(size_t(o.plan.w_bytes));
+  if (backward) {
+    o.G = take(size_t(T) * size_t(o.plan.ldg) * size_t(esz));
+    o.acc = take(size_t(T) * size_t(o.plan.ldp) * size_t(o.plan.slices) * 4);
+  } else {
+    o.part = take(size_t(T) * size_t(o.plan.parts) * 8);
+    o.tlogit = take(size_t(T) * 4);
+  }
+  o.total = off > 256 ? off : 256;
+  *out = o;
+  return FP4LIN_OK;
+}
+
+fp4lin_status head_call(const void* X, const void* W, fp4lin_dtype dt, fp4lin_head_layout layout,
+                        const int32_t* target, int64_t T, int64_t H, int64_t V, int64_t ldx,
+                        int64_t ldw, void* ws, size_t ws_bytes, bool backward, HeadLayout* o,
+                        fp4lin::HeadCall* c) {
+  const fp4lin_status s = head_layout(dt, layout, T, H, V, ldx, ldw, backward, o);
+  if (s != FP4LIN_OK) return s;
+  if (ws == nullptr) return FP4LIN_ERR_NULL;
+  if (!aligned16(ws) || !aligned16(X) || !aligned16(W)) return FP4LIN_ERR_ALIGN;
+  if (ws_bytes < o->total) return FP4LIN_ERR_WORKSPACE;
+  char* const base = static_cast<char*>(ws);
+  *c = fp4lin::HeadCall{};
+  c->X = X;
+  c->W = W;
+  c->T = T;
+  c->H = H;
+  c->V = V;
+  c->ldx = ldx;
+  c->ldw = ldw;
+  c->by_vocab = layout == FP4LIN_HEAD_VOCAB_MAJOR;
+  c->target = target;
+  c->packed_x = base + o->x;
+  c->packed_w = base + o->w;
+  c->part = base + o->part;
+  c->tlogit = reinterpret_cast<float*>(base + o->tlogit);
+  c->G = base + o->G;
+  c->acc = reinterpret_cast<float*>(base + o->acc);
+  return FP4LIN_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t fp4lin_head_loss_workspace_bytes(fp4lin_dtype dt, fp4lin_head_layout layout, int64_t T,
+                                        int64_t H, int64_t V, int64_t ldx, int64_t ldw) {
+  HeadLayout o;
+  return head_layout(dt, layout, T, H, V, ldx, ldw, false, &o) == FP4LIN_OK ? o.total : 0;
+}
+
+size_t fp4lin_head_loss_backward_workspace_bytes(fp4lin_dtype dt, fp4lin_head_layout layout,
+                                                 int64_t T, int64_t H, int64_t V, int64_t ldx,
+                                                 int64_t ldw) {
+  HeadLayout o;
+  return head_layout(dt, layout, T, H, V, ldx, ldw, true, &o) == FP4LIN_OK ? o.total : 0;
+}
+
+fp4lin_status fp4lin_head_loss(const void* X, const void* W, fp4lin_dtype dt,
+                               fp4lin_head_layout layout, const int32_t* target, int64_t T,
+                               int64_t H, int64_t V, int64_t ldx, int64_t ldw, float* loss,
+                               float* lse, void* ws, size_t ws_bytes, hipStream_t stream) {
+  if (W == nullptr ||
+      (T != 0 && (X == nullptr || target == nullptr || loss == nullptr || lse == nullptr)))
+    return FP4LIN_ERR_NULL;
+  HeadLayout o;
+  fp4lin::HeadCall c;
+  const fp4lin_status s =
+      head_call(X, W, dt, layout, target, T, H, V, ldx, ldw, ws, ws_bytes, false, &o, &c);
+  if (s != FP4LIN_OK || T == 0) return s;
+  c.loss = loss;
+  c.lse_out = lse;
+  return launch_status(fp4lin::launch_head_loss(c, dt == FP4LIN_BF16, o.plan, stream));
+}
+
+fp4lin_status fp4lin_head_loss_backward(const void* X, const void* W, fp4lin_dtype dt,
+                                        fp4lin_head_layout layout, const int32_t* target,
+                                        const float* lse, const float* dloss, int64_t T, int64_t H,
+                                        int64_t V, int64_t ldx, int64_t ldw, void* dX, int64_t lddx,
+                                        void* dW, int64_t lddw, void* ws, size_t ws_bytes,
+                                        hipStream_t stream) {
+  if (W == nullptr || dW == nullptr ||
+      (T != 0 && (X == nullptr || target == nullptr || lse == nullptr || dloss == nullptr ||
+                  dX == nullptr)))
+    return FP4LIN_ERR_NULL;
+  HeadLayout o;
+  fp4lin::HeadCall c;
+  const fp4lin_status s =
+      head_call(X, W, dt, layout, target, T, H, V, ldx, ldw, ws, ws_bytes, true, &o, &c);
+  if (s != FP4LIN_OK) return s;
+  if (lddx < H || lddw < (c.by_vocab ? H : V)) return FP4LIN_ERR_SHAPE;
+  c.lse = lse;
+  c.dloss = dloss;
+  c.dX = dX;
+  c.dW = dW;
+  c.lddx = lddx;
+  c.lddw = lddw;
+  return launch_status(fp4lin::launch_head_loss_backward(c, dt == FP4LIN_BF16, o.plan, stream));
+}
+
+}  // extern "C"
+
+// ---- gradient norm and clipping ---------------------------------------------------
+namespace {
+
+constexpr int64_t kMaxElements = int64_t(1) << 46;
+
+size_t clip_ws(int64_t count, int64_t elements) {
+  return round_up(16 + size_t(fp4lin::clip_parts(count, elements)) * 8, 256);
+}
+
+fp4lin_status clip_impl(const fp4lin_grad* grads, int64_t count, bool clip, double max_norm,
+                        float* norm, void* ws, size_t ws_bytes, hipStream_t stream) {
+  if (norm == nullptr || ws == nullptr || (count > 0 && grads == nullptr)) return FP4LIN_ERR_NULL;
+  if (count < 0 || count >= kMaxDim) return FP4LIN_ERR_SHAPE;
+  int64_t elements = 0;
+  for (int64_t i = 0; i < count; ++i) {
+    const fp4lin_grad& x = grads[i];
+    if (x.n < 0 || x.n > kMaxElements) return FP4LIN_ERR_SHAPE;
+    if (bad_dtype(x.dt)) return FP4LIN_ERR_DTYPE;
+    if (x.n > 0 && (x.g == nullptr || (clip && x.out == nullptr))) return FP4LIN_ERR_NULL;
+    // elements at their own alignment
+    const uintptr_t low = x.dt == FP4LIN_BF16 ? 1 : 3;
+    if (x.n > 0 && ((reinterpret_cast<uintptr_t>(x.g) & low) != 0 ||
+                    (clip && (reinterpret_cast<uintptr_t>(x.out) & low) != 0)))
+      return FP4LIN_ERR_ALIGN;
+    elements += x.n;
+    if (elements > kMaxElements) return FP4LIN_ERR_SHAPE;
+  }
+  if (clip && !(max_norm >= 0.0)) return FP4LIN_ERR_VALUE;
+  if (!aligned16(ws)) return FP4LIN_ERR_ALIGN;
+  if (ws_bytes < clip_ws(count, elements)) return FP4LIN_ERR_WORKSPACE;
+  return launch_status(
+      fp4lin::launch_clip(grads, count, elements, clip, float(max_norm), norm, ws, stream));
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t fp4lin_clip_workspace_bytes(int64_t count, int64_t elements) {
+  if (count < 0 || count >= kMaxDim || elements < 0 || elements > kMaxElements) return 0;
+  return clip_ws(count, elements);
+}
+
+fp4lin_status fp4lin_grad_norm(const fp4lin_grad* grads, int64_t count, float* norm, void* ws,
+                               size_t ws_bytes, hipStream_t stream) {
+  return clip_impl(grads, count, false, 0.0, norm, ws, ws_bytes, stream);
+}
+
+fp4lin_status fp4lin_clip_grads(const fp4lin_grad* grads, int64_t count, double max_norm,
+                                float* norm, void* ws, size_t ws_bytes, hipStream_t stream) {
+  return clip_impl(grads, count, true, max_norm, norm, ws, ws_bytes, stream);
 }
 
 }  // extern "C"

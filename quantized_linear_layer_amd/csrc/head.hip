@@ -1,0 +1,618 @@
+// Softmax cross entropy of a large vocabulary straight from the hidden states,
+// with its gradients: the T x V logits are never in memory as a whole.
+//
+//   l = X W                     X: T x H, W: H x V (or stored V x H)
+//   lse_t  = log sum_v exp l_tv
+//   loss_t = lse_t - l_(t, target_t)          0 for a target outside [0, V)
+//   G_tv   = (exp(l_tv - lse_t) - [v = target_t]) * dloss_t     likewise 0
+//   dX = G W^T,  dW = X^T G
+//
+// Forward: one product whose tiles keep, of each row, the maximum and the sum of
+// exponentials over the columns of a wave (fp32), and the target's logit where
+// the tile holds it; a second kernel joins the columns' pairs (m, s) of a row as
+//   M = max m_i,  lse = M + log sum_i s_i exp(m_i - M).
+//
+// Backward, in pieces of the vocabulary: the piece's logits are formed again,
+// turned into G in the tile's epilogue and written in the inputs' type, then
+// multiplied into dX (fp32, added up over the pieces) and into the piece's own
+// part of dW. A piece is as wide as lets its G stay in the last-level cache
+// between the three products (kPieceBytes), which is also what bounds the
+// workspace. G is rounded once to the inputs' type (bfloat16: 2^-9 of each
+// element, as the two products it feeds take bfloat16 operands); every sum is
+// fp32.
+//
+// dX sums over the vocabulary, so few rows leave few tiles: the reduction is
+// then split over workgroups, each adding into an fp32 array of its own, and the
+// arrays are added in a fixed order at the end. No atomics: results repeat bit
+// for bit.
+//
+// Operands whose rows do not start on 16 bytes or whose contiguous size is not a
+// multiple of 8 elements are first copied, padded with zeros (pack_kernel).
+#include <type_traits>
+
+#include "dense_core.hpp"
+#include "device_common.hpp"
+#include "gemm_core.hpp"
+#include "internal.hpp"
+
+namespace fp4lin {
+
+namespace {
+
+constexpr float kLog2e = 1.44269504088896340736f;
+
+__device__ inline float exp_diff(float x, float y) {
+  return __builtin_amdgcn_exp2f((x - y) * kLog2e);
+}
+
+// Reductions over the 32 lanes of a half wave, on every lane.
+__device__ inline float half_max(float v) {
+#pragma unroll
+  for (int off = 16; off >= 1; off >>= 1) v = fmaxf(v, __shfl_xor(v, off, kWave));
+  return v;
+}
+__device__ inline float half_sum(float v) {
+#pragma unroll
+  for (int off = 16; off >= 1; off >>= 1) v += __shfl_xor(v, off, kWave);
+  return v;
+}
+
+// Row of element r of a 32x32 fragment on this lane.
+__device__ inline int frag_row(int r, int lane) { return 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3); }
+
+// The tile's logits in f.acc (rows from m0, columns from n0).
+template <class C, class T, bool kBT>
+__device__ __attribute__((always_inline)) inline void logits_tile(
+    DenseFeed<C, T, false, kBT>& f, int H, uint8_t* st0, uint8_t* st1, uint8_t* st2) {
+  constexpr int kE = kStepElems<T>;
+  gemm_pipeline(f, (H + kE - 1) / kE, st0, st1, st2);
+}
+
+template <class T>
+struct HeadArgs {
+  DenseOperand<T> X, W;  // W: extent V
+  int T_, V, H;          // rows, columns, reduction
+  int v0, Vall;          // W's first column in the vocabulary, and its size
+  const int32_t* target;
+  // forward
+  float2* part;     // [columns / columns of a wave][T]: (m, s)
+  float* tlogit;    // [T]
+  // backward
+  const float* lse;
+  const float* dloss;
+  T* G;
+  int64_t ldg;
+};
+
+// One (m, s) a row and wave, and the targets' logits.
+template <class C, class T, bool kBT>
+__global__ __launch_bounds__(C::kThreads, C::kMinBlocks) void head_lse_kernel(HeadArgs<T> p) {
+  constexpr int FM = C::FM, FN = C::FN;
+  __shared__ __attribute__((aligned(16))) uint8_t st0[C::kStageBytes];
+  __shared__ __attribute__((aligned(16))) uint8_t st1[C::kStageBytes];
+  __shared__ __attribute__((aligned(16))) uint8_t st2[C::kStageBytes];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave / C::WN, wn = wave % C::WN;
+  const int tiles_m = (p.T_ + C::BM - 1) / C::BM, tiles_n = (p.V + C::BN - 1) / C::BN;
+  int tm, tn;
+  tile_of(xcd_run(blockIdx.x, tiles_m * tiles_n), tiles_m, tiles_n, tm, tn);
+  const int m0 = tm * C::BM, n0 = tn * C::BN;
+  DenseFeed<C, T, false, kBT> f(p.X, p.W, m0, n0, wave, lane);
+  logits_tile(f, p.H, st0, st1, st2);
+
+  const int row0 = m0 + wm * FM * 32, col0 = n0 + wn * FN * 32;
+  // the rows of this wave whose target it holds: few, so they are looked up one
+  // by one among the accumulators
+  const int trow = row0 + lane;
+  const int tcol = lane < FM * 32 && trow < p.T_ ? p.target[trow] : -1;
+  uint64_t hits = __ballot(tcol >= col0 && tcol < col0 + FN * 32 && tcol < p.V);
+  while (hits != 0) {
+    const int l = __builtin_ctzll(hits);
+    hits &= hits - 1;
+    const int c = __builtin_amdgcn_readlane(tcol, l) - col0;
+#pragma unroll
+    for (int fm = 0; fm < FM; ++fm)
+#pragma unroll
+      for (int fn = 0; fn < FN; ++fn)
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+          if (fm * 32 + frag_row(r, lane) == l && fn * 32 + (lane & 31) == c)
+            p.tlogit[row0 + l] = f.acc[fm][fn][r];
+  }
+  // columns past the vocabulary count as -inf
+#pragma unroll
+  for (int fn = 0; fn < FN; ++fn)
+    if (col0 + fn * 32 + (lane & 31) >= p.V) {
+#pragma unroll
+      for (int fm = 0; fm < FM; ++fm)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) f.acc[fm][fn][r] = -__builtin_huge_valf();
+    }
+  float2* const part = p.part + int64_t(tn * C::WN + wn) * p.T_;
+#pragma unroll
+  for (int fm = 0; fm < FM; ++fm)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      float m = f.acc[fm][0][r];
+#pragma unroll
+      for (int fn = 1; fn < FN; ++fn) m = fmaxf(m, f.acc[fm][fn][r]);
+      m = half_max(m);
+      const float ref = m == -__builtin_huge_valf() ? 0.0f : m;
+      float s = 0.0f;
+#pragma unroll
+      for (int fn = 0; fn < FN; ++fn) s += exp_diff(f.acc[fm][fn][r], ref);
+      s = half_sum(s);
+      const int row = row0 + fm * 32 + frag_row(r, lane);
+      if ((lane & 31) == 0 && row < p.T_) part[row] = make_float2(m, s);
+    }
+}
+
+// Joins a row's P pairs: 64 rows a workgroup, 4 threads a row.
+__global__ __launch_bounds__(256) void head_join_kernel(const float2* __restrict__ part, int P,
+                                                        int T, int V,
+                                                        const int32_t* __restrict__ target,
+                                                        const float* __restrict__ tlogit,
+                                                        float* __restrict__ loss,
+                                                        float* __restrict__ lse) {
+  __shared__ float2 sh[4][64];
+  const int q = threadIdx.x >> 6, i = threadIdx.x & 63;
+  const int row = blockIdx.x * 64 + i;
+  float m = -__builtin_huge_valf(), s = 0.0f;
+  auto join = [&](float m2, float s2) {
+    const float top = fmaxf(m, m2);
+    const float ref = top == -__builtin_huge_valf() ? 0.0f : top;
+    s = s * exp_diff(m, ref) + s2 * exp_diff(m2, ref);
+    m = top;
+  };
+  if (row < T)
+    for (int j = q; j < P; j += 4) {
+      const float2 o = part[int64_t(j) * T + row];
+      join(o.x, o.y);
+    }
+  sh[q][i] = make_float2(m, s);
+  __syncthreads();
+  if (q != 0 || row >= T) return;
+  for (int w = 1; w < 4; ++w) join(sh[w][i].x, sh[w][i].y);
+  const float l = m + logf(s);
+  lse[row] = l;
+  const int t = target[row];
+  loss[row] = t >= 0 && t < V ? l - tlogit[row] : 0.0f;
+}
+
+// G of a piece of the vocabulary, zeros in the columns that pad it to ldg's
+// multiple of 8.
+template <class C, class T, bool kBT>
+__global__ __launch_bounds__(C::kThreads, C::kMinBlocks) void head_grad_kernel(HeadArgs<T> p) {
+  constexpr int FM = C::FM, FN = C::FN;
+  __shared__ __attribute__((aligned(16))) uint8_t st0[C::kStageBytes];
+  __shared__ __attribute__((aligned(16))) uint8_t st1[C::kStageBytes];
+  __shared__ __attribute__((aligned(16))) uint8_t st2[C::kStageBytes];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave / C::WN, wn = wave % C::WN;
+  const int tiles_m = (p.T_ + C::BM - 1) / C::BM, tiles_n = (p.V + C::BN - 1) / C::BN;
+  int tm, tn;
+  tile_of(xcd_run(blockIdx.x, tiles_m * tiles_n), tiles_m, tiles_n, tm, tn);
+  const int m0 = tm * C::BM, n0 = tn * C::BN;
+  DenseFeed<C, T, false, kBT> f(p.X, p.W, m0, n0, wave, lane);
+  logits_tile(f, p.H, st0, st1, st2);
+
+  const int row0 = m0 + wm * FM * 32, col0 = n0 + wn * FN * 32;
+  float g[FM][16];  // dloss of this lane's rows, 0 where the row is left out
+#pragma unroll
+  for (int fm = 0; fm < FM; ++fm)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      const int row = row0 + fm * 32 + frag_row(r, lane);
+      const int at = row < p.T_ ? row : p.T_ - 1;
+      const float lse = p.lse[at];
+      const int t = p.target[at];
+      g[fm][r] = t >= 0 && t < p.Vall ? p.dloss[at] : 0.0f;
+#pragma unroll
+      for (int fn = 0; fn < FN; ++fn) f.acc[fm][fn][r] = exp_diff(f.acc[fm][fn][r], lse);
+    }
+  // the one-hot part, as in head_lse_kernel
+  const int trow = row0 + lane;
+  const int tcol = lane < FM * 32 && trow < p.T_ ? p.target[trow] : -1;
+  uint64_t hits = __ballot(tcol >= p.v0 + col0 && tcol < p.v0 + col0 + FN * 32);
+  while (hits != 0) {
+    const int l = __builtin_ctzll(hits);
+    hits &= hits - 1;
+    const int c = __builtin_amdgcn_readlane(tcol, l) - p.v0 - col0;
+#pragma unroll
+    for (int fm = 0; fm < FM; ++fm)
+#pragma unroll
+      for (int fn = 0; fn < FN; ++fn)
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+          if (fm * 32 + frag_row(r, lane) == l && fn * 32 + (lane & 31) == c)
+            f.acc[fm][fn][r] -= 1.0f;
+  }
+  // columns past the piece: the zeros that fill G's last 8
+#pragma unroll
+  for (int fn = 0; fn < FN; ++fn)
+    if (col0 + fn * 32 + (lane & 31) >= p.V) {
+#pragma unroll
+      for (int fm = 0; fm < FM; ++fm)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) f.acc[fm][fn][r] = 0.0f;
+    }
+  const int cols = (p.V + 7) & ~7;
+  emit_tile<C, kOutVec<T>>(st0, st1, st2, wave, lane, m0, n0,
+                           [&](int fm, int fn, int r) { return f.acc[fm][fn][r] * g[fm][r]; },
+                           [&](int gr, int gc, const float* v) {
+                             if (gr < p.T_) store_vec<false>(p.G + int64_t(gr) * p.ldg + gc, v, cols - gc, true);
+                           });
+}
+
+// A product of two operands, or of slice blockIdx.z of their reduction. kAdd: into
+// the fp32 array of the slice (Y + z * slice_elems), on top of what is there
+// unless `first`.
+template <class T, class Out>
+struct ProductArgs {
+  DenseOperand<T> A, B;
+  int M, N;     // output
+  int k_slice;  // reduction elements a slice (whole K steps)
+  Out* Y;
+  int64_t ldy;
+  int64_t slice_elems;
+  int first;
+};
+
+template <class C, class T, bool kAT, bool kBT, class Out, bool kAdd>
+__global__ __launch_bounds__(C::kThreads, C::kMinBlocks) void head_product_kernel(
+    ProductArgs<T, Out> p) {
+  __shared__ __attribute__((aligned(16))) uint8_t st0[C::kStageBytes];
+  __shared__ __attribute__((aligned(16))) uint8_t st1[C::kStageBytes];
+  __shared__ __attribute__((aligned(16))) uint8_t st2[C::kStageBytes];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int tiles_m = (p.M + C::BM - 1) / C::BM, tiles_n = (p.N + C::BN - 1) / C::BN;
+  int tm, tn;
+  tile_of(xcd_run(blockIdx.x, tiles_m * tiles_n), tiles_m, tiles_n, tm, tn);
+  const int m0 = tm * C::BM, n0 = tn * C::BN;
+  const int k0 = blockIdx.z * p.k_slice;
+  DenseOperand<T> A = p.A, B = p.B;
+  A.p += kAT ? k0 * A.ld : k0;
+  B.p += kBT ? k0 * B.ld : k0;
+  A.k = A.k - k0 < p.k_slice ? A.k - k0 : p.k_slice;
+  B.k = B.k - k0 < p.k_slice ? B.k - k0 : p.k_slice;
+  // (one of the two may be filled up to a multiple of 8 with zeros; the other
+  // then reads as zero there)
+  const int k = A.k > B.k ? A.k : B.k;
+  DenseFeed<C, T, kAT, kBT> f(A, B, m0, n0, wave, lane);
+  constexpr int kE = kStepElems<T>;
+  if (k > 0) gemm_pipeline(f, (k + kE - 1) / kE, st0, st1, st2);
+  Out* const Y = p.Y + blockIdx.z * p.slice_elems;
+  const bool vec = rows_vec(Y, p.ldy);
+  emit_tile<C, kOutVec<Out>>(
+      st0, st1, st2, wave, lane, m0, n0, [&](int fm, int fn, int r) { return f.acc[fm][fn][r]; },
+      [&](int gr, int gc, const float* v) {
+        if (gr >= p.M) return;
+        Out* const dst = Y + int64_t(gr) * p.ldy + gc;
+        if constexpr (kAdd) {
+          // H is padded to whole 16-byte groups in this array
+          if (gc >= p.ldy) return;
+          f32x4 o = {v[0], v[1], v[2], v[3]};
+          if (!p.first) o += *reinterpret_cast<const f32x4*>(dst);
+          *reinterpret_cast<f32x4*>(dst) = o;
+        } else {
+          store_vec<true>(dst, v, p.N - gc, vec);
+        }
+      });
+}
+
+// dX from the S arrays of its slices (T x ldp each), added in slice order.
+template <class Out>
+__global__ __launch_bounds__(256) void head_sum_kernel(const float* __restrict__ acc, int S,
+                                                       int64_t slice_elems, int64_t T, int H,
+                                                       int64_t ldp, Out* __restrict__ dX,
+                                                       int64_t lddx) {
+  const int64_t groups = ldp / 4;
+  const bool vec = (reinterpret_cast<uintptr_t>(dX) % (4 * sizeof(Out)) == 0) && lddx % 4 == 0;
+  for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < T * groups;
+       i += int64_t(gridDim.x) * 256) {
+    const int64_t row = i / groups;
+    const int c = int(i - row * groups) * 4;
+    f32x4 o = *reinterpret_cast<const f32x4*>(acc + row * ldp + c);
+    for (int s = 1; s < S; ++s)
+      o += *reinterpret_cast<const f32x4*>(acc + s * slice_elems + row * ldp + c);
+    Out* const dst = dX + row * lddx + c;
+    if constexpr (sizeof(Out) == 4) {
+      if (vec && c + 4 <= H) {
+        *reinterpret_cast<f32x4*>(dst) = o;
+        continue;
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (c + j < H) dst[j] = o[j];
+    } else {
+      const uint32_t u[2] = {bf16_pair(o[0], o[1]), bf16_pair(o[2], o[3])};
+      if (vec && c + 4 <= H) {
+        *reinterpret_cast<uint2*>(dst) = make_uint2(u[0], u[1]);
+        continue;
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (c + j < H) dst[j] = uint16_t(u[j >> 1] >> (16 * (j & 1)));
+    }
+  }
+}
+
+// R x C with row stride ld into rows of ldp (a multiple of 8) elements, zeros
+// after the C-th. One thread per 8 elements of the copy.
+template <class T>
+__global__ __launch_bounds__(256) void pack_kernel(const T* __restrict__ src, int64_t R, int64_t C,
+                                                   int64_t ld, T* __restrict__ dst, int64_t ldp) {
+  const int64_t groups = ldp / 8;
+  for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < R * groups;
+       i += int64_t(gridDim.x) * 256) {
+    const int64_t row = i / groups, c = (i - row * groups) * 8;
+    __attribute__((aligned(16))) T v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = c + j < C ? src[row * ld + c + j] : T(0);
+#pragma unroll
+    for (int j = 0; j < 8 * int(sizeof(T)); j += 16)
+      *reinterpret_cast<uint4*>(reinterpret_cast<char*>(dst + row * ldp + c) + j) =
+          *reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(v) + j);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Host: tiles, pieces, slices.
+// ---------------------------------------------------------------------------
+using LargeTile = GemmCfg<256, 256, 4, 2, 64, 1>;
+using MidTile = GemmCfg<128, 256, 2, 2, 64, 2>;
+using FewTile = GemmCfg<64, 128, 1, 4, 64, 2>;
+using F32Tile = GemmCfg<128, 128, 2, 2, 64, 2>;
+
+constexpr int64_t kPieceBytes = int64_t(128) << 20;  // of G
+constexpr int64_t kCUs = 256;
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int64_t round8(int64_t n) { return (n + 7) / 8 * 8; }
+int64_t round_256(int64_t n) { return (n + 255) / 256 * 256; }
+
+unsigned copy_blocks(int64_t threads) {
+  const int64_t b = ceil_div(threads, 256);
+  return unsigned(b < 4096 ? (b > 0 ? b : 1) : 4096);
+}
+
+enum class Tile { kLarge, kMid, kFew, kF32 };
+
+// Tile of an M x N product.
+Tile pick_tile(bool bf16, int64_t M, int64_t N) {
+  if (M <= 64) return Tile::kFew;
+  if (!bf16) return Tile::kF32;
+  if (ceil_div(M, 256) * ceil_div(N, 256) >= kCUs) return Tile::kLarge;
+  return Tile::kMid;
+}
+int64_t tile_rows(Tile t) {
+  return t == Tile::kLarge ? 256 : t == Tile::kFew ? 64 : 128;
+}
+int64_t tile_cols(Tile t) {
+  return t == Tile::kLarge || t == Tile::kMid ? 256 : 128;
+}
+// columns of a wave
+int64_t wave_cols(Tile t) {
+  return t == Tile::kFew ? 32 : t == Tile::kF32 ? 64 : 128;
+}
+int64_t tiles_of(Tile t, int64_t M, int64_t N) {
+  return ceil_div(M, tile_rows(t)) * ceil_div(N, tile_cols(t));
+}
+
+// Slices of dX's reduction over k elements: enough for two workgroups a CU, at
+// least 1024 elements each.
+int64_t dx_slices(Tile t, int64_t T, int64_t H, int64_t k) {
+  const int64_t want = ceil_div(2 * kCUs, tiles_of(t, T > 0 ? T : 1, H));
+  const int64_t most = k / 1024 > 1 ? k / 1024 : 1;
+  const int64_t s = want < most ? want : most;
+  return s < 32 ? s : 32;
+}
+
+// f(tile configuration) for a tile that pick_tile gives for T.
+template <class T, class F>
+hipError_t with_tile(Tile t, F&& f) {
+  if (t == Tile::kFew) return f(FewTile{});
+  if constexpr (sizeof(T) == 2) {
+    if (t == Tile::kLarge) return f(LargeTile{});
+    if (t == Tile::kMid) return f(MidTile{});
+  } else {
+    if (t == Tile::kF32) return f(F32Tile{});
+  }
+  return hipErrorInvalidValue;
+}
+
+}  // namespace
+
+HeadPlan head_plan(bool bf16, int64_t T, int64_t H, int64_t V, bool by_vocab, int64_t ldx,
+                   int64_t ldw) {
+  const int64_t esz = bf16 ? 2 : 4;
+  HeadPlan h{};
+  h.pack_x = H % 8 != 0 || (ldx * esz) % 16 != 0;
+  h.pack_w = (by_vocab ? H : V) % 8 != 0 || (ldw * esz) % 16 != 0;
+  h.ldx = h.pack_x ? round8(H) : ldx;
+  h.ldw = h.pack_w ? round8(by_vocab ? H : V) : ldw;
+  h.x_bytes = h.pack_x ? T * h.ldx * esz : 0;
+  h.w_bytes = h.pack_w ? (by_vocab ? V : H) * h.ldw * esz : 0;
+  const Tile t = pick_tile(bf16, T, V);
+  h.parts = ceil_div(V, tile_cols(t)) * (tile_cols(t) / wave_cols(t));
+  const int64_t pieces = ceil_div(T * V * esz, kPieceBytes);
+  h.piece = pieces > 1 ? round_256(ceil_div(V, pieces)) : V;
+  h.ldg = round8(h.piece);
+  const Tile tx = pick_tile(bf16, T, H);
+  h.slices = dx_slices(tx, T, H, h.piece);
+  h.ldp = round8(H);
+  return h;
+}
+
+namespace {
+
+template <class T>
+hipError_t pack(const void* src, int64_t R, int64_t C, int64_t ld, void* dst, int64_t ldp,
+                hipStream_t stream) {
+  pack_kernel<T><<<copy_blocks(R * (ldp / 8)), 256, 0, stream>>>(
+      static_cast<const T*>(src), R, C, ld, static_cast<T*>(dst), ldp);
+  return hipGetLastError();
+}
+
+// X and W as the products take them, packed where they have to be.
+template <class T>
+hipError_t operands(const HeadCall& c, const HeadPlan& h, DenseOperand<T>* X, const T** W,
+                    hipStream_t stream) {
+  const T* x = static_cast<const T*>(c.X);
+  const T* w = static_cast<const T*>(c.W);
+  if (h.pack_x) {
+    const hipError_t e = pack<T>(c.X, c.T, c.H, c.ldx, c.packed_x, h.ldx, stream);
+    if (e != hipSuccess) return e;
+    x = static_cast<const T*>(c.packed_x);
+  }
+  if (h.pack_w) {
+    const hipError_t e = pack<T>(c.W, c.by_vocab ? c.V : c.H, c.by_vocab ? c.H : c.V, c.ldw,
+                                 c.packed_w, h.ldw, stream);
+    if (e != hipSuccess) return e;
+    w = static_cast<const T*>(c.packed_w);
+  }
+  // the reduction of the logits, with its zeros
+  *X = DenseOperand<T>{x, h.ldx, int(c.T), int(round8(c.H))};
+  *W = w;
+  return hipSuccess;
+}
+
+template <class T, bool kGrad>
+hipError_t logits(Tile t, bool by_vocab, const HeadArgs<T>& a, hipStream_t stream) {
+  const int64_t tiles = tiles_of(t, a.T_, a.V);
+  if (tiles >= (int64_t(1) << 31)) return hipErrorInvalidValue;
+  return with_tile<T>(t, [&](auto c) -> hipError_t {
+    using C = decltype(c);
+    const dim3 grid(unsigned(tiles), 1, 1);
+    if constexpr (kGrad) {
+      if (by_vocab)
+        head_grad_kernel<C, T, false><<<grid, C::kThreads, 0, stream>>>(a);
+      else
+        head_grad_kernel<C, T, true><<<grid, C::kThreads, 0, stream>>>(a);
+    } else {
+      if (by_vocab)
+        head_lse_kernel<C, T, false><<<grid, C::kThreads, 0, stream>>>(a);
+      else
+        head_lse_kernel<C, T, true><<<grid, C::kThreads, 0, stream>>>(a);
+    }
+    return hipGetLastError();
+  });
+}
+
+template <class T, bool kAT, bool kBT, class Out, bool kAdd>
+hipError_t product(Tile t, const ProductArgs<T, Out>& a, int64_t slices, hipStream_t stream) {
+  return with_tile<T>(t, [&](auto c) -> hipError_t {
+    using C = decltype(c);
+    // a transposed A needs 128 rows a tile (the swizzle's segments)
+    if constexpr (kAT && C::BM < 128) {
+      return hipErrorInvalidValue;
+    } else {
+      const dim3 grid(unsigned(tiles_of(t, a.M, a.N)), 1, unsigned(slices));
+      head_product_kernel<C, T, kAT, kBT, Out, kAdd><<<grid, C::kThreads, 0, stream>>>(a);
+      return hipGetLastError();
+    }
+  });
+}
+
+template <class T>
+hipError_t run_forward(const HeadCall& c, const HeadPlan& h, hipStream_t stream) {
+  DenseOperand<T> X;
+  const T* W;
+  hipError_t e = operands<T>(c, h, &X, &W, stream);
+  if (e != hipSuccess) return e;
+  HeadArgs<T> a{};
+  a.X = X;
+  a.W = DenseOperand<T>{W, h.ldw, int(c.by_vocab ? c.V : round8(c.V)), int(c.by_vocab ? X.k : c.H)};
+  a.T_ = int(c.T);
+  a.V = a.Vall = int(c.V);
+  a.H = X.k;
+  a.target = c.target;
+  a.part = static_cast<float2*>(c.part);
+  a.tlogit = c.tlogit;
+  e = logits<T, false>(pick_tile(sizeof(T) == 2, c.T, c.V), c.by_vocab, a, stream);
+  if (e != hipSuccess) return e;
+  head_join_kernel<<<unsigned(ceil_div(c.T, 64)), 256, 0, stream>>>(
+      a.part, int(h.parts), int(c.T), int(c.V), c.target, c.tlogit, c.loss, c.lse_out);
+  return hipGetLastError();
+}
+
+template <class T>
+hipError_t run_backward(const HeadCall& c, const HeadPlan& h, hipStream_t stream) {
+  constexpr bool kBf16 = sizeof(T) == 2;
+  DenseOperand<T> X;
+  const T* W;
+  hipError_t e = operands<T>(c, h, &X, &W, stream);
+  if (e != hipSuccess) return e;
+  T* const dW = static_cast<T*>(c.dW);
+  const Tile tx = pick_tile(kBf16, c.T, c.H);
+  const bool direct = h.slices == 1 && h.piece >= c.V;
+  for (int64_t v0 = 0; v0 < c.V; v0 += h.piece) {
+    const int64_t n = c.V - v0 < h.piece ? c.V - v0 : h.piece;
+    const int n8 = int(round8(n));
+    if (c.T > 0) {
+      HeadArgs<T> a{};
+      a.X = X;
+      a.W = DenseOperand<T>{W + v0 * (c.by_vocab ? h.ldw : 1), h.ldw, c.by_vocab ? int(n) : n8,
+                            int(c.by_vocab ? X.k : c.H)};
+      a.T_ = int(c.T);
+      a.V = int(n);
+      a.Vall = int(c.V);
+      a.H = X.k;
+      a.v0 = int(v0);
+      a.target = c.target;
+      a.lse = c.lse;
+      a.dloss = c.dloss;
+      a.G = static_cast<T*>(c.G);
+      a.ldg = h.ldg;
+      e = logits<T, true>(pick_tile(kBf16, c.T, n), c.by_vocab, a, stream);
+      if (e != hipSuccess) return e;
+
+      // dX: G (T x n) times W's piece; the columns that fill n to n8 are zeros in
+      // G and, where W is read along them, in W
+      const DenseOperand<T> G{a.G, h.ldg, int(c.T), n8};
+      const int64_t per = ceil_div(ceil_div(n, h.slices), 64) * 64;
+      const DenseOperand<T> B{a.W.p, h.ldw, c.by_vocab ? X.k : int(c.H), c.by_vocab ? int(n) : n8};
+      if (direct) {
+        const ProductArgs<T, T> q{G, B, int(c.T), int(c.H), n8, static_cast<T*>(c.dX), c.lddx, 0, 1};
+        e = c.by_vocab ? product<T, false, true, T, false>(tx, q, 1, stream)
+                       : product<T, false, false, T, false>(tx, q, 1, stream);
+      } else {
+        const ProductArgs<T, float> q{G, B, int(c.T), int(c.H), int(per), c.acc, h.ldp,
+                                      c.T * h.ldp, v0 == 0};
+        e = c.by_vocab ? product<T, false, true, float, true>(tx, q, h.slices, stream)
+                       : product<T, false, false, float, true>(tx, q, h.slices, stream);
+      }
+      if (e != hipSuccess) return e;
+    }
+    // dW's piece: X^T G (H x n) or G^T X (n x H)
+    const DenseOperand<T> Gt{static_cast<const T*>(c.G), h.ldg, n8, int(c.T)};
+    const DenseOperand<T> Xt{X.p, h.ldx, X.k, int(c.T)};
+    const int64_t rows = c.by_vocab ? n : c.H, cols = c.by_vocab ? c.H : n;
+    // (A is read across its rows here: at least 128 rows a tile, see product)
+    const Tile tw = pick_tile(kBf16, rows > 64 ? rows : 65, cols);
+    const ProductArgs<T, T> q{c.by_vocab ? Gt : Xt, c.by_vocab ? Xt : Gt, int(rows), int(cols),
+                              int(c.T), dW + v0 * (c.by_vocab ? c.lddw : 1), c.lddw, 0, 1};
+    e = product<T, true, true, T, false>(tw, q, 1, stream);
+    if (e != hipSuccess) return e;
+  }
+  if (direct || c.T == 0) return hipSuccess;
+  head_sum_kernel<T><<<copy_blocks(c.T * (h.ldp / 4)), 256, 0, stream>>>(
+      c.acc, int(h.slices), c.T * h.ldp, c.T, int(c.H), h.ldp, static_cast<T*>(c.dX), c.lddx);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_head_loss(const HeadCall& c, bool bf16, const HeadPlan& h, hipStream_t stream) {
+  return bf16 ? run_forward<uint16_t>(c, h, stream) : run_forward<float>(c, h, stream);
+}
+
+hipError_t launch_head_loss_backward(const HeadCall& c, bool bf16, const HeadPlan& h,
+                                     hipStream_t stream) {
+  return bf16 ? run_backward<uint16_t>(c, h, stream) : run_backward<float>(c, h, stream);
+}
+
+}  // namespace fp4lin

@@ -5,6 +5,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "fp4lin.h"
+
 namespace fp4lin {
 
 size_t select_workspace_bytes(bool bf16, int64_t M);
@@ -101,5 +103,43 @@ hipError_t launch_experts_wgrad(const uint8_t* Aq, const uint8_t* As, const uint
                                 const uint8_t* Bs, const int32_t* row_end, int64_t E, int64_t M,
                                 int64_t K, int64_t N, void* dW, bool w_bf16, int64_t ldw,
                                 hipStream_t stream);
+
+// Head loss (head.hip). The plan follows from sizes and strides alone.
+struct HeadPlan {
+  bool pack_x, pack_w;       // operands copied into the workspace, padded
+  int64_t ldx, ldw;          // row strides the products use
+  int64_t x_bytes, w_bytes;  // of the copies
+  int64_t parts;             // (m, s) pairs a row
+  int64_t piece;             // vocabulary columns a piece of the backward
+  int64_t ldg;               // row stride of G
+  int64_t slices, ldp;       // dX: reduction slices, row stride of their arrays
+};
+HeadPlan head_plan(bool bf16, int64_t T, int64_t H, int64_t V, bool by_vocab, int64_t ldx,
+                   int64_t ldw);
+
+struct HeadCall {
+  const void *X, *W;
+  int64_t T, H, V, ldx, ldw;
+  bool by_vocab;
+  const int32_t* target;
+  // workspace
+  void *packed_x, *packed_w, *part, *G;
+  float *tlogit, *acc;
+  // forward
+  float *loss, *lse_out;
+  // backward
+  const float *lse, *dloss;
+  void *dX, *dW;
+  int64_t lddx, lddw;
+};
+hipError_t launch_head_loss(const HeadCall& c, bool bf16, const HeadPlan& h, hipStream_t stream);
+hipError_t launch_head_loss_backward(const HeadCall& c, bool bf16, const HeadPlan& h,
+                                     hipStream_t stream);
+
+// Gradient norm and clipping (clip.hip). clip_parts: partial sums that `count`
+// tensors of `elements` elements in all can need; ws holds two doubles more.
+int64_t clip_parts(int64_t count, int64_t elements);
+hipError_t launch_clip(const fp4lin_grad* grads, int64_t count, int64_t elements, bool clip,
+                       float max_norm, float* norm, void* ws, hipStream_t stream);
 
 }  // namespace fp4lin

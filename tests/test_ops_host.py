@@ -1,5 +1,5 @@
-"""Host-side checks of the C entries of the experts' products (no GPU work):
-every call here fails argument validation or is a pure host helper."""
+"""Host-side checks of the C entries of the experts' products, the head loss and
+the gradient clipping (no GPU work): every call here fails argument validation or is a pure host helper."""
 import ctypes
 import os
 
@@ -116,3 +116,108 @@ def test_experts_quantize_weight_refusals():
         assert q(**bad) == _lib.ERR_SHAPE, bad
     assert q(Wq=MISALIGNED) == _lib.ERR_ALIGN
     assert q(Ws=MISALIGNED) == _lib.ERR_ALIGN
+
+
+# ---- head loss -------------------------------------------------------------------
+HID, VOC = _lib.HEAD_HIDDEN_MAJOR, _lib.HEAD_VOCAB_MAJOR
+
+
+def head_ws(dt=1, layout=HID, T=64, H=64, V=512, ldx=64, ldw=512, backward=False):
+    f = L.fp4lin_head_loss_backward_workspace_bytes if backward else L.fp4lin_head_loss_workspace_bytes
+    return f(dt, layout, T, H, V, ldx, ldw)
+
+
+@pytest.mark.parametrize("backward", [False, True])
+def test_head_workspace_bytes(backward):
+    ok = dict(backward=backward)
+    assert head_ws(**ok) >= 256
+    assert head_ws(T=0, **ok) >= 256
+    # a padded copy of an operand whose rows are not whole 16-byte pieces
+    assert head_ws(V=511, ldw=511, **ok) >= head_ws(V=504, **ok) + 64 * 512 * 2
+    assert head_ws(ldx=67, **ok) >= head_ws(**ok) + 64 * 64 * 2
+    assert head_ws(layout=VOC, ldw=64, **ok) >= 256
+    for bad in (dict(dt=3), dict(layout=2), dict(T=-1), dict(H=0), dict(V=0), dict(ldx=63),
+                dict(ldw=511), dict(T=1 << 31), dict(ldw=1 << 23), dict(layout=VOC, ldw=63)):
+        assert head_ws(**{**bad, **ok}) == 0, bad
+    # the backward's G stays a piece of the vocabulary
+    assert head_ws(T=8192, H=4096, V=1 << 20, ldx=4096, ldw=1 << 20, backward=True) < 1 << 30
+
+
+def head(X=FAKE, W=FAKE, dt=1, layout=HID, target=FAKE, T=4, H=64, V=512, ldx=64, ldw=512, loss=FAKE,
+         lse=FAKE, ws=FAKE, n=BIG):
+    return L.fp4lin_head_loss(X, W, dt, layout, target, T, H, V, ldx, ldw, loss, lse, ws, n, None)
+
+
+def head_back(X=FAKE, W=FAKE, dt=1, layout=HID, target=FAKE, T=4, H=64, V=512, ldx=64, ldw=512,
+              lse=FAKE, dloss=FAKE, dX=FAKE, lddx=64, dW=FAKE, lddw=512, ws=FAKE, n=BIG):
+    return L.fp4lin_head_loss_backward(X, W, dt, layout, target, lse, dloss, T, H, V, ldx, ldw, dX,
+                                       lddx, dW, lddw, ws, n, None)
+
+
+@pytest.mark.parametrize("call,pointers", [
+    (head, ("X", "W", "target", "loss", "lse", "ws")),
+    (head_back, ("X", "W", "target", "lse", "dloss", "dX", "dW", "ws"))])
+def test_head_refusals(call, pointers):
+    for name in pointers:
+        assert call(**{name: None}) == _lib.ERR_NULL, name
+    assert call(dt=2) == _lib.ERR_DTYPE
+    for bad in (dict(layout=5), dict(T=-1), dict(H=0), dict(V=0), dict(ldx=63), dict(ldw=511)):
+        assert call(**bad) == _lib.ERR_SHAPE, bad
+    for name in ("X", "W", "ws"):
+        assert call(**{name: MISALIGNED}) == _lib.ERR_ALIGN, name
+    assert call(n=255) == _lib.ERR_WORKSPACE
+    if call is head_back:
+        assert call(lddx=63) == _lib.ERR_SHAPE
+        assert call(lddw=511) == _lib.ERR_SHAPE
+    else:
+        assert call(T=0, X=None, target=None, loss=None, lse=None) == _lib.OK
+
+
+# ---- clipping ----------------------------------------------------------------------
+def grads(*entries):
+    a = (_lib.Grad * max(len(entries), 1))()
+    for i, e in enumerate(entries):
+        a[i] = _lib.Grad(*e)
+    return a, len(entries)
+
+
+GOOD = (0x10000, 0x10000, 100, 0)
+
+
+def norm(entries=(GOOD,), out=FAKE, ws=FAKE, n=BIG):
+    a, count = grads(*entries)
+    return L.fp4lin_grad_norm(a, count, out, ws, n, None)
+
+
+def clip(entries=(GOOD,), out=FAKE, ws=FAKE, n=BIG, max_norm=1.0):
+    a, count = grads(*entries)
+    return L.fp4lin_clip_grads(a, count, max_norm, out, ws, n, None)
+
+
+@pytest.mark.parametrize("call", [norm, clip])
+def test_clip_refusals(call):
+    assert call(out=None) == _lib.ERR_NULL
+    assert call(ws=None) == _lib.ERR_NULL
+    assert call(entries=[GOOD, (None, 0x10000, 1, 0)]) == _lib.ERR_NULL
+    assert call(entries=[GOOD, (0x10000, 0x10000, -1, 0)]) == _lib.ERR_SHAPE
+    assert call(entries=[GOOD, (0x10000, 0x10000, 1 << 47, 0)]) == _lib.ERR_SHAPE
+    assert call(entries=[GOOD, (0x10000, 0x10000, 4, 2)]) == _lib.ERR_DTYPE
+    assert call(entries=[GOOD, (0x10002, 0x10000, 4, 0)]) == _lib.ERR_ALIGN
+    assert call(entries=[GOOD, (0x10001, 0x10000, 4, 1)]) == _lib.ERR_ALIGN
+    assert call(ws=MISALIGNED) == _lib.ERR_ALIGN
+    assert call(n=16) == _lib.ERR_WORKSPACE
+
+
+def test_clip_max_norm():
+    assert clip(max_norm=float("nan")) == _lib.ERR_VALUE
+    assert clip(max_norm=-0.5) == _lib.ERR_VALUE
+    assert clip(entries=[GOOD, (0x10000, None, 1, 0)]) == _lib.ERR_NULL
+    assert clip(entries=[GOOD, (0x10000, 0x10002, 1, 0)]) == _lib.ERR_ALIGN
+
+
+def test_clip_workspace_bytes():
+    assert L.fp4lin_clip_workspace_bytes(-1, 4) == 0
+    assert L.fp4lin_clip_workspace_bytes(1, -1) == 0
+    assert L.fp4lin_clip_workspace_bytes(0, 0) >= 16
+    # at most 2048 chunks and one more a tensor
+    assert L.fp4lin_clip_workspace_bytes(100, 1 << 40) <= 16 + 8 * (2048 + 100) + 256
