@@ -11,6 +11,8 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import itertools
+import struct
 
 from . import _lib
 from ._lib import BF16, F32, Coo, ForwardOffsets
@@ -367,47 +369,70 @@ def forward_mx(A, W, q, stream=None, return_workspace=False):
 
 
 # ---- products grouped by expert ------------------------------------------------------
-def _experts_weight(W, name):
-    """(E, K, N, ldw) of a stack of row-major matrices with one row stride throughout."""
-    if W.dim() != 3 or W.stride(2) != 1 or (W.shape[0] > 1 and W.stride(0) != W.shape[1] * W.stride(1)):
-        raise ValueError(f"{name} must be a 3-D tensor (experts, rows, columns) with unit column "
-                         "stride and experts that follow one another at the row stride")
-    return W.shape[0], W.shape[1], W.shape[2], _row_stride(W.stride(1), W.shape[2])
+# The helpers below are called with a few rows as well, where a call's host time
+# is what its user waits for: each argument is looked at once, pointers go to
+# ctypes as plain integers, and the device is only switched where it has to be.
+_CODES = {}
+
+
+def _code(t) -> int:
+    """_dtype_code from a table."""
+    if not _CODES:
+        torch = _torch()
+        _CODES.update({torch.float32: F32, torch.bfloat16: BF16})
+    code = _CODES.get(t.dtype)
+    return _dtype_code(t) if code is None else code
 
 
 def _row_stride(ld, cols):
     """A stride that a tensor of at most one row need not carry is the row length."""
-    return max(int(ld), int(cols))
+    return ld if ld > cols else cols
 
 
 def _rows(t, name):
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+    """(rows, columns, row stride) of a row-major matrix."""
+    size, stride = t.shape, t.stride()
+    if len(size) != 2 or (stride[1] != 1 and size[1] > 1):
         raise ValueError(f"{name} must be a 2-D row-major tensor with unit column stride")
-    if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+    if stride[0] < size[1] and size[0] > 1:
         raise ValueError(f"{name} must not have overlapping rows")
-    return t.shape[0], t.shape[1], _row_stride(t.stride(0), t.shape[1])
+    return size[0], size[1], _row_stride(stride[0], size[1])
+
+
+def _experts_weight(W, name):
+    """(E, K, N, ldw) of a stack of row-major matrices with one row stride throughout."""
+    size, stride = W.shape, W.stride()
+    if len(size) != 3 or (stride[2] != 1 and size[2] > 1) or \
+            (size[0] > 1 and stride[0] != size[1] * stride[1]) or \
+            (size[1] > 1 and stride[1] < size[2]):
+        raise ValueError(f"{name} must be a 3-D tensor (experts, rows, columns) with unit column "
+                         "stride and experts that follow one another at the row stride")
+    return size[0], size[1], size[2], _row_stride(stride[1], size[2])
+
+
+def _gpu(first, *others):
+    """The GPU that all of the (name, tensor) pairs are on."""
+    device = first[1].get_device()
+    if device < 0:
+        _dev(first[1], first[0])
+    for name, t in others:
+        if t.get_device() != device:
+            _dev(t, name)
+            raise ValueError(f"{name} is on {t.device}, {first[0]} on {first[1].device}")
+    return device
+
+
+def _same_dtype(a, b, names):
+    if a.dtype != b.dtype:
+        raise TypeError(f"{names} must have the same dtype")
 
 
 def _row_end(row_end, E):
-    torch = _torch()
-    if row_end.dtype != torch.int32 or row_end.dim() != 1 or not row_end.is_contiguous():
+    if row_end.dtype != _torch().int32 or row_end.dim() != 1 or not row_end.is_contiguous():
         raise TypeError("row_end must be a contiguous int32 vector")
     if row_end.numel() != E:
         raise ValueError(f"row_end has {row_end.numel()} entries for {E} experts")
-    return _dev(row_end, "row_end")
-
-
-def _same(what, **tensors):
-    """All on one GPU, and of one dtype where `what` says so."""
-    first = None
-    for name, t in tensors.items():
-        _dev(t, name)
-        if first is None:
-            first = (name, t)
-        elif t.device != first[1].device:
-            raise ValueError(f"{name} is on {t.device}, {first[0]} on {first[1].device}")
-        elif what == "dtype" and t.dtype != first[1].dtype:
-            raise TypeError(f"{first[0]} and {name} must have the same dtype")
+    return row_end.data_ptr()
 
 
 def _need(ok, message):
@@ -415,17 +440,34 @@ def _need(ok, message):
         raise ValueError(message)
 
 
-@contextlib.contextmanager
+_HERE = contextlib.nullcontext()
+
+
 def _on(t, stream):
-    """The device of t and the stream the call runs on, so that what is
-    allocated inside belongs to that stream."""
+    """A context with the device of t and the stream the call runs on, so that
+    what is allocated inside belongs to that stream."""
     torch = _torch()
-    with torch.cuda.device(t.device):
-        if stream is None:
-            yield
-        else:
-            with torch.cuda.stream(stream):
-                yield
+    device = t.get_device()
+    if device < 0 or (stream is None and device == torch.cuda.current_device()):
+        return _HERE
+    both = contextlib.ExitStack()
+    both.enter_context(torch.cuda.device(device))
+    if stream is not None:
+        both.enter_context(torch.cuda.stream(stream))
+    return both
+
+
+def _queue(stream, device):
+    """The HIP stream of a call on a device (the current one there if none is given)."""
+    torch = _torch()
+    if stream is not None:
+        return stream.cuda_stream
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # without a Stream object
+    return torch.cuda.current_stream(device).cuda_stream if raw is None else raw(device)
+
+
+def _nbytes(ws):
+    return ws.numel() * ws.element_size()
 
 
 def experts_workspace_bytes(which: int, E: int, M: int, K: int, N: int) -> int:
@@ -433,51 +475,53 @@ def experts_workspace_bytes(which: int, E: int, M: int, K: int, N: int) -> int:
 
 
 def _experts_ws(which, E, M, K, N, device, where):
-    n = experts_workspace_bytes(which, E, M, K, N)
+    n = lib().fp4lin_experts_workspace_bytes(which, E, M, K, N)
     if n == 0:
         raise Fp4linError(_lib.ERR_SHAPE, where)
-    return _empty((n,), _torch().uint8, device)
-
-
-def _nbytes(ws):
-    return ws.numel() * ws.element_size()
+    torch = _torch()
+    return torch.empty(n, dtype=torch.uint8, device=device)
 
 
 def fp4lin_experts_quantize_weight_mx(W, Wq, Ws, stream=None):
     E, K, N, ldw = _experts_weight(W, "W")
+    device = _gpu(("W", W), ("Wq", Wq), ("Ws", Ws))
     _check(lib().fp4lin_experts_quantize_weight_mx(
-        _dev(W, "W"), _dtype_code(W), E, K, N, ldw, _dev(Wq, "Wq"), _dev(Ws, "Ws"),
-        _stream(stream)), "fp4lin_experts_quantize_weight_mx")
+        W.data_ptr(), _code(W), E, K, N, ldw, Wq.data_ptr(), Ws.data_ptr(), _queue(stream, device)),
+        "fp4lin_experts_quantize_weight_mx")
 
 
 def fp4lin_experts_forward_mx(A, W, row_end, Y, ws, stream=None):
     M, K, lda = _rows(A, "A")
     E, K2, N, ldw = _experts_weight(W, "W")
     My, Ny, ldy = _rows(Y, "Y")
-    _same("dtype", A=A, W=W)
-    _same("", A=A, row_end=row_end, Y=Y, ws=ws)
-    _need(K2 == K, f"A is {M}x{K} but the weights are {K2}x{N}")
-    _need((My, Ny) == (M, N), f"Y is {My}x{Ny}, not {M}x{N}")
+    device = _gpu(("A", A), ("W", W), ("row_end", row_end), ("Y", Y), ("ws", ws))
+    _same_dtype(A, W, "A and W")
+    if K2 != K:
+        raise ValueError(f"A is {M}x{K} but the weights are {K2}x{N}")
+    if My != M or Ny != N:
+        raise ValueError(f"Y is {My}x{Ny}, not {M}x{N}")
     _check(lib().fp4lin_experts_forward_mx(
-        _dev(A, "A"), _dev(W, "W"), _dtype_code(A), _row_end(row_end, E), E, M, K, N, lda, ldw,
-        _dev(Y, "Y"), _dtype_code(Y), ldy, _dev(ws, "ws"), _nbytes(ws), _stream(stream)),
+        A.data_ptr(), W.data_ptr(), _code(A), _row_end(row_end, E), E, M, K, N, lda, ldw,
+        Y.data_ptr(), _code(Y), ldy, ws.data_ptr(), _nbytes(ws), _queue(stream, device)),
         "fp4lin_experts_forward_mx")
 
 
 def fp4lin_experts_apply_mx(A, Wq, Ws, row_end, Y, ws, stream=None):
-    torch = _torch()
     M, K, lda = _rows(A, "A")
     My, N, ldy = _rows(Y, "Y")
     E = row_end.numel()
-    _same("", A=A, Wq=Wq, Ws=Ws, row_end=row_end, Y=Y, ws=ws)
-    _need(My == M, f"Y has {My} rows, A {M}")
-    for name, t, want in (("Wq", Wq, E * N * packed_ld(K)), ("Ws", Ws, E * N * mx_scales_ld(K))):
-        if t.dtype != torch.uint8 or not t.is_contiguous():
+    device = _gpu(("A", A), ("Wq", Wq), ("Ws", Ws), ("row_end", row_end), ("Y", Y), ("ws", ws))
+    if My != M:
+        raise ValueError(f"Y has {My} rows, A {M}")
+    steps = (K + 127) // 128  # of 64 bytes of codes and 4 scales
+    for name, t, want in (("Wq", Wq, E * N * steps * 64), ("Ws", Ws, E * N * steps * 4)):
+        if t.dtype != _torch().uint8 or not t.is_contiguous():
             raise TypeError(f"{name} must be a contiguous uint8 tensor")
-        _need(t.numel() == want, f"{name} holds {t.numel()} bytes, not {want}")
+        if t.numel() != want:
+            raise ValueError(f"{name} holds {t.numel()} bytes, not {want}")
     _check(lib().fp4lin_experts_apply_mx(
-        _dev(A, "A"), _dtype_code(A), _dev(Wq, "Wq"), _dev(Ws, "Ws"), _row_end(row_end, E), E, M, K,
-        N, lda, _dev(Y, "Y"), _dtype_code(Y), ldy, _dev(ws, "ws"), _nbytes(ws), _stream(stream)),
+        A.data_ptr(), _code(A), Wq.data_ptr(), Ws.data_ptr(), _row_end(row_end, E), E, M, K, N, lda,
+        Y.data_ptr(), _code(Y), ldy, ws.data_ptr(), _nbytes(ws), _queue(stream, device)),
         "fp4lin_experts_apply_mx")
 
 
@@ -485,13 +529,15 @@ def fp4lin_experts_dgrad_mx(dY, W, row_end, dX, ws, stream=None):
     M, N, lddy = _rows(dY, "dY")
     E, K, N2, ldw = _experts_weight(W, "W")
     Mx, Kx, lddx = _rows(dX, "dX")
-    _same("dtype", dY=dY, W=W)
-    _same("", dY=dY, row_end=row_end, dX=dX, ws=ws)
-    _need(N2 == N, f"dY is {M}x{N} but the weights are {K}x{N2}")
-    _need((Mx, Kx) == (M, K), f"dX is {Mx}x{Kx}, not {M}x{K}")
+    device = _gpu(("dY", dY), ("W", W), ("row_end", row_end), ("dX", dX), ("ws", ws))
+    _same_dtype(dY, W, "dY and W")
+    if N2 != N:
+        raise ValueError(f"dY is {M}x{N} but the weights are {K}x{N2}")
+    if Mx != M or Kx != K:
+        raise ValueError(f"dX is {Mx}x{Kx}, not {M}x{K}")
     _check(lib().fp4lin_experts_dgrad_mx(
-        _dev(dY, "dY"), _dev(W, "W"), _dtype_code(dY), _row_end(row_end, E), E, M, K, N, lddy, ldw,
-        _dev(dX, "dX"), _dtype_code(dX), lddx, _dev(ws, "ws"), _nbytes(ws), _stream(stream)),
+        dY.data_ptr(), W.data_ptr(), _code(dY), _row_end(row_end, E), E, M, K, N, lddy, ldw,
+        dX.data_ptr(), _code(dX), lddx, ws.data_ptr(), _nbytes(ws), _queue(stream, device)),
         "fp4lin_experts_dgrad_mx")
 
 
@@ -499,13 +545,15 @@ def fp4lin_experts_wgrad_mx(A, dY, row_end, dW, ws, stream=None):
     M, K, lda = _rows(A, "A")
     My, N, lddy = _rows(dY, "dY")
     E, Kw, Nw, lddw = _experts_weight(dW, "dW")
-    _same("dtype", A=A, dY=dY)
-    _same("", A=A, row_end=row_end, dW=dW, ws=ws)
-    _need(My == M, f"dY has {My} rows, A {M}")
-    _need((Kw, Nw) == (K, N), f"dW holds {Kw}x{Nw} matrices, not {K}x{N}")
+    device = _gpu(("A", A), ("dY", dY), ("row_end", row_end), ("dW", dW), ("ws", ws))
+    _same_dtype(A, dY, "A and dY")
+    if My != M:
+        raise ValueError(f"dY has {My} rows, A {M}")
+    if Kw != K or Nw != N:
+        raise ValueError(f"dW holds {Kw}x{Nw} matrices, not {K}x{N}")
     _check(lib().fp4lin_experts_wgrad_mx(
-        _dev(A, "A"), _dev(dY, "dY"), _dtype_code(A), _row_end(row_end, E), E, M, K, N, lda, lddy,
-        _dev(dW, "dW"), _dtype_code(dW), lddw, _dev(ws, "ws"), _nbytes(ws), _stream(stream)),
+        A.data_ptr(), dY.data_ptr(), _code(A), _row_end(row_end, E), E, M, K, N, lda, lddy,
+        dW.data_ptr(), _code(dW), lddw, ws.data_ptr(), _nbytes(ws), _queue(stream, device)),
         "fp4lin_experts_wgrad_mx")
 
 
@@ -514,10 +562,9 @@ def experts_quantize_weight_mx(W, stream=None):
     packed_ld(K)), Ws uint8 (steps, E, N, 4)), the scales step-major."""
     torch = _torch()
     E, K, N, _ = _experts_weight(W, "W")
-    _dev(W, "W")
     with _on(W, stream):
-        Wq = _empty((E, N, packed_ld(K)), torch.uint8, W.device)
-        Ws = _empty((mx_scales_ld(K) // 4, E, N, 4), torch.uint8, W.device)
+        Wq = torch.empty((E, N, packed_ld(K)), dtype=torch.uint8, device=W.device)
+        Ws = torch.empty((mx_scales_ld(K) // 4, E, N, 4), dtype=torch.uint8, device=W.device)
         fp4lin_experts_quantize_weight_mx(W, Wq, Ws)
     return Wq, Ws
 
@@ -530,9 +577,8 @@ def experts_forward_mx(A, W, row_end, out_dtype=None, stream=None):
     torch = _torch()
     M, K, _ = _rows(A, "A")
     E, _, N, _ = _experts_weight(W, "W")
-    _dev(A, "A")
     with _on(A, stream):
-        Y = _empty((M, N), out_dtype or torch.float32, A.device)
+        Y = torch.empty((M, N), dtype=out_dtype or torch.float32, device=A.device)
         ws = _experts_ws(_lib.EXPERTS_FORWARD, E, M, K, N, A.device, "experts_forward_mx")
         fp4lin_experts_forward_mx(A, W, row_end, Y, ws)
     return Y
@@ -544,9 +590,8 @@ def experts_apply_mx(A, Wq, Ws, row_end, out_dtype=None, stream=None):
     M, K, _ = _rows(A, "A")
     _need(Wq.dim() == 3, "Wq must be (experts, columns, packed bytes)")
     E, N, _ = Wq.shape
-    _dev(A, "A")
     with _on(A, stream):
-        Y = _empty((M, N), out_dtype or torch.float32, A.device)
+        Y = torch.empty((M, N), dtype=out_dtype or torch.float32, device=A.device)
         ws = _experts_ws(_lib.EXPERTS_APPLY, E, M, K, N, A.device, "experts_apply_mx")
         fp4lin_experts_apply_mx(A, Wq, Ws, row_end, Y, ws)
     return Y
@@ -557,9 +602,8 @@ def experts_dgrad_mx(dY, W, row_end, out_dtype=None, stream=None):
     torch = _torch()
     M, N, _ = _rows(dY, "dY")
     E, K, _, _ = _experts_weight(W, "W")
-    _dev(dY, "dY")
     with _on(dY, stream):
-        dX = _empty((M, K), out_dtype or torch.float32, dY.device)
+        dX = torch.empty((M, K), dtype=out_dtype or torch.float32, device=dY.device)
         ws = _experts_ws(_lib.EXPERTS_DGRAD, E, M, K, N, dY.device, "experts_dgrad_mx")
         fp4lin_experts_dgrad_mx(dY, W, row_end, dX, ws)
     return dX
@@ -570,11 +614,10 @@ def experts_wgrad_mx(A, dY, row_end, out_dtype=None, stream=None):
     dY (M, N); zeros for an expert without rows."""
     torch = _torch()
     M, K, _ = _rows(A, "A")
-    N = dY.shape[1]
+    _, N, _ = _rows(dY, "dY")
     E = row_end.numel()
-    _dev(A, "A")
     with _on(A, stream):
-        dW = _empty((E, K, N), out_dtype or torch.float32, A.device)
+        dW = torch.empty((E, K, N), dtype=out_dtype or torch.float32, device=A.device)
         ws = _experts_ws(_lib.EXPERTS_WGRAD, E, M, K, N, A.device, "experts_wgrad_mx")
         fp4lin_experts_wgrad_mx(A, dY, row_end, dW, ws)
     return dW
@@ -589,49 +632,52 @@ def head_loss_workspace_bytes(dtype_code, by_vocab, T, H, V, ldx, ldw, backward=
 
 def _head_sizes(X, W, target, by_vocab):
     """(T, H, V, ldx, ldw) of matching X, W and targets."""
-    torch = _torch()
     T, H, ldx = _rows(X, "X")
     r, c, ldw = _rows(W, "W")
-    _same("dtype", X=X, W=W)
-    _same("", X=X, target=target)
-    _need((c if by_vocab else r) == H, f"X is {T}x{H} but W is {r}x{c}" +
-          (" (vocabulary first)" if by_vocab else ""))
-    if target.dtype != torch.int32 or target.dim() != 1 or not target.is_contiguous():
+    _same_dtype(X, W, "X and W")
+    if (c if by_vocab else r) != H:
+        raise ValueError(f"X is {T}x{H} but W is {r}x{c}" + (" (vocabulary first)" if by_vocab else ""))
+    if target.dtype != _torch().int32 or target.dim() != 1 or not target.is_contiguous():
         raise TypeError("target must be a contiguous int32 vector")
-    _need(target.numel() == T, f"{target.numel()} targets for {T} rows")
+    if target.numel() != T:
+        raise ValueError(f"{target.numel()} targets for {T} rows")
     return T, H, r if by_vocab else c, ldx, ldw
 
 
 def _row_floats(t, T, name):
-    torch = _torch()
-    if t.dtype != torch.float32 or t.dim() != 1 or not t.is_contiguous():
+    if t.dtype != _torch().float32 or t.dim() != 1 or not t.is_contiguous():
         raise TypeError(f"{name} must be a contiguous float32 vector")
-    _need(t.numel() == T, f"{name} has {t.numel()} entries for {T} rows")
-    return _dev(t, name)
+    if t.numel() != T:
+        raise ValueError(f"{name} has {t.numel()} entries for {T} rows")
+    return t.data_ptr()
 
 
 def fp4lin_head_loss(X, W, target, loss, lse, ws, by_vocab=False, stream=None):
     T, H, V, ldx, ldw = _head_sizes(X, W, target, by_vocab)
-    _same("", X=X, loss=loss, lse=lse, ws=ws)
+    device = _gpu(("X", X), ("W", W), ("target", target), ("loss", loss), ("lse", lse), ("ws", ws))
     _check(lib().fp4lin_head_loss(
-        _dev(X, "X"), _dev(W, "W"), _dtype_code(X), int(bool(by_vocab)), _dev(target, "target"), T,
-        H, V, ldx, ldw, _row_floats(loss, T, "loss"), _row_floats(lse, T, "lse"), _dev(ws, "ws"),
-        _nbytes(ws), _stream(stream)), "fp4lin_head_loss")
+        X.data_ptr(), W.data_ptr(), _code(X), int(bool(by_vocab)), target.data_ptr(), T, H, V, ldx,
+        ldw, _row_floats(loss, T, "loss"), _row_floats(lse, T, "lse"), ws.data_ptr(), _nbytes(ws),
+        _queue(stream, device)), "fp4lin_head_loss")
 
 
 def fp4lin_head_loss_backward(X, W, target, lse, dloss, dX, dW, ws, by_vocab=False, stream=None):
     T, H, V, ldx, ldw = _head_sizes(X, W, target, by_vocab)
-    _same("dtype", X=X, dX=dX, dW=dW)
-    _same("", X=X, lse=lse, dloss=dloss, ws=ws)
+    device = _gpu(("X", X), ("W", W), ("target", target), ("lse", lse), ("dloss", dloss), ("dX", dX),
+                  ("dW", dW), ("ws", ws))
+    _same_dtype(X, dX, "X and dX")
+    _same_dtype(X, dW, "X and dW")
     Tx, Hx, lddx = _rows(dX, "dX")
     r, c, lddw = _rows(dW, "dW")
-    _need((Tx, Hx) == (T, H), f"dX is {Tx}x{Hx}, not {T}x{H}")
-    _need((r, c) == tuple(W.shape), f"dW is {r}x{c}, W {W.shape[0]}x{W.shape[1]}")
+    if Tx != T or Hx != H:
+        raise ValueError(f"dX is {Tx}x{Hx}, not {T}x{H}")
+    if dW.shape != W.shape:
+        raise ValueError(f"dW is {r}x{c}, W {W.shape[0]}x{W.shape[1]}")
     _check(lib().fp4lin_head_loss_backward(
-        _dev(X, "X"), _dev(W, "W"), _dtype_code(X), int(bool(by_vocab)), _dev(target, "target"),
+        X.data_ptr(), W.data_ptr(), _code(X), int(bool(by_vocab)), target.data_ptr(),
         _row_floats(lse, T, "lse"), _row_floats(dloss, T, "dloss"), T, H, V, ldx, ldw,
-        _dev(dX, "dX"), lddx, _dev(dW, "dW"), lddw, _dev(ws, "ws"), _nbytes(ws), _stream(stream)),
-        "fp4lin_head_loss_backward")
+        dX.data_ptr(), lddx, dW.data_ptr(), lddw, ws.data_ptr(), _nbytes(ws),
+        _queue(stream, device)), "fp4lin_head_loss_backward")
 
 
 def _aligned(t):
@@ -639,11 +685,12 @@ def _aligned(t):
     return t if t.data_ptr() % 16 == 0 else t.clone(memory_format=_torch().contiguous_format)
 
 
-def _head_ws(X, W, T, H, V, ldx, ldw, by_vocab, backward, where):
-    n = head_loss_workspace_bytes(_dtype_code(X), by_vocab, T, H, V, ldx, ldw, backward)
+def _head_ws(X, sizes, by_vocab, backward, where):
+    torch = _torch()
+    n = head_loss_workspace_bytes(_code(X), by_vocab, *sizes, backward)
     if n == 0:
         raise Fp4linError(_lib.ERR_SHAPE, where)
-    return _empty((n,), _torch().uint8, X.device)
+    return torch.empty(n, dtype=torch.uint8, device=X.device)
 
 
 def head_loss(X, W, target, by_vocab=False, stream=None):
@@ -652,13 +699,13 @@ def head_loss(X, W, target, by_vocab=False, stream=None):
     bfloat16. Returns (loss, lse), float32 of T entries; a row whose target
     lies outside [0, V) has loss 0."""
     torch = _torch()
-    _head_sizes(X, W, target, by_vocab)
+    _gpu(("X", X), ("W", W))
     with _on(X, stream):
         X, W = _aligned(X), _aligned(W)
-        T, H, V, ldx, ldw = _head_sizes(X, W, target, by_vocab)
-        ws = _head_ws(X, W, T, H, V, ldx, ldw, by_vocab, False, "head_loss")
-        loss = _empty((T,), torch.float32, X.device)
-        lse = _empty((T,), torch.float32, X.device)
+        sizes = _head_sizes(X, W, target, by_vocab)
+        ws = _head_ws(X, sizes, by_vocab, False, "head_loss")
+        loss = torch.empty(sizes[0], dtype=torch.float32, device=X.device)
+        lse = torch.empty(sizes[0], dtype=torch.float32, device=X.device)
         fp4lin_head_loss(X, W, target, loss, lse, ws, by_vocab)
     return loss, lse
 
@@ -666,13 +713,14 @@ def head_loss(X, W, target, by_vocab=False, stream=None):
 def head_loss_backward(X, W, target, lse, dloss, by_vocab=False, stream=None):
     """Gradients of sum(dloss * loss) of head_loss: (dX, dW), of X's and W's
     shape and dtype. lse is head_loss's, dloss float32 of T entries."""
-    _head_sizes(X, W, target, by_vocab)
+    torch = _torch()
+    _gpu(("X", X), ("W", W))
     with _on(X, stream):
         X, W = _aligned(X), _aligned(W)
-        T, H, V, ldx, ldw = _head_sizes(X, W, target, by_vocab)
-        ws = _head_ws(X, W, T, H, V, ldx, ldw, by_vocab, True, "head_loss_backward")
-        dX = _empty((T, H), X.dtype, X.device)
-        dW = _empty(tuple(W.shape), W.dtype, W.device)
+        sizes = _head_sizes(X, W, target, by_vocab)
+        ws = _head_ws(X, sizes, by_vocab, True, "head_loss_backward")
+        dX = torch.empty((sizes[0], sizes[1]), dtype=X.dtype, device=X.device)
+        dW = torch.empty(tuple(W.shape), dtype=W.dtype, device=W.device)
         fp4lin_head_loss_backward(X, W, target, lse, dloss, dX, dW, ws, by_vocab)
     return dX, dW
 
@@ -684,64 +732,71 @@ def clip_workspace_bytes(count: int, elements: int) -> int:
 
 def _dense(t, name):
     """A tensor whose elements fill its memory without gaps or overlaps."""
-    if t.is_contiguous() or t.numel() == 0:
-        return
     at = 1
     for stride, size in sorted((t.stride(d), t.shape[d]) for d in range(t.dim()) if t.shape[d] > 1):
-        if stride != at:
+        if stride != at and t.numel() > 0:
             raise ValueError(f"{name} must be dense in memory")
         at *= size
 
 
 def _grads(tensors, out):
-    """The C array of a list of gradients and its outputs, and its elements."""
+    """The C array of a list of gradients and its outputs, their number and
+    elements, and the GPU they are on."""
+    torch = _torch()
+    T = torch.Tensor
     tensors = list(tensors)
-    out = tensors if out is None else list(out)
-    _need(len(out) == len(tensors), f"{len(out)} outputs for {len(tensors)} gradients")
-    array = (_lib.Grad * max(len(tensors), 1))()
-    elements, device = 0, None
-    for i, (g, o) in enumerate(zip(tensors, out)):
-        _dev(g, "gradient")
-        if device is None:
-            device = g.device
-        _need(g.device == device, f"gradient {i} is on {g.device}, the first on {device}")
-        _dense(g, f"gradient {i}")
-        if o is not g:
-            _dev(o, "output")
-            if o.dtype != g.dtype:
-                raise TypeError(f"output {i} is {o.dtype}, gradient {i} {g.dtype}")
-            _need(o.device == device and o.shape == g.shape and
-                  (o.stride() == g.stride() or (o.is_contiguous() and g.is_contiguous())),
-                  f"output {i} must have the shape, strides and device of gradient {i}")
-        array[i] = _lib.Grad(g.data_ptr(), o.data_ptr(), g.numel(), _dtype_code(g))
-        elements += g.numel()
-    return array, len(tensors), elements
+    own = out is None
+    out = tensors if own else list(out)
+    count = len(tensors)
+    _need(count > 0, "no gradients")
+    _need(len(out) == count, f"{len(out)} outputs for {count} gradients")
+    both = tensors if own else tensors + out
+    # whole lists at once: a call on many small tensors spends its time here
+    devices = set(map(T.get_device, both))
+    if len(devices) != 1 or min(devices) < 0:
+        for t in both:
+            _dev(t, "gradient")
+        raise ValueError("the gradients and outputs must be on one GPU")
+    codes = list(map(_code, tensors))
+    if not own and codes != list(map(_code, out)):
+        raise TypeError("an output must have its gradient's dtype")
+    if not own and list(map(T.size, tensors)) != list(map(T.size, out)):
+        raise ValueError("an output must have its gradient's shape")
+    if not all(map(T.is_contiguous, both)):
+        for i, (g, o) in enumerate(zip(tensors, out)):
+            _dense(g, f"gradient {i}")
+            _need(g.stride() == o.stride() or (g.is_contiguous() and o.is_contiguous()),
+                  f"output {i} must have the strides of gradient {i}")
+    sizes = list(map(T.numel, tensors))
+    pointers = list(map(T.data_ptr, tensors))
+    rows = zip(pointers, pointers if own else map(T.data_ptr, out), sizes, codes)
+    data = struct.pack("QQqi4x" * count, *itertools.chain.from_iterable(rows))
+    return (_lib.Grad * count).from_buffer_copy(data), count, sum(sizes), devices.pop()
 
 
 def fp4lin_grad_norm(tensors, norm, ws, stream=None):
-    array, count, _ = _grads(tensors, None)
-    _check(lib().fp4lin_grad_norm(array, count, _dev(norm, "norm"), _dev(ws, "ws"), _nbytes(ws),
-                                  _stream(stream)), "fp4lin_grad_norm")
+    array, count, _, device = _grads(tensors, None)
+    _gpu(("norm", norm), ("ws", ws))
+    _check(lib().fp4lin_grad_norm(array, count, norm.data_ptr(), ws.data_ptr(), _nbytes(ws),
+                                  _queue(stream, device)), "fp4lin_grad_norm")
 
 
 def fp4lin_clip_grads(tensors, max_norm, norm, ws, out=None, stream=None):
-    array, count, _ = _grads(tensors, out)
-    _check(lib().fp4lin_clip_grads(array, count, float(max_norm), _dev(norm, "norm"),
-                                   _dev(ws, "ws"), _nbytes(ws), _stream(stream)),
-           "fp4lin_clip_grads")
+    array, count, _, device = _grads(tensors, out)
+    _gpu(("norm", norm), ("ws", ws))
+    _check(lib().fp4lin_clip_grads(array, count, float(max_norm), norm.data_ptr(), ws.data_ptr(),
+                                   _nbytes(ws), _queue(stream, device)), "fp4lin_clip_grads")
 
 
 def _clip(tensors, max_norm, out, stream):
     torch = _torch()
     tensors = list(tensors)
-    _need(len(tensors) > 0, "no gradients")
-    array, count, elements = _grads(tensors, out)
-    _dev(tensors[0], "gradient")
+    array, count, elements, device = _grads(tensors, out)
     with _on(tensors[0], stream):
-        device = tensors[0].device
-        ws = _empty((clip_workspace_bytes(count, elements),), torch.uint8, device)
-        norm = _empty((), torch.float32, device)
-        args = (_dev(norm, "norm"), _dev(ws, "ws"), _nbytes(ws), _stream(None))
+        n = lib().fp4lin_clip_workspace_bytes(count, elements)
+        ws = torch.empty(n, dtype=torch.uint8, device=tensors[0].device)
+        norm = torch.empty((), dtype=torch.float32, device=tensors[0].device)
+        args = (norm.data_ptr(), ws.data_ptr(), n, _queue(None, device))
         if max_norm is None:
             _check(lib().fp4lin_grad_norm(array, count, *args), "grad_norm")
         else:

@@ -676,6 +676,10 @@ fp4lin_status fp4lin_experts_apply_mx(const void* A, fp4lin_dtype dt, const uint
   if (M == 0) return FP4LIN_OK;
   uint8_t* const base = static_cast<uint8_t*>(ws);
   const int64_t ldq = fp4lin_packed_ld(K);
+  if (fp4lin::experts_fused(M, K))
+    return launch_status(fp4lin::launch_experts_fused(A, dt == FP4LIN_BF16, lda, Wq, Ws, row_end, E,
+                                                      M, K, N, ldq, Y, ydt == FP4LIN_BF16, ldy,
+                                                      stream));
   s = launch_status(fp4lin::launch_quantize_rows_mx(A, dt == FP4LIN_BF16, M, K, lda, nullptr,
                                                     base + o.Aq, ldq, base + o.As, stream));
   if (s != FP4LIN_OK) return s;

@@ -123,12 +123,14 @@ struct DenseFeed {
     const int k0 = kt * kE;
     if constexpr (kT) {
       // the resource starts at the step's first reduction row and ends with its
-      // last one inside k, so rows past k read as zero
+      // last one inside k, so rows past k read as zero (and a step past k has none:
+      // (left - 1) * ld + cols <= 0 there, as ld >= cols)
       const int left = o.k - k0 < kE ? o.k - k0 : kE;
       const int cols = o.extent < BX ? o.extent : BX;
-      const int bytes = int(((left - 1) * o.ld + cols) * int64_t(sizeof(T)));
+      const int ldb = int(o.ld * int64_t(sizeof(T)));
+      const int end = (left - 1) * ldb + cols * int(sizeof(T));
       const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
-          const_cast<T*>(o.p + int64_t(k0) * o.ld), 0, bytes, kBufferFlags);
+          const_cast<T*>(o.p + int64_t(k0) * o.ld), 0, end > 0 ? end : 0, kBufferFlags);
 #pragma unroll
       for (int j = J0; j < J1; ++j) load_lds16(rs, dst + (j - J0) * kWaves * 1024, src_off[j]);
     } else {
@@ -151,28 +153,32 @@ struct DenseFeed {
     load<BN, kBT, kPerA, kPer>(B, kt, stage + BM * 64 + wave * 1024);
   }
 
+  // Fragment of rows x0 .. x0 + 31 in the sub-step kk of the operand staged at
+  // byte `at` of the stage. (Every address is one offset from the stage's own
+  // array: through longer chains the compiler loses which array a read is from
+  // and waits for all loads in flight.)
   template <int BX, bool kT>
-  __device__ inline Frag frag(const uint8_t* s, int x0, int kk) const {
+  __device__ inline Frag frag(const uint8_t* stage, int at, int x0, int kk) const {
     if constexpr (!kT) {
       const int r = x0 + (lane & 31);
       const int c = kk * 2 + (lane >> 5);
-      return *reinterpret_cast<const Frag*>(s + r * 64 + (swz<CPR>(r, c) << 4));
+      return *reinterpret_cast<const Frag*>(stage + (at + r * 64 + (swz<CPR>(r, c) << 4)));
     } else if constexpr (kBf16) {
       const int g = lane >> 4, i = lane & 15;
       const int row = kk * 16 + 8 * (g >> 1) + (i >> 2);
       const int x = x0 + 16 * (g & 1) + (i & 3) * 4;
       // rows row and row + 4 have the same swizzle key
-      const uint8_t* const p = s + across<BX>(row, x);
+      const int p = at + across<BX>(row, x);
       typedef __attribute__((address_space(3))) s16x4* lds_ptr;
-      const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)p);
-      const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(p + 4 * BX * 2));
+      const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(stage + p));
+      const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(stage + (p + 4 * BX * 2)));
       return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
     } else {
       const int row = kk * 8 + 4 * (lane >> 5);
-      const uint8_t* const p = s + across<BX>(row, x0 + (lane & 31));
+      const int p = at + across<BX>(row, x0 + (lane & 31));
       f32x4 v;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] = *reinterpret_cast<const float*>(p + j * BX * 4);
+      for (int j = 0; j < 4; ++j) v[j] = *reinterpret_cast<const float*>(stage + (p + j * BX * 4));
       return __builtin_bit_cast(Frag, v);
     }
   }
@@ -180,10 +186,10 @@ struct DenseFeed {
   __device__ inline void read_frags(const uint8_t* stage, int kk, Frag* af, Frag* bf) {
     const int wm = wave / WN, wn = wave % WN;
 #pragma unroll
-    for (int fm = 0; fm < FM; ++fm) af[fm] = frag<BM, kAT>(stage, (wm * FM + fm) * 32, kk);
+    for (int fm = 0; fm < FM; ++fm) af[fm] = frag<BM, kAT>(stage, 0, (wm * FM + fm) * 32, kk);
 #pragma unroll
     for (int fn = 0; fn < FN; ++fn)
-      bf[fn] = frag<BN, kBT>(stage + BM * 64, (wn * FN + fn) * 32, kk);
+      bf[fn] = frag<BN, kBT>(stage, BM * 64, (wn * FN + fn) * 32, kk);
   }
 
   __device__ inline void load_scales(int, uint32_t*) {}

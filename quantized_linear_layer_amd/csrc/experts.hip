@@ -237,21 +237,30 @@ __global__ __launch_bounds__(C::kThreads, C::kMinBlocks) void experts_gemm_kerne
 // ---------------------------------------------------------------------------
 // Few rows an expert (serving): bound by reading the weights' codes once.
 // ---------------------------------------------------------------------------
-// A workgroup of four waves owns 16 columns of one expert and walks its rows in
-// chunks of 16 * MF. The waves split K: wave w takes the K steps w, w + 4, ...,
-// so that the four read 256 contiguous bytes of each column's packed row. Codes
-// go from memory straight to the matrix core's registers (the 16x16x128 shape:
-// lane l holds the 32 codes of block l / 16 of the step for column l % 16, one
-// 16-byte load, and the block's scale byte); kAhead steps of loads are in
-// flight. The four partial sums are added in wave order through LDS.
-constexpr int kFewWaves = 4;
+// A workgroup of W waves owns 16 columns of one expert. The waves split K: wave
+// w takes the K steps w, w + W, ..., so that the waves read contiguous bytes of
+// each column's packed row. Codes go from memory straight to the matrix core's
+// registers (the 16x16x128 shape: lane l holds the 32 codes of block l / 16 of the
+// step for column l % 16, one 16-byte load, and the block's scale byte), kSteps
+// steps a wave at once, where they stay while the expert's rows go by in chunks
+// of 32: with K <= 128 kSteps W each code is read once, whatever the rows. The
+// waves' partial sums are added in wave order through LDS.
+//
+// kFused: the activations are not quantized by a launch of their own; every
+// workgroup quantizes its expert's few rows into LDS, which at this size costs
+// less than the launch (M <= 16 and M * K <= kFusedElems).
+constexpr int kSteps = 8;
+constexpr int64_t kFusedRows = 16, kFusedElems = 8192;
 
 typedef float v4f __attribute__((ext_vector_type(4)));
 
 struct FewArgs {
   const uint8_t *Aq, *As, *Bq, *Bs;
+  const void* A;  // kFused: the activations, M x K
+  int64_t lda;
+  int fast;       // kFused: A allows 16-byte loads of 8 elements
   const int32_t* row_end;
-  int E, M, N, ldq;
+  int E, M, K, N, ldq;
   void* Y;
   int64_t ldy;
 };
@@ -259,9 +268,45 @@ struct FewArgs {
 __device__ inline void store_out(float* p, float v) { *p = v; }
 __device__ inline void store_out(uint16_t* p, float v) { *p = uint16_t(bf16_pair(v, v)); }
 
-template <int MF, class Out>
-__global__ __launch_bounds__(kFewWaves * 64) void experts_few_kernel(FewArgs p) {
-  __shared__ v4f part[kFewWaves][MF][64];
+// Rows begin .. begin + rows - 1 of A as codes (ldq bytes a row) and scale
+// bytes (ldq / 16 a row) in LDS.
+template <class In>
+__device__ inline void quantize_few(const FewArgs& p, int begin, int rows, uint8_t* codes,
+                                    uint8_t* scales) {
+  const int cpr = p.ldq / 4;  // chunks of 8 codes a row; four lanes hold a block
+  for (int i = threadIdx.x; i < rows * cpr; i += blockDim.x) {
+    const int r = i / cpr, c = i - r * cpr;
+    const auto* row = static_cast<const typename In::T*>(p.A) + (begin + r) * p.lda;
+    Vec8<In> v;
+    if (p.fast)
+      load_chunk<In, true>(row, c * 8, p.K, v);
+    else
+      load_chunk<In, false>(row, c * 8, p.K, v);
+    float ax[8], m = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      ax[j] = fabsf(In::widen(v.v[j]));
+      m = fmaxf(m, ax[j]);
+    }
+    const int e = mx_exponent(quad_max(m));
+    uint32_t word = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      word |= (mx_magnitude(ax[j], e) | (In::sign_bit(v.v[j]) << 3)) << (4 * j);
+    *reinterpret_cast<uint32_t*>(codes + r * p.ldq + c * 4) = word;
+    if ((c & 3) == 0) scales[r * (p.ldq / 16) + c / 4] = uint8_t(e + 127);
+  }
+}
+
+// In: the activations' type with kFused, else void.
+template <int W, class In, class Out>
+__global__ __launch_bounds__(W * 64, 4) void experts_few_kernel(FewArgs p) {
+  constexpr bool kFused = !std::is_void<In>::value;
+  __shared__ v4f part[W][2][64];
+  // M * K <= kFusedElems: codes and padding of at most 16 rows
+  constexpr int kCodeBytes = kFused ? kFusedElems / 2 + kFusedRows * 64 : 16;
+  __shared__ __attribute__((aligned(16))) uint8_t codes[kCodeBytes];
+  __shared__ uint8_t scales[kFused ? kCodeBytes / 16 : 16];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const Group g = group_of_expert<16>(p.row_end, p.E, p.M, blockIdx.y);
@@ -274,60 +319,74 @@ __global__ __launch_bounds__(kFewWaves * 64) void experts_few_kernel(FewArgs p) 
   const uint8_t* const brow = p.Bq + bcol * p.ldq + q * 16;
   const uint8_t* const bsc = p.Bs + 4 * bcol + q;
   const int64_t bstep = 4 * int64_t(p.E) * p.N, astep = 4 * int64_t(p.M);
-  constexpr int kAhead = MF == 1 ? 8 : 4;
-  for (int r0 = 0; r0 < g.rows; r0 += 16 * MF) {
-    v4f acc[MF];
-    const uint8_t *arow[MF], *asc[MF];
+  const bool once = nkt <= kSteps * W;  // the codes stay in registers
+  uint4 b[kSteps];
+  int sb[kSteps];
+  // steps past the end repeat the last one and are not multiplied
+  auto step_of = [&](int s0, int u) { return s0 + u * W < nkt ? s0 + u * W : nkt - 1; };
+  auto load_b = [&](int s0) {
 #pragma unroll
-    for (int i = 0; i < MF; ++i) {
-      acc[i] = v4f{};
-      // rows past the group's end repeat its last row; they are not stored
-      const int r = r0 + 16 * i + (lane & 15);
-      const int64_t row = g.begin + (r < g.rows ? r : g.rows - 1);
-      arow[i] = p.Aq + row * p.ldq + q * 16;
-      asc[i] = p.As + 4 * row + q;
+    for (int u = 0; u < kSteps; ++u) {
+      const int s = step_of(s0, u);
+      b[u] = *reinterpret_cast<const uint4*>(brow + s * 64);
+      sb[u] = bsc[s * bstep];
     }
-    for (int s0 = wave; s0 < nkt; s0 += kFewWaves * kAhead) {
-      uint4 b[kAhead], a[kAhead][MF];
-      int sb[kAhead], sa[kAhead][MF];
-#pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        // steps past the end repeat the last one and are not multiplied
-        const int s = s0 + u * kFewWaves < nkt ? s0 + u * kFewWaves : nkt - 1;
-        b[u] = *reinterpret_cast<const uint4*>(brow + s * 64);
-        sb[u] = bsc[s * bstep];
-#pragma unroll
-        for (int i = 0; i < MF; ++i) {
-          a[u][i] = *reinterpret_cast<const uint4*>(arow[i] + s * 64);
-          sa[u][i] = asc[i][s * astep];
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        if (s0 + u * kFewWaves < nkt) {
-          const v8i bf{int(b[u].x), int(b[u].y), int(b[u].z), int(b[u].w), 0, 0, 0, 0};
-#pragma unroll
-          for (int i = 0; i < MF; ++i) {
-            const v8i af{int(a[u][i].x), int(a[u][i].y), int(a[u][i].z), int(a[u][i].w), 0, 0, 0, 0};
-            acc[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(af, bf, acc[i], 4, 4, 0,
-                                                                      sa[u][i], 0, sb[u]);
-          }
-        }
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < MF; ++i) part[wave][i][lane] = acc[i];
+  };
+  if (once && nkt > 0) load_b(wave);
+  if constexpr (kFused) {
+    if (nkt > 0) quantize_few<In>(p, g.begin, g.rows, codes, scales);
     __syncthreads();
-    // wave w finishes the fragments w, w + 4, ...
+  }
+  for (int r0 = 0; r0 < g.rows; r0 += 32) {
+    const bool two = g.rows > r0 + 16;
+    v4f acc[2] = {v4f{}, v4f{}};
+    // rows past the group's end repeat its last row; they are not stored
+    int ra[2];
 #pragma unroll
-    for (int i = 0; i < MF; ++i) {
-      if (i % kFewWaves != wave) continue;
-      v4f sum = part[0][i][lane];
+    for (int i = 0; i < 2; ++i) {
+      const int r = r0 + 16 * i + (lane & 15);
+      ra[i] = r < g.rows ? r : g.rows - 1;
+    }
+    auto multiply = [&](int s0, int i) {
+      uint4 a[kSteps];
+      int sa[kSteps];
 #pragma unroll
-      for (int w = 1; w < kFewWaves; ++w) sum += part[w][i][lane];
+      for (int u = 0; u < kSteps; ++u) {
+        const int s = step_of(s0, u);
+        if constexpr (kFused) {
+          a[u] = *reinterpret_cast<const uint4*>(codes + ra[i] * p.ldq + s * 64 + q * 16);
+          sa[u] = scales[ra[i] * (p.ldq / 16) + s * 4 + q];
+        } else {
+          const int64_t row = g.begin + ra[i];
+          a[u] = *reinterpret_cast<const uint4*>(p.Aq + row * p.ldq + s * 64 + q * 16);
+          sa[u] = p.As[s * astep + 4 * row + q];
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kSteps; ++u) {
+        if (s0 + u * W >= nkt) break;
+        const v8i af{int(a[u].x), int(a[u].y), int(a[u].z), int(a[u].w), 0, 0, 0, 0};
+        const v8i bf{int(b[u].x), int(b[u].y), int(b[u].z), int(b[u].w), 0, 0, 0, 0};
+        acc[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(af, bf, acc[i], 4, 4, 0, sa[u],
+                                                                  0, sb[u]);
+      }
+    };
+    for (int s0 = wave; s0 < nkt; s0 += W * kSteps) {
+      if (!once) load_b(s0);
+      multiply(s0, 0);
+      if (two) multiply(s0, 1);
+    }
+    part[wave][0][lane] = acc[0];
+    part[wave][1][lane] = acc[1];
+    __syncthreads();
+    // waves 0 and 1 finish the two fragments
+    if (wave < (two ? 2 : 1)) {
+      v4f sum = part[0][wave][lane];
+#pragma unroll
+      for (int w = 1; w < W; ++w) sum += part[w][wave][lane];
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        const int r = r0 + 16 * i + 4 * q + c;
+        const int r = r0 + 16 * wave + 4 * q + c;
         if (r < g.rows && n < p.N) store_out(Y + (g.begin + r) * p.ldy + n, sum[c]);
       }
     }
@@ -355,17 +414,36 @@ int64_t most_units(int64_t M, int64_t E, int64_t R) {
   return (M + groups * (R - 1)) / R;
 }
 
+template <class In, class Out>
+hipError_t run_few(const FewArgs& a, hipStream_t stream) {
+  const dim3 grid(unsigned(ceil_div(a.N, 16)), unsigned(a.E + 1));
+  const int steps = a.ldq / 64;
+  if (steps <= 4 * kSteps)
+    experts_few_kernel<4, In, Out><<<grid, 4 * 64, 0, stream>>>(a);
+  else if (steps <= 8 * kSteps || !std::is_void<In>::value)
+    experts_few_kernel<8, In, Out><<<grid, 8 * 64, 0, stream>>>(a);
+  else if constexpr (std::is_void<In>::value)
+    experts_few_kernel<16, In, Out><<<grid, 16 * 64, 0, stream>>>(a);
+  return hipGetLastError();
+}
+
 template <class Out>
 hipError_t run_rows(const TileArgs& p, hipStream_t stream) {
   const int64_t tiles_n = ceil_div(p.cols, 256);
-  if (p.M <= kFewRows * p.E && p.E < 65535) {
-    const FewArgs a{p.Aq, p.As, p.Bq, p.Bs, p.row_end, p.E, p.M, p.cols, p.ldq, p.Y, p.ldy};
-    const dim3 grid(unsigned(ceil_div(p.cols, 16)), unsigned(p.E + 1));
-    if (p.M <= 16 * p.E)
-      experts_few_kernel<1, Out><<<grid, kFewWaves * 64, 0, stream>>>(a);
-    else
-      experts_few_kernel<2, Out><<<grid, kFewWaves * 64, 0, stream>>>(a);
-    return hipGetLastError();
+  if (p.M <= kFewRows * p.E) {
+    FewArgs a{};
+    a.Aq = p.Aq;
+    a.As = p.As;
+    a.Bq = p.Bq;
+    a.Bs = p.Bs;
+    a.row_end = p.row_end;
+    a.E = p.E;
+    a.M = p.M;
+    a.N = p.cols;
+    a.ldq = p.ldq;
+    a.Y = p.Y;
+    a.ldy = p.ldy;
+    return run_few<void, Out>(a, stream);
   }
   if (ceil_div(p.M, LargeTile::BM) * tiles_n >= kLargeTilesMin)
     return run_tiles<LargeTile, Out, false>(p, most_units(p.M, p.E, LargeTile::BM) * tiles_n,
@@ -439,6 +517,31 @@ hipError_t launch_experts_rows(const uint8_t* Aq, const uint8_t* As, const uint8
                                hipStream_t stream) {
   const TileArgs p{Aq, As, Bq, Bs, row_end, int(E), int(M), 0, int(N), int(ldq), Y, ldy};
   return y_bf16 ? run_rows<uint16_t>(p, stream) : run_rows<float>(p, stream);
+}
+
+bool experts_fused(int64_t M, int64_t K) { return M <= kFusedRows && M * K <= kFusedElems; }
+
+hipError_t launch_experts_fused(const void* A, bool bf16, int64_t lda, const uint8_t* Bq,
+                                const uint8_t* Bs, const int32_t* row_end, int64_t E, int64_t M,
+                                int64_t K, int64_t N, int64_t ldq, void* Y, bool y_bf16,
+                                int64_t ldy, hipStream_t stream) {
+  FewArgs a{};
+  a.A = A;
+  a.lda = lda;
+  a.fast = reinterpret_cast<uintptr_t>(A) % 16 == 0 && (lda * (bf16 ? 2 : 4)) % 16 == 0 && K % 8 == 0;
+  a.Bq = Bq;
+  a.Bs = Bs;
+  a.row_end = row_end;
+  a.E = int(E);
+  a.M = int(M);
+  a.K = int(K);
+  a.N = int(N);
+  a.ldq = int(ldq);
+  a.Y = Y;
+  a.ldy = ldy;
+  if (bf16)
+    return y_bf16 ? run_few<BF16In, uint16_t>(a, stream) : run_few<BF16In, float>(a, stream);
+  return y_bf16 ? run_few<F32In, uint16_t>(a, stream) : run_few<F32In, float>(a, stream);
 }
 
 hipError_t launch_experts_wgrad(const uint8_t* Aq, const uint8_t* As, const uint8_t* Bq,

@@ -37,6 +37,9 @@ constexpr int waitcnt_vm_lgkm(int vm, int lgkm) {
   return (vm & 15) | ((vm >> 4) << 14) | (7 << 4) | (lgkm << 8);
 }
 
+// The same with lgkmcnt left alone.
+constexpr int waitcnt_vm(int vm) { return waitcnt_vm_lgkm(vm, 15); }
+
 // Physical 16-byte chunk of logical chunk c in staged row r. A fragment read
 // is a 128-bit LDS read of 32 consecutive rows at one logical chunk (lanes
 // 32..63 at the next chunk). On gfx950 such a read takes 4 LDS cycles when
@@ -342,6 +345,94 @@ __device__ __attribute__((always_inline)) inline void gemm_pipeline(F& f, int nk
   }
   if (kt0 < nkt) tail_step(st0, st1, kt0 + 1 < nkt, sc0);
   if (kt0 + 1 < nkt) tail_step(st1, st2, false, sc1);
+  __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm(0, 0));
+  raw_barrier();
+}
+
+// step(kt, 0), step(kt + 1, 1), ... up to S of them, while below end: nested,
+// so that no path skips a step and runs a later one.
+template <int S, class Step, int I>
+__device__ __attribute__((always_inline)) inline void steps_of(const Step& step, int kt, int end,
+                                                               std::integral_constant<int, I> i) {
+  if constexpr (I < S) {
+    if (kt < end) {
+      step(kt, i);
+      steps_of<S>(step, kt + 1, end, std::integral_constant<int, I + 1>{});
+    }
+  }
+}
+
+// The same product with the eight waves of a large tile in two groups that take
+// turns: waves w and w + 4 share a SIMD, and while one of them multiplies a
+// sub-step the other reads its next fragments and issues its loads. Phases are
+// separated by workgroup barriers; waves 4..7 pass one more barrier at the start
+// (waves 0..3 at the end), which is what shifts them by a phase. With j = 2 kt + kk
+// the sub-steps, a wave alternates
+//   L_j  reads the fragments of j + 1 (into the other register set); with kk = 0
+//        waits for its own loads of step kt + 1, with kk = 1 issues those of
+//        step kt + S - 1
+//   M_j  multiplies j
+// in phases 2j and 2j + 1 (waves 4..7: 2j + 1 and 2j + 2). Step kt + S - 1 goes
+// into the stage of step kt - 1: its last fragments, of sub-step 2 kt - 1, were
+// waited for by the MFMAs of M_(2 kt - 1), phase 4 kt at the latest, and the loads
+// are issued in phase 4 kt + 2 at the earliest. Step kt + 1 is read from phase
+// 4 kt + 2 on; every wave has waited for its loads of it by phase 4 kt + 1.
+// Steps past the last one are issued as loads that return nothing (F::dma), so
+// that the counts stay the same on every path.
+template <class F, int S>
+__device__ __attribute__((always_inline)) inline void gemm_pipeline_turns(F& f, int nkt,
+                                                                          uint8_t* const (&st)[S]) {
+  constexpr int kPer = F::kPer, NL = F::NL, NS = F::NS, FM = F::FM, FN = F::FN;
+  constexpr int kInFlight = (S - 3) * (kPer + NL) + NL;
+  static_assert((S - 1) * (kPer + NL) < 64, "vmcnt immediate");
+  uint32_t sc[S][NL > 0 ? NL : 1];
+  typename F::Frag a0[FM], b0[FN], a1[FM], b1[FN];
+  uint32_t scw[NS > 0 ? NS : 1];
+  auto step = [&](int kt, auto i_c) {
+    constexpr int i = decltype(i_c)::value;
+    constexpr int nxt = (i + 1) % S, prv = (i + S - 1) % S;
+    // L, kk = 0
+    f.read_frags(st[i], 1, a1, b1);
+    f.expand(sc[i], scw);
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_waitcnt(waitcnt_vm(kInFlight));
+    raw_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_setprio(1);
+    f.template mfmas<0>(a0, b0, scw);
+    __builtin_amdgcn_s_setprio(0);
+    __builtin_amdgcn_sched_barrier(0);
+    raw_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    // L, kk = 1
+    f.read_frags(st[nxt], 0, a0, b0);
+    f.dma(kt + S - 1, st[prv]);
+    f.load_scales(kt + S - 1 < nkt ? kt + S - 1 : nkt - 1, sc[prv]);
+    __builtin_amdgcn_sched_barrier(0);
+    raw_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_setprio(1);
+    f.template mfmas<1>(a1, b1, scw);
+    __builtin_amdgcn_s_setprio(0);
+    __builtin_amdgcn_sched_barrier(0);
+    raw_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+  };
+#pragma unroll
+  for (int s = 0; s < S - 1; ++s) {
+    f.dma(s, st[s]);
+    f.load_scales(s < nkt ? s : nkt - 1, sc[s]);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  __builtin_amdgcn_s_waitcnt(waitcnt_vm((S - 2) * (kPer + NL) + NL));  // step 0 landed
+  raw_barrier();
+  f.read_frags(st[0], 0, a0, b0);
+  const bool late = f.wave >= 4;
+  if (late) raw_barrier();
+  int kt = 0;
+  for (; kt + S <= nkt; kt += S) steps_of<S>(step, kt, kt + S, std::integral_constant<int, 0>{});
+  steps_of<S>(step, kt, nkt, std::integral_constant<int, 0>{});
+  if (!late) raw_barrier();
   __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm(0, 0));
   raw_barrier();
 }

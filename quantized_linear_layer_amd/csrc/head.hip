@@ -60,12 +60,20 @@ __device__ inline float half_sum(float v) {
 // Row of element r of a 32x32 fragment on this lane.
 __device__ inline int frag_row(int r, int lane) { return 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3); }
 
-// The tile's logits in f.acc (rows from m0, columns from n0).
-template <class C, class T, bool kBT>
-__device__ __attribute__((always_inline)) inline void logits_tile(
-    DenseFeed<C, T, false, kBT>& f, int H, uint8_t* st0, uint8_t* st1, uint8_t* st2) {
-  constexpr int kE = kStepElems<T>;
-  gemm_pipeline(f, (H + kE - 1) / kE, st0, st1, st2);
+// Tiles of eight waves run the two-group pipeline, on five stages.
+template <class C>
+constexpr bool kTurns = C::kThreads == 512;
+
+template <class C, class F>
+__device__ __attribute__((always_inline)) inline void product_tile(F& f, int nkt, uint8_t* st0,
+                                                                   uint8_t* st1, uint8_t* st2,
+                                                                   uint8_t* st3, uint8_t* st4) {
+  if constexpr (kTurns<C>) {
+    uint8_t* const st[5] = {st0, st1, st2, st3, st4};
+    gemm_pipeline_turns<F, 5>(f, nkt, st);
+  } else {
+    gemm_pipeline(f, nkt, st0, st1, st2);
+  }
 }
 
 template <class T>
@@ -75,7 +83,8 @@ struct HeadArgs {
   int v0, Vall;          // W's first column in the vocabulary, and its size
   const int32_t* target;
   // forward
-  float2* part;     // [columns / columns of a wave][T]: (m, s)
+  float2* part;     // [T][parts]: (m, s) of each group of columns
+  int parts;
   float* tlogit;    // [T]
   // backward
   const float* lse;
@@ -91,6 +100,8 @@ __global__ __launch_bounds__(C::kThreads, C::kMinBlocks) void head_lse_kernel(He
   __shared__ __attribute__((aligned(16))) uint8_t st0[C::kStageBytes];
   __shared__ __attribute__((aligned(16))) uint8_t st1[C::kStageBytes];
   __shared__ __attribute__((aligned(16))) uint8_t st2[C::kStageBytes];
+  __shared__ __attribute__((aligned(16))) uint8_t st3[kTurns<C> ? C::kStageBytes : 16];
+  __shared__ __attribute__((aligned(16))) uint8_t st4[kTurns<C> ? C::kStageBytes : 16];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / C::WN, wn = wave % C::WN;
@@ -99,7 +110,7 @@ __global__ __launch_bounds__(C::kThreads, C::kMinBlocks) void head_lse_kernel(He
   tile_of(xcd_run(blockIdx.x, tiles_m * tiles_n), tiles_m, tiles_n, tm, tn);
   const int m0 = tm * C::BM, n0 = tn * C::BN;
   DenseFeed<C, T, false, kBT> f(p.X, p.W, m0, n0, wave, lane);
-  logits_tile(f, p.H, st0, st1, st2);
+  product_tile<C>(f, (p.H + kStepElems<T> - 1) / kStepElems<T>, st0, st1, st2, st3, st4);
 
   const int row0 = m0 + wm * FM * 32, col0 = n0 + wn * FN * 32;
   // the rows of this wave whose target it holds: few, so they are looked up one
@@ -129,7 +140,7 @@ __global__ __launch_bounds__(C::kThreads, C::kMinBlocks) void head_lse_kernel(He
 #pragma unroll
         for (int r = 0; r < 16; ++r) f.acc[fm][fn][r] = -__builtin_huge_valf();
     }
-  float2* const part = p.part + int64_t(tn * C::WN + wn) * p.T_;
+  float2* const part = p.part + (tn * C::WN + wn);
 #pragma unroll
   for (int fm = 0; fm < FM; ++fm)
 #pragma unroll
@@ -144,20 +155,19 @@ __global__ __launch_bounds__(C::kThreads, C::kMinBlocks) void head_lse_kernel(He
       for (int fn = 0; fn < FN; ++fn) s += exp_diff(f.acc[fm][fn][r], ref);
       s = half_sum(s);
       const int row = row0 + fm * 32 + frag_row(r, lane);
-      if ((lane & 31) == 0 && row < p.T_) part[row] = make_float2(m, s);
+      if ((lane & 31) == 0 && row < p.T_) part[int64_t(row) * p.parts] = make_float2(m, s);
     }
 }
 
-// Joins a row's P pairs: 64 rows a workgroup, 4 threads a row.
-__global__ __launch_bounds__(256) void head_join_kernel(const float2* __restrict__ part, int P,
-                                                        int T, int V,
-                                                        const int32_t* __restrict__ target,
-                                                        const float* __restrict__ tlogit,
-                                                        float* __restrict__ loss,
-                                                        float* __restrict__ lse) {
-  __shared__ float2 sh[4][64];
-  const int q = threadIdx.x >> 6, i = threadIdx.x & 63;
-  const int row = blockIdx.x * 64 + i;
+// Joins a row's P pairs: one wave a row.
+constexpr int kJoinRows = 4;
+
+__global__ __launch_bounds__(kJoinRows * 64) void head_join_kernel(
+    const float2* __restrict__ part, int P, int T, int V, const int32_t* __restrict__ target,
+    const float* __restrict__ tlogit, float* __restrict__ loss, float* __restrict__ lse) {
+  const int lane = threadIdx.x & 63;
+  const int row = blockIdx.x * kJoinRows + (threadIdx.x >> 6);
+  if (row >= T) return;
   float m = -__builtin_huge_valf(), s = 0.0f;
   auto join = [&](float m2, float s2) {
     const float top = fmaxf(m, m2);
@@ -165,15 +175,14 @@ __global__ __launch_bounds__(256) void head_join_kernel(const float2* __restrict
     s = s * exp_diff(m, ref) + s2 * exp_diff(m2, ref);
     m = top;
   };
-  if (row < T)
-    for (int j = q; j < P; j += 4) {
-      const float2 o = part[int64_t(j) * T + row];
-      join(o.x, o.y);
-    }
-  sh[q][i] = make_float2(m, s);
-  __syncthreads();
-  if (q != 0 || row >= T) return;
-  for (int w = 1; w < 4; ++w) join(sh[w][i].x, sh[w][i].y);
+  const float2* const mine = part + int64_t(row) * P;
+  for (int j = lane; j < P; j += 64) join(mine[j].x, mine[j].y);
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) {
+    const float m2 = __shfl_xor(m, off, kWave), s2 = __shfl_xor(s, off, kWave);
+    join(m2, s2);
+  }
+  if (lane != 0) return;
   const float l = m + logf(s);
   lse[row] = l;
   const int t = target[row];
@@ -188,6 +197,8 @@ __global__ __launch_bounds__(C::kThreads, C::kMinBlocks) void head_grad_kernel(H
   __shared__ __attribute__((aligned(16))) uint8_t st0[C::kStageBytes];
   __shared__ __attribute__((aligned(16))) uint8_t st1[C::kStageBytes];
   __shared__ __attribute__((aligned(16))) uint8_t st2[C::kStageBytes];
+  __shared__ __attribute__((aligned(16))) uint8_t st3[kTurns<C> ? C::kStageBytes : 16];
+  __shared__ __attribute__((aligned(16))) uint8_t st4[kTurns<C> ? C::kStageBytes : 16];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / C::WN, wn = wave % C::WN;
@@ -196,7 +207,7 @@ __global__ __launch_bounds__(C::kThreads, C::kMinBlocks) void head_grad_kernel(H
   tile_of(xcd_run(blockIdx.x, tiles_m * tiles_n), tiles_m, tiles_n, tm, tn);
   const int m0 = tm * C::BM, n0 = tn * C::BN;
   DenseFeed<C, T, false, kBT> f(p.X, p.W, m0, n0, wave, lane);
-  logits_tile(f, p.H, st0, st1, st2);
+  product_tile<C>(f, (p.H + kStepElems<T> - 1) / kStepElems<T>, st0, st1, st2, st3, st4);
 
   const int row0 = m0 + wm * FM * 32, col0 = n0 + wn * FN * 32;
   float g[FM][16];  // dloss of this lane's rows, 0 where the row is left out
@@ -266,6 +277,8 @@ __global__ __launch_bounds__(C::kThreads, C::kMinBlocks) void head_product_kerne
   __shared__ __attribute__((aligned(16))) uint8_t st0[C::kStageBytes];
   __shared__ __attribute__((aligned(16))) uint8_t st1[C::kStageBytes];
   __shared__ __attribute__((aligned(16))) uint8_t st2[C::kStageBytes];
+  __shared__ __attribute__((aligned(16))) uint8_t st3[kTurns<C> ? C::kStageBytes : 16];
+  __shared__ __attribute__((aligned(16))) uint8_t st4[kTurns<C> ? C::kStageBytes : 16];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int tiles_m = (p.M + C::BM - 1) / C::BM, tiles_n = (p.N + C::BN - 1) / C::BN;
@@ -283,7 +296,7 @@ __global__ __launch_bounds__(C::kThreads, C::kMinBlocks) void head_product_kerne
   const int k = A.k > B.k ? A.k : B.k;
   DenseFeed<C, T, kAT, kBT> f(A, B, m0, n0, wave, lane);
   constexpr int kE = kStepElems<T>;
-  if (k > 0) gemm_pipeline(f, (k + kE - 1) / kE, st0, st1, st2);
+  if (k > 0) product_tile<C>(f, (k + kE - 1) / kE, st0, st1, st2, st3, st4);
   Out* const Y = p.Y + blockIdx.z * p.slice_elems;
   const bool vec = rows_vec(Y, p.ldy);
   emit_tile<C, kOutVec<Out>>(
@@ -531,10 +544,11 @@ hipError_t run_forward(const HeadCall& c, const HeadPlan& h, hipStream_t stream)
   a.H = X.k;
   a.target = c.target;
   a.part = static_cast<float2*>(c.part);
+  a.parts = int(h.parts);
   a.tlogit = c.tlogit;
   e = logits<T, false>(pick_tile(sizeof(T) == 2, c.T, c.V), c.by_vocab, a, stream);
   if (e != hipSuccess) return e;
-  head_join_kernel<<<unsigned(ceil_div(c.T, 64)), 256, 0, stream>>>(
+  head_join_kernel<<<unsigned(ceil_div(c.T, kJoinRows)), kJoinRows * 64, 0, stream>>>(
       a.part, int(h.parts), int(c.T), int(c.V), c.target, c.tlogit, c.loss, c.lse_out);
   return hipGetLastError();
 }

@@ -99,6 +99,12 @@ hipError_t launch_experts_rows(const uint8_t* Aq, const uint8_t* As, const uint8
                                const uint8_t* Bs, const int32_t* row_end, int64_t E, int64_t M,
                                int64_t N, int64_t ldq, void* Y, bool y_bf16, int64_t ldy,
                                hipStream_t stream);
+// The same for so few rows that the product quantizes them itself.
+bool experts_fused(int64_t M, int64_t K);
+hipError_t launch_experts_fused(const void* A, bool bf16, int64_t lda, const uint8_t* Bq,
+                                const uint8_t* Bs, const int32_t* row_end, int64_t E, int64_t M,
+                                int64_t K, int64_t N, int64_t ldq, void* Y, bool y_bf16,
+                                int64_t ldy, hipStream_t stream);
 hipError_t launch_experts_wgrad(const uint8_t* Aq, const uint8_t* As, const uint8_t* Bq,
                                 const uint8_t* Bs, const int32_t* row_end, int64_t E, int64_t M,
                                 int64_t K, int64_t N, void* dW, bool w_bf16, int64_t ldw,
