@@ -37,25 +37,24 @@ constexpr int kThreads = 256;
 // ---------------------------------------------------------------------------
 // Groups.
 // ---------------------------------------------------------------------------
-// Running maximum and sum across the wave (inclusive).
-__device__ inline int wave_scan_max(int v) {
-  const int lane = threadIdx.x & (kWave - 1);
-#pragma unroll
-  for (int off = 1; off < kWave; off <<= 1) {
-    const int o = __shfl_up(v, off, kWave);
-    if (lane >= off) v = v > o ? v : o;
-  }
+// Running maximum and sum across the wave (inclusive) of values >= 0, on the
+// vector unit: shifts within rows of 16 lanes (lanes without a source take 0),
+// then the last lane of a row to the next row and of the first half to the second.
+template <class Op>
+__device__ inline int wave_scan(int v, const Op& op) {
+  v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false));  // row_shr:1
+  v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false));
+  v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false));
+  v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false));
+  v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false));  // row_bcast:15
+  v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false));  // row_bcast:31
   return v;
 }
-
+__device__ inline int wave_scan_max(int v) {
+  return wave_scan(v, [](int a, int b) { return a > b ? a : b; });
+}
 __device__ inline int wave_scan_sum(int v) {
-  const int lane = threadIdx.x & (kWave - 1);
-#pragma unroll
-  for (int off = 1; off < kWave; off <<= 1) {
-    const int o = __shfl_up(v, off, kWave);
-    if (lane >= off) v += o;
-  }
-  return v;
+  return wave_scan(v, [](int a, int b) { return a + b; });
 }
 
 // A group of rows: expert e's, or with e == E the rows past the last expert's
@@ -90,32 +89,34 @@ struct GroupScan {
   }
 };
 
-// Number of units of all groups, the one past the last expert among them.
-template <int R>
-__device__ inline int total_units(const int32_t* row_end, int E, int M) {
-  int end0 = 0, units0 = 0;
-  for (int base = 0; base < E; base += kWave) {
+// The group of unit pick(total), total the number of units of all groups, the one
+// past the last expert among them; pick may answer none (negative): then e < 0.
+// Up to 64 experts are scanned once, more twice.
+template <int R, class Pick>
+__device__ inline Group group_of_unit(const int32_t* row_end, int E, int M, const Pick& pick) {
+  GroupScan<R> first;
+  first.read(row_end, 0, E, M, 0, 0);
+  int end = __builtin_amdgcn_readlane(first.end, kWave - 1);
+  int units = __builtin_amdgcn_readlane(first.upto, kWave - 1);
+  for (int base = kWave; base < E; base += kWave) {
     GroupScan<R> s;
-    s.read(row_end, base, E, M, end0, units0);
-    end0 = __builtin_amdgcn_readlane(s.end, kWave - 1);
-    units0 = __builtin_amdgcn_readlane(s.upto, kWave - 1);
+    s.read(row_end, base, E, M, end, units);
+    end = __builtin_amdgcn_readlane(s.end, kWave - 1);
+    units = __builtin_amdgcn_readlane(s.upto, kWave - 1);
   }
-  return units0 + (M - end0 + R - 1) / R;
-}
-
-// The group of unit u (0 <= u < total_units).
-template <int R>
-__device__ inline Group group_of_unit(const int32_t* row_end, int E, int M, int u) {
-  int end0 = 0, units0 = 0;
-  for (int base = 0; base < E; base += kWave) {
-    GroupScan<R> s;
-    s.read(row_end, base, E, M, end0, units0);
-    const uint64_t past = __ballot(u < s.upto);
-    if (past != 0) return s.group(base, __builtin_ctzll(past));
-    end0 = __builtin_amdgcn_readlane(s.end, kWave - 1);
-    units0 = __builtin_amdgcn_readlane(s.upto, kWave - 1);
+  const int u = pick(units + (M - end + R - 1) / R);
+  if (u < 0) return Group{-1, 0, 0, 0};
+  if (u >= units) return Group{E, end, M - end, units};
+  uint64_t past = __ballot(u < first.upto);
+  int base = 0;
+  while (past == 0) {
+    const int end0 = __builtin_amdgcn_readlane(first.end, kWave - 1);
+    const int units0 = __builtin_amdgcn_readlane(first.upto, kWave - 1);
+    base += kWave;
+    first.read(row_end, base, E, M, end0, units0);
+    past = __ballot(u < first.upto);
   }
-  return Group{E, end0, M - end0, units0};
+  return first.group(base, __builtin_ctzll(past));
 }
 
 // Group e (0 <= e <= E).
@@ -156,8 +157,8 @@ __global__ __launch_bounds__(kThreads) void experts_ragged_mx_kernel(
     const typename In::T* __restrict__ X, const int32_t* __restrict__ row_end, int E, int M,
     int64_t N, int64_t ldx, uint8_t* __restrict__ Xq, int64_t ldq, uint8_t* __restrict__ Xs) {
   const int s = blockIdx.y;
-  const Group g = group_of_unit<128>(row_end, E, M, s);
-  if (g.e == E) return;
+  const Group g = group_of_unit<128>(row_end, E, M, [&](int total) { return s < total ? s : -1; });
+  if (g.e < 0 || g.e == E) return;
   quantize_cols_mx_body<In, kAligned>(blockIdx.x, s - g.first, X + int64_t(g.begin) * ldx, g.rows,
                                       N, ldx, Xq + int64_t(g.first) * 64, ldq,
                                       Xs + int64_t(g.first) * 4 * N, N);
@@ -211,9 +212,12 @@ __global__ __launch_bounds__(C::kThreads, C::kMinBlocks) void experts_gemm_kerne
                    4 * p.cols, nkt * 4 * p.cols};
     Y += int64_t(e) * p.rows * p.ldy;
   } else {
-    const int t = xcd_run(blockIdx.x, total_units<C::BM>(p.row_end, p.E, p.M) * tiles_n);
-    if (t < 0) return;
-    const Group g = group_of_unit<C::BM>(p.row_end, p.E, p.M, t / tiles_n);
+    int t = -1;
+    const Group g = group_of_unit<C::BM>(p.row_end, p.E, p.M, [&](int total) {
+      t = xcd_run(blockIdx.x, total * tiles_n);
+      return t < 0 ? -1 : t / tiles_n;
+    });
+    if (g.e < 0) return;
     int tm, tn;
     tile_of(t - g.first * tiles_n, (g.rows + C::BM - 1) / C::BM, tiles_n, tm, tn);
     // the rows past the last expert's end: no steps, zeros
@@ -235,30 +239,28 @@ __global__ __launch_bounds__(C::kThreads, C::kMinBlocks) void experts_gemm_kerne
 }
 
 // ---------------------------------------------------------------------------
-// Few rows an expert (serving): bound by reading the weights' codes once.
+// A few rows in all (serving one or some tokens): bound by latency and by
+// reading the weights' codes once, in one launch.
 // ---------------------------------------------------------------------------
 // A workgroup of W waves owns 16 columns of one expert. The waves split K: wave
-// w takes the K steps w, w + W, ..., so that the waves read contiguous bytes of
-// each column's packed row. Codes go from memory straight to the matrix core's
-// registers (the 16x16x128 shape: lane l holds the 32 codes of block l / 16 of the
-// step for column l % 16, one 16-byte load, and the block's scale byte), kSteps
-// steps a wave at once, where they stay while the expert's rows go by in chunks
-// of 32: with K <= 128 kSteps W each code is read once, whatever the rows. The
-// waves' partial sums are added in wave order through LDS.
-//
-// kFused: the activations are not quantized by a launch of their own; every
-// workgroup quantizes its expert's few rows into LDS, which at this size costs
-// less than the launch (M <= 16 and M * K <= kFusedElems).
+// w takes the K steps w, w + W, ..., at most kSteps of them, so that the waves
+// read contiguous bytes of each column's packed row. Codes go from memory
+// straight to the matrix core's registers (the 16x16x128 shape: lane l holds the
+// 32 codes of block l / 16 of the step for column l % 16, one 16-byte load, and
+// the block's scale byte). While they are on their way the workgroup quantizes
+// its expert's rows into LDS: at this size that costs less than a launch of its
+// own would (one token, two of 8 experts 2048x5632: 11.3 against 14.2 us a call).
+// The waves' partial sums are added in wave order through LDS.
 constexpr int kSteps = 8;
-constexpr int64_t kFusedRows = 16, kFusedElems = 8192;
+constexpr int64_t kFusedRows = 16, kFusedElems = 8192;  // of the activations
 
 typedef float v4f __attribute__((ext_vector_type(4)));
 
 struct FewArgs {
-  const uint8_t *Aq, *As, *Bq, *Bs;
-  const void* A;  // kFused: the activations, M x K
+  const void* A;  // M x K
   int64_t lda;
-  int fast;       // kFused: A allows 16-byte loads of 8 elements
+  int fast;  // A allows 16-byte loads of 8 elements
+  const uint8_t *Bq, *Bs;
   const int32_t* row_end;
   int E, M, K, N, ldq;
   void* Y;
@@ -298,15 +300,13 @@ __device__ inline void quantize_few(const FewArgs& p, int begin, int rows, uint8
   }
 }
 
-// In: the activations' type with kFused, else void.
 template <int W, class In, class Out>
-__global__ __launch_bounds__(W * 64, 4) void experts_few_kernel(FewArgs p) {
-  constexpr bool kFused = !std::is_void<In>::value;
-  __shared__ v4f part[W][2][64];
-  // M * K <= kFusedElems: codes and padding of at most 16 rows
-  constexpr int kCodeBytes = kFused ? kFusedElems / 2 + kFusedRows * 64 : 16;
+__global__ __launch_bounds__(W * 64) void experts_few_kernel(FewArgs p) {
+  __shared__ v4f part[W][64];
+  // at most kFusedRows rows of M * K <= kFusedElems elements, each padded
+  constexpr int kCodeBytes = kFusedElems / 2 + kFusedRows * 64;
   __shared__ __attribute__((aligned(16))) uint8_t codes[kCodeBytes];
-  __shared__ uint8_t scales[kFused ? kCodeBytes / 16 : 16];
+  __shared__ uint8_t scales[kCodeBytes / 16];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const Group g = group_of_expert<16>(p.row_end, p.E, p.M, blockIdx.y);
@@ -314,89 +314,53 @@ __global__ __launch_bounds__(W * 64, 4) void experts_few_kernel(FewArgs p) {
   Out* const Y = static_cast<Out*>(p.Y);
   const int n = blockIdx.x * 16 + (lane & 15);
   const int q = lane >> 4;
-  const int nkt = g.e == p.E ? 0 : p.ldq / 64;
-  const int64_t bcol = int64_t(g.e == p.E ? 0 : g.e) * p.N + (n < p.N ? n : p.N - 1);
-  const uint8_t* const brow = p.Bq + bcol * p.ldq + q * 16;
-  const uint8_t* const bsc = p.Bs + 4 * bcol + q;
-  const int64_t bstep = 4 * int64_t(p.E) * p.N, astep = 4 * int64_t(p.M);
-  const bool once = nkt <= kSteps * W;  // the codes stay in registers
-  uint4 b[kSteps];
-  int sb[kSteps];
-  // steps past the end repeat the last one and are not multiplied
-  auto step_of = [&](int s0, int u) { return s0 + u * W < nkt ? s0 + u * W : nkt - 1; };
-  auto load_b = [&](int s0) {
+  v4f acc{};
+  if (g.e < p.E) {
+    const int nkt = p.ldq / 64;
+    const int64_t bcol = int64_t(g.e) * p.N + (n < p.N ? n : p.N - 1);
+    const int64_t bstep = 4 * int64_t(p.E) * p.N;
+    uint4 b[kSteps];
+    int sb[kSteps], at[kSteps];
 #pragma unroll
     for (int u = 0; u < kSteps; ++u) {
-      const int s = step_of(s0, u);
-      b[u] = *reinterpret_cast<const uint4*>(brow + s * 64);
-      sb[u] = bsc[s * bstep];
+      // steps past the end repeat the last one and are not multiplied
+      const int s = wave + u * W < nkt ? wave + u * W : nkt - 1;
+      at[u] = s;
+      b[u] = *reinterpret_cast<const uint4*>(p.Bq + bcol * p.ldq + s * 64 + q * 16);
+      sb[u] = p.Bs[s * bstep + 4 * bcol + q];
     }
-  };
-  if (once && nkt > 0) load_b(wave);
-  if constexpr (kFused) {
-    if (nkt > 0) quantize_few<In>(p, g.begin, g.rows, codes, scales);
+    quantize_few<In>(p, g.begin, g.rows, codes, scales);
     __syncthreads();
-  }
-  for (int r0 = 0; r0 < g.rows; r0 += 32) {
-    const bool two = g.rows > r0 + 16;
-    v4f acc[2] = {v4f{}, v4f{}};
     // rows past the group's end repeat its last row; they are not stored
-    int ra[2];
+    const int ra = (lane & 15) < g.rows ? (lane & 15) : g.rows - 1;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = r0 + 16 * i + (lane & 15);
-      ra[i] = r < g.rows ? r : g.rows - 1;
+    for (int u = 0; u < kSteps; ++u) {
+      if (wave + u * W >= nkt) break;
+      const uint4 a = *reinterpret_cast<const uint4*>(codes + ra * p.ldq + at[u] * 64 + q * 16);
+      const int sa = scales[ra * (p.ldq / 16) + at[u] * 4 + q];
+      const v8i af{int(a.x), int(a.y), int(a.z), int(a.w), 0, 0, 0, 0};
+      const v8i bf{int(b[u].x), int(b[u].y), int(b[u].z), int(b[u].w), 0, 0, 0, 0};
+      acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(af, bf, acc, 4, 4, 0, sa, 0, sb[u]);
     }
-    auto multiply = [&](int s0, int i) {
-      uint4 a[kSteps];
-      int sa[kSteps];
+  }
+  part[wave][lane] = acc;
+  __syncthreads();
+  if (wave != 0) return;
+  v4f sum = part[0][lane];
 #pragma unroll
-      for (int u = 0; u < kSteps; ++u) {
-        const int s = step_of(s0, u);
-        if constexpr (kFused) {
-          a[u] = *reinterpret_cast<const uint4*>(codes + ra[i] * p.ldq + s * 64 + q * 16);
-          sa[u] = scales[ra[i] * (p.ldq / 16) + s * 4 + q];
-        } else {
-          const int64_t row = g.begin + ra[i];
-          a[u] = *reinterpret_cast<const uint4*>(p.Aq + row * p.ldq + s * 64 + q * 16);
-          sa[u] = p.As[s * astep + 4 * row + q];
-        }
-      }
+  for (int w = 1; w < W; ++w) sum += part[w][lane];
 #pragma unroll
-      for (int u = 0; u < kSteps; ++u) {
-        if (s0 + u * W >= nkt) break;
-        const v8i af{int(a[u].x), int(a[u].y), int(a[u].z), int(a[u].w), 0, 0, 0, 0};
-        const v8i bf{int(b[u].x), int(b[u].y), int(b[u].z), int(b[u].w), 0, 0, 0, 0};
-        acc[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(af, bf, acc[i], 4, 4, 0, sa[u],
-                                                                  0, sb[u]);
-      }
-    };
-    for (int s0 = wave; s0 < nkt; s0 += W * kSteps) {
-      if (!once) load_b(s0);
-      multiply(s0, 0);
-      if (two) multiply(s0, 1);
-    }
-    part[wave][0][lane] = acc[0];
-    part[wave][1][lane] = acc[1];
-    __syncthreads();
-    // waves 0 and 1 finish the two fragments
-    if (wave < (two ? 2 : 1)) {
-      v4f sum = part[0][wave][lane];
-#pragma unroll
-      for (int w = 1; w < W; ++w) sum += part[w][wave][lane];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const int r = r0 + 16 * wave + 4 * q + c;
-        if (r < g.rows && n < p.N) store_out(Y + (g.begin + r) * p.ldy + n, sum[c]);
-      }
-    }
-    __syncthreads();
+  for (int c = 0; c < 4; ++c) {
+    const int r = 4 * q + c;
+    if (r < g.rows && n < p.N) store_out(Y + (g.begin + r) * p.ldy + n, sum[c]);
   }
 }
 
 using LargeTile = GemmCfg<256, 256, 4, 2, 64, 1>;
 using SmallTile = GemmCfg<128, 256, 2, 2, 64, 2>;
-constexpr int kLargeTilesMin = 512;
+using FewTile = GemmCfg<64, 128, 1, 2, 64, 2>;
+constexpr int64_t kLargeTilesMin = 512;
+constexpr int64_t kSmallTilesMin = 256;
 constexpr int64_t kFewRows = 32;  // rows an expert on average
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -417,38 +381,30 @@ int64_t most_units(int64_t M, int64_t E, int64_t R) {
 template <class In, class Out>
 hipError_t run_few(const FewArgs& a, hipStream_t stream) {
   const dim3 grid(unsigned(ceil_div(a.N, 16)), unsigned(a.E + 1));
-  const int steps = a.ldq / 64;
-  if (steps <= 4 * kSteps)
+  static_assert(kFusedElems <= 8 * kSteps * 128, "eight waves hold K");
+  if (a.ldq / 64 <= 4 * kSteps)
     experts_few_kernel<4, In, Out><<<grid, 4 * 64, 0, stream>>>(a);
-  else if (steps <= 8 * kSteps || !std::is_void<In>::value)
+  else
     experts_few_kernel<8, In, Out><<<grid, 8 * 64, 0, stream>>>(a);
-  else if constexpr (std::is_void<In>::value)
-    experts_few_kernel<16, In, Out><<<grid, 16 * 64, 0, stream>>>(a);
   return hipGetLastError();
 }
 
+// Tiles of 256 x 256 where they fill the CUs twice, of 128 x 256 where those
+// fill them once, else of 64 x 128; the last also for few rows an expert, where
+// a product is a read of the weights' codes and more workgroups on their way
+// read faster (8 experts 4096x11008, whole call: 128 rows 47 against 53 us with
+// 128 x 256 tiles, 256 rows 51 against 57, 512 rows 60 against 62).
 template <class Out>
 hipError_t run_rows(const TileArgs& p, hipStream_t stream) {
   const int64_t tiles_n = ceil_div(p.cols, 256);
-  if (p.M <= kFewRows * p.E) {
-    FewArgs a{};
-    a.Aq = p.Aq;
-    a.As = p.As;
-    a.Bq = p.Bq;
-    a.Bs = p.Bs;
-    a.row_end = p.row_end;
-    a.E = p.E;
-    a.M = p.M;
-    a.N = p.cols;
-    a.ldq = p.ldq;
-    a.Y = p.Y;
-    a.ldy = p.ldy;
-    return run_few<void, Out>(a, stream);
-  }
   if (ceil_div(p.M, LargeTile::BM) * tiles_n >= kLargeTilesMin)
     return run_tiles<LargeTile, Out, false>(p, most_units(p.M, p.E, LargeTile::BM) * tiles_n,
                                             stream);
-  return run_tiles<SmallTile, Out, false>(p, most_units(p.M, p.E, SmallTile::BM) * tiles_n, stream);
+  if (p.M > kFewRows * p.E && ceil_div(p.M, SmallTile::BM) * tiles_n >= kSmallTilesMin)
+    return run_tiles<SmallTile, Out, false>(p, most_units(p.M, p.E, SmallTile::BM) * tiles_n,
+                                            stream);
+  return run_tiles<FewTile, Out, false>(
+      p, most_units(p.M, p.E, FewTile::BM) * ceil_div(p.cols, FewTile::BN), stream);
 }
 
 template <class Out>

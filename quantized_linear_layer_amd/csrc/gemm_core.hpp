@@ -82,10 +82,13 @@ __device__ inline int xcd_run(int bid, int total) {
   return xcd * base + (xcd < rem ? xcd : rem) + idx;
 }
 
-// Tile u of a tiles_m x tiles_n grid, groups of 4 tile rows sweeping across
-// the columns.
+// Tile u of a tiles_m x tiles_n grid: groups of up to 6 tile rows, as even as they
+// come, sweeping across the columns. (The 32 tiles an XCD runs at a time then
+// share about 6 tile rows and 6 tile columns of operands in its L2; a group of
+// one leftover row would share one and 32.)
 __device__ inline void tile_of(int u, int tiles_m, int tiles_n, int& tm, int& tn) {
-  constexpr int G = 4;
+  const int groups = (tiles_m + 5) / 6;
+  const int G = (tiles_m + groups - 1) / groups;
   const int per_group = G * tiles_n;
   const int grp = u / per_group;
   const int first_m = grp * G;
