@@ -273,6 +273,19 @@ struct Fp4Feed {
   }
 };
 
+// step(kt, 0), step(kt + 1, 1), ... up to S of them, while below end: nested,
+// so that no path skips a step and runs a later one.
+template <int S, class Step, int I>
+__device__ __attribute__((always_inline)) inline void steps_of(const Step& step, int kt, int end,
+                                                               std::integral_constant<int, I> i) {
+  if constexpr (I < S) {
+    if (kt < end) {
+      step(kt, i);
+      steps_of<S>(step, kt + 1, end, std::integral_constant<int, I + 1>{});
+    }
+  }
+}
+
 // Pipeline over K steps (stage of step s: s mod 3). On entry to step kt the
 // first sub-step's fragments of stage kt are in registers. The step reads
 // its second sub-step's fragments, issues the first sub-step's MFMAs, then
@@ -352,17 +365,43 @@ __device__ __attribute__((always_inline)) inline void gemm_pipeline(F& f, int nk
   raw_barrier();
 }
 
-// step(kt, 0), step(kt + 1, 1), ... up to S of them, while below end: nested,
-// so that no path skips a step and runs a later one.
-template <int S, class Step, int I>
-__device__ __attribute__((always_inline)) inline void steps_of(const Step& step, int kt, int end,
-                                                               std::integral_constant<int, I> i) {
-  if constexpr (I < S) {
-    if (kt < end) {
-      step(kt, i);
-      steps_of<S>(step, kt + 1, end, std::integral_constant<int, I + 1>{});
-    }
+// The same on S stages, for feeds without block scales whose loads past the last
+// step read nothing: S - 1 steps are on their way while one is multiplied. For
+// tiles of few rows, whose product is a read of the other operand: the bytes in
+// flight set its rate.
+template <class F, int S>
+__device__ __attribute__((always_inline)) inline void gemm_pipeline_deep(F& f, int nkt,
+                                                                         uint8_t* const (&st)[S]) {
+  constexpr int kPer = F::kPer, FM = F::FM, FN = F::FN;
+  static_assert(F::NL == 0 && (S - 1) * kPer < 64, "vmcnt immediate");
+  typename F::Frag a0[FM], b0[FN], a1[FM], b1[FN];
+  auto step = [&](int kt, auto i_c) {
+    constexpr int i = decltype(i_c)::value;
+    f.read_frags(st[i], 1, a1, b1);
+    __builtin_amdgcn_sched_barrier(0);
+    f.template mfmas<0>(a0, b0, nullptr);
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm((S - 2) * kPer, 0));
+    raw_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    f.dma(kt + S, st[i]);
+    f.template mfmas<1>(a1, b1, nullptr);
+    __builtin_amdgcn_sched_barrier(0);
+    f.read_frags(st[(i + 1) % S], 0, a0, b0);
+  };
+#pragma unroll
+  for (int s = 0; s < S; ++s) {
+    f.dma(s, st[s]);
+    __builtin_amdgcn_sched_barrier(0);
   }
+  __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm((S - 1) * kPer, 0));  // step 0 landed
+  raw_barrier();
+  f.read_frags(st[0], 0, a0, b0);
+  int kt = 0;
+  for (; kt + S <= nkt; kt += S) steps_of<S>(step, kt, kt + S, std::integral_constant<int, 0>{});
+  steps_of<S>(step, kt, nkt, std::integral_constant<int, 0>{});
+  __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm(0, 0));
+  raw_barrier();
 }
 
 // The same product with the eight waves of a large tile in two groups that take

@@ -60,20 +60,22 @@ __device__ inline float half_sum(float v) {
 // Row of element r of a 32x32 fragment on this lane.
 __device__ inline int frag_row(int r, int lane) { return 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3); }
 
-// Tiles of eight waves run the two-group pipeline, on five stages.
+// LDS stages of a tile: eight waves have a CU to themselves and take turns on
+// all of its LDS; tiles of few rows keep more steps on their way.
 template <class C>
-constexpr bool kTurns = C::kThreads == 512;
+constexpr int kStages = C::kThreads == 512 ? 5 : C::BM == 64 ? 5 : 3;
 
 template <class C, class F>
 __device__ __attribute__((always_inline)) inline void product_tile(F& f, int nkt, uint8_t* st0,
                                                                    uint8_t* st1, uint8_t* st2,
                                                                    uint8_t* st3, uint8_t* st4) {
-  if constexpr (kTurns<C>) {
-    uint8_t* const st[5] = {st0, st1, st2, st3, st4};
+  uint8_t* const st[5] = {st0, st1, st2, st3, st4};
+  if constexpr (C::kThreads == 512)
     gemm_pipeline_turns<F, 5>(f, nkt, st);
-  } else {
+  else if constexpr (kStages<C> == 5)
+    gemm_pipeline_deep<F, 5>(f, nkt, st);
+  else
     gemm_pipeline(f, nkt, st0, st1, st2);
-  }
 }
 
 template <class T>
@@ -100,8 +102,8 @@ __global__ __launch_bounds__(C::kThreads, C::kMinBlocks) void head_lse_kernel(He
   __shared__ __attribute__((aligned(16))) uint8_t st0[C::kStageBytes];
   __shared__ __attribute__((aligned(16))) uint8_t st1[C::kStageBytes];
   __shared__ __attribute__((aligned(16))) uint8_t st2[C::kStageBytes];
-  __shared__ __attribute__((aligned(16))) uint8_t st3[kTurns<C> ? C::kStageBytes : 16];
-  __shared__ __attribute__((aligned(16))) uint8_t st4[kTurns<C> ? C::kStageBytes : 16];
+  __shared__ __attribute__((aligned(16))) uint8_t st3[kStages<C> > 3 ? C::kStageBytes : 16];
+  __shared__ __attribute__((aligned(16))) uint8_t st4[kStages<C> > 4 ? C::kStageBytes : 16];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / C::WN, wn = wave % C::WN;
@@ -197,8 +199,8 @@ __global__ __launch_bounds__(C::kThreads, C::kMinBlocks) void head_grad_kernel(H
   __shared__ __attribute__((aligned(16))) uint8_t st0[C::kStageBytes];
   __shared__ __attribute__((aligned(16))) uint8_t st1[C::kStageBytes];
   __shared__ __attribute__((aligned(16))) uint8_t st2[C::kStageBytes];
-  __shared__ __attribute__((aligned(16))) uint8_t st3[kTurns<C> ? C::kStageBytes : 16];
-  __shared__ __attribute__((aligned(16))) uint8_t st4[kTurns<C> ? C::kStageBytes : 16];
+  __shared__ __attribute__((aligned(16))) uint8_t st3[kStages<C> > 3 ? C::kStageBytes : 16];
+  __shared__ __attribute__((aligned(16))) uint8_t st4[kStages<C> > 4 ? C::kStageBytes : 16];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / C::WN, wn = wave % C::WN;
@@ -277,8 +279,8 @@ __global__ __launch_bounds__(C::kThreads, C::kMinBlocks) void head_product_kerne
   __shared__ __attribute__((aligned(16))) uint8_t st0[C::kStageBytes];
   __shared__ __attribute__((aligned(16))) uint8_t st1[C::kStageBytes];
   __shared__ __attribute__((aligned(16))) uint8_t st2[C::kStageBytes];
-  __shared__ __attribute__((aligned(16))) uint8_t st3[kTurns<C> ? C::kStageBytes : 16];
-  __shared__ __attribute__((aligned(16))) uint8_t st4[kTurns<C> ? C::kStageBytes : 16];
+  __shared__ __attribute__((aligned(16))) uint8_t st3[kStages<C> > 3 ? C::kStageBytes : 16];
+  __shared__ __attribute__((aligned(16))) uint8_t st4[kStages<C> > 4 ? C::kStageBytes : 16];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int tiles_m = (p.M + C::BM - 1) / C::BM, tiles_n = (p.N + C::BN - 1) / C::BN;
@@ -394,13 +396,6 @@ unsigned copy_blocks(int64_t threads) {
 
 enum class Tile { kLarge, kMid, kFew, kF32 };
 
-// Tile of an M x N product.
-Tile pick_tile(bool bf16, int64_t M, int64_t N) {
-  if (M <= 64) return Tile::kFew;
-  if (!bf16) return Tile::kF32;
-  if (ceil_div(M, 256) * ceil_div(N, 256) >= kCUs) return Tile::kLarge;
-  return Tile::kMid;
-}
 int64_t tile_rows(Tile t) {
   return t == Tile::kLarge ? 256 : t == Tile::kFew ? 64 : 128;
 }
@@ -415,13 +410,35 @@ int64_t tiles_of(Tile t, int64_t M, int64_t N) {
   return ceil_div(M, tile_rows(t)) * ceil_div(N, tile_cols(t));
 }
 
-// Slices of dX's reduction over k elements: enough for two workgroups a CU, at
-// least 1024 elements each.
+// Tile of an M x N product whose reduction may be cut in up to `slices` (1 where
+// it is not). bfloat16: 256 x 256 once those give every CU one. float32, whose
+// products are bound by the matrix core: of the two tiles the one whose busiest
+// CU has less to do (1001 x 5003: 64 x 128 tiles, 3 a CU, against 2 of 128 x 128).
+Tile pick_tile(bool bf16, int64_t M, int64_t N, int64_t slices = 1) {
+  if (M <= 64) return Tile::kFew;
+  if (!bf16) {
+    const int64_t f = ceil_div(tiles_of(Tile::kF32, M, N) * slices, kCUs) * 2;
+    return ceil_div(tiles_of(Tile::kFew, M, N) * slices, kCUs) < f ? Tile::kFew : Tile::kF32;
+  }
+  return tiles_of(Tile::kLarge, M, N) * slices >= kCUs ? Tile::kLarge : Tile::kMid;
+}
+
+// Tile of dX (T x H, reduction over the k columns of a piece), and the slices its
+// reduction is cut in: at least 1024 elements each, as many as give every CU a
+// workgroup (of 256 x 256) or two.
+constexpr int64_t kSliceElems = 1024, kMaxSlices = 32;
+
+int64_t dx_most(int64_t k) {
+  const int64_t most = k / kSliceElems > 1 ? k / kSliceElems : 1;
+  return most < kMaxSlices ? most : kMaxSlices;
+}
+Tile dx_tile(bool bf16, int64_t T, int64_t H, int64_t k) {
+  return pick_tile(bf16, T, H, dx_most(k));
+}
 int64_t dx_slices(Tile t, int64_t T, int64_t H, int64_t k) {
-  const int64_t want = ceil_div(2 * kCUs, tiles_of(t, T > 0 ? T : 1, H));
-  const int64_t most = k / 1024 > 1 ? k / 1024 : 1;
-  const int64_t s = want < most ? want : most;
-  return s < 32 ? s : 32;
+  const int64_t want = ceil_div((t == Tile::kLarge ? 1 : 2) * kCUs, tiles_of(t, T > 0 ? T : 1, H));
+  const int64_t most = dx_most(k);
+  return want < most ? want : most;
 }
 
 // f(tile configuration) for a tile that pick_tile gives for T.
@@ -454,7 +471,7 @@ HeadPlan head_plan(bool bf16, int64_t T, int64_t H, int64_t V, bool by_vocab, in
   const int64_t pieces = ceil_div(T * V * esz, kPieceBytes);
   h.piece = pieces > 1 ? round_256(ceil_div(V, pieces)) : V;
   h.ldg = round8(h.piece);
-  const Tile tx = pick_tile(bf16, T, H);
+  const Tile tx = dx_tile(bf16, T, H, h.piece);
   h.slices = dx_slices(tx, T, H, h.piece);
   h.ldp = round8(H);
   return h;
@@ -519,8 +536,8 @@ template <class T, bool kAT, bool kBT, class Out, bool kAdd>
 hipError_t product(Tile t, const ProductArgs<T, Out>& a, int64_t slices, hipStream_t stream) {
   return with_tile<T>(t, [&](auto c) -> hipError_t {
     using C = decltype(c);
-    // a transposed A needs 128 rows a tile (the swizzle's segments)
-    if constexpr (kAT && C::BM < 128) {
+    // bfloat16 read across its rows: the swizzle needs four 64-byte segments a row
+    if constexpr (kAT && sizeof(T) == 2 && C::BM < 128) {
       return hipErrorInvalidValue;
     } else {
       const dim3 grid(unsigned(tiles_of(t, a.M, a.N)), 1, unsigned(slices));
@@ -561,7 +578,7 @@ hipError_t run_backward(const HeadCall& c, const HeadPlan& h, hipStream_t stream
   hipError_t e = operands<T>(c, h, &X, &W, stream);
   if (e != hipSuccess) return e;
   T* const dW = static_cast<T*>(c.dW);
-  const Tile tx = pick_tile(kBf16, c.T, c.H);
+  const Tile tx = dx_tile(kBf16, c.T, c.H, h.piece);
   const bool direct = h.slices == 1 && h.piece >= c.V;
   for (int64_t v0 = 0; v0 < c.V; v0 += h.piece) {
     const int64_t n = c.V - v0 < h.piece ? c.V - v0 : h.piece;
@@ -605,8 +622,8 @@ hipError_t run_backward(const HeadCall& c, const HeadPlan& h, hipStream_t stream
     const DenseOperand<T> Gt{static_cast<const T*>(c.G), h.ldg, n8, int(c.T)};
     const DenseOperand<T> Xt{X.p, h.ldx, X.k, int(c.T)};
     const int64_t rows = c.by_vocab ? n : c.H, cols = c.by_vocab ? c.H : n;
-    // (A is read across its rows here: at least 128 rows a tile, see product)
-    const Tile tw = pick_tile(kBf16, rows > 64 ? rows : 65, cols);
+    // (A is read across its rows here: bfloat16 at least 128 rows a tile, see product)
+    const Tile tw = pick_tile(kBf16, kBf16 && rows <= 64 ? 65 : rows, cols);
     const ProductArgs<T, T> q{c.by_vocab ? Gt : Xt, c.by_vocab ? Xt : Gt, int(rows), int(cols),
                               int(c.T), dW + v0 * (c.by_vocab ? c.lddw : 1), c.lddw, 0, 1};
     e = product<T, true, true, T, false>(tw, q, 1, stream);
