@@ -45,16 +45,27 @@ __device__ inline float exp_diff(float x, float y) {
   return __builtin_amdgcn_exp2f((x - y) * kLog2e);
 }
 
-// Reductions over the 32 lanes of a half wave, on every lane.
+// Reductions over the 32 lanes of a half wave, on every lane and on the vector
+// unit: four exchanges within rows of 16 lanes (neighbours, pairs, mirrored 8,
+// mirrored 16), then the two rows of a half (v_permlane16_swap).
+template <class Op>
+__device__ inline float half_reduce(float v, const Op& op) {
+  auto dpp = [](float x, auto ctrl) {
+    const int i = __float_as_int(x);
+    return __int_as_float(__builtin_amdgcn_update_dpp(i, i, decltype(ctrl)::value, 0xf, 0xf, true));
+  };
+  v = op(v, dpp(v, std::integral_constant<int, 0xb1>{}));   // quad_perm [1, 0, 3, 2]
+  v = op(v, dpp(v, std::integral_constant<int, 0x4e>{}));   // quad_perm [2, 3, 0, 1]
+  v = op(v, dpp(v, std::integral_constant<int, 0x141>{}));  // row_half_mirror
+  v = op(v, dpp(v, std::integral_constant<int, 0x140>{}));  // row_mirror
+  const auto sw = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return op(__uint_as_float(sw[0]), __uint_as_float(sw[1]));
+}
 __device__ inline float half_max(float v) {
-#pragma unroll
-  for (int off = 16; off >= 1; off >>= 1) v = fmaxf(v, __shfl_xor(v, off, kWave));
-  return v;
+  return half_reduce(v, [](float a, float b) { return fmaxf(a, b); });
 }
 __device__ inline float half_sum(float v) {
-#pragma unroll
-  for (int off = 16; off >= 1; off >>= 1) v += __shfl_xor(v, off, kWave);
-  return v;
+  return half_reduce(v, [](float a, float b) { return a + b; });
 }
 
 // Row of element r of a 32x32 fragment on this lane.
@@ -424,9 +435,9 @@ Tile pick_tile(bool bf16, int64_t M, int64_t N, int64_t slices = 1) {
 }
 
 // Tile of dX (T x H, reduction over the k columns of a piece), and the slices its
-// reduction is cut in: at least 1024 elements each, as many as give every CU a
+// reduction is cut in: at least 512 elements each, as many as give every CU a
 // workgroup (of 256 x 256) or two.
-constexpr int64_t kSliceElems = 1024, kMaxSlices = 32;
+constexpr int64_t kSliceElems = 512, kMaxSlices = 32;
 
 int64_t dx_most(int64_t k) {
   const int64_t most = k / kSliceElems > 1 ? k / kSliceElems : 1;
