@@ -629,7 +629,7 @@ fp4lin_status fp4lin_experts_quantize_weight_mx(const void* W, fp4lin_dtype dt, 
   if (s != FP4LIN_OK) return s;
   if (ldw < N) return FP4LIN_ERR_SHAPE;
   if (!aligned16(Wq) || !aligned16(Ws)) return FP4LIN_ERR_ALIGN;
-  return launch_status(fp4lin::launch_experts_quantize_cols_mx(
+  return launch_status(fp4lin::launch_experts_quantize_weight_mx(
       W, dt == FP4LIN_BF16, E, K, N, ldw, Wq, fp4lin_packed_ld(K), Ws, stream));
 }
 
@@ -648,14 +648,12 @@ fp4lin_status fp4lin_experts_forward_mx(const void* A, const void* W, fp4lin_dty
   if (M == 0) return FP4LIN_OK;
   uint8_t* const base = static_cast<uint8_t*>(ws);
   const int64_t ldq = fp4lin_packed_ld(K);
-  s = launch_status(fp4lin::launch_quantize_rows_mx(A, dt == FP4LIN_BF16, M, K, lda, nullptr,
-                                                    base + o.Aq, ldq, base + o.As, stream));
-  if (s != FP4LIN_OK) return s;
-  s = launch_status(fp4lin::launch_experts_quantize_cols_mx(W, dt == FP4LIN_BF16, E, K, N, ldw,
-                                                            base + o.Bq, ldq, base + o.Bs, stream));
+  s = launch_status(fp4lin::launch_experts_quantize_forward(A, W, dt == FP4LIN_BF16, E, M, K, N, lda,
+                                                            ldw, base + o.Aq, base + o.As,
+                                                            base + o.Bq, base + o.Bs, stream));
   if (s != FP4LIN_OK) return s;
   return launch_status(fp4lin::launch_experts_rows(base + o.Aq, base + o.As, base + o.Bq,
-                                                   base + o.Bs, row_end, E, M, N, ldq, Y,
+                                                   base + o.Bs, row_end, E, M, N, ldq, false, Y,
                                                    ydt == FP4LIN_BF16, ldy, stream));
 }
 
@@ -680,11 +678,12 @@ fp4lin_status fp4lin_experts_apply_mx(const void* A, fp4lin_dtype dt, const uint
     return launch_status(fp4lin::launch_experts_fused(A, dt == FP4LIN_BF16, lda, Wq, Ws, row_end, E,
                                                       M, K, N, ldq, Y, ydt == FP4LIN_BF16, ldy,
                                                       stream));
-  s = launch_status(fp4lin::launch_quantize_rows_mx(A, dt == FP4LIN_BF16, M, K, lda, nullptr,
-                                                    base + o.Aq, ldq, base + o.As, stream));
+  s = launch_status(fp4lin::launch_experts_quantize_rows(A, dt == FP4LIN_BF16, M, K, lda,
+                                                         base + o.Aq, base + o.As, stream));
   if (s != FP4LIN_OK) return s;
   return launch_status(fp4lin::launch_experts_rows(base + o.Aq, base + o.As, Wq, Ws, row_end, E, M,
-                                                   N, ldq, Y, ydt == FP4LIN_BF16, ldy, stream));
+                                                   N, ldq, true, Y, ydt == FP4LIN_BF16, ldy,
+                                                   stream));
 }
 
 fp4lin_status fp4lin_experts_dgrad_mx(const void* dY, const void* W, fp4lin_dtype dt,
@@ -702,15 +701,12 @@ fp4lin_status fp4lin_experts_dgrad_mx(const void* dY, const void* W, fp4lin_dtyp
   if (M == 0) return FP4LIN_OK;
   uint8_t* const base = static_cast<uint8_t*>(ws);
   const int64_t ldq = fp4lin_packed_ld(N);
-  s = launch_status(fp4lin::launch_quantize_rows_mx(dY, dt == FP4LIN_BF16, M, N, lddy, nullptr,
-                                                    base + o.Aq, ldq, base + o.As, stream));
-  if (s != FP4LIN_OK) return s;
-  // the E * K rows of all weights are the packed rows the product reads
-  s = launch_status(fp4lin::launch_quantize_rows_mx(W, dt == FP4LIN_BF16, E * K, N, ldw, nullptr,
-                                                    base + o.Bq, ldq, base + o.Bs, stream));
+  s = launch_status(fp4lin::launch_experts_quantize_dgrad(dY, W, dt == FP4LIN_BF16, E, M, K, N, lddy,
+                                                          ldw, base + o.Aq, base + o.As,
+                                                          base + o.Bq, base + o.Bs, stream));
   if (s != FP4LIN_OK) return s;
   return launch_status(fp4lin::launch_experts_rows(base + o.Aq, base + o.As, base + o.Bq,
-                                                   base + o.Bs, row_end, E, M, K, ldq, dX,
+                                                   base + o.Bs, row_end, E, M, K, ldq, false, dX,
                                                    xdt == FP4LIN_BF16, lddx, stream));
 }
 
@@ -727,11 +723,9 @@ fp4lin_status fp4lin_experts_wgrad_mx(const void* A, const void* dY, fp4lin_dtyp
   if (s != FP4LIN_OK) return s;
   if (lda < K || lddy < N || lddw < N) return FP4LIN_ERR_SHAPE;
   uint8_t* const base = static_cast<uint8_t*>(ws);
-  s = launch_status(fp4lin::launch_experts_quantize_ragged_mx(
-      A, dt == FP4LIN_BF16, row_end, E, M, K, lda, base + o.Aq, base + o.As, stream));
-  if (s != FP4LIN_OK) return s;
-  s = launch_status(fp4lin::launch_experts_quantize_ragged_mx(
-      dY, dt == FP4LIN_BF16, row_end, E, M, N, lddy, base + o.Bq, base + o.Bs, stream));
+  s = launch_status(fp4lin::launch_experts_quantize_wgrad(A, dY, dt == FP4LIN_BF16, row_end, E, M, K,
+                                                          N, lda, lddy, base + o.Aq, base + o.As,
+                                                          base + o.Bq, base + o.Bs, stream));
   if (s != FP4LIN_OK) return s;
   return launch_status(fp4lin::launch_experts_wgrad(base + o.Aq, base + o.As, base + o.Bq,
                                                     base + o.Bs, row_end, E, M, K, N, dW,

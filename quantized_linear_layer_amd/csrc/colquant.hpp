@@ -2,7 +2,8 @@
 // E2M1 codes packed N-major, as device bodies of 256-thread workgroups that
 // take their workgroup coordinates as arguments: the column-max pass and the
 // encode pass of the token-wise format, and the one pass of the micro-scaled
-// format (blocks of 32 codes along K). The quantize_weight kernels launch
+// format (blocks of 32 codes along K); and the row pass of the micro-scaled format.
+// The quantize_weight kernels launch
 // them directly; the forward pairs them with the select's row kernels in
 // shared launches.
 #pragma once
@@ -130,14 +131,18 @@ __device__ __attribute__((always_inline)) inline void quantize_cols_body(int64_t
 // codes of one column are one 32-bit word of its packed row, and lanes
 // 4q .. 4q+3 share block q. Block scales go to the step-major array Ws (the
 // byte of block b of column n at (b / 4) * 4ns + 4n + b % 4, ns the rows of that
-// array: N, or those of all matrices whose scales share it).
+// array: N, or those of all matrices whose scales share it). The 64 bytes of
+// column n's codes in K step s go to Wq + n * ldq + s * step: with step 64 the
+// codes of a column are one packed row of ldq bytes; with ldq 64 and step 64 N
+// those of a step are together, and a tile's codes are 8 KiB in one piece.
 constexpr int kMxTK = 128;  // codes along K per column tile
 constexpr int kMxTN = 128;  // columns per tile
 
 template <class In, bool kAligned>
 __device__ __attribute__((always_inline)) inline void quantize_cols_mx_body(
     int64_t bx, int64_t by, const typename In::T* __restrict__ W, int64_t K, int64_t N,
-    int64_t ldw, uint8_t* __restrict__ Wq, int64_t ldq, uint8_t* __restrict__ Ws, int64_t ns) {
+    int64_t ldw, uint8_t* __restrict__ Wq, int64_t ldq, int64_t step, uint8_t* __restrict__ Ws,
+    int64_t ns) {
   const int t = threadIdx.x;
   const int kg = t & 15, g = t >> 4;
   const int64_t n0 = bx * kMxTN;
@@ -172,10 +177,71 @@ __device__ __attribute__((always_inline)) inline void quantize_cols_mx_body(
     for (int u = 0; u < 8; ++u)
       word |= (mx_magnitude(fabsf(In::widen(v[u].v[j])), e[j]) | (In::sign_bit(v[u].v[j]) << 3))
               << (4 * u);
-    *reinterpret_cast<uint32_t*>(Wq + (c + j) * ldq + kr / 2) = word;
+    *reinterpret_cast<uint32_t*>(Wq + (c + j) * ldq + (kr / 128) * step + (kr % 128) / 2) = word;
     // rows kr .. kr+7: block kr / 32 of K step kr / 128 (the tile's step by)
     if ((kg & 3) == 0) Ws[(kr / 128) * 4 * ns + 4 * (c + j) + ((kr / 32) & 3)] = uint8_t(e[j] + 127);
   }
+}
+
+// Row-wise (per row) micro-scaled quantization. Workgroup (bx, by) of gx x gy
+// takes groups of kRows consecutive rows by, by + gy, ... and in each the chunks
+// c = bx * 256 + t, c + 256 gx, ... (cpr = ldq / 4 chunks of 8 codes per padded
+// row, a multiple of 16). Four consecutive t hold one block and sit on four
+// consecutive lanes, and the chunk stride is a multiple of 4, so a block's lanes
+// are active together. kRows rows are loaded before the first is encoded, so that
+// a thread has that many loads in flight.
+//
+// Codes: rows in blocks of `block` rows (each block ldq bytes a row), and within a
+// block the 64 bytes of every row's K step 0, then of step 1, ...: with block 1
+// each row's codes are together (packed rows of ldq bytes), with block M those of
+// a step. Scales are step-major over all M rows.
+template <class In, bool kFast, int kRows>
+__device__ __attribute__((always_inline)) inline void quantize_rows_mx_body(
+    int64_t bx, int64_t gx, int64_t by, int64_t gy, const typename In::T* __restrict__ X, int64_t M,
+    int64_t K, int64_t ldx, float tau, uint8_t* __restrict__ Xq, int64_t ldq, int64_t block,
+    uint8_t* __restrict__ Xs) {
+  const int64_t cpr = ldq / 4;
+  for (int64_t r0 = by * kRows; r0 < M; r0 += gy * kRows)
+    for (int64_t c = bx * 256 + threadIdx.x; c < cpr; c += gx * 256) {
+      Vec8<In> v[kRows];
+#pragma unroll
+      for (int u = 0; u < kRows; ++u)
+        load_chunk<In, kFast>(X + (r0 + u < M ? r0 + u : M - 1) * ldx, c * 8, K, v[u]);
+#pragma unroll
+      for (int u = 0; u < kRows; ++u) {
+        const int64_t r = r0 + u;
+        if (r >= M) break;
+        float ax[8];
+        float m = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          ax[i] = fminf(fabsf(In::widen(v[u].v[i])), tau);
+          m = fmaxf(m, ax[i]);
+        }
+        const int e = mx_exponent(quad_max(m));
+        uint32_t word = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          word |= (mx_magnitude(ax[i], e) | (In::sign_bit(v[u].v[i]) << 3)) << (4 * i);
+        const int64_t first = block == 1 ? r : r / block * block;
+        *reinterpret_cast<uint32_t*>(Xq + first * ldq + (c / 16) * block * 64 + (r - first) * 64 +
+                                     (c % 16) * 4) = word;
+        // chunk c: block c / 4 = 4 * (c / 16) + (c / 4) % 4
+        if ((c & 3) == 0) Xs[(c / 16) * 4 * M + 4 * r + ((c / 4) & 3)] = uint8_t(e + 127);
+      }
+    }
+}
+
+// Packed bytes from which a thread takes four rows (2048 x 5632 weights of 16
+// experts: 97 us, one row a thread 123 us).
+constexpr int64_t kManyRowBytes = int64_t(8) << 20;
+
+// Workgroups: chunks of a row across x (at most 64), rows across y (at most 65535
+// groups of `rows`).
+inline dim3 mx_row_grid(int64_t M, int64_t cpr, int64_t rows) {
+  const int64_t bx = (cpr + 255) / 256;
+  const int64_t by = (M + rows - 1) / rows;
+  return dim3(unsigned(bx < 64 ? bx : 64), unsigned(by < 65535 ? by : 65535));
 }
 
 }  // namespace fp4lin

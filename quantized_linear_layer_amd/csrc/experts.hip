@@ -134,34 +134,91 @@ __device__ inline Group group_of_expert(const int32_t* row_end, int E, int M, in
 }
 
 // ---------------------------------------------------------------------------
-// Quantizers.
+// Quantizers. Operands that only a product of this file reads are kept with the
+// codes of a K step together (Fp4Operand), rows of one matrix or expert at a
+// time; the two operands of a product are quantized in one launch, whose first
+// workgroups take the first one.
 // ---------------------------------------------------------------------------
-// Weights, reduction along K (rows of W[e]): tile (blockIdx.x, blockIdx.y) of
-// expert blockIdx.z. Codes go to the N packed rows of expert e, scales to one
-// step-major array over the E * N columns of all experts.
-template <class In, bool kAligned>
-__global__ __launch_bounds__(kThreads) void experts_cols_mx_kernel(
-    const typename In::T* __restrict__ W, int64_t K, int64_t N, int64_t ldw, int64_t ns,
-    uint8_t* __restrict__ Wq, int64_t ldq, uint8_t* __restrict__ Ws) {
-  const int64_t e = blockIdx.z;
-  quantize_cols_mx_body<In, kAligned>(blockIdx.x, blockIdx.y, W + e * K * ldw, K, N, ldw,
-                                      Wq + e * N * ldq, ldq, Ws + 4 * e * N, ns);
+struct RowsArgs {
+  const void* X;
+  int64_t M, L, ldx;  // rows, reduction
+  int64_t block;      // rows whose codes of a step are together
+  uint8_t *q, *s;
+  int gx, gy;         // workgroups
+};
+
+struct ColsArgs {
+  const void* W;
+  int64_t E, K, N, ldw;
+  int64_t ld, step;  // of the codes (quantize_cols_mx_body), within an expert
+  uint8_t *q, *s;
+  int gx, gy;  // workgroups of an expert
+};
+
+template <class In, bool kFast, int kRows>
+__device__ inline void quantize_rows_part(const RowsArgs& p, int id) {
+  quantize_rows_mx_body<In, kFast, kRows>(
+      id % p.gx, p.gx, id / p.gx, p.gy, static_cast<const typename In::T*>(p.X), p.M, p.L, p.ldx,
+      __builtin_huge_valf(), p.q, (p.L + 127) / 128 * 64, p.block, p.s);
 }
 
-// Activations or gradients, reduction along each expert's own rows: K step
-// blockIdx.y of all experts' steps (128 rows each, the last one of an expert
-// filled with zeros) and 128 columns. Codes of global step s go to bytes
-// 64s .. 64s+63 of each column's packed row of ldq bytes.
+// Rows of two matrices (dgrad: dY and the weights; apply: the activations alone).
+template <class In, bool kFast, int kRows>
+__global__ __launch_bounds__(kThreads) void experts_rows_mx_kernel(RowsArgs a, RowsArgs b) {
+  const int id = blockIdx.x, na = a.gx * a.gy;
+  if (id < na)
+    quantize_rows_part<In, kFast, kRows>(a, id);
+  else
+    quantize_rows_part<In, kFast, kRows>(b, id - na);
+}
+
+// Weights along K (rows of W[e]), a 128 x 128 tile a workgroup; with kRows > 0
+// rows of the activations first. Scales go to one step-major array over the E * N
+// columns of all experts.
+template <class In, bool kFast, int kRows>
+__global__ __launch_bounds__(kThreads) void experts_cols_mx_kernel(RowsArgs a, ColsArgs w) {
+  int id = blockIdx.x;
+  if constexpr (kRows > 0) {
+    const int na = a.gx * a.gy;
+    if (id < na) {
+      quantize_rows_part<In, kFast, kRows>(a, id);
+      return;
+    }
+    id -= na;
+  }
+  const int64_t e = id / (w.gx * w.gy);
+  id -= int(e) * w.gx * w.gy;
+  quantize_cols_mx_body<In, kFast>(
+      id % w.gx, id / w.gx, static_cast<const typename In::T*>(w.W) + e * w.K * w.ldw, w.K, w.N,
+      w.ldw, w.q + e * w.N * ((w.K + 127) / 128 * 64), w.ld, w.step, w.s + 4 * e * w.N, w.E * w.N);
+}
+
+// Activations and gradients along each expert's own rows: K step blockIdx.y of
+// all experts' steps (128 rows each, the last one of an expert filled with zeros)
+// and 128 columns of A (K of them) or, past those, of dY (N).
+struct RaggedArgs {
+  const void *A, *dY;
+  const int32_t* row_end;
+  int E, M, K, N;
+  int64_t lda, lddy;
+  uint8_t *Aq, *As, *Dq, *Ds;
+};
+
 template <class In, bool kAligned>
-__global__ __launch_bounds__(kThreads) void experts_ragged_mx_kernel(
-    const typename In::T* __restrict__ X, const int32_t* __restrict__ row_end, int E, int M,
-    int64_t N, int64_t ldx, uint8_t* __restrict__ Xq, int64_t ldq, uint8_t* __restrict__ Xs) {
+__global__ __launch_bounds__(kThreads) void experts_ragged_mx_kernel(RaggedArgs p) {
+  using T = typename In::T;
   const int s = blockIdx.y;
-  const Group g = group_of_unit<128>(row_end, E, M, [&](int total) { return s < total ? s : -1; });
-  if (g.e < 0 || g.e == E) return;
-  quantize_cols_mx_body<In, kAligned>(blockIdx.x, s - g.first, X + int64_t(g.begin) * ldx, g.rows,
-                                      N, ldx, Xq + int64_t(g.first) * 64, ldq,
-                                      Xs + int64_t(g.first) * 4 * N, N);
+  const Group g =
+      group_of_unit<128>(p.row_end, p.E, p.M, [&](int total) { return s < total ? s : -1; });
+  if (g.e < 0 || g.e == p.E) return;
+  const int tiles = (p.K + kMxTN - 1) / kMxTN;
+  const bool first = int(blockIdx.x) < tiles;
+  const int64_t n = first ? p.K : p.N, ld = first ? p.lda : p.lddy;
+  quantize_cols_mx_body<In, kAligned>(
+      first ? blockIdx.x : blockIdx.x - tiles, s - g.first,
+      static_cast<const T*>(first ? p.A : p.dY) + int64_t(g.begin) * ld, g.rows, n, ld,
+      (first ? p.Aq : p.Dq) + int64_t(g.first) * 64 * n, 64, 64 * n,
+      (first ? p.As : p.Ds) + int64_t(g.first) * 4 * n, n);
 }
 
 // ---------------------------------------------------------------------------
@@ -172,15 +229,15 @@ struct TileArgs {
   const int32_t* row_end;
   int E, M;        // M: rows of the activations
   int rows, cols;  // of an expert's output (rows: wgrad only)
-  int ldq;         // bytes of a packed row
+  int ldq;         // bytes of a packed row (wgrad: of all experts' steps)
+  int packed;      // B in packed rows, not a step's rows together
   void* Y;
   int64_t ldy;
 };
 
-// kWgrad false: forward and dgrad, A the packed rows of the activations, B
-// the packed weights of all experts (cols rows each). kWgrad true: A and B
-// the column-packed activations and gradients, row stride ldq, expert e's
-// reduction steps a range of columns of both.
+// kWgrad false: forward and dgrad, A the rows of the activations, B the weights
+// of all experts (cols rows each). kWgrad true: A and B the columns of the
+// activations and gradients, expert e's steps a range of the steps of both.
 template <class C, class Out, bool kWgrad>
 __global__ __launch_bounds__(C::kThreads, C::kMinBlocks) void experts_gemm_kernel(TileArgs p) {
   constexpr int SB = C::kStageBytes;
@@ -205,11 +262,11 @@ __global__ __launch_bounds__(C::kThreads, C::kMinBlocks) void experts_gemm_kerne
     m0 = tm * C::BM;
     n0 = tn * C::BN;
     rows = p.rows;
-    const int64_t at = int64_t(g.first) * 64;
-    A = Fp4Operand{p.Aq + at, p.ldq, p.rows, nkt * 64, p.As + int64_t(g.first) * 4 * p.rows,
-                   4 * p.rows, nkt * 4 * p.rows};
-    B = Fp4Operand{p.Bq + at, p.ldq, p.cols, nkt * 64, p.Bs + int64_t(g.first) * 4 * p.cols,
-                   4 * p.cols, nkt * 4 * p.cols};
+    const int64_t s = g.first;
+    A = Fp4Operand{p.Aq + s * 64 * p.rows, 64, 64 * p.rows, p.rows, nkt * 64 * p.rows,
+                   p.As + s * 4 * p.rows, 4 * p.rows, nkt * 4 * p.rows};
+    B = Fp4Operand{p.Bq + s * 64 * p.cols, 64, 64 * p.cols, p.cols, nkt * 64 * p.cols,
+                   p.Bs + s * 4 * p.cols, 4 * p.cols, nkt * 4 * p.cols};
     Y += int64_t(e) * p.rows * p.ldy;
   } else {
     int t = -1;
@@ -226,9 +283,10 @@ __global__ __launch_bounds__(C::kThreads, C::kMinBlocks) void experts_gemm_kerne
     n0 = tn * C::BN;
     rows = g.rows;
     const int nblk = p.ldq / 16, all = p.E * p.cols, e = g.e == p.E ? 0 : g.e;
-    A = Fp4Operand{p.Aq + int64_t(g.begin) * p.ldq, p.ldq, g.rows, p.ldq,
+    A = Fp4Operand{p.Aq + int64_t(g.begin) * 64, 64, p.M * 64, g.rows, p.M * p.ldq - g.begin * 64,
                    p.As + 4 * int64_t(g.begin), 4 * p.M, p.M * nblk - 4 * g.begin};
-    B = Fp4Operand{p.Bq + int64_t(e) * p.cols * p.ldq, p.ldq, p.cols, p.ldq,
+    B = Fp4Operand{p.Bq + int64_t(e) * p.cols * p.ldq, p.packed ? p.ldq : 64,
+                   p.packed ? 64 : 64 * p.cols, p.cols, p.cols * p.ldq,
                    p.Bs + 4 * int64_t(e) * p.cols, 4 * all, all * nblk - 4 * e * p.cols};
     Y += int64_t(g.begin) * p.ldy;
   }
@@ -416,31 +474,71 @@ hipError_t run_wgrad(const TileArgs& p, hipStream_t stream) {
                                          stream);
 }
 
+bool rows_fast(const void* X, int64_t ldx, int64_t L, int bytes) {
+  return reinterpret_cast<uintptr_t>(X) % 16 == 0 && (ldx * bytes) % 16 == 0 && L % 8 == 0;
+}
+bool cols_fast(const void* X, int64_t ldx, int bytes) {
+  return reinterpret_cast<uintptr_t>(X) % 16 == 0 && (ldx * bytes) % 16 == 0;
+}
+
+void rows_grid(RowsArgs& a, int rows) {
+  if (a.M == 0) return;
+  const dim3 g = mx_row_grid(a.M, (a.L + 127) / 128 * 16, rows);
+  a.gx = int(g.x);
+  a.gy = int(g.y);
+}
+bool many(const RowsArgs& a) { return a.M * ((a.L + 127) / 128 * 64) >= kManyRowBytes; }
+
+// One or two (b.M > 0) matrices by rows.
 template <class In>
-hipError_t run_cols(const void* Wp, int64_t E, int64_t K, int64_t N, int64_t ldw, uint8_t* Wq,
-                    int64_t ldq, uint8_t* Ws, hipStream_t stream) {
-  const auto* W = static_cast<const typename In::T*>(Wp);
-  const bool aligned = (reinterpret_cast<uintptr_t>(Wp) % 16 == 0) && ((ldw * In::kBytes) % 16 == 0);
-  const dim3 grid(unsigned(ceil_div(N, kMxTN)), unsigned((ldq * 2) / kMxTK), unsigned(E));
-  if (aligned)
-    experts_cols_mx_kernel<In, true><<<grid, kThreads, 0, stream>>>(W, K, N, ldw, E * N, Wq, ldq, Ws);
+hipError_t run_rows_mx(RowsArgs a, RowsArgs b, hipStream_t stream) {
+  const bool fast = rows_fast(a.X, a.ldx, a.L, In::kBytes) &&
+                    (b.M == 0 || rows_fast(b.X, b.ldx, b.L, In::kBytes));
+  const int rows = fast && (many(a) || many(b)) ? 4 : 1;
+  rows_grid(a, rows);
+  rows_grid(b, rows);
+  const unsigned grid = unsigned(a.gx) * unsigned(a.gy) + unsigned(b.gx) * unsigned(b.gy);
+  if (rows == 4)
+    experts_rows_mx_kernel<In, true, 4><<<grid, kThreads, 0, stream>>>(a, b);
+  else if (fast)
+    experts_rows_mx_kernel<In, true, 1><<<grid, kThreads, 0, stream>>>(a, b);
   else
-    experts_cols_mx_kernel<In, false><<<grid, kThreads, 0, stream>>>(W, K, N, ldw, E * N, Wq, ldq, Ws);
+    experts_rows_mx_kernel<In, false, 1><<<grid, kThreads, 0, stream>>>(a, b);
+  return hipGetLastError();
+}
+
+// The weights along K, and (a.M > 0) rows of the activations.
+template <class In>
+hipError_t run_cols_mx(RowsArgs a, ColsArgs w, hipStream_t stream) {
+  const bool fast =
+      cols_fast(w.W, w.ldw, In::kBytes) && (a.M == 0 || rows_fast(a.X, a.ldx, a.L, In::kBytes));
+  const int rows = fast && many(a) ? 4 : 1;
+  rows_grid(a, rows);
+  w.gx = int(ceil_div(w.N, kMxTN));
+  w.gy = int(ceil_div(w.K, kMxTK));
+  const unsigned grid = unsigned(a.gx) * unsigned(a.gy) + unsigned(w.E * w.gx * w.gy);
+  if (a.M == 0) {
+    if (fast)
+      experts_cols_mx_kernel<In, true, 0><<<grid, kThreads, 0, stream>>>(a, w);
+    else
+      experts_cols_mx_kernel<In, false, 0><<<grid, kThreads, 0, stream>>>(a, w);
+  } else if (rows == 4) {
+    experts_cols_mx_kernel<In, true, 4><<<grid, kThreads, 0, stream>>>(a, w);
+  } else if (fast) {
+    experts_cols_mx_kernel<In, true, 1><<<grid, kThreads, 0, stream>>>(a, w);
+  } else {
+    experts_cols_mx_kernel<In, false, 1><<<grid, kThreads, 0, stream>>>(a, w);
+  }
   return hipGetLastError();
 }
 
 template <class In>
-hipError_t run_ragged(const void* Xp, const int32_t* row_end, int64_t E, int64_t M, int64_t N,
-                      int64_t ldx, uint8_t* Xq, int64_t steps, uint8_t* Xs, hipStream_t stream) {
-  const auto* X = static_cast<const typename In::T*>(Xp);
-  const bool aligned = (reinterpret_cast<uintptr_t>(Xp) % 16 == 0) && ((ldx * In::kBytes) % 16 == 0);
-  const dim3 grid(unsigned(ceil_div(N, kMxTN)), unsigned(steps));
-  if (aligned)
-    experts_ragged_mx_kernel<In, true><<<grid, kThreads, 0, stream>>>(X, row_end, int(E), int(M), N,
-                                                                      ldx, Xq, steps * 64, Xs);
+hipError_t run_ragged(const RaggedArgs& p, int64_t steps, hipStream_t stream) {
+  const dim3 grid(unsigned(ceil_div(p.K, kMxTN) + ceil_div(p.N, kMxTN)), unsigned(steps));
+  if (cols_fast(p.A, p.lda, In::kBytes) && cols_fast(p.dY, p.lddy, In::kBytes))
+    experts_ragged_mx_kernel<In, true><<<grid, kThreads, 0, stream>>>(p);
   else
-    experts_ragged_mx_kernel<In, false><<<grid, kThreads, 0, stream>>>(X, row_end, int(E), int(M),
-                                                                       N, ldx, Xq, steps * 64, Xs);
+    experts_ragged_mx_kernel<In, false><<<grid, kThreads, 0, stream>>>(p);
   return hipGetLastError();
 }
 
@@ -451,27 +549,53 @@ int64_t experts_steps(int64_t E, int64_t M) {
   return (M + groups * 127) / 128;
 }
 
-hipError_t launch_experts_quantize_cols_mx(const void* W, bool bf16, int64_t E, int64_t K,
-                                           int64_t N, int64_t ldw, uint8_t* Wq, int64_t ldq,
-                                           uint8_t* Ws, hipStream_t stream) {
-  return bf16 ? run_cols<BF16In>(W, E, K, N, ldw, Wq, ldq, Ws, stream)
-              : run_cols<F32In>(W, E, K, N, ldw, Wq, ldq, Ws, stream);
+hipError_t launch_experts_quantize_weight_mx(const void* W, bool bf16, int64_t E, int64_t K,
+                                             int64_t N, int64_t ldw, uint8_t* Wq, int64_t ldq,
+                                             uint8_t* Ws, hipStream_t stream) {
+  const ColsArgs w{W, E, K, N, ldw, ldq, 64, Wq, Ws, 0, 0};
+  return bf16 ? run_cols_mx<BF16In>(RowsArgs{}, w, stream) : run_cols_mx<F32In>(RowsArgs{}, w, stream);
 }
 
-hipError_t launch_experts_quantize_ragged_mx(const void* X, bool bf16, const int32_t* row_end,
-                                             int64_t E, int64_t M, int64_t N, int64_t ldx,
-                                             uint8_t* Xq, uint8_t* Xs, hipStream_t stream) {
+hipError_t launch_experts_quantize_forward(const void* A, const void* W, bool bf16, int64_t E,
+                                           int64_t M, int64_t K, int64_t N, int64_t lda,
+                                           int64_t ldw, uint8_t* Aq, uint8_t* As, uint8_t* Wq,
+                                           uint8_t* Ws, hipStream_t stream) {
+  const RowsArgs a{A, M, K, lda, M, Aq, As, 0, 0};
+  const ColsArgs w{W, E, K, N, ldw, 64, 64 * N, Wq, Ws, 0, 0};
+  return bf16 ? run_cols_mx<BF16In>(a, w, stream) : run_cols_mx<F32In>(a, w, stream);
+}
+
+hipError_t launch_experts_quantize_rows(const void* A, bool bf16, int64_t M, int64_t K, int64_t lda,
+                                        uint8_t* Aq, uint8_t* As, hipStream_t stream) {
+  const RowsArgs a{A, M, K, lda, M, Aq, As, 0, 0};
+  return bf16 ? run_rows_mx<BF16In>(a, RowsArgs{}, stream) : run_rows_mx<F32In>(a, RowsArgs{}, stream);
+}
+
+hipError_t launch_experts_quantize_dgrad(const void* dY, const void* W, bool bf16, int64_t E,
+                                         int64_t M, int64_t K, int64_t N, int64_t lddy, int64_t ldw,
+                                         uint8_t* Dq, uint8_t* Ds, uint8_t* Wq, uint8_t* Ws,
+                                         hipStream_t stream) {
+  const RowsArgs a{dY, M, N, lddy, M, Dq, Ds, 0, 0};
+  const RowsArgs w{W, E * K, N, ldw, K, Wq, Ws, 0, 0};
+  return bf16 ? run_rows_mx<BF16In>(a, w, stream) : run_rows_mx<F32In>(a, w, stream);
+}
+
+hipError_t launch_experts_quantize_wgrad(const void* A, const void* dY, bool bf16,
+                                         const int32_t* row_end, int64_t E, int64_t M, int64_t K,
+                                         int64_t N, int64_t lda, int64_t lddy, uint8_t* Aq,
+                                         uint8_t* As, uint8_t* Dq, uint8_t* Ds,
+                                         hipStream_t stream) {
   const int64_t steps = experts_steps(E, M);
   if (steps == 0) return hipSuccess;
-  return bf16 ? run_ragged<BF16In>(X, row_end, E, M, N, ldx, Xq, steps, Xs, stream)
-              : run_ragged<F32In>(X, row_end, E, M, N, ldx, Xq, steps, Xs, stream);
+  const RaggedArgs p{A, dY, row_end, int(E), int(M), int(K), int(N), lda, lddy, Aq, As, Dq, Ds};
+  return bf16 ? run_ragged<BF16In>(p, steps, stream) : run_ragged<F32In>(p, steps, stream);
 }
 
 hipError_t launch_experts_rows(const uint8_t* Aq, const uint8_t* As, const uint8_t* Bq,
                                const uint8_t* Bs, const int32_t* row_end, int64_t E, int64_t M,
-                               int64_t N, int64_t ldq, void* Y, bool y_bf16, int64_t ldy,
-                               hipStream_t stream) {
-  const TileArgs p{Aq, As, Bq, Bs, row_end, int(E), int(M), 0, int(N), int(ldq), Y, ldy};
+                               int64_t N, int64_t ldq, bool packed, void* Y, bool y_bf16,
+                               int64_t ldy, hipStream_t stream) {
+  const TileArgs p{Aq, As, Bq, Bs, row_end, int(E), int(M), 0, int(N), int(ldq), packed, Y, ldy};
   return y_bf16 ? run_rows<uint16_t>(p, stream) : run_rows<float>(p, stream);
 }
 
@@ -505,7 +629,7 @@ hipError_t launch_experts_wgrad(const uint8_t* Aq, const uint8_t* As, const uint
                                 int64_t K, int64_t N, void* dW, bool w_bf16, int64_t ldw,
                                 hipStream_t stream) {
   const TileArgs p{Aq, As, Bq, Bs, row_end, int(E), int(M), int(K), int(N),
-                   int(experts_steps(E, M) * 64), dW, ldw};
+                   int(experts_steps(E, M) * 64), 0, dW, ldw};
   return w_bf16 ? run_wgrad<uint16_t>(p, stream) : run_wgrad<float>(p, stream);
 }
 

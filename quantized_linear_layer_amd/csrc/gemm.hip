@@ -439,8 +439,8 @@ __global__ __launch_bounds__(C::kThreads, C::kMinBlocks) void fp4_gemm_kernel(
 
   using Feed = Fp4Feed<C, kMx>;
   const int nblk = ldq / 16;
-  Feed f(Fp4Operand{Aq, ldq, M, ldq, As, 4 * M, M * nblk},
-         Fp4Operand{Bq, ldq, N, ldq, Bs, 4 * N, N * nblk}, m0, n0, wave, lane);
+  Feed f(Fp4Operand{Aq, ldq, BKB, M, M * ldq, As, 4 * M, M * nblk},
+         Fp4Operand{Bq, ldq, BKB, N, N * ldq, Bs, 4 * N, N * nblk}, m0, n0, wave, lane);
   gemm_pipeline(f, nkt, st0, st1, st2);
   auto& acc = f.acc;
 

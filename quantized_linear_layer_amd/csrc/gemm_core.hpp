@@ -98,13 +98,16 @@ __device__ inline void tile_of(int u, int tiles_m, int tiles_n, int& tm, int& tn
   tn = within / gsize;
 }
 
-// One operand of an FP4 product, as a workgroup reads it: `rows` packed rows of
-// `row_bytes` bytes (whole K steps) with stride ld. With block scales, s is
+// One operand of an FP4 product, as a workgroup reads it: `rows` rows, of which K
+// step t is 64 bytes at row * ld + t * step; `bytes` of them in all. (Packed rows:
+// ld the row length, step 64. With a step's rows together, ld 64: a tile's step is
+// then whole cache lines, where 64 bytes of a packed row are half a line and as
+// many requests to L2 again.) With block scales, s is
 // the step-major scale array at the operand's first row and step, s_step the
 // bytes from one K step to the next and s_bytes what may be read from s on.
 struct Fp4Operand {
   const uint8_t* q;
-  int ld, rows, row_bytes;
+  int ld, step, rows, bytes;
   const uint8_t* s;
   int s_step, s_bytes;
 };
@@ -152,7 +155,7 @@ struct Fp4Feed {
   int src_off[kPer];
   int a_row[FM], b_row[FN];
   int sc_off[NL > 0 ? NL : 1];
-  int sa_step, sb_step;
+  int a_step, b_step, sa_step, sb_step;
   int wave, lane, hshift;
 
   // the tile's first rows of the two operands are m0 and n0
@@ -160,8 +163,9 @@ struct Fp4Feed {
                             int lane_)
       : wave(wave_), lane(lane_), hshift((lane_ >> 5) * 8) {
     const int wm = wave / WN, wn = wave % WN;
-    const int a_bytes = int(int64_t(A.rows - 1) * A.ld) + A.row_bytes;
-    const int b_bytes = int(int64_t(B.rows - 1) * B.ld) + B.row_bytes;
+    const int a_bytes = A.bytes, b_bytes = B.bytes;
+    a_step = A.step;
+    b_step = B.step;
     rsA = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(A.q), 0, a_bytes, kBufferFlags);
     rsB = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(B.q), 0, b_bytes, kBufferFlags);
 #pragma unroll
@@ -201,12 +205,12 @@ struct Fp4Feed {
   }
 
   __device__ inline void dma(int kt, uint8_t* stage) {
-    const int kb = kt * BKB;
+    const int ka = kt * a_step, kb = kt * b_step;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
       uint8_t* const dst = stage + (wave + j * kWaves) * 1024;
       if (j < kPerA)
-        load_lds16(rsA, dst, src_off[j] + kb);
+        load_lds16(rsA, dst, src_off[j] + ka);
       else
         load_lds16(rsB, dst, src_off[j] + kb);
     }

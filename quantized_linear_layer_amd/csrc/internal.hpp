@@ -86,19 +86,32 @@ hipError_t launch_fp4_gemm_mx(const uint8_t* Aq, const uint8_t* As, const uint8_
 // Products grouped by expert (experts.hip). experts_steps: the K steps (128
 // rows) of a reduction over each expert's own rows, for any split of M rows.
 int64_t experts_steps(int64_t E, int64_t M);
-hipError_t launch_experts_quantize_cols_mx(const void* W, bool bf16, int64_t E, int64_t K,
-                                           int64_t N, int64_t ldw, uint8_t* Wq, int64_t ldq,
+hipError_t launch_experts_quantize_weight_mx(const void* W, bool bf16, int64_t E, int64_t K,
+                                             int64_t N, int64_t ldw, uint8_t* Wq, int64_t ldq,
+                                             uint8_t* Ws, hipStream_t stream);
+// The operands of the products below, in the order of experts.hip (a K step's
+// rows together), both of a product in one launch.
+hipError_t launch_experts_quantize_rows(const void* A, bool bf16, int64_t M, int64_t K, int64_t lda,
+                                        uint8_t* Aq, uint8_t* As, hipStream_t stream);
+hipError_t launch_experts_quantize_forward(const void* A, const void* W, bool bf16, int64_t E,
+                                           int64_t M, int64_t K, int64_t N, int64_t lda,
+                                           int64_t ldw, uint8_t* Aq, uint8_t* As, uint8_t* Wq,
                                            uint8_t* Ws, hipStream_t stream);
-// Columns of X packed along each expert's rows: N rows of experts_steps * 64
-// bytes, scales step-major.
-hipError_t launch_experts_quantize_ragged_mx(const void* X, bool bf16, const int32_t* row_end,
-                                             int64_t E, int64_t M, int64_t N, int64_t ldx,
-                                             uint8_t* Xq, uint8_t* Xs, hipStream_t stream);
-// M rows against N packed columns of each expert (forward, dgrad, apply).
+hipError_t launch_experts_quantize_dgrad(const void* dY, const void* W, bool bf16, int64_t E,
+                                         int64_t M, int64_t K, int64_t N, int64_t lddy, int64_t ldw,
+                                         uint8_t* Dq, uint8_t* Ds, uint8_t* Wq, uint8_t* Ws,
+                                         hipStream_t stream);
+hipError_t launch_experts_quantize_wgrad(const void* A, const void* dY, bool bf16,
+                                         const int32_t* row_end, int64_t E, int64_t M, int64_t K,
+                                         int64_t N, int64_t lda, int64_t lddy, uint8_t* Aq,
+                                         uint8_t* As, uint8_t* Dq, uint8_t* Ds,
+                                         hipStream_t stream);
+// M rows against N columns of each expert (forward, dgrad, apply); packed: the
+// weights are in packed rows, as launch_experts_quantize_weight_mx leaves them.
 hipError_t launch_experts_rows(const uint8_t* Aq, const uint8_t* As, const uint8_t* Bq,
                                const uint8_t* Bs, const int32_t* row_end, int64_t E, int64_t M,
-                               int64_t N, int64_t ldq, void* Y, bool y_bf16, int64_t ldy,
-                               hipStream_t stream);
+                               int64_t N, int64_t ldq, bool packed, void* Y, bool y_bf16,
+                               int64_t ldy, hipStream_t stream);
 // The same for so few rows that the product quantizes them itself.
 bool experts_fused(int64_t M, int64_t K);
 hipError_t launch_experts_fused(const void* A, bool bf16, int64_t lda, const uint8_t* Bq,

@@ -44,52 +44,17 @@ namespace fp4lin {
 namespace {
 
 constexpr int kMxThreads = 256;
-// Packed bytes from which the row kernel takes four rows a thread.
-constexpr int64_t kManyRowBytes = int64_t(8) << 20;
 
-// Workgroup (bx, by) takes rows by, by + gridDim.y, ... and in each the chunks
-// c = bx * 256 + t, c + 256 * gridDim.x, ... (cpr = ldq / 4 chunks of 8 codes
-// per padded row, a multiple of 16). Four consecutive t hold one block and sit
-// on four consecutive lanes, and the chunk stride is a multiple of 4, so a
-// block's lanes are active together. kRows rows are loaded before the first is
-// encoded, so that a thread has that many loads in flight.
+// Chunks of a row across blockIdx.x, groups of kRows rows across blockIdx.y
+// (quantize_rows_mx_body).
 template <class In, bool kFast, int kRows>
 __global__ __launch_bounds__(kMxThreads) void quantize_rows_mx_kernel(
     const typename In::T* __restrict__ X, int64_t M, int64_t K, int64_t ldx,
     const float* __restrict__ tau_p, uint8_t* __restrict__ Xq, int64_t ldq,
     uint8_t* __restrict__ Xs) {
   const float tau = tau_p ? *tau_p : __builtin_huge_valf();
-  const int64_t cpr = ldq / 4;
-  for (int64_t r0 = blockIdx.y; r0 < M; r0 += int64_t(gridDim.y) * kRows)
-  for (int64_t c = int64_t(blockIdx.x) * kMxThreads + threadIdx.x; c < cpr;
-       c += int64_t(gridDim.x) * kMxThreads) {
-    Vec8<In> v[kRows];
-#pragma unroll
-    for (int u = 0; u < kRows; ++u) {
-      const int64_t r = r0 + int64_t(u) * gridDim.y;
-      load_chunk<In, kFast>(X + (r < M ? r : M - 1) * ldx, c * 8, K, v[u]);
-    }
-#pragma unroll
-    for (int u = 0; u < kRows; ++u) {
-      const int64_t r = r0 + int64_t(u) * gridDim.y;
-      if (r >= M) break;
-      float ax[8];
-      float m = 0.0f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        ax[i] = fminf(fabsf(In::widen(v[u].v[i])), tau);
-        m = fmaxf(m, ax[i]);
-      }
-      const int e = mx_exponent(quad_max(m));
-      uint32_t word = 0;
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        word |= (mx_magnitude(ax[i], e) | (In::sign_bit(v[u].v[i]) << 3)) << (4 * i);
-      *reinterpret_cast<uint32_t*>(Xq + r * ldq + c * 4) = word;
-      // chunk c: block c / 4 = 4 * (c / 16) + (c / 4) % 4
-      if ((c & 3) == 0) Xs[(c / 16) * 4 * M + 4 * r + ((c / 4) & 3)] = uint8_t(e + 127);
-    }
-  }
+  quantize_rows_mx_body<In, kFast, kRows>(blockIdx.x, gridDim.x, blockIdx.y, gridDim.y, X, M, K, ldx,
+                                          tau, Xq, ldq, 1, Xs);
 }
 
 // One workgroup per 128 x 128 tile of W (quantize_cols_mx_body).
@@ -97,15 +62,7 @@ template <class In, bool kAligned>
 __global__ __launch_bounds__(kMxThreads) void quantize_cols_mx_kernel(
     const typename In::T* __restrict__ W, int64_t K, int64_t N, int64_t ldw,
     uint8_t* __restrict__ Wq, int64_t ldq, uint8_t* __restrict__ Ws) {
-  quantize_cols_mx_body<In, kAligned>(blockIdx.x, blockIdx.y, W, K, N, ldw, Wq, ldq, Ws, N);
-}
-
-// Chunks of a row across x (at most 64 workgroups), rows across y (at most 65535
-// workgroups of kRows rows).
-dim3 mx_row_grid(int64_t M, int64_t cpr, int64_t rows) {
-  const int64_t bx = (cpr + kMxThreads - 1) / kMxThreads;
-  const int64_t by = (M + rows - 1) / rows;
-  return dim3(unsigned(bx < 64 ? bx : 64), unsigned(by < 65535 ? by : 65535));
+  quantize_cols_mx_body<In, kAligned>(blockIdx.x, blockIdx.y, W, K, N, ldw, Wq, ldq, 64, Ws, N);
 }
 
 template <class In>

@@ -974,7 +974,7 @@ __global__ __launch_bounds__(kRowWaves * kWave) void count_wpass_kernel(
                                                       gsum, amax);
   else if constexpr (kMx)
     quantize_cols_mx_body<In, kWAligned>(i % wp.gx, i / wp.gx, static_cast<const T*>(wp.W), wp.K,
-                                         wp.N, wp.ldw, wp.Wq, wp.ldq,
+                                         wp.N, wp.ldw, wp.Wq, wp.ldq, 64,
                                          static_cast<uint8_t*>(wp.sW), wp.N);
   else
     colmax_body<In, kWAligned>(i % wp.gx, i / wp.gx, static_cast<const T*>(wp.W), wp.K, wp.N,
