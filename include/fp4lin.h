@@ -473,7 +473,8 @@ fp4lin_status fp4lin_experts_wgrad_mx(const void* A, const void* dY, fp4lin_dtyp
  * dimensions (where a row of X or W is not a multiple of 8 elements or its
  * stride not one of 16 bytes, a padded copy is kept in the workspace).
  * T = 0 is a valid batch (a weight gradient is all zeros). Sums are fp32; in
- * the backward G is rounded to dt before the two products that take it.
+ * the backward G, over the largest |dloss| of the rows that count, is rounded to
+ * dt before the two products that take it.
  * Limits: 256 * ld * element size < 2^31 for every leading dimension. */
 typedef enum { FP4LIN_HEAD_HIDDEN_MAJOR = 0, FP4LIN_HEAD_VOCAB_MAJOR = 1 } fp4lin_head_layout;
 

@@ -739,7 +739,7 @@ namespace {
 
 struct HeadLayout {
   fp4lin::HeadPlan plan;
-  size_t x, w, part, tlogit, G, acc, total;
+  size_t x, w, part, tlogit, G, acc, top, total;
 };
 
 // Sizes and strides that both calls check, and where they keep what they keep.
@@ -768,6 +768,7 @@ fp4lin_status head_layout(fp4lin_dtype dt, fp4lin_head_layout layout, int64_t T,
   if (backward) {
     o.G = take(size_t(T) * size_t(o.plan.ldg) * size_t(esz));
     o.acc = take(size_t(T) * size_t(o.plan.ldp) * size_t(o.plan.slices) * 4);
+    o.top = take(4);
   } else {
     o.part = take(size_t(T) * size_t(o.plan.parts) * 8);
     o.tlogit = take(size_t(T) * 4);
@@ -803,6 +804,7 @@ fp4lin_status head_call(const void* X, const void* W, fp4lin_dtype dt, fp4lin_he
   c->tlogit = reinterpret_cast<float*>(base + o->tlogit);
   c->G = base + o->G;
   c->acc = reinterpret_cast<float*>(base + o->acc);
+  c->top = reinterpret_cast<float*>(base + o->top);
   return FP4LIN_OK;
 }
 

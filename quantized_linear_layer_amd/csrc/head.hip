@@ -102,6 +102,7 @@ struct HeadArgs {
   // backward
   const float* lse;
   const float* dloss;
+  const float* top;  // largest |dloss| of the rows that count
   T* G;
   int64_t ldg;
 };
@@ -202,8 +203,27 @@ __global__ __launch_bounds__(kJoinRows * 64) void head_join_kernel(
   loss[row] = t >= 0 && t < V ? l - tlogit[row] : 0.0f;
 }
 
-// G of a piece of the vocabulary, zeros in the columns that pad it to ldg's
-// multiple of 8.
+// The largest |dloss| of the rows whose target lies in the vocabulary, one
+// workgroup.
+__global__ __launch_bounds__(1024) void head_top_kernel(const float* __restrict__ dloss,
+                                                        const int32_t* __restrict__ target, int T,
+                                                        int V, float* __restrict__ top) {
+  __shared__ float sh[16];
+  float m = 0.0f;
+  for (int i = threadIdx.x; i < T; i += 1024) {
+    const int t = target[i];
+    if (t >= 0 && t < V) m = fmaxf(m, fabsf(dloss[i]));
+  }
+  m = wave_max(m);
+  if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = m;
+  __syncthreads();
+  if (threadIdx.x >= 64) return;
+  m = wave_max(threadIdx.x < 16 ? sh[threadIdx.x] : 0.0f);
+  if (threadIdx.x == 0) *top = m;
+}
+
+// G of a piece of the vocabulary over the largest |dloss|, zeros in the columns
+// that pad it to a multiple of 8.
 template <class C, class T, bool kBT>
 __global__ __launch_bounds__(C::kThreads, C::kMinBlocks) void head_grad_kernel(HeadArgs<T> p) {
   constexpr int FM = C::FM, FN = C::FN;
@@ -223,7 +243,8 @@ __global__ __launch_bounds__(C::kThreads, C::kMinBlocks) void head_grad_kernel(H
   product_tile<C>(f, (p.H + kStepElems<T> - 1) / kStepElems<T>, st0, st1, st2, st3, st4);
 
   const int row0 = m0 + wm * FM * 32, col0 = n0 + wn * FN * 32;
-  float g[FM][16];  // dloss of this lane's rows, 0 where the row is left out
+  float g[FM][16];  // dloss of this lane's rows over the largest, 0 where the row is left out
+  const float top = *p.top;
 #pragma unroll
   for (int fm = 0; fm < FM; ++fm)
 #pragma unroll
@@ -232,7 +253,7 @@ __global__ __launch_bounds__(C::kThreads, C::kMinBlocks) void head_grad_kernel(H
       const int at = row < p.T_ ? row : p.T_ - 1;
       const float lse = p.lse[at];
       const int t = p.target[at];
-      g[fm][r] = t >= 0 && t < p.Vall ? p.dloss[at] : 0.0f;
+      g[fm][r] = t >= 0 && t < p.Vall && top != 0.0f ? p.dloss[at] / top : 0.0f;
 #pragma unroll
       for (int fn = 0; fn < FN; ++fn) f.acc[fm][fn][r] = exp_diff(f.acc[fm][fn][r], lse);
     }
@@ -282,6 +303,7 @@ struct ProductArgs {
   int64_t ldy;
   int64_t slice_elems;
   int first;
+  const float* scale;  // of the result (not of the slices' arrays)
 };
 
 template <class C, class T, bool kAT, bool kBT, class Out, bool kAdd>
@@ -312,8 +334,11 @@ __global__ __launch_bounds__(C::kThreads, C::kMinBlocks) void head_product_kerne
   if (k > 0) product_tile<C>(f, (k + kE - 1) / kE, st0, st1, st2, st3, st4);
   Out* const Y = p.Y + blockIdx.z * p.slice_elems;
   const bool vec = rows_vec(Y, p.ldy);
+  float scale = 1.0f;
+  if constexpr (!kAdd) scale = *p.scale;
   emit_tile<C, kOutVec<Out>>(
-      st0, st1, st2, wave, lane, m0, n0, [&](int fm, int fn, int r) { return f.acc[fm][fn][r]; },
+      st0, st1, st2, wave, lane, m0, n0,
+      [&](int fm, int fn, int r) { return kAdd ? f.acc[fm][fn][r] : f.acc[fm][fn][r] * scale; },
       [&](int gr, int gc, const float* v) {
         if (gr >= p.M) return;
         Out* const dst = Y + int64_t(gr) * p.ldy + gc;
@@ -329,12 +354,14 @@ __global__ __launch_bounds__(C::kThreads, C::kMinBlocks) void head_product_kerne
       });
 }
 
-// dX from the S arrays of its slices (T x ldp each), added in slice order.
+// dX from the S arrays of its slices (T x ldp each), added in slice order, times
+// *scale.
 template <class Out>
 __global__ __launch_bounds__(256) void head_sum_kernel(const float* __restrict__ acc, int S,
                                                        int64_t slice_elems, int64_t T, int H,
-                                                       int64_t ldp, Out* __restrict__ dX,
-                                                       int64_t lddx) {
+                                                       int64_t ldp, const float* __restrict__ scale,
+                                                       Out* __restrict__ dX, int64_t lddx) {
+  const float g = *scale;
   const int64_t groups = ldp / 4;
   const bool vec = (reinterpret_cast<uintptr_t>(dX) % (4 * sizeof(Out)) == 0) && lddx % 4 == 0;
   for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < T * groups;
@@ -344,6 +371,7 @@ __global__ __launch_bounds__(256) void head_sum_kernel(const float* __restrict__
     f32x4 o = *reinterpret_cast<const f32x4*>(acc + row * ldp + c);
     for (int s = 1; s < S; ++s)
       o += *reinterpret_cast<const f32x4*>(acc + s * slice_elems + row * ldp + c);
+    o *= g;
     Out* const dst = dX + row * lddx + c;
     if constexpr (sizeof(Out) == 4) {
       if (vec && c + 4 <= H) {
@@ -589,6 +617,9 @@ hipError_t run_backward(const HeadCall& c, const HeadPlan& h, hipStream_t stream
   hipError_t e = operands<T>(c, h, &X, &W, stream);
   if (e != hipSuccess) return e;
   T* const dW = static_cast<T*>(c.dW);
+  head_top_kernel<<<1, 1024, 0, stream>>>(c.dloss, c.target, int(c.T), int(c.V), c.top);
+  e = hipGetLastError();
+  if (e != hipSuccess) return e;
   const Tile tx = dx_tile(kBf16, c.T, c.H, h.piece);
   const bool direct = h.slices == 1 && h.piece >= c.V;
   for (int64_t v0 = 0; v0 < c.V; v0 += h.piece) {
@@ -607,6 +638,7 @@ hipError_t run_backward(const HeadCall& c, const HeadPlan& h, hipStream_t stream
       a.target = c.target;
       a.lse = c.lse;
       a.dloss = c.dloss;
+      a.top = c.top;
       a.G = static_cast<T*>(c.G);
       a.ldg = h.ldg;
       e = logits<T, true>(pick_tile(kBf16, c.T, n), c.by_vocab, a, stream);
@@ -618,12 +650,13 @@ hipError_t run_backward(const HeadCall& c, const HeadPlan& h, hipStream_t stream
       const int64_t per = ceil_div(ceil_div(n, h.slices), 64) * 64;
       const DenseOperand<T> B{a.W.p, h.ldw, c.by_vocab ? X.k : int(c.H), c.by_vocab ? int(n) : n8};
       if (direct) {
-        const ProductArgs<T, T> q{G, B, int(c.T), int(c.H), n8, static_cast<T*>(c.dX), c.lddx, 0, 1};
+        const ProductArgs<T, T> q{G, B, int(c.T), int(c.H), n8, static_cast<T*>(c.dX), c.lddx, 0, 1,
+                                  c.top};
         e = c.by_vocab ? product<T, false, true, T, false>(tx, q, 1, stream)
                        : product<T, false, false, T, false>(tx, q, 1, stream);
       } else {
         const ProductArgs<T, float> q{G, B, int(c.T), int(c.H), int(per), c.acc, h.ldp,
-                                      c.T * h.ldp, v0 == 0};
+                                      c.T * h.ldp, v0 == 0, nullptr};
         e = c.by_vocab ? product<T, false, true, float, true>(tx, q, h.slices, stream)
                        : product<T, false, false, float, true>(tx, q, h.slices, stream);
       }
@@ -636,13 +669,14 @@ hipError_t run_backward(const HeadCall& c, const HeadPlan& h, hipStream_t stream
     // (A is read across its rows here: bfloat16 at least 128 rows a tile, see product)
     const Tile tw = pick_tile(kBf16, kBf16 && rows <= 64 ? 65 : rows, cols);
     const ProductArgs<T, T> q{c.by_vocab ? Gt : Xt, c.by_vocab ? Xt : Gt, int(rows), int(cols),
-                              int(c.T), dW + v0 * (c.by_vocab ? c.lddw : 1), c.lddw, 0, 1};
+                              int(c.T), dW + v0 * (c.by_vocab ? c.lddw : 1), c.lddw, 0, 1, c.top};
     e = product<T, true, true, T, false>(tw, q, 1, stream);
     if (e != hipSuccess) return e;
   }
   if (direct || c.T == 0) return hipSuccess;
   head_sum_kernel<T><<<copy_blocks(c.T * (h.ldp / 4)), 256, 0, stream>>>(
-      c.acc, int(h.slices), c.T * h.ldp, c.T, int(c.H), h.ldp, static_cast<T*>(c.dX), c.lddx);
+      c.acc, int(h.slices), c.T * h.ldp, c.T, int(c.H), h.ldp, c.top, static_cast<T*>(c.dX),
+      c.lddx);
   return hipGetLastError();
 }
 

@@ -143,7 +143,7 @@ struct HeadCall {
   const int32_t* target;
   // workspace
   void *packed_x, *packed_w, *part, *G;
-  float *tlogit, *acc;
+  float *tlogit, *acc, *top;
   // forward
   float *loss, *lse_out;
   // backward

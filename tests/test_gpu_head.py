@@ -149,6 +149,23 @@ def test_head_loss_large_tiles_and_pieces(ql, by_vocab):
         assert rel <= 2.0 ** -8, f"{name}: {rel}"
 
 
+def test_head_loss_mean_is_not_rounded_as_a_whole(ql):
+    """All rows weighted alike by (1 + 2^-8) 2^-12, halfway between two bfloat16
+    numbers: the gradients carry the roundings of G's and of their own entries,
+    2^-9 / sqrt(3) of their norm each at most where they are independent, and not
+    the 2^-8 of the weight. 1.5 * sqrt(2 / 3) * 2^-9 leaves room for half as much
+    again."""
+    T, H, V = 512, 256, 1024
+    X, W, target, _ = inputs(T, H, V, wl.BF16, seed=3)
+    dloss = np.full(T, (1 + 2.0 ** -8) * 2.0 ** -12, np.float32)
+    got = as64(run(ql, X, W, target, dloss, False))
+    r = reference(X.f32.astype(np.float64), W.f32.astype(np.float64), target, dloss.astype(np.float64))
+    for k in ("dX", "dW"):
+        rel = np.linalg.norm(got[k] - r[k]) / np.linalg.norm(r[k])
+        log(f"head loss {k}: {rel:.2e}")
+        assert rel <= 1.5 * np.sqrt(2 / 3) * 2.0 ** -9
+
+
 @pytest.mark.parametrize("dtype", [wl.F32, wl.BF16])
 def test_head_loss_left_out_rows(ql, dtype):
     """Targets outside the vocabulary: loss 0 and exactly no gradient; the rows
