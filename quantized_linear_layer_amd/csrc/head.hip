@@ -27,7 +27,7 @@
 // for bit.
 //
 // Operands whose rows do not start on 16 bytes or whose contiguous size is not a
-// multiple of 8 elements are first copied, padded with zeros (pack_kernel).
+// multiple of 8 elements are first copied, padded with zeros.
 #include <type_traits>
 
 #include "dense_core.hpp"
@@ -203,25 +203,6 @@ __global__ __launch_bounds__(kJoinRows * 64) void head_join_kernel(
   loss[row] = t >= 0 && t < V ? l - tlogit[row] : 0.0f;
 }
 
-// The largest |dloss| of the rows whose target lies in the vocabulary, one
-// workgroup.
-__global__ __launch_bounds__(1024) void head_top_kernel(const float* __restrict__ dloss,
-                                                        const int32_t* __restrict__ target, int T,
-                                                        int V, float* __restrict__ top) {
-  __shared__ float sh[16];
-  float m = 0.0f;
-  for (int i = threadIdx.x; i < T; i += 1024) {
-    const int t = target[i];
-    if (t >= 0 && t < V) m = fmaxf(m, fabsf(dloss[i]));
-  }
-  m = wave_max(m);
-  if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = m;
-  __syncthreads();
-  if (threadIdx.x >= 64) return;
-  m = wave_max(threadIdx.x < 16 ? sh[threadIdx.x] : 0.0f);
-  if (threadIdx.x == 0) *top = m;
-}
-
 // G of a piece of the vocabulary over the largest |dloss|, zeros in the columns
 // that pad it to a multiple of 8.
 template <class C, class T, bool kBT>
@@ -394,23 +375,69 @@ __global__ __launch_bounds__(256) void head_sum_kernel(const float* __restrict__
   }
 }
 
-// R x C with row stride ld into rows of ldp (a multiple of 8) elements, zeros
-// after the C-th. One thread per 8 elements of the copy.
+// What the products need first, in one launch: padded copies of X and W where
+// they have to be, and for the backward the largest |dloss| of the rows whose
+// target lies in the vocabulary (the last workgroup).
 template <class T>
-__global__ __launch_bounds__(256) void pack_kernel(const T* __restrict__ src, int64_t R, int64_t C,
-                                                   int64_t ld, T* __restrict__ dst, int64_t ldp) {
-  const int64_t groups = ldp / 8;
-  for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < R * groups;
-       i += int64_t(gridDim.x) * 256) {
+struct PackArgs {
+  const T* src;
+  int64_t R, C, ld;  // R = 0: no copy
+  T* dst;
+  int64_t ldp;  // a multiple of 8; zeros from the C-th element on
+  int blocks;
+};
+
+template <class T>
+struct PrepareArgs {
+  PackArgs<T> x, w;
+  const float* dloss;  // NULL in the forward
+  const int32_t* target;
+  int T_, V;
+  float* top;
+};
+
+// One thread per 8 elements of the copy.
+template <class T>
+__device__ inline void pack(const PackArgs<T>& p, int block) {
+  const int64_t groups = p.ldp / 8;
+  for (int64_t i = int64_t(block) * 256 + threadIdx.x; i < p.R * groups;
+       i += int64_t(p.blocks) * 256) {
     const int64_t row = i / groups, c = (i - row * groups) * 8;
     __attribute__((aligned(16))) T v[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = c + j < C ? src[row * ld + c + j] : T(0);
+    for (int j = 0; j < 8; ++j) v[j] = c + j < p.C ? p.src[row * p.ld + c + j] : T(0);
 #pragma unroll
     for (int j = 0; j < 8 * int(sizeof(T)); j += 16)
-      *reinterpret_cast<uint4*>(reinterpret_cast<char*>(dst + row * ldp + c) + j) =
+      *reinterpret_cast<uint4*>(reinterpret_cast<char*>(p.dst + row * p.ldp + c) + j) =
           *reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(v) + j);
   }
+}
+
+template <class T>
+__global__ __launch_bounds__(256) void head_prepare_kernel(PrepareArgs<T> p) {
+  const int b = blockIdx.x;
+  if (b < p.x.blocks) return pack(p.x, b);
+  if (b < p.x.blocks + p.w.blocks) return pack(p.w, b - p.x.blocks);
+  __shared__ float sh[4];
+  float m = 0.0f;
+  constexpr int U = 8;  // rows in flight a thread
+  for (int i0 = threadIdx.x; i0 < p.T_; i0 += 256 * U) {
+    float g[U];
+    int t[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * 256 < p.T_ ? i0 + u * 256 : p.T_ - 1;
+      g[u] = p.dloss[i];
+      t[u] = p.target[i];
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (t[u] >= 0 && t[u] < p.V) m = fmaxf(m, fabsf(g[u]));
+  }
+  m = wave_max(m);
+  if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = m;
+  __syncthreads();
+  if (threadIdx.x == 0) *p.top = fmaxf(fmaxf(sh[0], sh[1]), fmaxf(sh[2], sh[3]));
 }
 
 // ---------------------------------------------------------------------------
@@ -518,35 +545,33 @@ HeadPlan head_plan(bool bf16, int64_t T, int64_t H, int64_t V, bool by_vocab, in
 
 namespace {
 
+// X and W as the products take them, packed where they have to be; with dloss,
+// its largest besides.
 template <class T>
-hipError_t pack(const void* src, int64_t R, int64_t C, int64_t ld, void* dst, int64_t ldp,
-                hipStream_t stream) {
-  pack_kernel<T><<<copy_blocks(R * (ldp / 8)), 256, 0, stream>>>(
-      static_cast<const T*>(src), R, C, ld, static_cast<T*>(dst), ldp);
-  return hipGetLastError();
-}
-
-// X and W as the products take them, packed where they have to be.
-template <class T>
-hipError_t operands(const HeadCall& c, const HeadPlan& h, DenseOperand<T>* X, const T** W,
-                    hipStream_t stream) {
-  const T* x = static_cast<const T*>(c.X);
-  const T* w = static_cast<const T*>(c.W);
-  if (h.pack_x) {
-    const hipError_t e = pack<T>(c.X, c.T, c.H, c.ldx, c.packed_x, h.ldx, stream);
-    if (e != hipSuccess) return e;
-    x = static_cast<const T*>(c.packed_x);
-  }
-  if (h.pack_w) {
-    const hipError_t e = pack<T>(c.W, c.by_vocab ? c.V : c.H, c.by_vocab ? c.H : c.V, c.ldw,
-                                 c.packed_w, h.ldw, stream);
-    if (e != hipSuccess) return e;
-    w = static_cast<const T*>(c.packed_w);
-  }
+hipError_t prepare(const HeadCall& c, const HeadPlan& h, bool backward, DenseOperand<T>* X,
+                   const T** W, hipStream_t stream) {
+  const T* const x = static_cast<const T*>(c.X);
+  const T* const w = static_cast<const T*>(c.W);
+  const int64_t wr = c.by_vocab ? c.V : c.H, wc = c.by_vocab ? c.H : c.V;
+  PrepareArgs<T> p{};
+  if (h.pack_x && c.T > 0)
+    p.x = PackArgs<T>{x, c.T, c.H, c.ldx, static_cast<T*>(c.packed_x), h.ldx,
+                      int(copy_blocks(c.T * (h.ldx / 8)))};
+  if (h.pack_w)
+    p.w = PackArgs<T>{w, wr, wc, c.ldw, static_cast<T*>(c.packed_w), h.ldw,
+                      int(copy_blocks(wr * (h.ldw / 8)))};
+  p.dloss = c.dloss;
+  p.target = c.target;
+  p.T_ = int(c.T);
+  p.V = int(c.V);
+  p.top = c.top;
+  const int blocks = p.x.blocks + p.w.blocks + (backward ? 1 : 0);
+  if (blocks > 0) head_prepare_kernel<T><<<unsigned(blocks), 256, 0, stream>>>(p);
   // the reduction of the logits, with its zeros
-  *X = DenseOperand<T>{x, h.ldx, int(c.T), int(round8(c.H))};
-  *W = w;
-  return hipSuccess;
+  *X = DenseOperand<T>{h.pack_x ? static_cast<const T*>(c.packed_x) : x, h.ldx, int(c.T),
+                       int(round8(c.H))};
+  *W = h.pack_w ? static_cast<const T*>(c.packed_w) : w;
+  return hipGetLastError();
 }
 
 template <class T, bool kGrad>
@@ -590,7 +615,7 @@ template <class T>
 hipError_t run_forward(const HeadCall& c, const HeadPlan& h, hipStream_t stream) {
   DenseOperand<T> X;
   const T* W;
-  hipError_t e = operands<T>(c, h, &X, &W, stream);
+  hipError_t e = prepare<T>(c, h, false, &X, &W, stream);
   if (e != hipSuccess) return e;
   HeadArgs<T> a{};
   a.X = X;
@@ -614,12 +639,9 @@ hipError_t run_backward(const HeadCall& c, const HeadPlan& h, hipStream_t stream
   constexpr bool kBf16 = sizeof(T) == 2;
   DenseOperand<T> X;
   const T* W;
-  hipError_t e = operands<T>(c, h, &X, &W, stream);
+  hipError_t e = prepare<T>(c, h, true, &X, &W, stream);
   if (e != hipSuccess) return e;
   T* const dW = static_cast<T*>(c.dW);
-  head_top_kernel<<<1, 1024, 0, stream>>>(c.dloss, c.target, int(c.T), int(c.V), c.top);
-  e = hipGetLastError();
-  if (e != hipSuccess) return e;
   const Tile tx = dx_tile(kBf16, c.T, c.H, h.piece);
   const bool direct = h.slices == 1 && h.piece >= c.V;
   for (int64_t v0 = 0; v0 < c.V; v0 += h.piece) {
