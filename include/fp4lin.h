@@ -471,11 +471,13 @@ fp4lin_status fp4lin_experts_wgrad_mx(const void* A, const void* dY, fp4lin_dtyp
  *            0, no gradient. (lse is that of the row's logits all the same.)
  * X, W and the workspace must be 16-byte aligned; any sizes and leading
  * dimensions (where a row of X or W is not a multiple of 8 elements or its
- * stride not one of 16 bytes, a padded copy is kept in the workspace).
+ * stride not one of 16 bytes, a padded copy is kept in the workspace; so is a
+ * copy of bfloat16 X in the order of the products).
  * T = 0 is a valid batch (a weight gradient is all zeros). Sums are fp32; in
  * the backward G, over the largest |dloss| of the rows that count, is rounded to
  * dt before the two products that take it.
- * Limits: 256 * ld * element size < 2^31 for every leading dimension. */
+ * Limits: T <= 2^22, and 256 * ld * element size < 2^31 for the leading
+ * dimensions of X and W. */
 typedef enum { FP4LIN_HEAD_HIDDEN_MAJOR = 0, FP4LIN_HEAD_VOCAB_MAJOR = 1 } fp4lin_head_layout;
 
 /* Bytes of workspace of the two calls (at least 256); 0 for invalid

@@ -752,11 +752,12 @@ fp4lin_status head_layout(fp4lin_dtype dt, fp4lin_head_layout layout, int64_t T,
   const int64_t most = kMaxDim / 256 / esz - 16;  // of a leading dimension
   if (!ok_rows(T) || !ok_dim(H) || !ok_dim(V) || ldx < H || ldw < (by_vocab ? H : V))
     return FP4LIN_ERR_SHAPE;
-  if (ldx > most || ldw > most || H > most || V > most) return FP4LIN_ERR_SHAPE;
+  if (ldx > most || ldw > most || H > most || V > most || T > (int64_t(1) << 22))
+    return FP4LIN_ERR_SHAPE;
   // tiles index a grid of at most 2^31 - 1 workgroups
   if ((double(T) / 64 + 1) * (double(V) / 128 + 1) >= double(kMaxDim)) return FP4LIN_ERR_SHAPE;
   HeadLayout o{};
-  o.plan = fp4lin::head_plan(dt == FP4LIN_BF16, T, H, V, by_vocab, ldx, ldw);
+  o.plan = fp4lin::head_plan(dt == FP4LIN_BF16, backward, T, H, V, by_vocab, ldx, ldw);
   size_t off = 0;
   auto take = [&](size_t bytes) {
     const size_t at = off;

@@ -3,12 +3,20 @@
 // row, 32 bfloat16 or 16 float elements.
 //
 // An operand is a matrix of `extent` output rows (or columns) by `k` elements of
-// the reduction, in memory either along the reduction (kT false: element (i, j)
-// at p[i * ld + j]) or across it (kT true: at p[j * ld + i]). Both are staged by
-// 16-byte loads straight into LDS and read back as MFMA fragments, so no matrix
-// is ever transposed in memory:
-//  * along: 64-byte rows, as the FP4 feed stages them; a lane's 16 bytes of a
-//    fragment are consecutive in the reduction.
+// the reduction, in one of three orders:
+//  * kAlong: element (i, j) at p[i * ld + (j / kE) * step + j % kE], kE the
+//    elements of a K step: rows along the reduction (step kE), or the rows of a
+//    step together (ld kE, step kE times the rows). The second makes a tile's
+//    step whole cache lines, where 64 bytes of a longer row are half of one and
+//    twice the requests to L2.
+//  * kAcross: element (i, j) at p[j * ld + i]: rows across the reduction.
+//  * kPieces (bfloat16): element (i, j) at p[(i / 32) * step + j * 32 + i % 32]:
+//    the second form of kAlong of a matrix whose rows are this operand's
+//    reduction.
+// All are staged by 16-byte loads straight into LDS and read back as MFMA
+// fragments, so no matrix is ever transposed in memory:
+//  * along: rows of a step's bytes, as the FP4 feed stages them; a lane's 16
+//    bytes of a fragment are consecutive in the reduction.
 //  * across: rows of the reduction, BM elements each. bfloat16 fragments come
 //    out of the transposing LDS read: 16 lanes name 4 reduction rows x 16
 //    columns (8 bytes each) and lane i gets column i's four values. float32
@@ -16,15 +24,18 @@
 //    64-byte (bfloat16) or 128-byte (float32) segments of a staged row are
 //    XOR-swizzled with the reduction row, so that the rows one read touches
 //    lie in distinct banks.
+//  * pieces: the step's 32 reduction rows of one 32-column piece after the other,
+//    64 bytes each: the four rows of a transposing read are 256 bytes in a row.
 // For the 32x32 shapes a lane supplies the row (lane % 32) and one half of the
 // reduction range of a sub-step (lane / 32); A and B use the same assignment, so
 // the order inside a sub-step does not matter. A 16-byte fragment holds the
 // operand of one 32x32x16 bfloat16 MFMA or of four 32x32x2 float32 ones.
 //
-// Requirements, checked by the callers: p 16-byte aligned, ld * size a multiple
-// of 16, and the contiguous size (k along, extent across) a multiple of 8
+// Requirements, checked by the callers: p 16-byte aligned, ld and step whole
+// 16-byte pieces, and the contiguous size (k along, extent across) a multiple of 8
 // elements, so that every 16-byte piece lies wholly inside a row or outside.
-// Pieces past either size read as zero.
+// Pieces past either size read as zero (kPieces: the rest of the last 32 columns
+// is read as it is).
 #pragma once
 
 #include "gemm_core.hpp"
@@ -35,17 +46,19 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
+enum { kAlong = 0, kAcross = 1, kPieces = 2 };
+
 template <class T>
 struct DenseOperand {
   const T* p;
-  int64_t ld;
+  int64_t ld, step;
   int extent, k;
 };
 
 template <class T>
 constexpr int kStepElems = 64 / int(sizeof(T));  // reduction elements of a K step
 
-template <class C, class T, bool kAT, bool kBT>
+template <class C, class T, int kAT, int kBT>
 struct DenseFeed {
   static constexpr int BM = C::BM, BN = C::BN, WN = C::WN, CPR = C::CPR;
   static constexpr int FM = C::FM, FN = C::FN;
@@ -87,9 +100,9 @@ struct DenseFeed {
 #pragma unroll
       for (int j = 0; j < FN; ++j) acc[i][j] = v16f{};
     // from here on the operands start at the tile
-    A.p += kAT ? m0 : m0 * A.ld;
+    A.p += at_row<kAT>(A, m0);
     A.extent -= m0;
-    B.p += kBT ? n0 : n0 * B.ld;
+    B.p += at_row<kBT>(B, n0);
     B.extent -= n0;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
@@ -99,11 +112,22 @@ struct DenseFeed {
     }
   }
 
-  // Source byte offset (from the operand's tile, its first K step) of this
-  // lane's 16 bytes of 1 KiB block b; past the extent: outside any resource.
-  template <int BX, bool kT>
+  // Elements from row 0 to row x (of the output; a tile's, so a multiple of 32).
+  template <int kT>
+  __device__ static inline int64_t at_row(const DenseOperand<T>& o, int x) {
+    return kT == kAlong ? x * o.ld : kT == kAcross ? int64_t(x) : x / 32 * o.step;
+  }
+
+  // Source byte offset (from the operand's tile and its K step) of this lane's
+  // 16 bytes of 1 KiB block b; past the extent: outside any resource.
+  template <int BX, int kT>
   __device__ inline int offset(const DenseOperand<T>& o, int b) const {
-    if constexpr (kT) {
+    if constexpr (kT == kPieces) {
+      // block b: 16 reduction rows of piece b / 2
+      return (b >> 1) * 32 < o.extent
+                 ? int((b >> 1) * o.step * int64_t(sizeof(T))) + (b & 1) * 1024 + lane * 16
+                 : kOut;
+    } else if constexpr (kT == kAcross) {
       constexpr int kChunks = BX * int(sizeof(T)) / 16;  // of a staged row
       const int row = b * (64 / kChunks) + lane / kChunks;
       const int at = lane % kChunks;  // physical piece
@@ -118,34 +142,35 @@ struct DenseFeed {
   }
   static constexpr int kOut = 0x7fffffff;
 
-  template <int BX, bool kT, int J0, int J1>
+  // Loads J0 .. J1 - 1 (blocks of one operand) of step kt. The resource starts at
+  // the step and ends with what of it lies inside k; a step past k has none.
+  template <int BX, int kT, int J0, int J1>
   __device__ inline void load(const DenseOperand<T>& o, int kt, uint8_t* dst) {
-    const int k0 = kt * kE;
-    if constexpr (kT) {
-      // the resource starts at the step's first reduction row and ends with its
-      // last one inside k, so rows past k read as zero (and a step past k has none:
-      // (left - 1) * ld + cols <= 0 there, as ld >= cols)
-      const int left = o.k - k0 < kE ? o.k - k0 : kE;
-      const int cols = o.extent < BX ? o.extent : BX;
-      const int ldb = int(o.ld * int64_t(sizeof(T)));
-      const int end = (left - 1) * ldb + cols * int(sizeof(T));
-      const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
-          const_cast<T*>(o.p + int64_t(k0) * o.ld), 0, end > 0 ? end : 0, kBufferFlags);
-#pragma unroll
-      for (int j = J0; j < J1; ++j) load_lds16(rs, dst + (j - J0) * kWaves * 1024, src_off[j]);
+    const int left = o.k - kt * kE < kE ? o.k - kt * kE : kE;  // of the reduction
+    const int most = o.extent < BX ? o.extent : BX;            // of the output
+    const int ldb = int(o.ld * int64_t(sizeof(T)));
+    const T* p;
+    int bytes;
+    bool in = true;  // this lane's pieces (the same of every block) lie inside k
+    if constexpr (kT == kAlong) {
+      p = o.p + kt * o.step;
+      bytes = (most - 1) * ldb + left * int(sizeof(T));
+      in = ((lane & 3) ^ swz<CPR>(lane >> 2, 0)) * 16 < left * int(sizeof(T));
+    } else if constexpr (kT == kAcross) {
+      // (left - 1) * ld + most <= 0 where left <= 0, as ld >= most
+      p = o.p + kt * kE * o.ld;
+      bytes = (left - 1) * ldb + most * int(sizeof(T));
     } else {
-      const int rows = o.extent < BX ? o.extent : BX;
-      const int bytes = int(((rows - 1) * o.ld + o.k) * int64_t(sizeof(T)));
-      const __amdgpu_buffer_rsrc_t rs =
-          __builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(o.p), 0, bytes, kBufferFlags);
-      // this lane's piece of the step (the same of every block) lies inside k
-      const int c = (lane & 3) ^ swz<CPR>(lane >> 2, 0);
-      const bool in = k0 * int(sizeof(T)) + c * 16 < o.k * int(sizeof(T));
-#pragma unroll
-      for (int j = J0; j < J1; ++j)
-        load_lds16(rs, dst + (j - J0) * kWaves * 1024,
-                   in && src_off[j] != kOut ? src_off[j] + k0 * int(sizeof(T)) : kOut);
+      p = o.p + int64_t(kt) * kE * 32;
+      bytes = (most - 1) / 32 * int(o.step * int64_t(sizeof(T))) + left * 64;
+      in = (wave & 1) * 16 + (lane >> 2) < left;  // kWaves is even: every block's rows
+      static_assert(kT != kPieces || kWaves % 2 == 0, "");
     }
+    const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<T*>(p), 0, left > 0 && bytes > 0 ? bytes : 0, kBufferFlags);
+#pragma unroll
+    for (int j = J0; j < J1; ++j)
+      load_lds16(rs, dst + (j - J0) * kWaves * 1024, in ? src_off[j] : kOut);
   }
 
   __device__ inline void dma(int kt, uint8_t* stage) {
@@ -157,9 +182,17 @@ struct DenseFeed {
   // byte `at` of the stage. (Every address is one offset from the stage's own
   // array: through longer chains the compiler loses which array a read is from
   // and waits for all loads in flight.)
-  template <int BX, bool kT>
+  template <int BX, int kT>
   __device__ inline Frag frag(const uint8_t* stage, int at, int x0, int kk) const {
-    if constexpr (!kT) {
+    if constexpr (kT == kPieces) {
+      const int g = lane >> 4, i = lane & 15;
+      const int row = kk * 16 + 8 * (g >> 1) + (i >> 2);
+      const int p = at + x0 * 64 + row * 64 + (16 * (g & 1) + (i & 3) * 4) * 2;
+      typedef __attribute__((address_space(3))) s16x4* lds_ptr;
+      const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(stage + p));
+      const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(stage + (p + 4 * 64)));
+      return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    } else if constexpr (kT == kAlong) {
       const int r = x0 + (lane & 31);
       const int c = kk * 2 + (lane >> 5);
       return *reinterpret_cast<const Frag*>(stage + (at + r * 64 + (swz<CPR>(r, c) << 4)));

@@ -108,7 +108,7 @@ struct HeadArgs {
 };
 
 // One (m, s) a row and wave, and the targets' logits.
-template <class C, class T, bool kBT>
+template <class C, class T, int kBT>
 __global__ __launch_bounds__(C::kThreads, C::kMinBlocks) void head_lse_kernel(HeadArgs<T> p) {
   constexpr int FM = C::FM, FN = C::FN;
   __shared__ __attribute__((aligned(16))) uint8_t st0[C::kStageBytes];
@@ -123,7 +123,7 @@ __global__ __launch_bounds__(C::kThreads, C::kMinBlocks) void head_lse_kernel(He
   int tm, tn;
   tile_of(xcd_run(blockIdx.x, tiles_m * tiles_n), tiles_m, tiles_n, tm, tn);
   const int m0 = tm * C::BM, n0 = tn * C::BN;
-  DenseFeed<C, T, false, kBT> f(p.X, p.W, m0, n0, wave, lane);
+  DenseFeed<C, T, kAlong, kBT> f(p.X, p.W, m0, n0, wave, lane);
   product_tile<C>(f, (p.H + kStepElems<T> - 1) / kStepElems<T>, st0, st1, st2, st3, st4);
 
   const int row0 = m0 + wm * FM * 32, col0 = n0 + wn * FN * 32;
@@ -203,9 +203,15 @@ __global__ __launch_bounds__(kJoinRows * 64) void head_join_kernel(
   loss[row] = t >= 0 && t < V ? l - tlogit[row] : 0.0f;
 }
 
+// bfloat16 G is kept in pieces of 32 columns, the rows of a piece together: the
+// order in which dX reads it along (kAlong, a K step's rows together) and dW
+// across (kPieces) in whole cache lines. float32 G is kept by rows.
+template <class T>
+constexpr bool kGPieces = sizeof(T) == 2;
+
 // G of a piece of the vocabulary over the largest |dloss|, zeros in the columns
-// that pad it to a multiple of 8.
-template <class C, class T, bool kBT>
+// that pad it to a multiple of 32 (float32: 8).
+template <class C, class T, int kBT>
 __global__ __launch_bounds__(C::kThreads, C::kMinBlocks) void head_grad_kernel(HeadArgs<T> p) {
   constexpr int FM = C::FM, FN = C::FN;
   __shared__ __attribute__((aligned(16))) uint8_t st0[C::kStageBytes];
@@ -220,7 +226,7 @@ __global__ __launch_bounds__(C::kThreads, C::kMinBlocks) void head_grad_kernel(H
   int tm, tn;
   tile_of(xcd_run(blockIdx.x, tiles_m * tiles_n), tiles_m, tiles_n, tm, tn);
   const int m0 = tm * C::BM, n0 = tn * C::BN;
-  DenseFeed<C, T, false, kBT> f(p.X, p.W, m0, n0, wave, lane);
+  DenseFeed<C, T, kAlong, kBT> f(p.X, p.W, m0, n0, wave, lane);
   product_tile<C>(f, (p.H + kStepElems<T> - 1) / kStepElems<T>, st0, st1, st2, st3, st4);
 
   const int row0 = m0 + wm * FM * 32, col0 = n0 + wn * FN * 32;
@@ -255,7 +261,7 @@ __global__ __launch_bounds__(C::kThreads, C::kMinBlocks) void head_grad_kernel(H
           if (fm * 32 + frag_row(r, lane) == l && fn * 32 + (lane & 31) == c)
             f.acc[fm][fn][r] -= 1.0f;
   }
-  // columns past the piece: the zeros that fill G's last 8
+  // columns past the piece: the zeros that pad G
 #pragma unroll
   for (int fn = 0; fn < FN; ++fn)
     if (col0 + fn * 32 + (lane & 31) >= p.V) {
@@ -264,12 +270,22 @@ __global__ __launch_bounds__(C::kThreads, C::kMinBlocks) void head_grad_kernel(H
 #pragma unroll
         for (int r = 0; r < 16; ++r) f.acc[fm][fn][r] = 0.0f;
     }
-  const int cols = (p.V + 7) & ~7;
-  emit_tile<C, kOutVec<T>>(st0, st1, st2, wave, lane, m0, n0,
-                           [&](int fm, int fn, int r) { return f.acc[fm][fn][r] * g[fm][r]; },
-                           [&](int gr, int gc, const float* v) {
-                             if (gr < p.T_) store_vec<false>(p.G + int64_t(gr) * p.ldg + gc, v, cols - gc, true);
-                           });
+  const int cols = kGPieces<T> ? (p.V + 31) & ~31 : (p.V + 7) & ~7;
+  emit_tile<C, kOutVec<T>>(
+      st0, st1, st2, wave, lane, m0, n0,
+      [&](int fm, int fn, int r) { return f.acc[fm][fn][r] * g[fm][r]; },
+      [&](int gr, int gc, const float* v) {
+        if (gr >= p.T_) return;
+        T* const dst = kGPieces<T> ? p.G + (gc / 32 * int64_t(p.T_) + gr) * 32 + gc % 32
+                                   : p.G + int64_t(gr) * p.ldg + gc;
+        store_vec<false>(dst, v, cols - gc, true);
+      });
+}
+
+// Elements from an operand's reduction element 0 to k0, a multiple of a K step.
+template <class C, class T, int kT>
+__device__ inline int64_t at_step(const DenseOperand<T>& o, int k0) {
+  return kT == kAlong ? k0 / kStepElems<T> * o.step : kT == kAcross ? k0 * o.ld : int64_t(k0) * 32;
 }
 
 // A product of two operands, or of slice blockIdx.z of their reduction. kAdd: into
@@ -287,7 +303,7 @@ struct ProductArgs {
   const float* scale;  // of the result (not of the slices' arrays)
 };
 
-template <class C, class T, bool kAT, bool kBT, class Out, bool kAdd>
+template <class C, class T, int kAT, int kBT, class Out, bool kAdd>
 __global__ __launch_bounds__(C::kThreads, C::kMinBlocks) void head_product_kernel(
     ProductArgs<T, Out> p) {
   __shared__ __attribute__((aligned(16))) uint8_t st0[C::kStageBytes];
@@ -303,8 +319,8 @@ __global__ __launch_bounds__(C::kThreads, C::kMinBlocks) void head_product_kerne
   const int m0 = tm * C::BM, n0 = tn * C::BN;
   const int k0 = blockIdx.z * p.k_slice;
   DenseOperand<T> A = p.A, B = p.B;
-  A.p += kAT ? k0 * A.ld : k0;
-  B.p += kBT ? k0 * B.ld : k0;
+  A.p += at_step<C, T, kAT>(A, k0);
+  B.p += at_step<C, T, kBT>(B, k0);
   A.k = A.k - k0 < p.k_slice ? A.k - k0 : p.k_slice;
   B.k = B.k - k0 < p.k_slice ? B.k - k0 : p.k_slice;
   // (one of the two may be filled up to a multiple of 8 with zeros; the other
@@ -383,7 +399,8 @@ struct PackArgs {
   const T* src;
   int64_t R, C, ld;  // R = 0: no copy
   T* dst;
-  int64_t ldp;  // a multiple of 8; zeros from the C-th element on
+  int64_t ldp;   // a multiple of 8 (steps: of 32); zeros from the C-th element on
+  int steps;     // the rows of 32 columns together (kAlong's second form), not rows of ldp
   int blocks;
 };
 
@@ -406,17 +423,55 @@ __device__ inline void pack(const PackArgs<T>& p, int block) {
     __attribute__((aligned(16))) T v[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = c + j < p.C ? p.src[row * p.ld + c + j] : T(0);
+    T* const dst = p.dst + row * p.ldp + c;
 #pragma unroll
     for (int j = 0; j < 8 * int(sizeof(T)); j += 16)
-      *reinterpret_cast<uint4*>(reinterpret_cast<char*>(p.dst + row * p.ldp + c) + j) =
+      *reinterpret_cast<uint4*>(reinterpret_cast<char*>(dst) + j) =
           *reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(v) + j);
+  }
+}
+
+// The same with the rows of 32 columns together (bfloat16): a wave takes 16 rows,
+// four lanes each, and four steps of them at a time, so that it reads 256 bytes of
+// a row and writes 1 KiB in one piece.
+__device__ inline void pack_steps(const PackArgs<uint16_t>& p, int block) {
+  const int lane = threadIdx.x & 63;
+  const int64_t quads = (p.ldp / 32 + 3) / 4, tiles = (p.R + 15) / 16 * quads;
+  const bool fast = reinterpret_cast<uintptr_t>(p.src) % 16 == 0 && p.ld % 8 == 0 && p.C % 8 == 0;
+  for (int64_t t = int64_t(block) * 4 + (threadIdx.x >> 6); t < tiles; t += int64_t(p.blocks) * 4) {
+    const int64_t r0 = t / quads * 16, s0 = (t - t / quads * quads) * 4;
+    const int64_t row = r0 + (lane >> 2);
+    if (row >= p.R) continue;
+    Vec8<BF16In> v[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int64_t c = (s0 + u) * 32 + (lane & 3) * 8;
+      if (fast)
+        load_chunk<BF16In, true>(p.src + row * p.ld, c, p.C, v[u]);
+      else
+        load_chunk<BF16In, false>(p.src + row * p.ld, c, p.C, v[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      if ((s0 + u) * 32 >= p.ldp) break;
+      uint4 o;
+      o.x = v[u].v[0] | uint32_t(v[u].v[1]) << 16;
+      o.y = v[u].v[2] | uint32_t(v[u].v[3]) << 16;
+      o.z = v[u].v[4] | uint32_t(v[u].v[5]) << 16;
+      o.w = v[u].v[6] | uint32_t(v[u].v[7]) << 16;
+      *reinterpret_cast<uint4*>(p.dst + ((s0 + u) * p.R + row) * 32 + (lane & 3) * 8) = o;
+    }
   }
 }
 
 template <class T>
 __global__ __launch_bounds__(256) void head_prepare_kernel(PrepareArgs<T> p) {
   const int b = blockIdx.x;
-  if (b < p.x.blocks) return pack(p.x, b);
+  if (b < p.x.blocks) {
+    if constexpr (sizeof(T) == 2)
+      if (p.x.steps) return pack_steps(p.x, b);
+    return pack(p.x, b);
+  }
   if (b < p.x.blocks + p.w.blocks) return pack(p.w, b - p.x.blocks);
   __shared__ float sh[4];
   float m = 0.0f;
@@ -453,6 +508,7 @@ constexpr int64_t kCUs = 256;
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t round8(int64_t n) { return (n + 7) / 8 * 8; }
+int64_t round32(int64_t n) { return (n + 31) / 32 * 32; }
 int64_t round_256(int64_t n) { return (n + 255) / 256 * 256; }
 
 unsigned copy_blocks(int64_t threads) {
@@ -522,21 +578,25 @@ hipError_t with_tile(Tile t, F&& f) {
 
 }  // namespace
 
-HeadPlan head_plan(bool bf16, int64_t T, int64_t H, int64_t V, bool by_vocab, int64_t ldx,
-                   int64_t ldw) {
+HeadPlan head_plan(bool bf16, bool backward, int64_t T, int64_t H, int64_t V, bool by_vocab,
+                   int64_t ldx, int64_t ldw) {
   const int64_t esz = bf16 ? 2 : 4;
   HeadPlan h{};
   h.pack_x = H % 8 != 0 || (ldx * esz) % 16 != 0;
   h.pack_w = (by_vocab ? H : V) % 8 != 0 || (ldw * esz) % 16 != 0;
+  // bfloat16: X with a K step's rows together, for the logits of more than a few
+  // rows and as dW's operand
+  h.step_x = bf16 && (backward || T > 64);
+  h.pack_x = h.pack_x && !h.step_x;
   h.ldx = h.pack_x ? round8(H) : ldx;
   h.ldw = h.pack_w ? round8(by_vocab ? H : V) : ldw;
-  h.x_bytes = h.pack_x ? T * h.ldx * esz : 0;
+  h.x_bytes = h.step_x ? T * round32(H) * esz : h.pack_x ? T * h.ldx * esz : 0;
   h.w_bytes = h.pack_w ? (by_vocab ? V : H) * h.ldw * esz : 0;
   const Tile t = pick_tile(bf16, T, V);
   h.parts = ceil_div(V, tile_cols(t)) * (tile_cols(t) / wave_cols(t));
   const int64_t pieces = ceil_div(T * V * esz, kPieceBytes);
   h.piece = pieces > 1 ? round_256(ceil_div(V, pieces)) : V;
-  h.ldg = round8(h.piece);
+  h.ldg = bf16 ? round32(h.piece) : round8(h.piece);
   const Tile tx = dx_tile(bf16, T, H, h.piece);
   h.slices = dx_slices(tx, T, H, h.piece);
   h.ldp = round8(H);
@@ -547,18 +607,23 @@ namespace {
 
 // X and W as the products take them, packed where they have to be; with dloss,
 // its largest besides.
+// X and W as the products take them, copied where they have to be; for the
+// backward the largest |dloss| besides. X: as the logits read it.
 template <class T>
 hipError_t prepare(const HeadCall& c, const HeadPlan& h, bool backward, DenseOperand<T>* X,
                    const T** W, hipStream_t stream) {
   const T* const x = static_cast<const T*>(c.X);
   const T* const w = static_cast<const T*>(c.W);
+  T* const xc = static_cast<T*>(c.packed_x);
   const int64_t wr = c.by_vocab ? c.V : c.H, wc = c.by_vocab ? c.H : c.V;
   PrepareArgs<T> p{};
-  if (h.pack_x && c.T > 0)
-    p.x = PackArgs<T>{x, c.T, c.H, c.ldx, static_cast<T*>(c.packed_x), h.ldx,
-                      int(copy_blocks(c.T * (h.ldx / 8)))};
+  if (h.step_x && c.T > 0)
+    p.x = PackArgs<T>{x, c.T, c.H, c.ldx, xc, round32(c.H), 1,
+                      int(copy_blocks(ceil_div(c.T, 16) * ceil_div(c.H, 128) * 64))};
+  else if (h.pack_x && c.T > 0)
+    p.x = PackArgs<T>{x, c.T, c.H, c.ldx, xc, h.ldx, 0, int(copy_blocks(c.T * (h.ldx / 8)))};
   if (h.pack_w)
-    p.w = PackArgs<T>{w, wr, wc, c.ldw, static_cast<T*>(c.packed_w), h.ldw,
+    p.w = PackArgs<T>{w, wr, wc, c.ldw, static_cast<T*>(c.packed_w), h.ldw, 0,
                       int(copy_blocks(wr * (h.ldw / 8)))};
   p.dloss = c.dloss;
   p.target = c.target;
@@ -567,11 +632,20 @@ hipError_t prepare(const HeadCall& c, const HeadPlan& h, bool backward, DenseOpe
   p.top = c.top;
   const int blocks = p.x.blocks + p.w.blocks + (backward ? 1 : 0);
   if (blocks > 0) head_prepare_kernel<T><<<unsigned(blocks), 256, 0, stream>>>(p);
-  // the reduction of the logits, with its zeros
-  *X = DenseOperand<T>{h.pack_x ? static_cast<const T*>(c.packed_x) : x, h.ldx, int(c.T),
-                       int(round8(c.H))};
+  constexpr int kE = kStepElems<T>;
+  *X = h.step_x ? DenseOperand<T>{xc, kE, c.T * kE, int(c.T), int(round32(c.H))}
+                : DenseOperand<T>{h.pack_x ? xc : x, h.ldx, kE, int(c.T), int(round8(c.H))};
   *W = h.pack_w ? static_cast<const T*>(c.packed_w) : w;
   return hipGetLastError();
+}
+
+// Columns v0 .. v0 + n - 1 of the vocabulary as the logits read W's.
+template <class T>
+DenseOperand<T> weight_columns(const HeadCall& c, const HeadPlan& h, const T* W, int64_t v0,
+                               int64_t n) {
+  if (c.by_vocab)
+    return DenseOperand<T>{W + v0 * h.ldw, h.ldw, kStepElems<T>, int(n), int(round8(c.H))};
+  return DenseOperand<T>{W + v0, h.ldw, 0, int(round8(n)), int(c.H)};
 }
 
 template <class T, bool kGrad>
@@ -583,31 +657,26 @@ hipError_t logits(Tile t, bool by_vocab, const HeadArgs<T>& a, hipStream_t strea
     const dim3 grid(unsigned(tiles), 1, 1);
     if constexpr (kGrad) {
       if (by_vocab)
-        head_grad_kernel<C, T, false><<<grid, C::kThreads, 0, stream>>>(a);
+        head_grad_kernel<C, T, kAlong><<<grid, C::kThreads, 0, stream>>>(a);
       else
-        head_grad_kernel<C, T, true><<<grid, C::kThreads, 0, stream>>>(a);
+        head_grad_kernel<C, T, kAcross><<<grid, C::kThreads, 0, stream>>>(a);
     } else {
       if (by_vocab)
-        head_lse_kernel<C, T, false><<<grid, C::kThreads, 0, stream>>>(a);
+        head_lse_kernel<C, T, kAlong><<<grid, C::kThreads, 0, stream>>>(a);
       else
-        head_lse_kernel<C, T, true><<<grid, C::kThreads, 0, stream>>>(a);
+        head_lse_kernel<C, T, kAcross><<<grid, C::kThreads, 0, stream>>>(a);
     }
     return hipGetLastError();
   });
 }
 
-template <class T, bool kAT, bool kBT, class Out, bool kAdd>
+template <class T, int kAT, int kBT, class Out, bool kAdd>
 hipError_t product(Tile t, const ProductArgs<T, Out>& a, int64_t slices, hipStream_t stream) {
   return with_tile<T>(t, [&](auto c) -> hipError_t {
     using C = decltype(c);
-    // bfloat16 read across its rows: the swizzle needs four 64-byte segments a row
-    if constexpr (kAT && sizeof(T) == 2 && C::BM < 128) {
-      return hipErrorInvalidValue;
-    } else {
-      const dim3 grid(unsigned(tiles_of(t, a.M, a.N)), 1, unsigned(slices));
-      head_product_kernel<C, T, kAT, kBT, Out, kAdd><<<grid, C::kThreads, 0, stream>>>(a);
-      return hipGetLastError();
-    }
+    const dim3 grid(unsigned(tiles_of(t, a.M, a.N)), 1, unsigned(slices));
+    head_product_kernel<C, T, kAT, kBT, Out, kAdd><<<grid, C::kThreads, 0, stream>>>(a);
+    return hipGetLastError();
   });
 }
 
@@ -619,10 +688,10 @@ hipError_t run_forward(const HeadCall& c, const HeadPlan& h, hipStream_t stream)
   if (e != hipSuccess) return e;
   HeadArgs<T> a{};
   a.X = X;
-  a.W = DenseOperand<T>{W, h.ldw, int(c.by_vocab ? c.V : round8(c.V)), int(c.by_vocab ? X.k : c.H)};
+  a.W = weight_columns(c, h, W, 0, c.V);
   a.T_ = int(c.T);
   a.V = a.Vall = int(c.V);
-  a.H = X.k;
+  a.H = int(c.H);
   a.target = c.target;
   a.part = static_cast<float2*>(c.part);
   a.parts = int(h.parts);
@@ -647,52 +716,59 @@ hipError_t run_backward(const HeadCall& c, const HeadPlan& h, hipStream_t stream
   for (int64_t v0 = 0; v0 < c.V; v0 += h.piece) {
     const int64_t n = c.V - v0 < h.piece ? c.V - v0 : h.piece;
     const int n8 = int(round8(n));
+    T* const G = static_cast<T*>(c.G);
     if (c.T > 0) {
       HeadArgs<T> a{};
       a.X = X;
-      a.W = DenseOperand<T>{W + v0 * (c.by_vocab ? h.ldw : 1), h.ldw, c.by_vocab ? int(n) : n8,
-                            int(c.by_vocab ? X.k : c.H)};
+      a.W = weight_columns(c, h, W, v0, n);
       a.T_ = int(c.T);
       a.V = int(n);
       a.Vall = int(c.V);
-      a.H = X.k;
+      a.H = int(c.H);
       a.v0 = int(v0);
       a.target = c.target;
       a.lse = c.lse;
       a.dloss = c.dloss;
       a.top = c.top;
-      a.G = static_cast<T*>(c.G);
+      a.G = G;
       a.ldg = h.ldg;
       e = logits<T, true>(pick_tile(kBf16, c.T, n), c.by_vocab, a, stream);
       if (e != hipSuccess) return e;
 
-      // dX: G (T x n) times W's piece; the columns that fill n to n8 are zeros in
-      // G and, where W is read along them, in W
-      const DenseOperand<T> G{a.G, h.ldg, int(c.T), n8};
+      // dX: G (T x n) times W's piece transposed; the columns that fill n to n8 are
+      // zeros in G and, where W is read along them, in W
+      constexpr int kE = kStepElems<T>;
+      const DenseOperand<T> A = kGPieces<T> ? DenseOperand<T>{G, kE, c.T * kE, int(c.T), n8}
+                                            : DenseOperand<T>{G, h.ldg, kE, int(c.T), n8};
+      const DenseOperand<T> B =
+          c.by_vocab ? DenseOperand<T>{a.W.p, h.ldw, 0, int(round8(c.H)), int(n)}
+                     : DenseOperand<T>{a.W.p, h.ldw, kE, int(c.H), n8};
       const int64_t per = ceil_div(ceil_div(n, h.slices), 64) * 64;
-      const DenseOperand<T> B{a.W.p, h.ldw, c.by_vocab ? X.k : int(c.H), c.by_vocab ? int(n) : n8};
       if (direct) {
-        const ProductArgs<T, T> q{G, B, int(c.T), int(c.H), n8, static_cast<T*>(c.dX), c.lddx, 0, 1,
+        const ProductArgs<T, T> q{A, B, int(c.T), int(c.H), n8, static_cast<T*>(c.dX), c.lddx, 0, 1,
                                   c.top};
-        e = c.by_vocab ? product<T, false, true, T, false>(tx, q, 1, stream)
-                       : product<T, false, false, T, false>(tx, q, 1, stream);
+        e = c.by_vocab ? product<T, kAlong, kAcross, T, false>(tx, q, 1, stream)
+                       : product<T, kAlong, kAlong, T, false>(tx, q, 1, stream);
       } else {
-        const ProductArgs<T, float> q{G, B, int(c.T), int(c.H), int(per), c.acc, h.ldp,
+        const ProductArgs<T, float> q{A, B, int(c.T), int(c.H), int(per), c.acc, h.ldp,
                                       c.T * h.ldp, v0 == 0, nullptr};
-        e = c.by_vocab ? product<T, false, true, float, true>(tx, q, h.slices, stream)
-                       : product<T, false, false, float, true>(tx, q, h.slices, stream);
+        e = c.by_vocab ? product<T, kAlong, kAcross, float, true>(tx, q, h.slices, stream)
+                       : product<T, kAlong, kAlong, float, true>(tx, q, h.slices, stream);
       }
       if (e != hipSuccess) return e;
     }
-    // dW's piece: X^T G (H x n) or G^T X (n x H)
-    const DenseOperand<T> Gt{static_cast<const T*>(c.G), h.ldg, n8, int(c.T)};
-    const DenseOperand<T> Xt{X.p, h.ldx, X.k, int(c.T)};
+    // dW's piece: X^T G (H x n) or G^T X (n x H), reduction over the rows
     const int64_t rows = c.by_vocab ? n : c.H, cols = c.by_vocab ? c.H : n;
-    // (A is read across its rows here: bfloat16 at least 128 rows a tile, see product)
-    const Tile tw = pick_tile(kBf16, kBf16 && rows <= 64 ? 65 : rows, cols);
+    constexpr int kAcrossRows = kGPieces<T> ? kPieces : kAcross;
+    const DenseOperand<T> Gt = kGPieces<T>
+                                   ? DenseOperand<T>{G, 0, c.T * 32, int(round32(n)), int(c.T)}
+                                   : DenseOperand<T>{G, h.ldg, 0, n8, int(c.T)};
+    const DenseOperand<T> Xt =
+        kGPieces<T> ? DenseOperand<T>{X.p, 0, c.T * 32, int(round32(c.H)), int(c.T)}
+                    : DenseOperand<T>{X.p, X.ld, 0, int(round8(c.H)), int(c.T)};
     const ProductArgs<T, T> q{c.by_vocab ? Gt : Xt, c.by_vocab ? Xt : Gt, int(rows), int(cols),
                               int(c.T), dW + v0 * (c.by_vocab ? c.lddw : 1), c.lddw, 0, 1, c.top};
-    e = product<T, true, true, T, false>(tw, q, 1, stream);
+    e = product<T, kAcrossRows, kAcrossRows, T, false>(pick_tile(kBf16, rows, cols), q, 1, stream);
     if (e != hipSuccess) return e;
   }
   if (direct || c.T == 0) return hipSuccess;

@@ -126,6 +126,7 @@ hipError_t launch_experts_wgrad(const uint8_t* Aq, const uint8_t* As, const uint
 // Head loss (head.hip). The plan follows from sizes and strides alone.
 struct HeadPlan {
   bool pack_x, pack_w;       // operands copied into the workspace, padded
+  bool step_x;               // X copied with a K step's rows together
   int64_t ldx, ldw;          // row strides the products use
   int64_t x_bytes, w_bytes;  // of the copies
   int64_t parts;             // (m, s) pairs a row
@@ -133,8 +134,8 @@ struct HeadPlan {
   int64_t ldg;               // row stride of G
   int64_t slices, ldp;       // dX: reduction slices, row stride of their arrays
 };
-HeadPlan head_plan(bool bf16, int64_t T, int64_t H, int64_t V, bool by_vocab, int64_t ldx,
-                   int64_t ldw);
+HeadPlan head_plan(bool bf16, bool backward, int64_t T, int64_t H, int64_t V, bool by_vocab,
+                   int64_t ldx, int64_t ldw);
 
 struct HeadCall {
   const void *X, *W;
