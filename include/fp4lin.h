@@ -468,14 +468,16 @@ fp4lin_status fp4lin_experts_wgrad_mx(const void* A, const void* dY, fp4lin_dtyp
  *            FP4LIN_HEAD_HIDDEN_MAJOR, in-features x out-features) or V x H
  *            (FP4LIN_HEAD_VOCAB_MAJOR, as an embedding shares it)
  *   target   device, T int32. A target outside [0, V) leaves its row out: loss
- *            0, no gradient. (lse is that of the row's logits all the same.)
+ *            0 and no part in the gradients, whatever X and dloss hold there.
+ *            (lse is that of the row's logits all the same.)
  * X, W and the workspace must be 16-byte aligned; any sizes and leading
  * dimensions (where a row of X or W is not a multiple of 8 elements or its
  * stride not one of 16 bytes, a padded copy is kept in the workspace; so is a
- * copy of bfloat16 X in the order of the products).
+ * copy of X in the order of the products, by the backward always).
  * T = 0 is a valid batch (a weight gradient is all zeros). Sums are fp32; in
- * the backward G, over the largest |dloss| of the rows that count, is rounded to
- * dt before the two products that take it.
+ * the backward G, over the largest finite |dloss| of the rows that count, is
+ * rounded to dt before the two products that take it. An infinity or NaN among a
+ * row's logits makes its loss NaN, and of the gradients the row's dX and all dW.
  * Limits: T <= 2^22, and 256 * ld * element size < 2^31 for the leading
  * dimensions of X and W. */
 typedef enum { FP4LIN_HEAD_HIDDEN_MAJOR = 0, FP4LIN_HEAD_VOCAB_MAJOR = 1 } fp4lin_head_layout;

@@ -27,7 +27,9 @@
 // for bit.
 //
 // Operands whose rows do not start on 16 bytes or whose contiguous size is not a
-// multiple of 8 elements are first copied, padded with zeros.
+// multiple of 8 elements are first copied, padded with zeros. The backward always
+// takes a copy of X, in which the rows that are left out are zero: what they hold,
+// infinities and NaN included, reaches no gradient.
 #include <type_traits>
 
 #include "dense_core.hpp"
@@ -102,7 +104,7 @@ struct HeadArgs {
   // backward
   const float* lse;
   const float* dloss;
-  const float* top;  // largest |dloss| of the rows that count
+  const float* top;  // G's scale, see head_prepare_kernel
   T* G;
   int64_t ldg;
 };
@@ -230,7 +232,7 @@ __global__ __launch_bounds__(C::kThreads, C::kMinBlocks) void head_grad_kernel(H
   product_tile<C>(f, (p.H + kStepElems<T> - 1) / kStepElems<T>, st0, st1, st2, st3, st4);
 
   const int row0 = m0 + wm * FM * 32, col0 = n0 + wn * FN * 32;
-  float g[FM][16];  // dloss of this lane's rows over the largest, 0 where the row is left out
+  float g[FM][16];  // dloss of this lane's rows over the largest
   const float top = *p.top;
 #pragma unroll
   for (int fm = 0; fm < FM; ++fm)
@@ -240,9 +242,13 @@ __global__ __launch_bounds__(C::kThreads, C::kMinBlocks) void head_grad_kernel(H
       const int at = row < p.T_ ? row : p.T_ - 1;
       const float lse = p.lse[at];
       const int t = p.target[at];
-      g[fm][r] = t >= 0 && t < p.Vall && top != 0.0f ? p.dloss[at] / top : 0.0f;
+      g[fm][r] = p.dloss[at] / top;
+      // a row that is left out: zeros, whatever its lse and dloss
+      const bool out = t < 0 || t >= p.Vall;
+      if (out) g[fm][r] = 0.0f;
 #pragma unroll
-      for (int fn = 0; fn < FN; ++fn) f.acc[fm][fn][r] = exp_diff(f.acc[fm][fn][r], lse);
+      for (int fn = 0; fn < FN; ++fn)
+        f.acc[fm][fn][r] = out ? 0.0f : exp_diff(f.acc[fm][fn][r], lse);
     }
   // the one-hot part, as in head_lse_kernel
   const int trow = row0 + lane;
@@ -391,23 +397,32 @@ __global__ __launch_bounds__(256) void head_sum_kernel(const float* __restrict__
   }
 }
 
-// What the products need first, in one launch: padded copies of X and W where
-// they have to be, and for the backward the largest |dloss| of the rows whose
-// target lies in the vocabulary (the last workgroup).
+// What the products need first, in one launch: copies of X and W where they have
+// to be, and for the backward the largest finite |dloss| of the rows whose target
+// lies in the vocabulary, 1 if that is 0 (the last workgroup). An infinite dloss is
+// left to its own row: as the scale it would make NaN of the others' zeros.
 template <class T>
 struct PackArgs {
   const T* src;
-  int64_t R, C, ld;  // R = 0: no copy
+  int64_t R, C, ld;
   T* dst;
   int64_t ldp;   // a multiple of 8 (steps: of 32); zeros from the C-th element on
   int steps;     // the rows of 32 columns together (kAlong's second form), not rows of ldp
-  int blocks;
+  int blocks;    // 0: no copy
+  const int32_t* target;  // not NULL: zeros in the rows whose target is not in [0, V)
+  int V;
+
+  __device__ int64_t columns(int64_t row) const {
+    if (target == nullptr) return C;
+    const int t = target[row];
+    return t >= 0 && t < V ? C : 0;
+  }
 };
 
 template <class T>
 struct PrepareArgs {
   PackArgs<T> x, w;
-  const float* dloss;  // NULL in the forward
+  const float* dloss;
   const int32_t* target;
   int T_, V;
   float* top;
@@ -419,10 +434,10 @@ __device__ inline void pack(const PackArgs<T>& p, int block) {
   const int64_t groups = p.ldp / 8;
   for (int64_t i = int64_t(block) * 256 + threadIdx.x; i < p.R * groups;
        i += int64_t(p.blocks) * 256) {
-    const int64_t row = i / groups, c = (i - row * groups) * 8;
+    const int64_t row = i / groups, c = (i - row * groups) * 8, C = p.columns(row);
     __attribute__((aligned(16))) T v[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = c + j < p.C ? p.src[row * p.ld + c + j] : T(0);
+    for (int j = 0; j < 8; ++j) v[j] = c + j < C ? p.src[row * p.ld + c + j] : T(0);
     T* const dst = p.dst + row * p.ldp + c;
 #pragma unroll
     for (int j = 0; j < 8 * int(sizeof(T)); j += 16)
@@ -442,14 +457,15 @@ __device__ inline void pack_steps(const PackArgs<uint16_t>& p, int block) {
     const int64_t r0 = t / quads * 16, s0 = (t - t / quads * quads) * 4;
     const int64_t row = r0 + (lane >> 2);
     if (row >= p.R) continue;
+    const int64_t C = p.columns(row);
     Vec8<BF16In> v[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const int64_t c = (s0 + u) * 32 + (lane & 3) * 8;
       if (fast)
-        load_chunk<BF16In, true>(p.src + row * p.ld, c, p.C, v[u]);
+        load_chunk<BF16In, true>(p.src + row * p.ld, c < C ? c : p.C, p.C, v[u]);
       else
-        load_chunk<BF16In, false>(p.src + row * p.ld, c, p.C, v[u]);
+        load_chunk<BF16In, false>(p.src + row * p.ld, c, C, v[u]);
     }
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
@@ -487,12 +503,15 @@ __global__ __launch_bounds__(256) void head_prepare_kernel(PrepareArgs<T> p) {
     }
 #pragma unroll
     for (int u = 0; u < U; ++u)
-      if (t[u] >= 0 && t[u] < p.V) m = fmaxf(m, fabsf(g[u]));
+      if (t[u] >= 0 && t[u] < p.V && fabsf(g[u]) < __builtin_huge_valf()) m = fmaxf(m, fabsf(g[u]));
   }
   m = wave_max(m);
   if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = m;
   __syncthreads();
-  if (threadIdx.x == 0) *p.top = fmaxf(fmaxf(sh[0], sh[1]), fmaxf(sh[2], sh[3]));
+  if (threadIdx.x == 0) {
+    m = fmaxf(fmaxf(sh[0], sh[1]), fmaxf(sh[2], sh[3]));
+    *p.top = m != 0.0f ? m : 1.0f;
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -582,7 +601,7 @@ HeadPlan head_plan(bool bf16, bool backward, int64_t T, int64_t H, int64_t V, bo
                    int64_t ldx, int64_t ldw) {
   const int64_t esz = bf16 ? 2 : 4;
   HeadPlan h{};
-  h.pack_x = H % 8 != 0 || (ldx * esz) % 16 != 0;
+  h.pack_x = backward || H % 8 != 0 || (ldx * esz) % 16 != 0;
   h.pack_w = (by_vocab ? H : V) % 8 != 0 || (ldw * esz) % 16 != 0;
   // bfloat16: X with a K step's rows together, for the logits of more than a few
   // rows and as dW's operand
@@ -605,8 +624,6 @@ HeadPlan head_plan(bool bf16, bool backward, int64_t T, int64_t H, int64_t V, bo
 
 namespace {
 
-// X and W as the products take them, packed where they have to be; with dloss,
-// its largest besides.
 // X and W as the products take them, copied where they have to be; for the
 // backward the largest |dloss| besides. X: as the logits read it.
 template <class T>
@@ -619,12 +636,17 @@ hipError_t prepare(const HeadCall& c, const HeadPlan& h, bool backward, DenseOpe
   PrepareArgs<T> p{};
   if (h.step_x && c.T > 0)
     p.x = PackArgs<T>{x, c.T, c.H, c.ldx, xc, round32(c.H), 1,
-                      int(copy_blocks(ceil_div(c.T, 16) * ceil_div(c.H, 128) * 64))};
+                      int(copy_blocks(ceil_div(c.T, 16) * ceil_div(c.H, 128) * 64)), nullptr, 0};
   else if (h.pack_x && c.T > 0)
-    p.x = PackArgs<T>{x, c.T, c.H, c.ldx, xc, h.ldx, 0, int(copy_blocks(c.T * (h.ldx / 8)))};
+    p.x = PackArgs<T>{x, c.T, c.H, c.ldx, xc, h.ldx, 0, int(copy_blocks(c.T * (h.ldx / 8))),
+                      nullptr, 0};
+  if (backward) {
+    p.x.target = c.target;
+    p.x.V = int(c.V);
+  }
   if (h.pack_w)
     p.w = PackArgs<T>{w, wr, wc, c.ldw, static_cast<T*>(c.packed_w), h.ldw, 0,
-                      int(copy_blocks(wr * (h.ldw / 8)))};
+                      int(copy_blocks(wr * (h.ldw / 8))), nullptr, 0};
   p.dloss = c.dloss;
   p.target = c.target;
   p.T_ = int(c.T);

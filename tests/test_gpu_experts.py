@@ -228,6 +228,40 @@ def test_experts_row_end_is_clamped(ql, M):
             assert_within(dW[e], want, mag, M, False, f"dW of expert {e}")
 
 
+@pytest.mark.parametrize("M", [16, 300])
+def test_experts_rows_keep_to_themselves(ql, M):
+    """Infinities and NaN past the last expert's end reach nothing, those of one
+    expert's rows none of the others' results."""
+    K, N = 256, 130
+    rng = np.random.default_rng(M + 1)
+    A = wl.random_matrix(rng, M, K, wl.F32)
+    dY = wl.random_matrix(rng, M, N, wl.F32)
+    W = [wl.random_matrix(rng, K, N, wl.F32, scale=0.02) for _ in range(3)]
+    ends = [M // 4, M // 4 + 5, M - 3]
+    Ad, dYd, Wd, re = to_device(A), to_device(dY), stack3(W, wl.F32), upload_ends(ends)
+    Wq, Ws = ql.experts_quantize_weight_mx(Wd)
+
+    def all_of():
+        return (ql.experts_forward_mx(Ad, Wd, re), ql.experts_apply_mx(Ad, Wq, Ws, re),
+                ql.experts_dgrad_mx(dYd, Wd, re), ql.experts_wgrad_mx(Ad, dYd, re))
+
+    want = [host(x) for x in all_of()]
+    for bad in (float("nan"), float("inf"), -float("inf")):
+        log(f"experts {M} rows, {bad} past the last end, then in one expert")
+        Ad[ends[2]:], dYd[ends[2]:] = bad, bad
+        for name, x, y in zip(("Y", "Y applied", "dX", "dW"), all_of(), want):
+            assert_bits_equal(host(x), y, name)
+        saved = Ad[ends[0]:ends[1]].clone(), dYd[ends[0]:ends[1]].clone()
+        Ad[ends[0]:ends[1]], dYd[ends[0]:ends[1]] = bad, bad
+        *rows, dW = (host(x) for x in all_of())
+        for name, x, y in zip(("Y", "Y applied", "dX"), rows, want):
+            assert_bits_equal(x[:ends[0]], y[:ends[0]], name)
+            assert_bits_equal(x[ends[1]:], y[ends[1]:], name)
+        for e in (0, 2):
+            assert_bits_equal(dW[e], want[3][e], f"dW of expert {e}")
+        Ad[ends[0]:ends[1]], dYd[ends[0]:ends[1]] = saved
+
+
 def test_experts_no_rows(ql):
     """A batch without rows: empty outputs, a zero weight gradient."""
     t = torch()

@@ -191,6 +191,62 @@ def test_head_loss_left_out_rows(ql, dtype):
     assert_bits_equal(host(none["lse"]), host(full["lse"]), "lse")
 
 
+@pytest.mark.parametrize("by_vocab", [False, True], ids=["HxV", "VxH"])
+@pytest.mark.parametrize("H", [72, 67])
+@pytest.mark.parametrize("dtype", [wl.F32, wl.BF16])
+def test_head_loss_left_out_rows_hold_anything(ql, dtype, H, by_vocab):
+    """Infinities and NaN in X and dloss of rows that are left out: the losses and
+    gradients are bit for bit those with finite numbers there."""
+    T, V = 140, 333
+    X, W, target, dloss = inputs(T, H, V, dtype, seed=7)
+    target[1::4] = [-1, V] * 17 + [-100]
+    out = (target < 0) | (target >= V)
+    log(f"head loss {dtype}: {out.sum()} rows of infinities and NaN left out")
+    want = run(ql, X, W, target, dloss, by_vocab)
+    t = torch()
+    rows = t.from_numpy(np.nonzero(out)[0]).to("cuda:0")
+    Xd, Wd = to_device(X).clone(), to_device(W)
+    Wd = Wd.t().contiguous() if by_vocab else Wd
+    gd, td = t.from_numpy(dloss).to("cuda:0"), t.from_numpy(target).to("cuda:0")
+    for bad in (float("nan"), float("inf"), -float("inf")):
+        Xd[rows] = bad
+        gd[rows] = bad
+        loss, lse = ql.head_loss(Xd, Wd, td, by_vocab=by_vocab)
+        dX, dW = ql.head_loss_backward(Xd, Wd, td, lse, gd, by_vocab=by_vocab)
+        dW = dW.t().contiguous() if by_vocab else dW
+        assert_bits_equal(host(loss), host(want["loss"]), "loss")
+        assert_bits_equal(host(lse)[~out], host(want["lse"])[~out], "lse")
+        assert_bits_equal(host(dX), host(want["dX"]), "dX")
+        assert_bits_equal(host(dW), host(want["dW"]), "dW")
+
+
+@pytest.mark.parametrize("dtype", [wl.F32, wl.BF16])
+def test_head_loss_rows_keep_to_themselves(ql, dtype):
+    """A NaN row of X and an infinite dloss that count: NaN in that row's loss
+    and dX and in dW, and every other row's loss and dX as without them."""
+    T, H, V = 70, 40, 300
+    X, W, target, dloss = inputs(T, H, V, dtype, seed=9)
+    dloss[:] = 0.5
+    want = run(ql, X, W, target, dloss, False)
+    t = torch()
+    Xd, Wd = to_device(X).clone(), to_device(W)
+    gd, td = t.from_numpy(dloss).to("cuda:0"), t.from_numpy(target).to("cuda:0")
+    Xd[5] = float("nan")
+    gd[33] = float("inf")
+    log(f"head loss {dtype}: a NaN row and an infinite weight")
+    loss, lse = ql.head_loss(Xd, Wd, td)
+    dX, dW = ql.head_loss_backward(Xd, Wd, td, lse, gd)
+    rest = np.ones(T, bool)
+    rest[5] = False
+    assert np.isnan(host(loss)[5])
+    assert_bits_equal(host(loss)[rest], host(want["loss"])[rest], "loss")
+    rest[33] = False
+    d = host(dX.float())
+    assert np.isnan(d[5]).all() and not np.isfinite(d[33]).any()
+    assert_bits_equal(d[rest], host(want["dX"].float())[rest], "dX")
+    assert not np.isfinite(host(dW.float())).any()
+
+
 @pytest.mark.parametrize("scale", [1.0, 200.0])
 def test_head_loss_large_logits(ql, scale):
     """Logits of some hundred, all negative or positive: no overflow, the
