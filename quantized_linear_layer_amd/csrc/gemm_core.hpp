@@ -497,7 +497,8 @@ __device__ __attribute__((always_inline)) inline void emit_tile(uint8_t* st0, ui
                                                                 const Emit& emit) {
   constexpr int FM = C::FM, FN = C::FN, kWaves = C::kThreads / kWave;
   constexpr int kPair = FN % 2 == 0 && 3 * (C::kStageBytes / (32 * 72 * 4)) >= kWaves ? 2 : 1;
-  constexpr int kER = 32 * kPair + 8;  // padded row of a 32 x (32 * kPair) chunk (floats)
+  // row of a 32 x (32 * kPair) chunk (floats), padded where there is room
+  constexpr int kER = 32 * kPair + (3 * (C::kStageBytes / (32 * 40 * 4)) >= kWaves ? 8 : 0);
   const int wm = wave / C::WN, wn = wave % C::WN;
   const int col_l = lane & 31;
   // each stage buffer holds the blocks of kEpiPer waves

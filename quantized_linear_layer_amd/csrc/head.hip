@@ -74,9 +74,10 @@ __device__ inline float half_sum(float v) {
 __device__ inline int frag_row(int r, int lane) { return 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3); }
 
 // LDS stages of a tile: eight waves have a CU to themselves and take turns on
-// all of its LDS; tiles of few rows keep more steps on their way.
+// all of its LDS; tiles of few rows keep more steps on their way, those of 64 x 64
+// as many as let five of them have a CU together.
 template <class C>
-constexpr int kStages = C::kThreads == 512 ? 5 : C::BM == 64 ? 5 : 3;
+constexpr int kStages = C::kThreads == 512 ? 5 : C::BM == 64 ? (C::BN == 64 ? 4 : 5) : 3;
 
 template <class C, class F>
 __device__ __attribute__((always_inline)) inline void product_tile(F& f, int nkt, uint8_t* st0,
@@ -87,6 +88,8 @@ __device__ __attribute__((always_inline)) inline void product_tile(F& f, int nkt
     gemm_pipeline_turns<F, 5>(f, nkt, st);
   else if constexpr (kStages<C> == 5)
     gemm_pipeline_deep<F, 5>(f, nkt, st);
+  else if constexpr (kStages<C> == 4)
+    gemm_pipeline_deep<F, 4>(f, nkt, {st0, st1, st2, st3});
   else
     gemm_pipeline(f, nkt, st0, st1, st2);
 }
@@ -521,6 +524,7 @@ using LargeTile = GemmCfg<256, 256, 4, 2, 64, 1>;
 using MidTile = GemmCfg<128, 256, 2, 2, 64, 2>;
 using FewTile = GemmCfg<64, 128, 1, 4, 64, 2>;
 using F32Tile = GemmCfg<128, 128, 2, 2, 64, 2>;
+using F32Small = GemmCfg<64, 64, 2, 2, 64, 4>;
 
 constexpr int64_t kPieceBytes = int64_t(128) << 20;  // of G
 constexpr int64_t kCUs = 256;
@@ -535,51 +539,66 @@ unsigned copy_blocks(int64_t threads) {
   return unsigned(b < 4096 ? (b > 0 ? b : 1) : 4096);
 }
 
-enum class Tile { kLarge, kMid, kFew, kF32 };
+enum class Tile { kLarge, kMid, kFew, kF32, kF32Small };
 
 int64_t tile_rows(Tile t) {
-  return t == Tile::kLarge ? 256 : t == Tile::kFew ? 64 : 128;
+  return t == Tile::kLarge ? 256 : t == Tile::kMid || t == Tile::kF32 ? 128 : 64;
 }
 int64_t tile_cols(Tile t) {
-  return t == Tile::kLarge || t == Tile::kMid ? 256 : 128;
+  return t == Tile::kLarge || t == Tile::kMid ? 256 : t == Tile::kF32Small ? 64 : 128;
 }
 // columns of a wave
 int64_t wave_cols(Tile t) {
-  return t == Tile::kFew ? 32 : t == Tile::kF32 ? 64 : 128;
+  return t == Tile::kLarge || t == Tile::kMid ? 128 : t == Tile::kF32 ? 64 : 32;
 }
 int64_t tiles_of(Tile t, int64_t M, int64_t N) {
   return ceil_div(M, tile_rows(t)) * ceil_div(N, tile_cols(t));
 }
 
-// Tile of an M x N product whose reduction may be cut in up to `slices` (1 where
-// it is not). bfloat16: 256 x 256 once those give every CU one. float32, whose
-// products are bound by the matrix core: of the two tiles the one whose busiest
-// CU has less to do (1001 x 5003: 64 x 128 tiles, 3 a CU, against 2 of 128 x 128).
-Tile pick_tile(bool bf16, int64_t M, int64_t N, int64_t slices = 1) {
-  if (M <= 64) return Tile::kFew;
-  if (!bf16) {
-    const int64_t f = ceil_div(tiles_of(Tile::kF32, M, N) * slices, kCUs) * 2;
-    return ceil_div(tiles_of(Tile::kFew, M, N) * slices, kCUs) < f ? Tile::kFew : Tile::kF32;
-  }
-  return tiles_of(Tile::kLarge, M, N) * slices >= kCUs ? Tile::kLarge : Tile::kMid;
-}
+// Tile of an M x N product and the slices its reduction is cut in (at most `most`).
+struct Shape {
+  Tile tile;
+  int64_t slices;
+};
 
-// Tile of dX (T x H, reduction over the k columns of a piece), and the slices its
-// reduction is cut in: at least 512 elements each, as many as give every CU a
-// workgroup (of 256 x 256) or two.
+// bfloat16: 256 x 256 once those give every CU one, and as many slices as give
+// every CU a workgroup (of 256 x 256) or two.
+// float32, whose products are bound by the matrix core: the tile and the slices
+// whose busiest CU has least to do, of equal ones the larger tile and the fewer
+// slices, which read and add less; two workgroups a CU where slices can give them.
+// Measured, loss and gradients of T x H x V, all three tiles against the larger
+// two: 1001x515x5003 237 against 294 us, 300x256x3000 57 against 87,
+// 700x1000x10000 494 against 541.
+Shape pick(bool bf16, int64_t M, int64_t N, int64_t most) {
+  if (bf16 || M <= 64) {
+    const Tile t = M <= 64 ? Tile::kFew
+                           : tiles_of(Tile::kLarge, M, N) * most >= kCUs ? Tile::kLarge : Tile::kMid;
+    const int64_t want = ceil_div((t == Tile::kLarge ? 1 : 2) * kCUs, tiles_of(t, M > 0 ? M : 1, N));
+    return Shape{t, want < most ? want : most};
+  }
+  Shape best{};
+  double least = 0.0;
+  for (Tile t : {Tile::kF32, Tile::kFew, Tile::kF32Small}) {
+    const int64_t tiles = tiles_of(t, M, N);
+    for (int64_t s = 1; s <= most && (s == 1 || tiles * s <= 4 * kCUs); ++s) {
+      if (s < most && tiles * s < 2 * kCUs) continue;
+      const double work = double(ceil_div(tiles * s, kCUs) * tile_rows(t) * tile_cols(t)) / double(s);
+      if (least == 0.0 || work < least) {
+        least = work;
+        best = Shape{t, s};
+      }
+    }
+  }
+  return best;
+}
+Tile pick_tile(bool bf16, int64_t M, int64_t N) { return pick(bf16, M, N, 1).tile; }
+
+// dX (T x H, reduction over the k columns of a piece): slices of at least 512.
 constexpr int64_t kSliceElems = 512, kMaxSlices = 32;
 
-int64_t dx_most(int64_t k) {
+Shape pick_dx(bool bf16, int64_t T, int64_t H, int64_t k) {
   const int64_t most = k / kSliceElems > 1 ? k / kSliceElems : 1;
-  return most < kMaxSlices ? most : kMaxSlices;
-}
-Tile dx_tile(bool bf16, int64_t T, int64_t H, int64_t k) {
-  return pick_tile(bf16, T, H, dx_most(k));
-}
-int64_t dx_slices(Tile t, int64_t T, int64_t H, int64_t k) {
-  const int64_t want = ceil_div((t == Tile::kLarge ? 1 : 2) * kCUs, tiles_of(t, T > 0 ? T : 1, H));
-  const int64_t most = dx_most(k);
-  return want < most ? want : most;
+  return pick(bf16, T, H, most < kMaxSlices ? most : kMaxSlices);
 }
 
 // f(tile configuration) for a tile that pick_tile gives for T.
@@ -591,6 +610,7 @@ hipError_t with_tile(Tile t, F&& f) {
     if (t == Tile::kMid) return f(MidTile{});
   } else {
     if (t == Tile::kF32) return f(F32Tile{});
+    if (t == Tile::kF32Small) return f(F32Small{});
   }
   return hipErrorInvalidValue;
 }
@@ -616,8 +636,7 @@ HeadPlan head_plan(bool bf16, bool backward, int64_t T, int64_t H, int64_t V, bo
   const int64_t pieces = ceil_div(T * V * esz, kPieceBytes);
   h.piece = pieces > 1 ? round_256(ceil_div(V, pieces)) : V;
   h.ldg = bf16 ? round32(h.piece) : round8(h.piece);
-  const Tile tx = dx_tile(bf16, T, H, h.piece);
-  h.slices = dx_slices(tx, T, H, h.piece);
+  h.slices = pick_dx(bf16, T, H, h.piece).slices;
   h.ldp = round8(H);
   return h;
 }
@@ -733,7 +752,7 @@ hipError_t run_backward(const HeadCall& c, const HeadPlan& h, hipStream_t stream
   hipError_t e = prepare<T>(c, h, true, &X, &W, stream);
   if (e != hipSuccess) return e;
   T* const dW = static_cast<T*>(c.dW);
-  const Tile tx = dx_tile(kBf16, c.T, c.H, h.piece);
+  const Tile tx = pick_dx(kBf16, c.T, c.H, h.piece).tile;
   const bool direct = h.slices == 1 && h.piece >= c.V;
   for (int64_t v0 = 0; v0 < c.V; v0 += h.piece) {
     const int64_t n = c.V - v0 < h.piece ? c.V - v0 : h.piece;
