@@ -15,7 +15,12 @@
 // workgroup adds them once.
 //
 // Bound by memory: each gradient is read for the norm and once more for the
-// clipping (from the last-level cache, if all fit there), and written once.
+// clipping, and written once. The clipping takes the chunks in the other order,
+// as the last ones that the norm read are still in the last-level cache (310
+// million bfloat16: the call 364 against 370 us). Measured there: the norm 136 us
+// (4.6 TB/s), the clipping 222 us (5.6 TB/s read and written; a copy reaches 5.2);
+// six small tensors: 4.4 and 5.2 us of a call of 33 us, which the host's side
+// takes.
 #include "device_common.hpp"
 #include "internal.hpp"
 
@@ -26,7 +31,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kBatch = 128;
 constexpr int64_t kMinChunk = 8192;    // elements
-constexpr int64_t kWantChunks = 2048;  // eight workgroups a CU
+constexpr int64_t kMostChunks = 2048;  // eight workgroups a CU
 
 struct Batch {
   const void* g[kBatch];
@@ -180,7 +185,7 @@ __global__ __launch_bounds__(kThreads) void grad_scale_kernel(Batch t, const dou
                                                               int parts, float max_norm,
                                                               float* norm) {
   const float total = float(sqrt(sum_parts(part, parts)));
-  const int b = blockIdx.x;
+  const int b = gridDim.x - 1 - blockIdx.x;
   if (norm != nullptr && b == 0 && threadIdx.x == 0) *norm = total;
   float c = max_norm / (total + 1e-6f);
   c = c > 1.0f ? 1.0f : c;  // NaN stays NaN
@@ -195,22 +200,27 @@ __global__ __launch_bounds__(kThreads) void grad_scale_kernel(Batch t, const dou
     scale<F32In>(static_cast<const float*>(t.g[i]) + at, static_cast<float*>(t.out[i]) + at, n, c);
 }
 
-int64_t chunk_length(int64_t elements) {
-  const int64_t c = (elements / kWantChunks + 63) / 64 * 64;
+// The chunks of one batch of tensors (were all batches alike) fit the GPU at once,
+// the last, part full chunk of each tensor counted: a few more than fit would run
+// alone after the others (310 million bfloat16: the call 370 against 383 us).
+int64_t chunk_length(int64_t count, int64_t elements) {
+  const int64_t batches = count > 0 ? (count + kBatch - 1) / kBatch : 1;
+  const int64_t whole = batches * kMostChunks - count;
+  const int64_t c = ((elements + whole - 1) / whole + 63) / 64 * 64;
   return c > kMinChunk ? c : kMinChunk;
 }
 
 }  // namespace
 
 int64_t clip_parts(int64_t count, int64_t elements) {
-  return elements / chunk_length(elements) + count;
+  return elements / chunk_length(count, elements) + count;
 }
 
 hipError_t launch_clip(const fp4lin_grad* grads, int64_t count, int64_t elements, bool clip,
                        float max_norm, float* norm, void* ws, hipStream_t stream) {
   double* const total = static_cast<double*>(ws);
   double* const part = total + 2;  // 16 bytes on
-  const int64_t chunk = chunk_length(elements);
+  const int64_t chunk = chunk_length(count, elements);
   auto fill = [&](Batch& t, int64_t& next) {
     t = Batch{};
     t.chunk = chunk;
