@@ -126,15 +126,22 @@ __device__ __attribute__((always_inline)) inline void quantize_cols_body(int64_t
 }
 
 // Micro-scaled tile (bx, by): columns bx*128 .. +127, rows by*128 .. +127
-// (rows past K read as zero and give the zero padding). Thread (kg, g) =
-// (t % 16, t / 16) owns rows k0 + 8kg .. +7 of columns n0 + 8g .. +7: the 8
-// codes of one column are one 32-bit word of its packed row, and lanes
-// 4q .. 4q+3 share block q. Block scales go to the step-major array Ws (the
+// (rows past K read as zero and give the zero padding). Wave w takes block w, rows
+// k0 + 32w .. +31: lane 4g + q owns rows 8q .. +7 of them in columns n0 + 8g .. +7,
+// so that a load of the wave is 4 rows of 256 bytes (bfloat16), the 8 codes of one
+// column are one 32-bit word and a quad of lanes shares a block. The words meet in
+// LDS (a group of 8 columns every 528 bytes: the wave's 64 words lie in distinct
+// banks) and leave as 16-byte pieces of whole columns, the scale bytes as words.
+// Block scales go to the step-major array Ws (the
 // byte of block b of column n at (b / 4) * 4ns + 4n + b % 4, ns the rows of that
 // array: N, or those of all matrices whose scales share it). The 64 bytes of
 // column n's codes in K step s go to Wq + n * ldq + s * step: with step 64 the
 // codes of a column are one packed row of ldq bytes; with ldq 64 and step 64 N
 // those of a step are together, and a tile's codes are 8 KiB in one piece.
+// ldq and step are whole 64 bytes, Wq 16-byte and Ws 4-byte aligned. All threads
+// of a workgroup of 256 call it. (8 experts 4096 x 11008 with their product: 424 us; a
+// wave over all four blocks of 32 columns, words stored as they come: 446. W with the
+// non-temporal hint: 500, as the next call finds none of it in the last-level cache.)
 constexpr int kMxTK = 128;  // codes along K per column tile
 constexpr int kMxTN = 128;  // columns per tile
 
@@ -143,13 +150,15 @@ __device__ __attribute__((always_inline)) inline void quantize_cols_mx_body(
     int64_t bx, int64_t by, const typename In::T* __restrict__ W, int64_t K, int64_t N,
     int64_t ldw, uint8_t* __restrict__ Wq, int64_t ldq, int64_t step, uint8_t* __restrict__ Ws,
     int64_t ns) {
+  constexpr int kGroup = 8 * 64 + 16;  // bytes of 8 columns in LDS
+  __shared__ __attribute__((aligned(16))) uint8_t codes[kMxTN / 8 * kGroup];
+  __shared__ __attribute__((aligned(4))) uint8_t scales[kMxTN * 4];
   const int t = threadIdx.x;
-  const int kg = t & 15, g = t >> 4;
+  const int b = t >> 6, q = t & 3, g = (t >> 2) & 15;
   const int64_t n0 = bx * kMxTN;
-  const int64_t k0 = by * kMxTK;
   const int64_t c = n0 + g * 8;
   const int64_t valid = N - c;
-  const int64_t kr = k0 + kg * 8;
+  const int64_t kr = by * kMxTK + b * 32 + q * 8;
   Vec8<In> v[8];
 #pragma unroll
   for (int u = 0; u < 8; ++u) {
@@ -168,19 +177,27 @@ __device__ __attribute__((always_inline)) inline void quantize_cols_mx_body(
     for (int u = 0; u < 8; ++u) m = fmaxf(m, fabsf(In::widen(v[u].v[j])));
     e[j] = mx_exponent(quad_max(m));
   }
-  if (valid <= 0) return;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    if (j >= valid) break;
     uint32_t word = 0;
 #pragma unroll
     for (int u = 0; u < 8; ++u)
       word |= (mx_magnitude(fabsf(In::widen(v[u].v[j])), e[j]) | (In::sign_bit(v[u].v[j]) << 3))
               << (4 * u);
-    *reinterpret_cast<uint32_t*>(Wq + (c + j) * ldq + (kr / 128) * step + (kr % 128) / 2) = word;
-    // rows kr .. kr+7: block kr / 32 of K step kr / 128 (the tile's step by)
-    if ((kg & 3) == 0) Ws[(kr / 128) * 4 * ns + 4 * (c + j) + ((kr / 32) & 3)] = uint8_t(e[j] + 127);
+    *reinterpret_cast<uint32_t*>(codes + g * kGroup + j * 64 + b * 16 + q * 4) = word;
+    if (q == 0) scales[(g * 8 + j) * 4 + b] = uint8_t(e[j] + 127);
   }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int at = (i * 256 + t) * 16, col = at / 64;
+    if (n0 + col < N)
+      *reinterpret_cast<uint4*>(Wq + (n0 + col) * ldq + by * step + at % 64) =
+          *reinterpret_cast<const uint4*>(codes + col / 8 * kGroup + at % 512);
+  }
+  if (t < kMxTN && n0 + t < N)
+    *reinterpret_cast<uint32_t*>(Ws + by * 4 * ns + 4 * (n0 + t)) =
+        *reinterpret_cast<const uint32_t*>(scales + t * 4);
 }
 
 // Row-wise (per row) micro-scaled quantization. Workgroup (bx, by) of gx x gy

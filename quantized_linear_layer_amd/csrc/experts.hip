@@ -176,8 +176,8 @@ __global__ __launch_bounds__(kThreads) void experts_rows_mx_kernel(RowsArgs a, R
 
 // Weights along K (rows of W[e]), a 128 x 128 tile a workgroup; with kRows > 0
 // rows of the activations first. Scales go to one step-major array over the E * N
-// columns of all experts. Bound by memory: 8 experts 4096 x 11008 and 8192 rows 209
-// to 227 us for 788 MB read and 209 MB written (4.4 to 4.8 TB/s; a copy reaches 5.2).
+// columns of all experts. Bound by memory: 8 experts 4096 x 11008 and 8192 rows 188
+// us for 788 MB read and 209 MB written (5.3 TB/s; a copy reaches 5.2).
 template <class In, bool kFast, int kRows>
 __global__ __launch_bounds__(kThreads) void experts_cols_mx_kernel(RowsArgs a, ColsArgs w) {
   int id = blockIdx.x;
@@ -198,7 +198,7 @@ __global__ __launch_bounds__(kThreads) void experts_cols_mx_kernel(RowsArgs a, C
 
 // Activations and gradients along each expert's own rows: K step blockIdx.y of
 // all experts' steps (128 rows each, the last one of an expert filled with zeros)
-// and 128 columns of A (K of them) or, past those, of dY (N). 70 to 80 us for 247 MB
+// and 128 columns of A (K of them) or, past those, of dY (N). 67 to 84 us for 247 MB
 // read and 66 MB written (8192 rows, 4096 and 11008 columns).
 struct RaggedArgs {
   const void *A, *dY;
@@ -462,7 +462,8 @@ hipError_t run_few(const FewArgs& a, hipStream_t stream) {
 // fill them once, else of 64 x 128; the last also for few rows an expert, where
 // a product is a read of the weights' codes and more workgroups on their way
 // read faster (8 experts 4096x11008, whole call: 128 rows 47 against 53 us with
-// 128 x 256 tiles, 256 rows 51 against 57, 512 rows 60 against 62). Whole calls with
+// 128 x 256 tiles, 256 rows 51 against 57, 512 rows 60 against 62). Whole calls (when
+// the first took 20 us longer to quantize its operands than it does now) with
 // 256 x 256 / 128 x 256 / 64 x 128 tiles alone: forward of 8192 rows, 8 experts
 // 4096x11008 445 / 453 / 514 us, of 2048 rows 283 / 269 / 286, of 1024 rows, 8 experts
 // 2048x5632 71 / 74 / 69; dgrad of 8192 rows, 16 experts 2048x5632 202 / 199 / 210.
