@@ -382,7 +382,10 @@ fp4lin_status fp4lin_forward(const void* A, const void* W, fp4lin_dtype dt, int6
  * Quantization is that of the micro-scaled variant (32 codes along the
  * product's reduction, one E8M0 byte each), without a clamp and without
  * compensation. Every product accumulates in fp32 and is rounded once where
- * the output is bfloat16.
+ * the output is bfloat16. A block of an operand that holds an infinity or NaN has
+ * no scale: its byte is 255 (E8M0's NaN) and every element of the result that the
+ * block has a part in is NaN, whatever the other operand holds; no other element
+ * changes.
  * Weights of all experts are one array: expert e's K x N matrix starts at row
  * e * K (E * K rows, leading dimension ldw).
  * Limits: E <= 65534; packed operands of one expert and the scales of all
@@ -400,7 +403,7 @@ size_t fp4lin_experts_workspace_bytes(fp4lin_experts_pass pass, int64_t E, int64
                                       int64_t N);
 
 /* Weights of all experts, quantized along K as fp4lin_quantize_weight_mx does
- * for one.
+ * for one (but for blocks that hold an infinity or NaN, see above).
  *   Wq       device, E * N rows of fp4lin_packed_ld(K) bytes (output)
  *   Ws       device, E * N * fp4lin_mx_scales_ld(K) bytes: step-major over the
  *            E * N rows (the byte of block b of column n of expert e is at

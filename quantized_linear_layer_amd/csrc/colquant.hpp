@@ -139,13 +139,13 @@ __device__ __attribute__((always_inline)) inline void quantize_cols_body(int64_t
 // codes of a column are one packed row of ldq bytes; with ldq 64 and step 64 N
 // those of a step are together, and a tile's codes are 8 KiB in one piece.
 // ldq and step are whole 64 bytes, Wq 16-byte and Ws 4-byte aligned. All threads
-// of a workgroup of 256 call it. (8 experts 4096 x 11008 with their product: 424 us; a
+// of a workgroup of 256 call it. kNan: see BlockMax. (8 experts 4096 x 11008 with their product: 424 us; a
 // wave over all four blocks of 32 columns, words stored as they come: 446. W with the
 // non-temporal hint: 500, as the next call finds none of it in the last-level cache.)
 constexpr int kMxTK = 128;  // codes along K per column tile
 constexpr int kMxTN = 128;  // columns per tile
 
-template <class In, bool kAligned>
+template <class In, bool kAligned, bool kNan = false>
 __device__ __attribute__((always_inline)) inline void quantize_cols_mx_body(
     int64_t bx, int64_t by, const typename In::T* __restrict__ W, int64_t K, int64_t N,
     int64_t ldw, uint8_t* __restrict__ Wq, int64_t ldq, int64_t step, uint8_t* __restrict__ Ws,
@@ -172,10 +172,10 @@ __device__ __attribute__((always_inline)) inline void quantize_cols_mx_body(
   int e[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    float m = 0.0f;
+    BlockMax<kNan> m;
 #pragma unroll
-    for (int u = 0; u < 8; ++u) m = fmaxf(m, fabsf(In::widen(v[u].v[j])));
-    e[j] = mx_exponent(quad_max(m));
+    for (int u = 0; u < 8; ++u) m.take(fabsf(In::widen(v[u].v[j])));
+    e[j] = m.exponent();
   }
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
@@ -211,8 +211,9 @@ __device__ __attribute__((always_inline)) inline void quantize_cols_mx_body(
 // Codes: rows in blocks of `block` rows (each block ldq bytes a row), and within a
 // block the 64 bytes of every row's K step 0, then of step 1, ...: with block 1
 // each row's codes are together (packed rows of ldq bytes), with block M those of
-// a step. Scales are step-major over all M rows.
-template <class In, bool kFast, int kRows>
+// a step. Scales are step-major over all M rows. |x| is clamped to tau, which makes
+// tau of a NaN; kNan (see BlockMax): it is not.
+template <class In, bool kFast, int kRows, bool kNan = false>
 __device__ __attribute__((always_inline)) inline void quantize_rows_mx_body(
     int64_t bx, int64_t gx, int64_t by, int64_t gy, const typename In::T* __restrict__ X, int64_t M,
     int64_t K, int64_t ldx, float tau, uint8_t* __restrict__ Xq, int64_t ldq, int64_t block,
@@ -229,13 +230,14 @@ __device__ __attribute__((always_inline)) inline void quantize_rows_mx_body(
         const int64_t r = r0 + u;
         if (r >= M) break;
         float ax[8];
-        float m = 0.0f;
+        BlockMax<kNan> m;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          ax[i] = fminf(fabsf(In::widen(v[u].v[i])), tau);
-          m = fmaxf(m, ax[i]);
+          ax[i] = fabsf(In::widen(v[u].v[i]));
+          if constexpr (!kNan) ax[i] = fminf(ax[i], tau);
+          m.take(ax[i]);
         }
-        const int e = mx_exponent(quad_max(m));
+        const int e = m.exponent();
         uint32_t word = 0;
 #pragma unroll
         for (int i = 0; i < 8; ++i)

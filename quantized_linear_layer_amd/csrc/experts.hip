@@ -9,7 +9,9 @@
 //   wgrad    dW[e]    = Q(A_e)^T . Q(dY_e)          over e's rows; blocks of 32
 //                                                   rows count from its first row
 // Each is a sum over blocks of 2^(eA + eB) * (FP4 dot product), accumulated in
-// fp32 by the matrix core and written once, in fp32 or rounded to bfloat16.
+// fp32 by the matrix core and written once, in fp32 or rounded to bfloat16. A block
+// that holds an infinity or NaN has the scale NaN in every form of the products
+// (BlockMax), so that none of them turns one into a number.
 //
 // Ragged groups without a host copy of row_end: a launch covers the most tiles
 // that any split of the rows over the experts can need, every wave finds its
@@ -157,7 +159,7 @@ struct ColsArgs {
 
 template <class In, bool kFast, int kRows>
 __device__ inline void quantize_rows_part(const RowsArgs& p, int id) {
-  quantize_rows_mx_body<In, kFast, kRows>(
+  quantize_rows_mx_body<In, kFast, kRows, true>(
       id % p.gx, p.gx, id / p.gx, p.gy, static_cast<const typename In::T*>(p.X), p.M, p.L, p.ldx,
       __builtin_huge_valf(), p.q, (p.L + 127) / 128 * 64, p.block, p.s);
 }
@@ -191,7 +193,7 @@ __global__ __launch_bounds__(kThreads) void experts_cols_mx_kernel(RowsArgs a, C
   }
   const int64_t e = id / (w.gx * w.gy);
   id -= int(e) * w.gx * w.gy;
-  quantize_cols_mx_body<In, kFast>(
+  quantize_cols_mx_body<In, kFast, true>(
       id % w.gx, id / w.gx, static_cast<const typename In::T*>(w.W) + e * w.K * w.ldw, w.K, w.N,
       w.ldw, w.q + e * w.N * ((w.K + 127) / 128 * 64), w.ld, w.step, w.s + 4 * e * w.N, w.E * w.N);
 }
@@ -218,7 +220,7 @@ __global__ __launch_bounds__(kThreads) void experts_ragged_mx_kernel(RaggedArgs 
   const int tiles = (p.K + kMxTN - 1) / kMxTN;
   const bool first = int(blockIdx.x) < tiles;
   const int64_t n = first ? p.K : p.N, ld = first ? p.lda : p.lddy;
-  quantize_cols_mx_body<In, kAligned>(
+  quantize_cols_mx_body<In, kAligned, true>(
       first ? blockIdx.x : blockIdx.x - tiles, s - g.first,
       static_cast<const T*>(first ? p.A : p.dY) + int64_t(g.begin) * ld, g.rows, n, ld,
       (first ? p.Aq : p.Dq) + int64_t(g.first) * 64 * n, 64, 64 * n,
@@ -353,13 +355,14 @@ __device__ inline void quantize_few(const FewArgs& p, int begin, int rows, uint8
       load_chunk<In, true>(row, c * 8, p.K, v);
     else
       load_chunk<In, false>(row, c * 8, p.K, v);
-    float ax[8], m = 0.0f;
+    float ax[8];
+    BlockMax<true> m;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       ax[j] = fabsf(In::widen(v.v[j]));
-      m = fmaxf(m, ax[j]);
+      m.take(ax[j]);
     }
-    const int e = mx_exponent(quad_max(m));
+    const int e = m.exponent();
     uint32_t word = 0;
 #pragma unroll
     for (int j = 0; j < 8; ++j)

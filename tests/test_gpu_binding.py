@@ -1,0 +1,56 @@
+"""GPU tests of what the binding accepts and refuses: strides that a single row
+need not have, and buffers that do not fit a call."""
+import pytest
+
+from gpu_util import assert_bits_equal, host, log
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def ql():
+    torch = pytest.importorskip("torch")
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import quantized_linear_layer_amd as q
+    q.lib()
+    return q
+
+
+def torch():
+    import torch as t
+    return t
+
+
+@pytest.mark.parametrize("length", [70000, 70001])
+def test_one_row_of_a_long_sequence(ql, length):
+    """The last position of one sequence, hidden[:, -1]: one row whose stride is
+    the whole sequence, beyond the largest leading dimension."""
+    t = torch()
+    H, V, N = 65, 300, 40
+    log(f"one row with a stride of {length * H}")
+    hidden = t.randn((1, length, H), device="cuda:0").bfloat16()
+    x = hidden[:, -1]
+    assert x.stride(0) == length * H
+    W = (t.randn((H, V), device="cuda:0") * 0.05).bfloat16()
+    target, dloss = t.tensor([7], dtype=t.int32, device="cuda:0"), t.ones(1, device="cuda:0")
+    y = x.clone(memory_format=t.contiguous_format)
+    for a, b in zip(ql.head_loss(x, W, target), ql.head_loss(y, W, target)):
+        assert_bits_equal(host(a), host(b), "loss")
+    lse = ql.head_loss(y, W, target)[1]
+    for a, b in zip(ql.head_loss_backward(x, W, target, lse, dloss), ql.head_loss_backward(y, W, target, lse, dloss)):
+        assert_bits_equal(host(a), host(b), "gradients")
+    E = t.randn((2, H, N), device="cuda:0").bfloat16()
+    re = t.tensor([0, 1], dtype=t.int32, device="cuda:0")
+    assert_bits_equal(host(ql.experts_forward_mx(x, E, re)), host(ql.experts_forward_mx(y, E, re)), "Y")
+
+
+def test_weights_of_one_row_an_expert(ql):
+    """K = 1: the row stride is the experts', whatever the middle stride says."""
+    t = torch()
+    E, N = 3, 24
+    W = t.randn((E, 5, N), device="cuda:0")[:, 2:3]
+    A, re = t.randn((4, 1), device="cuda:0"), t.tensor([1, 1, 4], dtype=t.int32, device="cuda:0")
+    log("experts of one row each")
+    want = ql.experts_forward_mx(A, W.contiguous(), re)
+    assert_bits_equal(host(ql.experts_forward_mx(A, W, re)), host(want), "Y")
