@@ -384,30 +384,31 @@ def _code(t) -> int:
     return _dtype_code(t) if code is None else code
 
 
-def _row_stride(ld, cols):
-    """A stride that a tensor of at most one row need not carry is the row length."""
-    return ld if ld > cols else cols
-
-
 def _rows(t, name):
-    """(rows, columns, row stride) of a row-major matrix."""
+    """(rows, columns, row stride) of a row-major matrix. A single row needs no
+    stride and may carry any (hidden[:, -1] of one long sequence): its length is
+    taken."""
     size, stride = t.shape, t.stride()
     if len(size) != 2 or (stride[1] != 1 and size[1] > 1):
         raise ValueError(f"{name} must be a 2-D row-major tensor with unit column stride")
-    if stride[0] < size[1] and size[0] > 1:
+    if size[0] <= 1:
+        return size[0], size[1], size[1]
+    if stride[0] < size[1]:
         raise ValueError(f"{name} must not have overlapping rows")
-    return size[0], size[1], _row_stride(stride[0], size[1])
+    return size[0], size[1], stride[0]
 
 
 def _experts_weight(W, name):
-    """(E, K, N, ldw) of a stack of row-major matrices with one row stride throughout."""
+    """(E, K, N, ldw) of a stack of row-major matrices with one row stride throughout
+    (that of the experts where they have one row each)."""
     size, stride = W.shape, W.stride()
-    if len(size) != 3 or (stride[2] != 1 and size[2] > 1) or \
-            (size[0] > 1 and stride[0] != size[1] * stride[1]) or \
-            (size[1] > 1 and stride[1] < size[2]):
-        raise ValueError(f"{name} must be a 3-D tensor (experts, rows, columns) with unit column "
-                         "stride and experts that follow one another at the row stride")
-    return size[0], size[1], size[2], _row_stride(stride[1], size[2])
+    if len(size) == 3 and (stride[2] == 1 or size[2] <= 1):
+        E, K, N = size
+        ldw = stride[1] if K > 1 else stride[0] if E > 1 else N
+        if ldw >= N and (E <= 1 or stride[0] == K * ldw):
+            return E, K, N, ldw
+    raise ValueError(f"{name} must be a 3-D tensor (experts, rows, columns) with unit column "
+                     "stride and experts that follow one another at the row stride")
 
 
 def _gpu(first, *others):
