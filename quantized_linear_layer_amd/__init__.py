@@ -775,16 +775,26 @@ def _grads(tensors, out):
     return (_lib.Grad * count).from_buffer_copy(data), count, sum(sizes), devices.pop()
 
 
+def _norm_out(norm, ws, device):
+    """Checks that norm can take the call's float32 and that norm and ws are on the
+    gradients' GPU."""
+    if _gpu(("norm", norm), ("ws", ws)) != device:
+        raise ValueError(f"norm and ws are on {norm.device}, the gradients on cuda:{device}")
+    if norm.dtype != _torch().float32:
+        raise TypeError("norm must be float32")
+    _need(norm.numel() == 1, f"norm has {norm.numel()} elements, not one")
+
+
 def fp4lin_grad_norm(tensors, norm, ws, stream=None):
     array, count, _, device = _grads(tensors, None)
-    _gpu(("norm", norm), ("ws", ws))
+    _norm_out(norm, ws, device)
     _check(lib().fp4lin_grad_norm(array, count, norm.data_ptr(), ws.data_ptr(), _nbytes(ws),
                                   _queue(stream, device)), "fp4lin_grad_norm")
 
 
 def fp4lin_clip_grads(tensors, max_norm, norm, ws, out=None, stream=None):
     array, count, _, device = _grads(tensors, out)
-    _gpu(("norm", norm), ("ws", ws))
+    _norm_out(norm, ws, device)
     _check(lib().fp4lin_clip_grads(array, count, float(max_norm), norm.data_ptr(), ws.data_ptr(),
                                    _nbytes(ws), _queue(stream, device)), "fp4lin_clip_grads")
 

@@ -54,3 +54,24 @@ def test_weights_of_one_row_an_expert(ql):
     log("experts of one row each")
     want = ql.experts_forward_mx(A, W.contiguous(), re)
     assert_bits_equal(host(ql.experts_forward_mx(A, W, re)), host(want), "Y")
+
+
+def test_clip_norm_buffer(ql):
+    """norm takes one float32: other types and sizes are refused, and nothing is
+    written then."""
+    t = torch()
+    g = t.full((100,), 3.0, device="cuda:0")
+    ws = t.empty(ql.clip_workspace_bytes(1, 100), dtype=t.uint8, device="cuda:0")
+    log("norm buffers of other types and sizes")
+    for bad, error in ((t.zeros((), dtype=t.float64, device="cuda:0"), TypeError),
+                       (t.zeros((), dtype=t.bfloat16, device="cuda:0"), TypeError),
+                       (t.zeros(0, device="cuda:0"), ValueError), (t.zeros(2, device="cuda:0"), ValueError),
+                       (t.zeros(()), ValueError)):
+        with pytest.raises(error):
+            ql.fp4lin_grad_norm([g], bad, ws)
+        with pytest.raises(error):
+            ql.fp4lin_clip_grads([g], 1.0, bad, ws)
+        assert not bool(bad.any()) and bool((g == 3.0).all())
+    for norm in (t.zeros((), device="cuda:0"), t.zeros((1, 1), device="cuda:0")):
+        ql.fp4lin_grad_norm([g], norm, ws)
+        assert float(norm) == 30.0
