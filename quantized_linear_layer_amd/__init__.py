@@ -483,9 +483,18 @@ def _experts_ws(which, E, M, K, N, device, where):
     return torch.empty(n, dtype=torch.uint8, device=device)
 
 
+def _packed_bytes(Wq, Ws, E, K, N):
+    """(name, tensor, bytes) of the codes and scales of E matrices of K x N."""
+    steps = (K + 127) // 128  # of 64 bytes of codes and 4 scales
+    return ("Wq", Wq, E * N * steps * 64), ("Ws", Ws, E * N * steps * 4)
+
+
 def fp4lin_experts_quantize_weight_mx(W, Wq, Ws, stream=None):
     E, K, N, ldw = _experts_weight(W, "W")
     device = _gpu(("W", W), ("Wq", Wq), ("Ws", Ws))
+    for name, t, want in _packed_bytes(Wq, Ws, E, K, N):
+        _need(t.is_contiguous(), f"{name} must be contiguous")
+        _need(_nbytes(t) >= want, f"{name} holds {_nbytes(t)} bytes, not {want}")
     _check(lib().fp4lin_experts_quantize_weight_mx(
         W.data_ptr(), _code(W), E, K, N, ldw, Wq.data_ptr(), Ws.data_ptr(), _queue(stream, device)),
         "fp4lin_experts_quantize_weight_mx")
@@ -514,8 +523,7 @@ def fp4lin_experts_apply_mx(A, Wq, Ws, row_end, Y, ws, stream=None):
     device = _gpu(("A", A), ("Wq", Wq), ("Ws", Ws), ("row_end", row_end), ("Y", Y), ("ws", ws))
     if My != M:
         raise ValueError(f"Y has {My} rows, A {M}")
-    steps = (K + 127) // 128  # of 64 bytes of codes and 4 scales
-    for name, t, want in (("Wq", Wq, E * N * steps * 64), ("Ws", Ws, E * N * steps * 4)):
+    for name, t, want in _packed_bytes(Wq, Ws, E, K, N):
         if t.dtype != _torch().uint8 or not t.is_contiguous():
             raise TypeError(f"{name} must be a contiguous uint8 tensor")
         if t.numel() != want:

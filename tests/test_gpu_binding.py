@@ -75,3 +75,18 @@ def test_clip_norm_buffer(ql):
     for norm in (t.zeros((), device="cuda:0"), t.zeros((1, 1), device="cuda:0")):
         ql.fp4lin_grad_norm([g], norm, ws)
         assert float(norm) == 30.0
+
+
+def test_packed_weight_buffers(ql):
+    """Buffers for quantized weights that are too small are refused."""
+    t = torch()
+    W = t.randn((3, 130, 5), device="cuda:0")
+    Wq, Ws = ql.experts_quantize_weight_mx(W)
+    log("packed weights into given buffers")
+    for q, s in ((Wq[:2], Ws), (Wq, Ws[:1]), (Wq[:, ::2], Ws)):
+        with pytest.raises(ValueError):
+            ql.fp4lin_experts_quantize_weight_mx(W, q, s)
+    q, s = t.full_like(Wq, 255), t.full_like(Ws, 255)
+    ql.fp4lin_experts_quantize_weight_mx(W, q, s)
+    assert_bits_equal(host(q), host(Wq), "codes")
+    assert_bits_equal(host(s), host(Ws), "scales")
