@@ -444,13 +444,20 @@ def _need(ok, message):
 _HERE = contextlib.nullcontext()
 
 
+def _current():
+    """The current GPU."""
+    torch = _torch()
+    raw = getattr(torch._C, "_cuda_getDevice", None)  # tensors are there: no set-up to look for
+    return torch.cuda.current_device() if raw is None else raw()
+
+
 def _on(t, stream):
     """A context with the device of t and the stream the call runs on, so that
     what is allocated inside belongs to that stream."""
-    torch = _torch()
     device = t.get_device()
-    if device < 0 or (stream is None and device == torch.cuda.current_device()):
+    if device < 0 or (stream is None and device == _current()):
         return _HERE
+    torch = _torch()
     both = contextlib.ExitStack()
     both.enter_context(torch.cuda.device(device))
     if stream is not None:
@@ -465,6 +472,16 @@ def _queue(stream, device):
         return stream.cuda_stream
     raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # without a Stream object
     return torch.cuda.current_stream(device).cuda_stream if raw is None else raw(device)
+
+
+def _call(device, name, *args):
+    """Calls a C entry on `device`: the null stream is that of the current GPU."""
+    f = getattr(lib(), name)
+    if device == _current():
+        _check(f(*args), name)
+    else:
+        with _torch().cuda.device(device):
+            _check(f(*args), name)
 
 
 def _nbytes(ws):
@@ -495,9 +512,8 @@ def fp4lin_experts_quantize_weight_mx(W, Wq, Ws, stream=None):
     for name, t, want in _packed_bytes(Wq, Ws, E, K, N):
         _need(t.is_contiguous(), f"{name} must be contiguous")
         _need(_nbytes(t) >= want, f"{name} holds {_nbytes(t)} bytes, not {want}")
-    _check(lib().fp4lin_experts_quantize_weight_mx(
-        W.data_ptr(), _code(W), E, K, N, ldw, Wq.data_ptr(), Ws.data_ptr(), _queue(stream, device)),
-        "fp4lin_experts_quantize_weight_mx")
+    _call(device, "fp4lin_experts_quantize_weight_mx", W.data_ptr(), _code(W), E, K, N, ldw,
+          Wq.data_ptr(), Ws.data_ptr(), _queue(stream, device))
 
 
 def fp4lin_experts_forward_mx(A, W, row_end, Y, ws, stream=None):
@@ -510,10 +526,9 @@ def fp4lin_experts_forward_mx(A, W, row_end, Y, ws, stream=None):
         raise ValueError(f"A is {M}x{K} but the weights are {K2}x{N}")
     if My != M or Ny != N:
         raise ValueError(f"Y is {My}x{Ny}, not {M}x{N}")
-    _check(lib().fp4lin_experts_forward_mx(
-        A.data_ptr(), W.data_ptr(), _code(A), _row_end(row_end, E), E, M, K, N, lda, ldw,
-        Y.data_ptr(), _code(Y), ldy, ws.data_ptr(), _nbytes(ws), _queue(stream, device)),
-        "fp4lin_experts_forward_mx")
+    _call(device, "fp4lin_experts_forward_mx", A.data_ptr(), W.data_ptr(), _code(A),
+          _row_end(row_end, E), E, M, K, N, lda, ldw, Y.data_ptr(), _code(Y), ldy, ws.data_ptr(),
+          _nbytes(ws), _queue(stream, device))
 
 
 def fp4lin_experts_apply_mx(A, Wq, Ws, row_end, Y, ws, stream=None):
@@ -523,15 +538,15 @@ def fp4lin_experts_apply_mx(A, Wq, Ws, row_end, Y, ws, stream=None):
     device = _gpu(("A", A), ("Wq", Wq), ("Ws", Ws), ("row_end", row_end), ("Y", Y), ("ws", ws))
     if My != M:
         raise ValueError(f"Y has {My} rows, A {M}")
+    byte = _torch().uint8
     for name, t, want in _packed_bytes(Wq, Ws, E, K, N):
-        if t.dtype != _torch().uint8 or not t.is_contiguous():
+        if t.dtype != byte or not t.is_contiguous():
             raise TypeError(f"{name} must be a contiguous uint8 tensor")
         if t.numel() != want:
             raise ValueError(f"{name} holds {t.numel()} bytes, not {want}")
-    _check(lib().fp4lin_experts_apply_mx(
-        A.data_ptr(), _code(A), Wq.data_ptr(), Ws.data_ptr(), _row_end(row_end, E), E, M, K, N, lda,
-        Y.data_ptr(), _code(Y), ldy, ws.data_ptr(), _nbytes(ws), _queue(stream, device)),
-        "fp4lin_experts_apply_mx")
+    _call(device, "fp4lin_experts_apply_mx", A.data_ptr(), _code(A), Wq.data_ptr(), Ws.data_ptr(),
+          _row_end(row_end, E), E, M, K, N, lda, Y.data_ptr(), _code(Y), ldy, ws.data_ptr(),
+          _nbytes(ws), _queue(stream, device))
 
 
 def fp4lin_experts_dgrad_mx(dY, W, row_end, dX, ws, stream=None):
@@ -544,10 +559,9 @@ def fp4lin_experts_dgrad_mx(dY, W, row_end, dX, ws, stream=None):
         raise ValueError(f"dY is {M}x{N} but the weights are {K}x{N2}")
     if Mx != M or Kx != K:
         raise ValueError(f"dX is {Mx}x{Kx}, not {M}x{K}")
-    _check(lib().fp4lin_experts_dgrad_mx(
-        dY.data_ptr(), W.data_ptr(), _code(dY), _row_end(row_end, E), E, M, K, N, lddy, ldw,
-        dX.data_ptr(), _code(dX), lddx, ws.data_ptr(), _nbytes(ws), _queue(stream, device)),
-        "fp4lin_experts_dgrad_mx")
+    _call(device, "fp4lin_experts_dgrad_mx", dY.data_ptr(), W.data_ptr(), _code(dY),
+          _row_end(row_end, E), E, M, K, N, lddy, ldw, dX.data_ptr(), _code(dX), lddx,
+          ws.data_ptr(), _nbytes(ws), _queue(stream, device))
 
 
 def fp4lin_experts_wgrad_mx(A, dY, row_end, dW, ws, stream=None):
@@ -560,10 +574,9 @@ def fp4lin_experts_wgrad_mx(A, dY, row_end, dW, ws, stream=None):
         raise ValueError(f"dY has {My} rows, A {M}")
     if Kw != K or Nw != N:
         raise ValueError(f"dW holds {Kw}x{Nw} matrices, not {K}x{N}")
-    _check(lib().fp4lin_experts_wgrad_mx(
-        A.data_ptr(), dY.data_ptr(), _code(A), _row_end(row_end, E), E, M, K, N, lda, lddy,
-        dW.data_ptr(), _code(dW), lddw, ws.data_ptr(), _nbytes(ws), _queue(stream, device)),
-        "fp4lin_experts_wgrad_mx")
+    _call(device, "fp4lin_experts_wgrad_mx", A.data_ptr(), dY.data_ptr(), _code(A),
+          _row_end(row_end, E), E, M, K, N, lda, lddy, dW.data_ptr(), _code(dW), lddw,
+          ws.data_ptr(), _nbytes(ws), _queue(stream, device))
 
 
 def experts_quantize_weight_mx(W, stream=None):
@@ -664,10 +677,9 @@ def _row_floats(t, T, name):
 def fp4lin_head_loss(X, W, target, loss, lse, ws, by_vocab=False, stream=None):
     T, H, V, ldx, ldw = _head_sizes(X, W, target, by_vocab)
     device = _gpu(("X", X), ("W", W), ("target", target), ("loss", loss), ("lse", lse), ("ws", ws))
-    _check(lib().fp4lin_head_loss(
-        X.data_ptr(), W.data_ptr(), _code(X), int(bool(by_vocab)), target.data_ptr(), T, H, V, ldx,
-        ldw, _row_floats(loss, T, "loss"), _row_floats(lse, T, "lse"), ws.data_ptr(), _nbytes(ws),
-        _queue(stream, device)), "fp4lin_head_loss")
+    _call(device, "fp4lin_head_loss", X.data_ptr(), W.data_ptr(), _code(X), int(bool(by_vocab)),
+          target.data_ptr(), T, H, V, ldx, ldw, _row_floats(loss, T, "loss"),
+          _row_floats(lse, T, "lse"), ws.data_ptr(), _nbytes(ws), _queue(stream, device))
 
 
 def fp4lin_head_loss_backward(X, W, target, lse, dloss, dX, dW, ws, by_vocab=False, stream=None):
@@ -682,11 +694,10 @@ def fp4lin_head_loss_backward(X, W, target, lse, dloss, dX, dW, ws, by_vocab=Fal
         raise ValueError(f"dX is {Tx}x{Hx}, not {T}x{H}")
     if dW.shape != W.shape:
         raise ValueError(f"dW is {r}x{c}, W {W.shape[0]}x{W.shape[1]}")
-    _check(lib().fp4lin_head_loss_backward(
-        X.data_ptr(), W.data_ptr(), _code(X), int(bool(by_vocab)), target.data_ptr(),
-        _row_floats(lse, T, "lse"), _row_floats(dloss, T, "dloss"), T, H, V, ldx, ldw,
-        dX.data_ptr(), lddx, dW.data_ptr(), lddw, ws.data_ptr(), _nbytes(ws),
-        _queue(stream, device)), "fp4lin_head_loss_backward")
+    _call(device, "fp4lin_head_loss_backward", X.data_ptr(), W.data_ptr(), _code(X),
+          int(bool(by_vocab)), target.data_ptr(), _row_floats(lse, T, "lse"),
+          _row_floats(dloss, T, "dloss"), T, H, V, ldx, ldw, dX.data_ptr(), lddx, dW.data_ptr(),
+          lddw, ws.data_ptr(), _nbytes(ws), _queue(stream, device))
 
 
 def _aligned(t):
@@ -796,15 +807,15 @@ def _norm_out(norm, ws, device):
 def fp4lin_grad_norm(tensors, norm, ws, stream=None):
     array, count, _, device = _grads(tensors, None)
     _norm_out(norm, ws, device)
-    _check(lib().fp4lin_grad_norm(array, count, norm.data_ptr(), ws.data_ptr(), _nbytes(ws),
-                                  _queue(stream, device)), "fp4lin_grad_norm")
+    _call(device, "fp4lin_grad_norm", array, count, norm.data_ptr(), ws.data_ptr(), _nbytes(ws),
+          _queue(stream, device))
 
 
 def fp4lin_clip_grads(tensors, max_norm, norm, ws, out=None, stream=None):
     array, count, _, device = _grads(tensors, out)
     _norm_out(norm, ws, device)
-    _check(lib().fp4lin_clip_grads(array, count, float(max_norm), norm.data_ptr(), ws.data_ptr(),
-                                   _nbytes(ws), _queue(stream, device)), "fp4lin_clip_grads")
+    _call(device, "fp4lin_clip_grads", array, count, float(max_norm), norm.data_ptr(),
+          ws.data_ptr(), _nbytes(ws), _queue(stream, device))
 
 
 def _clip(tensors, max_norm, out, stream):
