@@ -169,23 +169,19 @@ __device__ __attribute__((always_inline)) inline void quantize_cols_mx_body(
       for (int j = 0; j < 8; ++j) v[u].v[j] = typename In::T(0);
     }
   }
-  int e[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     BlockMax<kNan> m;
 #pragma unroll
     for (int u = 0; u < 8; ++u) m.take(fabsf(In::widen(v[u].v[j])));
-    e[j] = m.exponent();
-  }
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
+    const int e = m.exponent();
     uint32_t word = 0;
 #pragma unroll
     for (int u = 0; u < 8; ++u)
-      word |= (mx_magnitude(fabsf(In::widen(v[u].v[j])), e[j]) | (In::sign_bit(v[u].v[j]) << 3))
+      word |= (mx_magnitude(fabsf(In::widen(v[u].v[j])), e) | (In::sign_bit(v[u].v[j]) << 3))
               << (4 * u);
     *reinterpret_cast<uint32_t*>(codes + g * kGroup + j * 64 + b * 16 + q * 4) = word;
-    if (q == 0) scales[(g * 8 + j) * 4 + b] = uint8_t(e[j] + 127);
+    if (q == 0) scales[(g * 8 + j) * 4 + b] = uint8_t(e + 127);
   }
   __syncthreads();
 #pragma unroll
