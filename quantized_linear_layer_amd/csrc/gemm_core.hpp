@@ -139,7 +139,7 @@ struct Fp4Feed {
   // codes 32h .. 32h+31 of each 64-code sub-step, i.e. block 4kt + 2kk + h in
   // sub-step kk: the word shifted right by 8h, byte kk*2 of it picked by the
   // instruction's op_sel. Rows past M (N) take the scales of the last row:
-  // their codes are zero, so any finite scale gives zero. One load serves two
+  // their results, zero or NaN with the scale, are not stored. One load serves two
   // fragments (A's two, then B's in pairs): lanes 0..31 read the rows of the
   // first, lanes 32..63 those of the second (64 consecutive rows, 256
   // contiguous bytes), and a lane-half swap (v_permlane32_swap) then gives
@@ -204,15 +204,17 @@ struct Fp4Feed {
     }
   }
 
+  // (offsets are added as unsigned: that of a row outside the operand is its size,
+  // below 2^31, and may pass 2^31 with the step's; it stays past the resource's end)
   __device__ inline void dma(int kt, uint8_t* stage) {
-    const int ka = kt * a_step, kb = kt * b_step;
+    const uint32_t ka = kt * a_step, kb = kt * b_step;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
       uint8_t* const dst = stage + (wave + j * kWaves) * 1024;
       if (j < kPerA)
-        load_lds16(rsA, dst, src_off[j] + ka);
+        load_lds16(rsA, dst, int(uint32_t(src_off[j]) + ka));
       else
-        load_lds16(rsB, dst, src_off[j] + kb);
+        load_lds16(rsB, dst, int(uint32_t(src_off[j]) + kb));
     }
   }
 

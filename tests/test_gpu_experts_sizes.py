@@ -194,3 +194,29 @@ def test_experts_apply_spread_exponents(ql, M, E, K, N, dtype):
     Yb = ql.experts_apply_mx(x, Wq, Ws, re, out_dtype=t.bfloat16)
     assert_bits_equal(host(Yb), host(Y.bfloat16()), "apply in bfloat16")
     check_rows(ql.experts_forward_mx(x, W, re), x, W, counts, 0, "forward")
+
+
+@pytest.mark.parametrize("name", ["forward", "apply"])
+def test_experts_offsets_near_32_bits(ql, name):
+    """2.05 GB of codes of the rows: the offsets of rows outside an expert and of late
+    K steps together pass 2^31. The rows around each expert's ends."""
+    t = torch()
+    counts, K, n = [250001, 0, 249990], 8192, 40
+    M = sum(counts) + 7
+    log(f"experts {name} of {M} x {K}")
+    x = t.empty((M, K), dtype=t.bfloat16, device="cuda:0")
+    g = t.Generator(device="cuda").manual_seed(12)
+    for part in x.split(50000):
+        part.copy_(t.randn(part.shape, generator=g, device="cuda"))
+    W, re = randn((len(counts), K, n), t.bfloat16, 13, 0.02), ends_of(counts)
+    if name == "apply":
+        Y = ql.experts_apply_mx(x, *ql.experts_quantize_weight_mx(W), re)
+    else:
+        Y = ql.experts_forward_mx(x, W, re)
+    assert not bool(Y[sum(counts):].any())
+    for e, (b, end) in enumerate(spans(counts)):
+        w = quantized(W[e], 0)
+        for rows in (slice(b, min(b + 300, end)), slice(max(b, end - 300), end)):
+            if rows.stop > rows.start:
+                q = quantized(x[rows], 1)
+                assert_within(Y[rows], q @ w, q.abs() @ w.abs(), K, f"expert {e}, rows {rows}")
