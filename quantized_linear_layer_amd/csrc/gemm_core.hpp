@@ -426,28 +426,24 @@ __device__ __attribute__((always_inline)) inline void gemm_pipeline_deep(F& f, i
 // are issued in phase 4 kt + 2 at the earliest. Step kt + 1 is read from phase
 // 4 kt + 2 on; every wave has waited for its loads of it by phase 4 kt + 1.
 // Steps past the last one are issued as loads that return nothing (F::dma), so
-// that the counts stay the same on every path.
+// that the counts stay the same on every path. For feeds without block scales.
 template <class F, int S>
 __device__ __attribute__((always_inline)) inline void gemm_pipeline_turns(F& f, int nkt,
                                                                           uint8_t* const (&st)[S]) {
-  constexpr int kPer = F::kPer, NL = F::NL, NS = F::NS, FM = F::FM, FN = F::FN;
-  constexpr int kInFlight = (S - 3) * (kPer + NL) + NL;
-  static_assert((S - 1) * (kPer + NL) < 64, "vmcnt immediate");
-  uint32_t sc[S][NL > 0 ? NL : 1];
+  constexpr int kPer = F::kPer, FM = F::FM, FN = F::FN;
+  static_assert(F::NL == 0 && (S - 1) * kPer < 64, "vmcnt immediate");
   typename F::Frag a0[FM], b0[FN], a1[FM], b1[FN];
-  uint32_t scw[NS > 0 ? NS : 1];
   auto step = [&](int kt, auto i_c) {
     constexpr int i = decltype(i_c)::value;
     constexpr int nxt = (i + 1) % S, prv = (i + S - 1) % S;
     // L, kk = 0
     f.read_frags(st[i], 1, a1, b1);
-    f.expand(sc[i], scw);
     __builtin_amdgcn_sched_barrier(0);
-    __builtin_amdgcn_s_waitcnt(waitcnt_vm(kInFlight));
+    __builtin_amdgcn_s_waitcnt(waitcnt_vm((S - 3) * kPer));
     raw_barrier();
     __builtin_amdgcn_sched_barrier(0);
     __builtin_amdgcn_s_setprio(1);
-    f.template mfmas<0>(a0, b0, scw);
+    f.template mfmas<0>(a0, b0, nullptr);
     __builtin_amdgcn_s_setprio(0);
     __builtin_amdgcn_sched_barrier(0);
     raw_barrier();
@@ -455,12 +451,11 @@ __device__ __attribute__((always_inline)) inline void gemm_pipeline_turns(F& f, 
     // L, kk = 1
     f.read_frags(st[nxt], 0, a0, b0);
     f.dma(kt + S - 1, st[prv]);
-    f.load_scales(kt + S - 1 < nkt ? kt + S - 1 : nkt - 1, sc[prv]);
     __builtin_amdgcn_sched_barrier(0);
     raw_barrier();
     __builtin_amdgcn_sched_barrier(0);
     __builtin_amdgcn_s_setprio(1);
-    f.template mfmas<1>(a1, b1, scw);
+    f.template mfmas<1>(a1, b1, nullptr);
     __builtin_amdgcn_s_setprio(0);
     __builtin_amdgcn_sched_barrier(0);
     raw_barrier();
@@ -469,10 +464,9 @@ __device__ __attribute__((always_inline)) inline void gemm_pipeline_turns(F& f, 
 #pragma unroll
   for (int s = 0; s < S - 1; ++s) {
     f.dma(s, st[s]);
-    f.load_scales(s < nkt ? s : nkt - 1, sc[s]);
     __builtin_amdgcn_sched_barrier(0);
   }
-  __builtin_amdgcn_s_waitcnt(waitcnt_vm((S - 2) * (kPer + NL) + NL));  // step 0 landed
+  __builtin_amdgcn_s_waitcnt(waitcnt_vm((S - 2) * kPer));  // step 0 landed
   raw_barrier();
   f.read_frags(st[0], 0, a0, b0);
   const bool late = f.wave >= 4;
