@@ -479,8 +479,10 @@ fp4lin_status fp4lin_experts_wgrad_mx(const void* A, const void* dY, fp4lin_dtyp
  * copy of X in the order of the products, by the backward always).
  * T = 0 is a valid batch (a weight gradient is all zeros). Sums are fp32; in
  * the backward G, over the largest finite |dloss| of the rows that count, is
- * rounded to dt before the two products that take it. An infinity or NaN among a
- * row's logits makes its loss NaN, and of the gradients the row's dX and all dW.
+ * rounded to dt before the two products that take it. A NaN or +infinity among a
+ * row's logits makes its loss NaN, and of the gradients the row's dX and all dW. A
+ * logit of -infinity has the probability 0 (the target's: loss +infinity) and a finite
+ * G; dX is then what the product with the infinity in W gives.
  * Limits: T <= 2^22, and 256 * ld * element size < 2^31 for the leading
  * dimensions of X and W. */
 typedef enum { FP4LIN_HEAD_HIDDEN_MAJOR = 0, FP4LIN_HEAD_VOCAB_MAJOR = 1 } fp4lin_head_layout;
@@ -514,7 +516,8 @@ fp4lin_status fp4lin_head_loss_backward(const void* X, const void* W, fp4lin_dty
 
 /* ---- Global gradient norm and clipping -------------------------------------
  * Over the elements of all tensors together,
- *   norm = sqrt(sum g^2)     (summed in double, in an order that the sizes fix)
+ *   norm = sqrt(sum g^2)     (summed in double, in an order that the sizes and the
+ *                             tensors' 16-byte alignment fix)
  *   out  = g * c,  c = min(1, max_norm / (norm + 1e-6))    (fp32, rounded once)
  * A NaN in any tensor makes norm and every output NaN; an infinity makes norm
  * infinite, c zero and the infinite elements NaN. */
