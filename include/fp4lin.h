@@ -81,7 +81,8 @@ typedef enum {
   FP4LIN_ERR_WORKSPACE = 7,  /* workspace smaller than the *_workspace_bytes   */
   FP4LIN_ERR_LAUNCH = 8,     /* the HIP runtime rejected a kernel launch        */
   FP4LIN_ERR_SCRATCH = 9,    /* beyond the allocation-free call's static scratch */
-  FP4LIN_ERR_VALUE = 10      /* a number argument is NaN or outside its range   */
+  FP4LIN_ERR_VALUE = 10,     /* a number argument is NaN or outside its range   */
+  FP4LIN_ERR_OVERLAP = 11    /* memory that is written overlaps an operand's    */
 } fp4lin_status;
 
 typedef enum { FP4LIN_F32 = 0, FP4LIN_BF16 = 1 } fp4lin_dtype;
@@ -541,9 +542,10 @@ fp4lin_status fp4lin_grad_norm(const fp4lin_grad* grads /* host */, int64_t coun
                                void* ws, size_t ws_bytes, hipStream_t stream);
 
 /* The norm and the clipped gradients. With out = g nothing is written where
- * c = 1. max_norm must be a number >= 0, else FP4LIN_ERR_VALUE. A tensor must
- * not be listed twice.
- * Errors: NULL, SHAPE, DTYPE, VALUE, ALIGN, WORKSPACE, LAUNCH. */
+ * c = 1. max_norm must be a number >= 0, else FP4LIN_ERR_VALUE. No output may
+ * overlap another or a gradient that is not its own (nor its own, but as out = g),
+ * else FP4LIN_ERR_OVERLAP: a tensor that is clipped in place is listed once.
+ * Errors: NULL, SHAPE, DTYPE, VALUE, ALIGN, OVERLAP, WORKSPACE, LAUNCH. */
 fp4lin_status fp4lin_clip_grads(const fp4lin_grad* grads /* host */, int64_t count,
                                 double max_norm, float* norm, void* ws, size_t ws_bytes,
                                 hipStream_t stream);

@@ -842,5 +842,7 @@ def grad_norm(tensors, stream=None):
 
 def clip_grads(tensors, max_norm, out=None, stream=None):
     """Scales the tensors by min(1, max_norm / (norm + 1e-6)), norm their global
-    2-norm, in place or into the list `out`; returns norm (on the GPU)."""
+    2-norm, in place or into the list `out`; returns norm (on the GPU). No output may
+    overlap another tensor of the lists but its own gradient: a gradient that two
+    weights share is listed once."""
     return _clip(tensors, max_norm, out, stream)

@@ -14,7 +14,7 @@ c_int = ctypes.c_int
 
 # enum values of fp4lin_status / fp4lin_dtype
 OK, ERR_NULL, ERR_SHAPE, ERR_DTYPE, ERR_QUANTILE, ERR_CAPACITY, ERR_ALIGN, ERR_WORKSPACE, \
-    ERR_LAUNCH, ERR_SCRATCH, ERR_VALUE = range(11)
+    ERR_LAUNCH, ERR_SCRATCH, ERR_VALUE, ERR_OVERLAP = range(12)
 F32, BF16 = 0, 1
 # fp4lin_head_layout
 HEAD_HIDDEN_MAJOR, HEAD_VOCAB_MAJOR = 0, 1

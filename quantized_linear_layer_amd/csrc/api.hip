@@ -1,6 +1,7 @@
 // C ABI of libfp4lin.so: argument checks, workspace layout and launches.
 // Every check runs on the host before anything is enqueued; no call allocates,
 // frees, synchronises or reads device memory.
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <mutex>
@@ -171,6 +172,7 @@ const char* fp4lin_status_str(fp4lin_status s) {
     case FP4LIN_ERR_LAUNCH: return "kernel launch failed";
     case FP4LIN_ERR_SCRATCH: return "input needs more than the static scratch of the allocation-free call";
     case FP4LIN_ERR_VALUE: return "a number argument is NaN or out of range";
+    case FP4LIN_ERR_OVERLAP: return "an output overlaps another one or an operand";
   }
   return "unknown status";
 }
@@ -879,6 +881,53 @@ size_t clip_ws(int64_t count, int64_t elements) {
   return round_up(16 + size_t(fp4lin::clip_parts(count, elements)) * 8, 256);
 }
 
+// Whether memory that one workgroup writes is read or written by another tensor's:
+// an output over another output or over a gradient not its own. (Gradients that are
+// only read may overlap.) Sorted spans, kBlock tensors at a time on the stack; of more,
+// every two blocks together. 42 tensors: below 1 us.
+constexpr int64_t kBlock = 512;
+struct Span {
+  uintptr_t begin, end;
+  bool written;
+};
+
+int spans_of(const fp4lin_grad* grads, int64_t count, int64_t block, Span* s) {
+  int n = 0;
+  const int64_t last = std::min(count, (block + 1) * kBlock);
+  for (int64_t i = block * kBlock; i < last; ++i) {
+    const fp4lin_grad& x = grads[i];
+    if (x.n == 0) continue;
+    const uintptr_t bytes = uintptr_t(x.n) * (x.dt == FP4LIN_BF16 ? 2 : 4);
+    const uintptr_t out = reinterpret_cast<uintptr_t>(x.out), g = reinterpret_cast<uintptr_t>(x.g);
+    s[n++] = Span{out, out + bytes, true};
+    if (g != out) s[n++] = Span{g, g + bytes, false};
+  }
+  return n;
+}
+
+bool spans_meet(Span* s, int n) {
+  std::sort(s, s + n, [](const Span& a, const Span& b) { return a.begin < b.begin; });
+  uintptr_t read = 0, written = 0;  // ends of what came before
+  for (int i = 0; i < n; ++i) {
+    if (s[i].begin < written || (s[i].written && s[i].begin < read)) return true;
+    uintptr_t& end = s[i].written ? written : read;
+    end = std::max(end, s[i].end);
+  }
+  return false;
+}
+
+bool outputs_overlap(const fp4lin_grad* grads, int64_t count) {
+  Span s[4 * kBlock];
+  const int64_t blocks = (count + kBlock - 1) / kBlock;
+  if (blocks <= 1) return spans_meet(s, spans_of(grads, count, 0, s));
+  for (int64_t i = 0; i < blocks; ++i)
+    for (int64_t j = i + 1; j < blocks; ++j) {
+      const int n = spans_of(grads, count, i, s);
+      if (spans_meet(s, n + spans_of(grads, count, j, s + n))) return true;
+    }
+  return false;
+}
+
 fp4lin_status clip_impl(const fp4lin_grad* grads, int64_t count, bool clip, double max_norm,
                         float* norm, void* ws, size_t ws_bytes, hipStream_t stream) {
   if (norm == nullptr || ws == nullptr || (count > 0 && grads == nullptr)) return FP4LIN_ERR_NULL;
@@ -899,6 +948,7 @@ fp4lin_status clip_impl(const fp4lin_grad* grads, int64_t count, bool clip, doub
   }
   if (clip && !(max_norm >= 0.0)) return FP4LIN_ERR_VALUE;
   if (!aligned16(ws)) return FP4LIN_ERR_ALIGN;
+  if (clip && outputs_overlap(grads, count)) return FP4LIN_ERR_OVERLAP;
   if (ws_bytes < clip_ws(count, elements)) return FP4LIN_ERR_WORKSPACE;
   return launch_status(
       fp4lin::launch_clip(grads, count, elements, clip, float(max_norm), norm, ws, stream));

@@ -90,3 +90,29 @@ def test_packed_weight_buffers(ql):
     ql.fp4lin_experts_quantize_weight_mx(W, q, s)
     assert_bits_equal(host(q), host(Wq), "codes")
     assert_bits_equal(host(s), host(Ws), "scales")
+
+
+def test_clip_refuses_shared_memory(ql):
+    """Two workgroups would scale the same elements: an output listed twice, or one
+    that is another output's gradient. The norm alone may count a tensor twice, and
+    tensors without elements may share their address."""
+    t = torch()
+    a, b = t.full((100,), 3.0, device="cuda:0"), t.full((100,), 4.0, device="cuda:0")
+    none = t.empty(0, device="cuda:0")
+    log("clipping of shared memory")
+    c, d = t.empty_like(a), t.empty_like(a)
+    ws, norm = t.empty(4096, dtype=t.uint8, device="cuda:0"), t.zeros((), device="cuda:0")
+    for grads, out in (([a, b, a], None), ([a, b], [c, c]), ([a, b], [b, c]), ([a, b], [b, a]), ([a, a], [a, c]),
+                       ([a[1:]], [a[:-1]])):
+        with pytest.raises(ql.Fp4linError):
+            ql.clip_grads(grads, 1.0, out=out)
+        with pytest.raises(ql.Fp4linError):
+            ql.fp4lin_clip_grads(grads, 1.0, norm, ws, out=out)
+    assert bool((a == 3.0).all()) and bool((b == 4.0).all())
+    assert float(ql.grad_norm([a, a])) == pytest.approx(1800 ** 0.5)
+    assert float(ql.clip_grads([a, none, b, none], 1e9, out=[c, none, d, none])) == 50.0
+    assert t.equal(a, c) and t.equal(b, d)
+    ql.clip_grads([a, a], 1e9, out=[c, d])
+    ql.clip_grads([a, b, none], 1e9, out=[a, c, none])
+    ql.clip_grads([none, a, none, b], 1e9)
+    assert t.equal(b, c) and t.equal(a, d) and bool((a == 3.0).all())
