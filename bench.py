@@ -111,6 +111,20 @@ def file_sha(path):
         return hashlib.sha256(f.read()).hexdigest()
 
 
+def measured_traffic(name):
+    """HBM bytes a launch of a profile's summary, or None if there is none or one of the
+    kernel's sources (the file, and the header its pipeline is in) has changed since."""
+    path = os.path.join(ROOT, "profiles", name)
+    if not os.path.exists(path):
+        return None
+    with open(path) as f:
+        tr = json.load(f)
+    sources = {tr["source"]: tr["source_sha256"], **tr.get("headers_sha256", {})}
+    if any(file_sha(os.path.join(ROOT, source)) != sha for source, sha in sources.items()):
+        return None
+    return tr.get("bytes_per_launch")
+
+
 class Step:
     """Marshals the four stage calls once; each call is then a bare C call."""
 
@@ -288,13 +302,9 @@ def run_forward_mx(args):
     kernels["sparse"].update({"bound": "alu", "fp32_TFLOP/s": round(sp_tf, 2),
                               "alu_frac": round(sp_tf / VALU_FP32_PEAK_TFLOPS, 4)})
     dom = max(STAGES, key=lambda n: stage_ms[n])
-    traffic = None
     tname = {"gemm": f"traffic_gemm_{args.workload}_mx.json",
              "sparse": f"traffic_sparse_{args.workload}_mx.json"}.get(dom)
-    if tname and os.path.exists(os.path.join(ROOT, "profiles", tname)):
-        tr = json.load(open(os.path.join(ROOT, "profiles", tname)))
-        if tr.get("source_sha256") == file_sha(os.path.join(ROOT, tr["source"])):
-            traffic = tr.get("bytes_per_launch")
+    traffic = measured_traffic(tname) if tname else None
     if dom == "sparse":
         roof = {"bound": "alu", "kernel": "sparse_add_kernel", "achieved": round(sp_tf, 2),
                 "peak": VALU_FP32_PEAK_TFLOPS, "unit": "TFLOP/s",
@@ -487,13 +497,8 @@ def run_backward(args):
                            "bound": "hbm"},
                "gemm": {"ms": round(stage_ms["gemm"], 5), "TFLOP/s": round(gemm_tf, 1),
                         "mfma_frac": round(gemm_tf / FP4_PEAK_TFLOPS, 4), "bound": "mfma"}}
-    traffic = None
     tag = f"{args.workload}_{args.which}" + ("_mx" if mx else "")
-    tfile = os.path.join(ROOT, "profiles", f"traffic_gemm_{tag}.json")
-    if os.path.exists(tfile):
-        tr = json.load(open(tfile))
-        if tr.get("source_sha256") == file_sha(os.path.join(ROOT, tr["source"])):
-            traffic = tr.get("bytes_per_launch")
+    traffic = measured_traffic(f"traffic_gemm_{tag}.json")
     value = flops / (ms_per_step * 1e-3) / 1e12
     what = {"dgrad": "dX = Q(dY) Q(W)^T", "wgrad": "dW = Q(A)^T Q(dY)"}[args.which]
     out = {
@@ -714,12 +719,7 @@ def main():
     for name in ("select", "quant_a", "quant_w"):
         kernels[name]["bound"] = "hbm"
     dom = max(STAGES, key=lambda n: stage_ms[n])
-    traffic = None
-    tfile = os.path.join(ROOT, "profiles", f"traffic_{dom}_{args.workload}.json")
-    if os.path.exists(tfile):
-        tr = json.load(open(tfile))
-        if tr.get("source_sha256") == file_sha(os.path.join(ROOT, tr["source"])):
-            traffic = tr.get("bytes_per_launch")
+    traffic = measured_traffic(f"traffic_{dom}_{args.workload}.json")
     if dom == "gemm":
         roof = {"bound": "mfma", "kernel": "fp4_gemm_kernel", "achieved": round(gemm_tf, 2),
                 "peak": FP4_PEAK_TFLOPS, "unit": "TFLOP/s", "frac": round(gemm_tf / FP4_PEAK_TFLOPS, 4),
