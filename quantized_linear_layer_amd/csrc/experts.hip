@@ -165,8 +165,8 @@ __device__ inline void quantize_rows_part(const RowsArgs& p, int id) {
 }
 
 // Rows of two matrices (dgrad: dY and the weights; apply: the activations alone).
-// Bound by memory: 16 experts 2048 x 5632 and 8192 rows 128 us for 461 MB read and
-// 122 MB written (4.6 TB/s).
+// Bound by memory: 16 experts 2048 x 5632 and 8192 rows 122 us for 461 MB read and
+// 122 MB written (4.8 TB/s).
 template <class In, bool kFast, int kRows>
 __global__ __launch_bounds__(kThreads) void experts_rows_mx_kernel(RowsArgs a, RowsArgs b) {
   const int id = blockIdx.x, na = a.gx * a.gy;
@@ -178,8 +178,8 @@ __global__ __launch_bounds__(kThreads) void experts_rows_mx_kernel(RowsArgs a, R
 
 // Weights along K (rows of W[e]), a 128 x 128 tile a workgroup; with kRows > 0
 // rows of the activations first. Scales go to one step-major array over the E * N
-// columns of all experts. Bound by memory: 8 experts 4096 x 11008 and 8192 rows 188
-// us for 788 MB read and 209 MB written (5.3 TB/s; a copy reaches 5.2).
+// columns of all experts. Bound by memory: 8 experts 4096 x 11008 and 8192 rows 192
+// us for 788 MB read and 209 MB written (5.2 TB/s, as a copy).
 template <class In, bool kFast, int kRows>
 __global__ __launch_bounds__(kThreads) void experts_cols_mx_kernel(RowsArgs a, ColsArgs w) {
   int id = blockIdx.x;
@@ -200,8 +200,8 @@ __global__ __launch_bounds__(kThreads) void experts_cols_mx_kernel(RowsArgs a, C
 
 // Activations and gradients along each expert's own rows: K step blockIdx.y of
 // all experts' steps (128 rows each, the last one of an expert filled with zeros)
-// and 128 columns of A (K of them) or, past those, of dY (N). 67 to 84 us for 247 MB
-// read and 66 MB written (8192 rows, 4096 and 11008 columns).
+// and 128 columns of A (K of them) or, past those, of dY (N). 60 us for 247 MB read
+// and 66 MB written (8192 rows, 4096 and 11008 columns; 5.2 TB/s).
 struct RaggedArgs {
   const void *A, *dY;
   const int32_t* row_end;
@@ -242,10 +242,12 @@ struct TileArgs {
 };
 
 // Bound by what the tiles write and by the matrix core in turn, as a 256 x 256 tile
-// has a CU to itself: the forward of 8192 rows, 8 experts 4096 x 11008, 230 us (3.2
-// PFLOP/s), of which 60 are the 361 MB of fp32 output; without it the loop runs at 4.2
-// PFLOP/s (the instruction stream alone reaches 5.7). The wgrad there has four or
-// five K steps a tile and writes 1.44 GB: 350 us, 276 of them for the writes alone.
+// has a CU to itself. Launched alone, one after the other: the product of the forward
+// of 8192 rows, 8 experts 4096 x 11008, 218 us (3.4 PFLOP/s); without its stores (361
+// MB of fp32) 174 us, 4.2 PFLOP/s (the instruction stream alone reaches 5.7), without
+// its loop 72. The wgrad there has four or five K steps a tile and writes 1.44 GB: 390
+// us, 248 without the stores, 281 without the loop. (Under the profiler, at lower
+// clocks, 285 and 387.)
 //
 // kWgrad false: forward and dgrad, A the rows of the activations, B the weights
 // of all experts (cols rows each). kWgrad true: A and B the columns of the
@@ -465,11 +467,11 @@ hipError_t run_few(const FewArgs& a, hipStream_t stream) {
 // fill them once, else of 64 x 128; the last also for few rows an expert, where
 // a product is a read of the weights' codes and more workgroups on their way
 // read faster (8 experts 4096x11008, whole call: 128 rows 47 against 53 us with
-// 128 x 256 tiles, 256 rows 51 against 57, 512 rows 60 against 62). Whole calls (when
-// the first took 20 us longer to quantize its operands than it does now) with
-// 256 x 256 / 128 x 256 / 64 x 128 tiles alone: forward of 8192 rows, 8 experts
-// 4096x11008 445 / 453 / 514 us, of 2048 rows 283 / 269 / 286, of 1024 rows, 8 experts
-// 2048x5632 71 / 74 / 69; dgrad of 8192 rows, 16 experts 2048x5632 202 / 199 / 210.
+// 128 x 256 tiles, 256 rows 51 against 57, 512 rows 60 against 62). Whole calls with 256 x
+// 256 / 128 x 256 / 64 x 128 tiles alone: forward of 8192 rows, 8 experts 4096x11008
+// 429 / 437 / 488 us, of 2048 rows 275 / 261 / 284, of 1024 rows, 8 experts 2048x5632
+// 61 / 64 / 62, of 8192 rows, 16 experts 189 / 198 / 221 and 64 experts (whose large
+// tiles are half empty) 509 / 494 / 511; dgrad of 8192 rows, 16 experts 202 / 195 / 212.
 template <class Out>
 hipError_t run_rows(const TileArgs& p, hipStream_t stream) {
   const int64_t tiles_n = ceil_div(p.cols, 256);
@@ -483,9 +485,9 @@ hipError_t run_rows(const TileArgs& p, hipStream_t stream) {
       p, most_units(p.M, p.E, FewTile::BM) * ceil_div(p.cols, FewTile::BN), stream);
 }
 
-// The same choice: 4096 rows, 8 experts 1024x2816 41 us with 256 x 256 tiles, 37 with
-// 128 x 256 (352 large tiles); 8192 rows, 8 experts 4096x11008 434 and 430, 16384 rows,
-// 4 experts 2048x5632 191 and 192.
+// The same choice: 4096 rows, 8 experts 1024x2816 42 us with 256 x 256 tiles, 39 with
+// 128 x 256 (352 large tiles); 16384 rows, 4 experts 2048x5632 211 and 217. (8192 rows,
+// 8 experts 4096x11008, with few K steps a tile: 454 and 438, on another card 434 and 430.)
 template <class Out>
 hipError_t run_wgrad(const TileArgs& p, hipStream_t stream) {
   const int64_t tiles_n = ceil_div(p.cols, 256);

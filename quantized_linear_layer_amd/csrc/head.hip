@@ -19,7 +19,10 @@
 // between the three products (kPieceBytes), which is also what bounds the
 // workspace. G is rounded once to the inputs' type (bfloat16: 2^-9 of each
 // element, as the two products it feeds take bfloat16 operands); every sum is
-// fp32.
+// fp32. Both sides of that choice, bfloat16 4096 x 2048 and 8192 x 4096 by 32000: as it
+// is the gradients are off by 0.0019 of their norm, and loss and gradients take 1.93
+// and 7.16 ms; with G in two bfloat16 parts, which makes both products twice as long,
+// they are off by 0.0017, their own rounding to bfloat16 alone, and take 2.88 and 10.73.
 //
 // dX sums over the vocabulary, so few rows leave few tiles: the reduction is
 // then split over workgroups, each adding into an fp32 array of its own, and the
@@ -113,11 +116,11 @@ struct HeadArgs {
 };
 
 // One (m, s) a row and wave, and the targets' logits. Bound by the matrix core and
-// its clock under load: 8192 x 4096 by 32000 in bfloat16 1.77 ms (1.22 PFLOP/s, the
+// its clock under load: 8192 x 4096 by 32000 in bfloat16 1.83 ms (1.18 PFLOP/s, the
 // matrix core busy 0.77 at 1.63 GHz; a library's plain product of the size reaches
 // 1.42). The pair leaves instead of 256 columns of logits, so the tile's way out is
 // 8 bytes a row and wave. With 32 rows the kernel is a read of W: 43 us for 262 MB
-// (6.1 TB/s). float32 1001 x 515 by 5003: 59 us (87 TFLOP/s).
+// (6.1 TB/s). float32 1001 x 515 by 5003: 64 us (81 TFLOP/s).
 template <class C, class T, int kBT>
 __global__ __launch_bounds__(C::kThreads, C::kMinBlocks) void head_lse_kernel(HeadArgs<T> p) {
   constexpr int FM = C::FM, FN = C::FN;
@@ -222,7 +225,7 @@ constexpr bool kGPieces = sizeof(T) == 2;
 
 // G of a piece of the vocabulary over the largest |dloss|, zeros in the columns
 // that pad it to a multiple of 32 (float32: 8). As head_lse_kernel bound by the
-// matrix core: 8192 x 4096 by 8192 columns in 450 us (1.22 PFLOP/s).
+// matrix core: 8192 x 4096 by 8192 columns in 471 us (1.17 PFLOP/s).
 template <class C, class T, int kBT>
 __global__ __launch_bounds__(C::kThreads, C::kMinBlocks) void head_grad_kernel(HeadArgs<T> p) {
   constexpr int FM = C::FM, FN = C::FN;
@@ -307,7 +310,7 @@ __device__ inline int64_t at_step(const DenseOperand<T>& o, int k0) {
 // A product of two operands, or of slice blockIdx.z of their reduction. kAdd: into
 // the fp32 array of the slice (Y + z * slice_elems), on top of what is there
 // unless `first`. Measured on a piece of 8192 columns, 8192 x 4096 in bfloat16: dX
-// 441 us (1.25 PFLOP/s, matrix core busy 0.76), dW 403 us (1.36, busy 0.82; both
+// 461 us (1.19 PFLOP/s, matrix core busy 0.76), dW 427 us (1.29, busy 0.82; both
 // operands are read in whole cache lines).
 template <class T, class Out>
 struct ProductArgs {
