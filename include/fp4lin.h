@@ -460,6 +460,99 @@ fp4lin_status fp4lin_experts_wgrad_mx(const void* A, const void* dY, fp4lin_dtyp
                                       fp4lin_dtype wdt, int64_t lddw, void* ws, size_t ws_bytes,
                                       hipStream_t stream);
 
+/* ---- Rows of tokens to their experts and back --------------------------------
+ * T tokens go to k experts each. Slot t * k + j is token t's j-th; the M = T * k
+ * slots are sorted by expert, slots of one expert in their order. A slot whose
+ * expert lies outside [0, E) carries nothing: it comes last, behind row_end[E-1].
+ *   expert    device, M int32
+ *   row_end   device, E int32: the ends of the experts' rows, as the products above
+ *             take them
+ *   slot_row  device, M int32: the row of each slot, all of 0 .. M - 1 once
+ * Rows of any length and stride, at the alignment of their elements. Sums are fp32,
+ * a token's slots in order, rounded once where the output is bfloat16. No output
+ * may overlap another array of the call, but for out = residual at the same stride.
+ * T = 0 is a valid batch (row_end is zeros; the other pointers may be NULL).
+ * Limits: M <= 2^30, E <= 65534, T * ceil(H / 8) < 2^32. */
+
+/* Xs[slot_row[t * k + j], :] = X[t, :], zeros for a slot that carries nothing.
+ *   X         device, T x H, dtype dt, leading dimension ldx
+ *   Xs        device, M x H, dtype dt, leading dimension ldxs (output)
+ *   row_end, slot_row  outputs
+ * Errors: NULL, SHAPE, DTYPE, ALIGN, LAUNCH. */
+fp4lin_status fp4lin_experts_dispatch(const void* X, fp4lin_dtype dt, const int32_t* expert,
+                                      int64_t T, int64_t k, int64_t E, int64_t H, int64_t ldx,
+                                      void* Xs, int64_t ldxs, int32_t* row_end, int32_t* slot_row,
+                                      hipStream_t stream);
+
+/* out[t, :] = residual[t, :] + sum_j weight[t * k + j] * Y[slot_row[t * k + j], :]
+ * over the slots whose row lies below row_end[E-1]; what Y holds elsewhere (and the
+ * other slots' weights) has no part. Without weights and residual it is the gradient
+ * of the dispatch.
+ *   Y         device, M x H, dtype ydt, leading dimension ldy
+ *   slot_row, row_end  as the dispatch leaves them (a row outside [0, M) counts as
+ *             one that carries nothing)
+ *   weight    device, M floats, or NULL: ones
+ *   residual  device, T x H, dtype odt, leading dimension ldr, or NULL: zeros
+ *   out       device, T x H, dtype odt, leading dimension ldo (output)
+ * Errors: NULL, SHAPE, DTYPE, ALIGN, LAUNCH. */
+fp4lin_status fp4lin_experts_combine(const void* Y, fp4lin_dtype ydt, const int32_t* slot_row,
+                                     const int32_t* row_end, const float* weight,
+                                     const void* residual, int64_t T, int64_t k, int64_t E,
+                                     int64_t H, int64_t ldy, int64_t ldr, void* out,
+                                     fp4lin_dtype odt, int64_t ldo, hipStream_t stream);
+
+/* Gradients of the above (that of the residual is dout itself):
+ *   dY[slot_row[t * k + j], :] = weight[t * k + j] * dout[t, :]
+ *   dweight[t * k + j]         = sum_h dout[t, h] * Y[slot_row[t * k + j], h]
+ * Zeros in the rows from row_end[E-1] on and for their slots' weights.
+ *   dout      device, T x H, dtype odt, leading dimension lddo
+ *   Y         device, M x H, dtype ydt, leading dimension ldy (without dweight not
+ *             read and may be NULL)
+ *   weight    device, M floats, or NULL: ones
+ *   dY        device, M x H, dtype dydt, leading dimension lddy (output)
+ *   dweight   device, M floats, or NULL: not computed (output)
+ * Errors: NULL, SHAPE, DTYPE, ALIGN, LAUNCH. */
+fp4lin_status fp4lin_experts_combine_backward(const void* dout, fp4lin_dtype odt, const void* Y,
+                                              fp4lin_dtype ydt, const int32_t* slot_row,
+                                              const int32_t* row_end, const float* weight,
+                                              int64_t T, int64_t k, int64_t E, int64_t H,
+                                              int64_t lddo, int64_t ldy, void* dY,
+                                              fp4lin_dtype dydt, int64_t lddy, float* dweight,
+                                              hipStream_t stream);
+
+/* ---- Embedding ------------------------------------------------------------------
+ * Rows of any length and stride, at the alignment of their elements. No output may
+ * overlap another array of the call. T = 0 is a valid batch.
+ * Limits: T, V <= 2^30; T * ceil(H / 8) and V * ceil(H / 8) < 2^32. */
+
+/* out[t, :] = scale * table[token[t], :], zeros for a token outside [0, V).
+ *   table     device, V x H, dtype dt, leading dimension ldt
+ *   token     device, T int32
+ *   scale     rounded to fp32; a number, else FP4LIN_ERR_VALUE
+ *   out       device, T x H, dtype odt, leading dimension ldo (output), rounded once
+ * Errors: NULL, SHAPE, DTYPE, VALUE, ALIGN, LAUNCH. */
+fp4lin_status fp4lin_embed(const void* table, fp4lin_dtype dt, const int32_t* token, int64_t T,
+                           int64_t V, int64_t H, int64_t ldt, double scale, void* out,
+                           fp4lin_dtype odt, int64_t ldo, hipStream_t stream);
+
+/* Bytes of workspace of the gradient (at least 256); 0 for invalid arguments. */
+size_t fp4lin_embed_backward_workspace_bytes(int64_t T, int64_t V, int64_t H);
+
+/* dE[v, :] = scale * sum of dX[t, :] over the positions t with token[t] = v, in fp32 in
+ * an order that the tokens fix: results repeat bit for bit. Rows without a position
+ * are zeros. Positions whose token lies outside [0, V) have no part, whatever dX
+ * holds there.
+ *   dX        device, T x H, dtype dt, leading dimension lddx
+ *   add       not 0: dE += instead, the sum rounded once to dE's type with what was
+ *             there; rows without a position stay as they are
+ *   dE        device, V x H, dtype edt, leading dimension ldde (output)
+ *   ws        device, 16-byte aligned, >= fp4lin_embed_backward_workspace_bytes
+ * Errors: NULL, SHAPE, DTYPE, VALUE, ALIGN, WORKSPACE, LAUNCH. */
+fp4lin_status fp4lin_embed_backward(const void* dX, fp4lin_dtype dt, const int32_t* token, int64_t T,
+                                    int64_t V, int64_t H, int64_t lddx, double scale, int add,
+                                    void* dE, fp4lin_dtype edt, int64_t ldde, void* ws,
+                                    size_t ws_bytes, hipStream_t stream);
+
 /* ---- Head loss: softmax cross entropy of a large vocabulary ----------------
  *   l = X W,  lse_t = log sum_v exp l_tv,  loss_t = lse_t - l_(t, target_t)
  *   G_tv = (exp(l_tv - lse_t) - [v = target_t]) * dloss_t

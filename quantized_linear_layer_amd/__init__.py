@@ -29,6 +29,9 @@ __all__ = [
     "fp4lin_experts_apply_mx", "fp4lin_experts_dgrad_mx", "fp4lin_experts_wgrad_mx",
     "experts_quantize_weight_mx", "experts_forward_mx", "experts_apply_mx", "experts_dgrad_mx",
     "experts_wgrad_mx",
+    "fp4lin_experts_dispatch", "fp4lin_experts_combine", "fp4lin_experts_combine_backward",
+    "experts_dispatch", "experts_combine", "experts_combine_backward",
+    "embed_backward_workspace_bytes", "fp4lin_embed", "fp4lin_embed_backward", "embed", "embed_backward",
     "head_loss_workspace_bytes", "fp4lin_head_loss", "fp4lin_head_loss_backward", "head_loss",
     "head_loss_backward", "clip_workspace_bytes", "fp4lin_grad_norm", "fp4lin_clip_grads",
     "grad_norm", "clip_grads",
@@ -643,6 +646,193 @@ def experts_wgrad_mx(A, dY, row_end, out_dtype=None, stream=None):
         ws = _experts_ws(_lib.EXPERTS_WGRAD, E, M, K, N, A.device, "experts_wgrad_mx")
         fp4lin_experts_wgrad_mx(A, dY, row_end, dW, ws)
     return dW
+
+
+# ---- rows of tokens to their experts and back --------------------------------------------
+def _vector(t, dtype, n, name):
+    """The address of a contiguous array of n elements."""
+    if t.dtype != dtype or not t.is_contiguous():
+        raise TypeError(f"{name} must be a contiguous {dtype} tensor")
+    if t.numel() != n:
+        raise ValueError(f"{name} has {t.numel()} entries, not {n}")
+    return t.data_ptr()
+
+
+def _slots(t, name, T=None):
+    """(tokens, slots a token) of an int32 array (tokens, slots), or (tokens,) of one each."""
+    size = t.shape
+    if t.dtype != _torch().int32 or not t.is_contiguous():
+        raise TypeError(f"{name} must be a contiguous int32 tensor")
+    if len(size) not in (1, 2) or (len(size) == 2 and size[1] < 1):
+        raise ValueError(f"{name} must be (tokens, slots) or (tokens,)")
+    if T is not None and size[0] != T:
+        raise ValueError(f"{name} is for {size[0]} tokens, not {T}")
+    return size[0], size[1] if len(size) == 2 else 1
+
+
+def _matrix_of(t, rows, columns, name):
+    """The row stride of a rows x columns matrix."""
+    r, c, ld = _rows(t, name)
+    if r != rows or c != columns:
+        raise ValueError(f"{name} is {r}x{c}, not {rows}x{columns}")
+    return ld
+
+
+def fp4lin_experts_dispatch(X, expert, Xs, row_end, slot_row, stream=None):
+    T, H, ldx = _rows(X, "X")
+    T, k = _slots(expert, "expert", T)
+    device = _gpu(("X", X), ("expert", expert), ("Xs", Xs), ("row_end", row_end), ("slot_row", slot_row))
+    _same_dtype(X, Xs, "X and Xs")
+    E = row_end.numel()
+    ldxs = _matrix_of(Xs, T * k, H, "Xs")
+    _call(device, "fp4lin_experts_dispatch", X.data_ptr(), _code(X), expert.data_ptr(), T, k, E, H, ldx,
+          Xs.data_ptr(), ldxs, _row_end(row_end, E),
+          _vector(slot_row, expert.dtype, T * k, "slot_row"), _queue(stream, device))
+
+
+def _weight(weight, T, k):
+    return None if weight is None else _vector(weight, _torch().float32, T * k, "weight")
+
+
+def fp4lin_experts_combine(Y, slot_row, row_end, out, weight=None, residual=None, stream=None):
+    T, H, ldo = _rows(out, "out")
+    T, k = _slots(slot_row, "slot_row", T)
+    ldy = _matrix_of(Y, T * k, H, "Y")
+    some = [(n, t) for n, t in (("weight", weight), ("residual", residual)) if t is not None]
+    device = _gpu(("Y", Y), ("slot_row", slot_row), ("row_end", row_end), ("out", out), *some)
+    ldr, res = 0, None
+    if residual is not None:
+        _same_dtype(residual, out, "residual and out")
+        ldr, res = _matrix_of(residual, T, H, "residual"), residual.data_ptr()
+    E = row_end.numel()
+    _call(device, "fp4lin_experts_combine", Y.data_ptr(), _code(Y), slot_row.data_ptr(),
+          _row_end(row_end, E), _weight(weight, T, k), res, T, k, E, H, ldy, ldr, out.data_ptr(),
+          _code(out), ldo, _queue(stream, device))
+
+
+def fp4lin_experts_combine_backward(dout, Y, slot_row, row_end, dY, weight=None, dweight=None, stream=None):
+    T, H, lddo = _rows(dout, "dout")
+    T, k = _slots(slot_row, "slot_row", T)
+    lddy = _matrix_of(dY, T * k, H, "dY")
+    some = [(n, t) for n, t in (("Y", Y), ("weight", weight), ("dweight", dweight)) if t is not None]
+    device = _gpu(("dout", dout), ("slot_row", slot_row), ("row_end", row_end), ("dY", dY), *some)
+    y, ydt, ldy, dw = None, F32, 0, None
+    if dweight is not None:
+        _need(Y is not None, "dweight needs Y")
+        y, ydt, ldy = Y.data_ptr(), _code(Y), _matrix_of(Y, T * k, H, "Y")
+        dw = _vector(dweight, _torch().float32, T * k, "dweight")
+    E = row_end.numel()
+    _call(device, "fp4lin_experts_combine_backward", dout.data_ptr(), _code(dout), y, ydt,
+          slot_row.data_ptr(), _row_end(row_end, E), _weight(weight, T, k), T, k, E, H, lddo, ldy,
+          dY.data_ptr(), _code(dY), lddy, dw, _queue(stream, device))
+
+
+def experts_dispatch(X, expert, experts, stream=None):
+    """The rows of X (T, H) sorted by expert, as the products above take them. expert
+    (T, k) or (T,) int32: each token's experts; one outside [0, experts) carries
+    nothing. Returns (Xs (T * k, H), row_end (experts,), slot_row of expert's shape):
+    slot_row is each slot's row, the rows from row_end[-1] on are zeros. The gradient
+    of X is experts_combine(dXs, slot_row, row_end)."""
+    torch = _torch()
+    T, H, _ = _rows(X, "X")
+    T, k = _slots(expert, "expert", T)
+    with _on(X, stream):
+        Xs = torch.empty((T * k, H), dtype=X.dtype, device=X.device)
+        row_end = torch.empty(experts, dtype=torch.int32, device=X.device)
+        slot_row = torch.empty_like(expert)
+        fp4lin_experts_dispatch(X, expert, Xs, row_end, slot_row)
+    return Xs, row_end, slot_row
+
+
+def experts_combine(Y, slot_row, row_end, weight=None, residual=None, out_dtype=None, stream=None):
+    """out (T, H) = residual + the sum over a token's slots of weight (float32, of
+    slot_row's shape) times their rows of Y (T * k, H). slot_row and row_end are
+    experts_dispatch's; slots that carry nothing have no part. out_dtype: the
+    residual's, else Y's by default."""
+    torch = _torch()
+    T, k = _slots(slot_row, "slot_row")
+    H = _rows(Y, "Y")[1]
+    with _on(Y, stream):
+        dtype = out_dtype or (Y if residual is None else residual).dtype
+        out = torch.empty((T, H), dtype=dtype, device=Y.device)
+        fp4lin_experts_combine(Y, slot_row, row_end, out, weight, residual)
+    return out
+
+
+def experts_combine_backward(dout, Y, slot_row, row_end, weight=None, out_dtype=None, stream=None):
+    """Gradients of experts_combine from that of its output, dout (T, H): (dY (T * k, H)
+    of out_dtype, dout's by default, dweight float32 of slot_row's shape). Without weight
+    Y may be None, and dweight is None. The residual's gradient is dout."""
+    torch = _torch()
+    T, H, _ = _rows(dout, "dout")
+    T, k = _slots(slot_row, "slot_row", T)
+    with _on(dout, stream):
+        dY = torch.empty((T * k, H), dtype=out_dtype or dout.dtype, device=dout.device)
+        dweight = None if weight is None else torch.empty(slot_row.shape, dtype=torch.float32,
+                                                          device=dout.device)
+        fp4lin_experts_combine_backward(dout, Y, slot_row, row_end, dY, weight, dweight)
+    return dY, dweight
+
+
+# ---- embedding --------------------------------------------------------------------------
+def embed_backward_workspace_bytes(T: int, V: int, H: int) -> int:
+    return int(lib().fp4lin_embed_backward_workspace_bytes(T, V, H))
+
+
+def _tokens(token, T):
+    return _vector(token, _torch().int32, T, "token")
+
+
+def fp4lin_embed(table, token, out, scale=1.0, stream=None):
+    V, H, ldt = _rows(table, "table")
+    T, _, ldo = _rows(out, "out")
+    device = _gpu(("table", table), ("token", token), ("out", out))
+    _matrix_of(out, T, H, "out")
+    _call(device, "fp4lin_embed", table.data_ptr(), _code(table), _tokens(token, T), T, V, H, ldt,
+          float(scale), out.data_ptr(), _code(out), ldo, _queue(stream, device))
+
+
+def fp4lin_embed_backward(dX, token, dE, ws, scale=1.0, add=False, stream=None):
+    T, H, lddx = _rows(dX, "dX")
+    V, _, ldde = _rows(dE, "dE")
+    device = _gpu(("dX", dX), ("token", token), ("dE", dE), ("ws", ws))
+    _matrix_of(dE, V, H, "dE")
+    _call(device, "fp4lin_embed_backward", dX.data_ptr(), _code(dX), _tokens(token, T), T, V, H, lddx,
+          float(scale), int(bool(add)), dE.data_ptr(), _code(dE), ldde, ws.data_ptr(), _nbytes(ws),
+          _queue(stream, device))
+
+
+def embed(table, token, scale=1.0, out_dtype=None, stream=None):
+    """out (*token.shape, H) = scale times the rows of table (V, H) that token (int32)
+    names, zeros for a token outside [0, V). out_dtype: the table's by default."""
+    torch = _torch()
+    H = _rows(table, "table")[1]
+    with _on(table, stream):
+        out = torch.empty((token.numel(), H), dtype=out_dtype or table.dtype, device=table.device)
+        fp4lin_embed(table, token, out, scale)
+    return out if token.dim() == 1 else out.view(*token.shape, H)
+
+
+def embed_backward(dX, token, vocab, scale=1.0, out_dtype=None, add_to=None, stream=None):
+    """The gradient of embed's table (vocab, H) from that of its output, dX (T, H) or
+    (*token.shape, H): each row scale times the sum of dX over its positions, in
+    float32 and in the order of the positions. add_to: a gradient of the table (the
+    head's, where the two share it) that the result is added to in place and that is
+    returned; its rows without a position stay as they are."""
+    torch = _torch()
+    with _on(dX, stream):
+        if dX.dim() != 2:
+            dX = dX.reshape(token.numel(), dX.shape[-1])
+        T, H, _ = _rows(dX, "dX")
+        n = lib().fp4lin_embed_backward_workspace_bytes(T, vocab, H)
+        if n == 0:
+            raise Fp4linError(_lib.ERR_SHAPE, "embed_backward")
+        ws = torch.empty(n, dtype=torch.uint8, device=dX.device)
+        dE = torch.empty((vocab, H), dtype=out_dtype or dX.dtype, device=dX.device) if add_to is None \
+            else add_to
+        _need(dE.shape[0] == vocab, f"add_to has {dE.shape[0]} rows, not {vocab}")
+        fp4lin_embed_backward(dX, token, dE, ws, scale, add_to is not None)
+    return dE
 
 
 # ---- head loss -------------------------------------------------------------------------

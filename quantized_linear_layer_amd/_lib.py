@@ -87,6 +87,18 @@ SIGNATURES = {
                                         c_i64, c_i64, c_ptr, c_int, c_i64, c_ptr, c_size, c_ptr]),
     "fp4lin_experts_wgrad_mx": (c_int, [c_ptr, c_ptr, c_int, c_ptr, c_i64, c_i64, c_i64, c_i64,
                                         c_i64, c_i64, c_ptr, c_int, c_i64, c_ptr, c_size, c_ptr]),
+    "fp4lin_experts_dispatch": (c_int, [c_ptr, c_int, c_ptr, c_i64, c_i64, c_i64, c_i64, c_i64,
+                                        c_ptr, c_i64, c_ptr, c_ptr, c_ptr]),
+    "fp4lin_experts_combine": (c_int, [c_ptr, c_int, c_ptr, c_ptr, c_ptr, c_ptr, c_i64, c_i64,
+                                       c_i64, c_i64, c_i64, c_i64, c_ptr, c_int, c_i64, c_ptr]),
+    "fp4lin_experts_combine_backward": (c_int, [c_ptr, c_int, c_ptr, c_int, c_ptr, c_ptr, c_ptr,
+                                                c_i64, c_i64, c_i64, c_i64, c_i64, c_i64, c_ptr,
+                                                c_int, c_i64, c_ptr, c_ptr]),
+    "fp4lin_embed": (c_int, [c_ptr, c_int, c_ptr, c_i64, c_i64, c_i64, c_i64, c_dbl, c_ptr, c_int,
+                             c_i64, c_ptr]),
+    "fp4lin_embed_backward_workspace_bytes": (c_size, [c_i64, c_i64, c_i64]),
+    "fp4lin_embed_backward": (c_int, [c_ptr, c_int, c_ptr, c_i64, c_i64, c_i64, c_i64, c_dbl, c_int,
+                                      c_ptr, c_int, c_i64, c_ptr, c_size, c_ptr]),
     "fp4lin_head_loss_workspace_bytes": (c_size, [c_int, c_int, c_i64, c_i64, c_i64, c_i64, c_i64]),
     "fp4lin_head_loss_backward_workspace_bytes": (c_size, [c_int, c_int, c_i64, c_i64, c_i64, c_i64,
                                                            c_i64]),

@@ -736,6 +736,225 @@ fp4lin_status fp4lin_experts_wgrad_mx(const void* A, const void* dY, fp4lin_dtyp
 
 }  // extern "C"
 
+// ---- rows of tokens to their experts and back, embedding ----------------------------
+namespace {
+
+// Positions and keys that the sort counts in 32 bits.
+constexpr int64_t kMaxSort = int64_t(1) << 30;
+
+// rows of H elements in groups of eight that a thread each takes
+bool items_fit(int64_t rows, int64_t H) {
+  return double(rows) * double((H + 7) / 8) < 4294967296.0;
+}
+
+fp4lin_status route_sizes(int64_t T, int64_t k, int64_t E, int64_t H) {
+  if (T < 0 || T > kMaxSort || k < 1 || k > kMaxSort || T * k > kMaxSort || E < 1 ||
+      E > kMaxExperts || !ok_dim(H) || !items_fit(T, H))
+    return FP4LIN_ERR_SHAPE;
+  return FP4LIN_OK;
+}
+
+// Arrays at the alignment of their elements.
+bool aligned_to(const void* p, fp4lin_dtype dt) {
+  return reinterpret_cast<uintptr_t>(p) % (dt == FP4LIN_BF16 ? 2 : 4) == 0;
+}
+bool aligned4(const void* p) { return aligned_to(p, FP4LIN_F32); }
+
+fp4lin::RouteCall route_call(int64_t T, int64_t k, int64_t E, int64_t H) {
+  fp4lin::RouteCall c{};
+  c.T = T;
+  c.k = k;
+  c.E = E;
+  c.H = H;
+  return c;
+}
+
+fp4lin_status embed_sizes(int64_t T, int64_t V, int64_t H, int64_t rows) {
+  if (T < 0 || T > kMaxSort || V < 1 || V > kMaxSort || !ok_dim(H) || !items_fit(rows, H))
+    return FP4LIN_ERR_SHAPE;
+  return FP4LIN_OK;
+}
+
+// The gradient's workspace: the sort's results and the sums of long lists' pieces.
+struct EmbedLayout {
+  size_t order, ends, part, total;
+};
+
+fp4lin_status embed_layout(int64_t T, int64_t V, int64_t H, EmbedLayout* out) {
+  fp4lin_status s = embed_sizes(T, V, H, T);
+  if (s == FP4LIN_OK) s = embed_sizes(T, V, H, V);
+  if (s != FP4LIN_OK) return s;
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off = round_up(off + bytes, 256);
+    return at;
+  };
+  EmbedLayout o{};
+  o.order = take(size_t(T) * 4);
+  o.ends = take(size_t(V) * 4);
+  o.part = take(size_t(fp4lin::embed_pieces(T)) * 2 * (size_t(H + 7) / 8 * 8) * 4);
+  o.total = off;
+  *out = o;
+  return FP4LIN_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+fp4lin_status fp4lin_experts_dispatch(const void* X, fp4lin_dtype dt, const int32_t* expert,
+                                      int64_t T, int64_t k, int64_t E, int64_t H, int64_t ldx,
+                                      void* Xs, int64_t ldxs, int32_t* row_end, int32_t* slot_row,
+                                      hipStream_t stream) {
+  if (row_end == nullptr ||
+      (T != 0 && (X == nullptr || expert == nullptr || Xs == nullptr || slot_row == nullptr)))
+    return FP4LIN_ERR_NULL;
+  if (bad_dtype(dt)) return FP4LIN_ERR_DTYPE;
+  const fp4lin_status s = route_sizes(T, k, E, H);
+  if (s != FP4LIN_OK) return s;
+  if (ldx < H || ldxs < H) return FP4LIN_ERR_SHAPE;
+  if (!aligned_to(X, dt) || !aligned_to(Xs, dt) || !aligned4(expert) || !aligned4(row_end) ||
+      !aligned4(slot_row))
+    return FP4LIN_ERR_ALIGN;
+  fp4lin::RouteCall c = route_call(T, k, E, H);
+  c.X = X;
+  c.ldx = ldx;
+  c.expert = expert;
+  c.Xs = Xs;
+  c.ldxs = ldxs;
+  c.row_end_out = row_end;
+  c.slot_row_out = slot_row;
+  return launch_status(fp4lin::launch_experts_dispatch(c, dt == FP4LIN_BF16, stream));
+}
+
+fp4lin_status fp4lin_experts_combine(const void* Y, fp4lin_dtype ydt, const int32_t* slot_row,
+                                     const int32_t* row_end, const float* weight,
+                                     const void* residual, int64_t T, int64_t k, int64_t E,
+                                     int64_t H, int64_t ldy, int64_t ldr, void* out,
+                                     fp4lin_dtype odt, int64_t ldo, hipStream_t stream) {
+  if (T != 0 && (Y == nullptr || slot_row == nullptr || row_end == nullptr || out == nullptr))
+    return FP4LIN_ERR_NULL;
+  if (bad_dtype(ydt) || bad_dtype(odt)) return FP4LIN_ERR_DTYPE;
+  const fp4lin_status s = route_sizes(T, k, E, H);
+  if (s != FP4LIN_OK) return s;
+  if (ldy < H || ldo < H || (residual != nullptr && ldr < H)) return FP4LIN_ERR_SHAPE;
+  if (!aligned_to(Y, ydt) || !aligned_to(residual, odt) || !aligned_to(out, odt) ||
+      !aligned4(slot_row) || !aligned4(row_end) || !aligned4(weight))
+    return FP4LIN_ERR_ALIGN;
+  if (T == 0) return FP4LIN_OK;
+  fp4lin::RouteCall c = route_call(T, k, E, H);
+  c.Y = Y;
+  c.ldy = ldy;
+  c.slot_row = slot_row;
+  c.row_end = row_end;
+  c.weight = weight;
+  c.residual = residual;
+  c.ldr = ldr;
+  c.out = out;
+  c.ldo = ldo;
+  return launch_status(
+      fp4lin::launch_experts_combine(c, ydt == FP4LIN_BF16, odt == FP4LIN_BF16, stream));
+}
+
+fp4lin_status fp4lin_experts_combine_backward(const void* dout, fp4lin_dtype odt, const void* Y,
+                                              fp4lin_dtype ydt, const int32_t* slot_row,
+                                              const int32_t* row_end, const float* weight,
+                                              int64_t T, int64_t k, int64_t E, int64_t H,
+                                              int64_t lddo, int64_t ldy, void* dY,
+                                              fp4lin_dtype dydt, int64_t lddy, float* dweight,
+                                              hipStream_t stream) {
+  if (T != 0 && (dout == nullptr || slot_row == nullptr || row_end == nullptr || dY == nullptr ||
+                 (dweight != nullptr && Y == nullptr)))
+    return FP4LIN_ERR_NULL;
+  if (bad_dtype(odt) || bad_dtype(ydt) || bad_dtype(dydt)) return FP4LIN_ERR_DTYPE;
+  const fp4lin_status s = route_sizes(T, k, E, H);
+  if (s != FP4LIN_OK) return s;
+  if (lddo < H || lddy < H || (dweight != nullptr && ldy < H)) return FP4LIN_ERR_SHAPE;
+  if (!aligned_to(dout, odt) || !aligned_to(dY, dydt) || !aligned_to(Y, ydt) ||
+      !aligned4(slot_row) || !aligned4(row_end) || !aligned4(weight) || !aligned4(dweight))
+    return FP4LIN_ERR_ALIGN;
+  if (T == 0) return FP4LIN_OK;
+  fp4lin::RouteCall c = route_call(T, k, E, H);
+  c.dout = dout;
+  c.lddo = lddo;
+  c.Y = Y;
+  c.ldy = ldy;
+  c.slot_row = slot_row;
+  c.row_end = row_end;
+  c.weight = weight;
+  c.dY = dY;
+  c.lddy = lddy;
+  c.dweight = dweight;
+  return launch_status(fp4lin::launch_experts_combine_backward(
+      c, ydt == FP4LIN_BF16, odt == FP4LIN_BF16, dydt == FP4LIN_BF16, stream));
+}
+
+fp4lin_status fp4lin_embed(const void* table, fp4lin_dtype dt, const int32_t* token, int64_t T,
+                           int64_t V, int64_t H, int64_t ldt, double scale, void* out,
+                           fp4lin_dtype odt, int64_t ldo, hipStream_t stream) {
+  if (T != 0 && (table == nullptr || token == nullptr || out == nullptr)) return FP4LIN_ERR_NULL;
+  if (bad_dtype(dt) || bad_dtype(odt)) return FP4LIN_ERR_DTYPE;
+  const fp4lin_status s = embed_sizes(T, V, H, T);
+  if (s != FP4LIN_OK) return s;
+  if (ldt < H || ldo < H) return FP4LIN_ERR_SHAPE;
+  if (!std::isfinite(scale)) return FP4LIN_ERR_VALUE;
+  if (!aligned_to(table, dt) || !aligned_to(out, odt) || !aligned4(token)) return FP4LIN_ERR_ALIGN;
+  if (T == 0) return FP4LIN_OK;
+  fp4lin::EmbedCall c{};
+  c.T = T;
+  c.V = V;
+  c.H = H;
+  c.token = token;
+  c.scale = float(scale);
+  c.table = table;
+  c.ldt = ldt;
+  c.out = out;
+  c.ldo = ldo;
+  return launch_status(fp4lin::launch_embed(c, dt == FP4LIN_BF16, odt == FP4LIN_BF16, stream));
+}
+
+size_t fp4lin_embed_backward_workspace_bytes(int64_t T, int64_t V, int64_t H) {
+  EmbedLayout o;
+  return embed_layout(T, V, H, &o) == FP4LIN_OK ? o.total : 0;
+}
+
+fp4lin_status fp4lin_embed_backward(const void* dX, fp4lin_dtype dt, const int32_t* token, int64_t T,
+                                    int64_t V, int64_t H, int64_t lddx, double scale, int add,
+                                    void* dE, fp4lin_dtype edt, int64_t ldde, void* ws,
+                                    size_t ws_bytes, hipStream_t stream) {
+  if (dE == nullptr || ws == nullptr || (T != 0 && (dX == nullptr || token == nullptr)))
+    return FP4LIN_ERR_NULL;
+  if (bad_dtype(dt) || bad_dtype(edt)) return FP4LIN_ERR_DTYPE;
+  EmbedLayout o;
+  const fp4lin_status s = embed_layout(T, V, H, &o);
+  if (s != FP4LIN_OK) return s;
+  if (lddx < H || ldde < H) return FP4LIN_ERR_SHAPE;
+  if (!std::isfinite(scale)) return FP4LIN_ERR_VALUE;
+  if (!aligned_to(dX, dt) || !aligned_to(dE, edt) || !aligned4(token) || !aligned16(ws))
+    return FP4LIN_ERR_ALIGN;
+  if (ws_bytes < o.total) return FP4LIN_ERR_WORKSPACE;
+  char* const base = static_cast<char*>(ws);
+  fp4lin::EmbedCall c{};
+  c.T = T;
+  c.V = V;
+  c.H = H;
+  c.token = token;
+  c.scale = float(scale);
+  c.dX = dX;
+  c.lddx = lddx;
+  c.add = add != 0;
+  c.dE = dE;
+  c.ldde = ldde;
+  c.order = reinterpret_cast<int32_t*>(base + o.order);
+  c.ends = reinterpret_cast<int32_t*>(base + o.ends);
+  c.part = reinterpret_cast<float*>(base + o.part);
+  return launch_status(
+      fp4lin::launch_embed_backward(c, dt == FP4LIN_BF16, edt == FP4LIN_BF16, stream));
+}
+
+}  // extern "C"
+
 // ---- head loss ------------------------------------------------------------------
 namespace {
 

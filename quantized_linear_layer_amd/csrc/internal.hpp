@@ -156,6 +156,61 @@ hipError_t launch_head_loss(const HeadCall& c, bool bf16, const HeadPlan& h, hip
 hipError_t launch_head_loss_backward(const HeadCall& c, bool bf16, const HeadPlan& h,
                                      hipStream_t stream);
 
+// Rows of tokens to their experts and back (route.hip): T tokens, k slots each.
+struct RouteCall {
+  int64_t T, k, E, H;
+  // dispatch
+  const void* X;
+  int64_t ldx;
+  const int32_t* expert;
+  void* Xs;
+  int64_t ldxs;
+  int32_t *row_end_out, *slot_row_out;
+  // the way back
+  const int32_t *slot_row, *row_end;
+  const float* weight;  // may be NULL
+  const void* Y;
+  int64_t ldy;
+  const void* residual;  // may be NULL
+  int64_t ldr;
+  void* out;
+  int64_t ldo;
+  // and its gradient
+  const void* dout;
+  int64_t lddo;
+  void* dY;
+  int64_t lddy;
+  float* dweight;  // may be NULL
+};
+hipError_t launch_experts_dispatch(const RouteCall& c, bool bf16, hipStream_t stream);
+hipError_t launch_experts_combine(const RouteCall& c, bool y_bf16, bool out_bf16, hipStream_t stream);
+hipError_t launch_experts_combine_backward(const RouteCall& c, bool y_bf16, bool dout_bf16,
+                                           bool dy_bf16, hipStream_t stream);
+
+// Embedding (embed.hip). embed_pieces: pieces of up to T positions; the gradient
+// keeps two fp32 rows of each, H rounded up to 8.
+struct EmbedCall {
+  int64_t T, V, H;
+  const int32_t* token;
+  float scale;
+  // lookup
+  const void* table;
+  int64_t ldt;
+  void* out;
+  int64_t ldo;
+  // gradient
+  const void* dX;
+  int64_t lddx;
+  bool add;
+  void* dE;
+  int64_t ldde;
+  int32_t *order, *ends;
+  float* part;
+};
+hipError_t launch_embed(const EmbedCall& c, bool table_bf16, bool out_bf16, hipStream_t stream);
+int64_t embed_pieces(int64_t T);
+hipError_t launch_embed_backward(const EmbedCall& c, bool dx_bf16, bool de_bf16, hipStream_t stream);
+
 // Gradient norm and clipping (clip.hip). clip_parts: partial sums that `count`
 // tensors of `elements` elements in all can need; ws holds two doubles more.
 int64_t clip_parts(int64_t count, int64_t elements);

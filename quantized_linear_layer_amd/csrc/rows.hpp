@@ -1,0 +1,246 @@
+// Pieces of the kernels that move rows by index (route.hip, embed.hip): eight
+// elements a thread at any alignment, division of an item by the groups of a row,
+// and a stable sort by small keys.
+#pragma once
+
+#include <type_traits>
+
+#include "device_common.hpp"
+#include "gemm_core.hpp"
+
+namespace fp4lin {
+
+// ---------------------------------------------------------------------------
+// Eight consecutive elements of a row, whatever the alignment of its first one:
+// global accesses of 16 bytes take any address on gfx950, so rows whose length or
+// stride is no multiple of 16 bytes need no path of their own.
+// ---------------------------------------------------------------------------
+struct __attribute__((packed, aligned(2))) Bytes16 {
+  uint32_t w[4];
+};
+
+// kWhole: all eight are there. Otherwise the first `valid` of them (zeros are read
+// past them).
+template <class In, bool kWhole>
+__device__ inline void get8(const typename In::T* __restrict__ p, int64_t valid, Vec8<In>& v) {
+  if constexpr (kWhole) {
+    constexpr int kPieces = In::kBytes / 2;
+    Bytes16 b[kPieces];
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) b[i] = reinterpret_cast<const Bytes16*>(p)[i];
+    __builtin_memcpy(&v, b, sizeof(v));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v.v[i] = i < valid ? p[i] : typename In::T(0);
+  }
+}
+
+template <class In, bool kWhole>
+__device__ inline void put8(typename In::T* __restrict__ p, int64_t valid, const Vec8<In>& v) {
+  if constexpr (kWhole) {
+    constexpr int kPieces = In::kBytes / 2;
+    Bytes16 b[kPieces];
+    __builtin_memcpy(b, &v, sizeof(v));
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) reinterpret_cast<Bytes16*>(p)[i] = b[i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < valid) p[i] = v.v[i];
+  }
+}
+
+// f(whole) once for a group of `valid` columns: one branch for everything that is
+// read and written there, so that no load waits behind another's branch.
+template <class F>
+__device__ inline void by_width(int64_t valid, const F& f) {
+  if (valid >= 8)
+    f(std::true_type{});
+  else
+    f(std::false_type{});
+}
+
+// fp32 values to the stored type: float as they are, bfloat16 rounded to nearest even.
+template <class In>
+__device__ inline Vec8<In> rounded(const float (&f)[8]) {
+  Vec8<In> v;
+  if constexpr (In::kBytes == 2) {
+    const uint32_t u[4] = {bf16_pair(f[0], f[1]), bf16_pair(f[2], f[3]), bf16_pair(f[4], f[5]),
+                           bf16_pair(f[6], f[7])};
+    __builtin_memcpy(&v, u, sizeof(v));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v.v[i] = f[i];
+  }
+  return v;
+}
+
+// Exact n / d for 32-bit n, by the multiplication of Granlund and Montgomery,
+// "Division by Invariant Integers using Multiplication" (1994), figure 4.1.
+struct Divisor {
+  uint32_t d, m, s1, s2;
+
+  explicit Divisor(uint32_t d_) : d(d_) {
+    int l = 0;
+    while ((uint64_t(1) << l) < d) ++l;
+    m = uint32_t(((uint64_t(1) << 32) * ((uint64_t(1) << l) - d)) / d + 1);
+    s1 = l < 1 ? l : 1;
+    s2 = l > 1 ? l - 1 : 0;
+  }
+  __device__ inline uint32_t operator()(uint32_t n) const {
+    const uint32_t t = __umulhi(m, n);
+    return (t + ((n - t) >> s1)) >> s2;
+  }
+};
+
+// A thread's item: eight columns from c on of a row; the rows' groups of eight
+// follow one another, so that narrow rows leave no lane idle.
+struct Item {
+  uint32_t row;
+  int64_t c;
+  bool in;
+};
+__device__ inline Item item_of(uint32_t items, const Divisor& groups) {
+  const uint64_t i = uint64_t(blockIdx.x) * blockDim.x + threadIdx.x;
+  const uint32_t row = groups(uint32_t(i));
+  return Item{row, int64_t(uint32_t(i) - row * groups.d) * 8, i < items};
+}
+
+// f(type of the elements), on the host
+template <class F>
+hipError_t with_type(bool bf16, F&& f) {
+  return bf16 ? f(BF16In{}) : f(F32In{});
+}
+
+constexpr int kRowThreads = 256;
+__host__ inline uint32_t row_groups(int64_t H) { return uint32_t((H + 7) / 8); }
+__host__ inline unsigned item_blocks(uint64_t items) {
+  return unsigned((items + kRowThreads - 1) / kRowThreads);
+}
+
+// ---------------------------------------------------------------------------
+// Stable sort of n elements by keys 0 .. keys - 1; an element with any other key
+// comes last (key `keys`). One launch: each workgroup owns `per` neighbouring keys
+// and reads all elements, counting those below its keys and its own ones, so that
+// it knows where its keys begin without hearing from the others. Its 16 waves take
+// consecutive parts of the elements; counts by key and wave, scanned in that
+// order, are where each wave places its elements in a second reading. Lanes of a
+// wave with one key find each other by ballots over the key's bits, so the time
+// does not depend on how the keys are distributed. No atomics that return: the
+// order is that of the elements.
+//   ends[k]   number of elements with a key <= k, for k < keys
+//   order     elements by key (not needed: NULL)
+//   place     where each element came to be (not needed: NULL)
+// ---------------------------------------------------------------------------
+struct SortArgs {
+  const int32_t* key;
+  int32_t n, keys, per;
+  int32_t *ends, *order, *place;
+};
+
+constexpr int kSortWaves = 16;
+constexpr int kSortKeys = 512;  // most keys a workgroup
+
+struct SortPlan {
+  int32_t per;
+  unsigned blocks;
+};
+// As many workgroups as CUs where the keys allow it, more where a workgroup's
+// keys would outgrow its counters.
+__host__ inline SortPlan sort_plan(int64_t keys) {
+  const int64_t all = keys + 1;
+  int64_t per = (all + 255) / 256;
+  if (per > kSortKeys) per = kSortKeys;
+  return SortPlan{int32_t(per), unsigned((all + per - 1) / per)};
+}
+
+// (in a header that several sources include, each with a kernel of its own)
+__device__ inline void sort_body(const SortArgs& p) {
+  constexpr int U = 8;  // loads in flight a lane
+  __shared__ int32_t cnt[kSortWaves][kSortKeys];
+  __shared__ int32_t sums[kSortWaves];
+  __shared__ int32_t below_all;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int32_t lo = blockIdx.x * p.per;
+  const int32_t left = p.keys + 1 - lo;
+  const int32_t mine = left < p.per ? left : p.per;
+  for (int i = threadIdx.x; i < kSortWaves * mine; i += kSortWaves * 64)
+    cnt[i / mine][i % mine] = 0;
+  if (threadIdx.x == 0) below_all = 0;
+  __syncthreads();
+
+  const int64_t seg = (int64_t(p.n) + kSortWaves * 64 - 1) / (kSortWaves * 64) * 64;
+  const int64_t first = wave * seg, past = first + seg < p.n ? first + seg : p.n;
+  // key of element i relative to lo; one that is not there counts as above
+  auto load = [&](int64_t i0, int32_t (&k)[U]) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t i = i0 + u * 64 + lane;
+      const int32_t raw = i < past ? p.key[i] : 0;
+      k[u] = i >= past ? p.keys + 1 : (raw >= 0 && raw < p.keys) ? raw : p.keys;
+    }
+  };
+  int32_t below = 0;
+  for (int64_t i0 = first; i0 < past; i0 += U * 64) {
+    int32_t k[U];
+    load(i0, k);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      below += k[u] < lo;
+      if (k[u] >= lo && k[u] - lo < mine) atomicAdd(&cnt[wave][k[u] - lo], 1);
+    }
+  }
+  below = int32_t(wave_sum_u32(uint32_t(below)));
+  if (lane == 0) atomicAdd(&below_all, below);
+  __syncthreads();
+
+  // counts to starts: thread k takes key lo + k of every wave
+  const int k = threadIdx.x;
+  uint32_t total = 0;
+  if (k < mine)
+    for (int w = 0; w < kSortWaves; ++w) total += uint32_t(cnt[w][k]);
+  uint32_t in_wave;
+  const uint32_t ahead = wave_exclusive_scan(total, in_wave);
+  if (lane == 0) sums[wave] = int32_t(in_wave);
+  __syncthreads();
+  uint32_t start = uint32_t(below_all) + ahead;
+  for (int w = 0; w < wave; ++w) start += uint32_t(sums[w]);
+  if (k < mine) {
+    if (lo + k < p.keys) p.ends[lo + k] = int32_t(start + total);
+    for (int w = 0; w < kSortWaves; ++w) {
+      const uint32_t c = uint32_t(cnt[w][k]);
+      cnt[w][k] = int32_t(start);
+      start += c;
+    }
+  }
+  __syncthreads();
+
+  const int bits = mine > 1 ? 32 - __builtin_clz(mine - 1) : 0;
+  for (int64_t i0 = first; i0 < past; i0 += U * 64) {
+    int32_t key[U];
+    load(i0, key);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int32_t r = key[u] - lo;
+      const bool in = r >= 0 && r < mine;
+      uint64_t same = __ballot(in);
+      if (same == 0) continue;
+      for (int b = 0; b < bits; ++b) {
+        const uint64_t set = __ballot((r >> b) & 1);
+        same &= (r >> b) & 1 ? set : ~set;
+      }
+      if (in) {
+        const int32_t base = cnt[wave][r];
+        const int32_t at = base + __builtin_popcountll(same & ((uint64_t(1) << lane) - 1));
+        const int64_t i = i0 + u * 64 + lane;
+        if (p.order != nullptr) p.order[at] = int32_t(i);
+        if (p.place != nullptr) p.place[i] = at;
+        // the last of them moves the start on, for all have read it
+        if ((same >> lane) == 1) cnt[wave][r] = at + 1;
+      }
+    }
+  }
+}
+
+}  // namespace fp4lin
