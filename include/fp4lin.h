@@ -608,6 +608,59 @@ fp4lin_status fp4lin_head_loss_backward(const void* X, const void* W, fp4lin_dty
                                         void* dW, int64_t lddw, void* ws, size_t ws_bytes,
                                         hipStream_t stream);
 
+/* ---- Head loss against a teacher's top logits (distillation) -----------------
+ * As the head loss, with the softmax of a teacher over the k indices that it lists
+ * for a row in the place of the one target:
+ *   z = X W / temperature,  lse_t = log sum_v exp z_tv
+ *   p_tj = exp(u_tj / temperature) / sum_i exp(u_ti / temperature)
+ *   loss_t = sum_j p_tj (log p_tj - (z_(t, index_tj) - lse_t))
+ *   G_tv = (exp(z_tv - lse_t) - sum over index_tj = v of p_tj) * dloss_t / temperature
+ *   dX = G W^T,  dW = X^T G
+ * (the divergence of the student's distribution over the whole vocabulary from the
+ * teacher's over its list; no factor temperature^2).
+ *   index    device, T x k int32, contiguous. Entries outside [0, V) are left out, from
+ *            p's sum too; an index listed twice counts twice, each time with its own u
+ *   teacher  device, T x k, contiguous, dtype tdt: the logits u. One of -infinity has
+ *            p = 0 and is left out; a NaN or +infinity among those that are not makes
+ *            the row's loss NaN, and of the gradients its dX and all dW
+ * A row with no entry left has loss 0 and no part in the gradients, whatever X and dloss
+ * hold there (lse is that of the row's z all the same). p and every sum are fp32; G is
+ * rounded as in the head loss, and what is said there of X, W, dloss, the workspace and
+ * of infinite logits holds here (a z of -infinity at an entry with p > 0: loss +infinity).
+ * temperature is rounded to fp32: a number > 0 whose reciprocal is finite there, else
+ * FP4LIN_ERR_VALUE.
+ * Limits: those of the head loss, and k <= 1024. */
+
+/* Bytes of workspace of the two calls (at least 256); 0 for invalid
+ * arguments. */
+size_t fp4lin_head_distill_workspace_bytes(fp4lin_dtype dt, fp4lin_head_layout layout, int64_t T,
+                                           int64_t H, int64_t V, int64_t k, int64_t ldx,
+                                           int64_t ldw);
+size_t fp4lin_head_distill_backward_workspace_bytes(fp4lin_dtype dt, fp4lin_head_layout layout,
+                                                    int64_t T, int64_t H, int64_t V, int64_t k,
+                                                    int64_t ldx, int64_t ldw);
+
+/*   loss, lse  device, T floats each (outputs)
+ * Errors: NULL, SHAPE, DTYPE, VALUE, ALIGN, WORKSPACE, LAUNCH. */
+fp4lin_status fp4lin_head_distill(const void* X, const void* W, fp4lin_dtype dt,
+                                  fp4lin_head_layout layout, const int32_t* index,
+                                  const void* teacher, fp4lin_dtype tdt, int64_t k,
+                                  double temperature, int64_t T, int64_t H, int64_t V, int64_t ldx,
+                                  int64_t ldw, float* loss, float* lse, void* ws, size_t ws_bytes,
+                                  hipStream_t stream);
+
+/*   lse      device, T floats, from fp4lin_head_distill on the same X, W, temperature
+ *   dloss, dX, dW  as in fp4lin_head_loss_backward
+ * Errors: NULL, SHAPE, DTYPE, VALUE, ALIGN, WORKSPACE, LAUNCH. */
+fp4lin_status fp4lin_head_distill_backward(const void* X, const void* W, fp4lin_dtype dt,
+                                           fp4lin_head_layout layout, const int32_t* index,
+                                           const void* teacher, fp4lin_dtype tdt, int64_t k,
+                                           double temperature, const float* lse, const float* dloss,
+                                           int64_t T, int64_t H, int64_t V, int64_t ldx,
+                                           int64_t ldw, void* dX, int64_t lddx, void* dW,
+                                           int64_t lddw, void* ws, size_t ws_bytes,
+                                           hipStream_t stream);
+
 /* ---- Global gradient norm and clipping -------------------------------------
  * Over the elements of all tensors together,
  *   norm = sqrt(sum g^2)     (summed in double, in an order that the sizes and the

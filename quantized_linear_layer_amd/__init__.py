@@ -33,7 +33,8 @@ __all__ = [
     "experts_dispatch", "experts_combine", "experts_combine_backward",
     "embed_backward_workspace_bytes", "fp4lin_embed", "fp4lin_embed_backward", "embed", "embed_backward",
     "head_loss_workspace_bytes", "fp4lin_head_loss", "fp4lin_head_loss_backward", "head_loss",
-    "head_loss_backward", "clip_workspace_bytes", "fp4lin_grad_norm", "fp4lin_clip_grads",
+    "head_loss_backward", "head_distill_workspace_bytes", "fp4lin_head_distill",
+    "fp4lin_head_distill_backward", "head_distill", "head_distill_backward", "clip_workspace_bytes", "fp4lin_grad_norm", "fp4lin_clip_grads",
     "grad_norm", "clip_grads",
 ]
 
@@ -842,18 +843,25 @@ def head_loss_workspace_bytes(dtype_code, by_vocab, T, H, V, ldx, ldw, backward=
     return int(f(dtype_code, int(bool(by_vocab)), T, H, V, ldx, ldw))
 
 
-def _head_sizes(X, W, target, by_vocab):
-    """(T, H, V, ldx, ldw) of matching X, W and targets."""
+def _head_operands(X, W, by_vocab):
+    """(T, H, V, ldx, ldw) of matching X and W."""
     T, H, ldx = _rows(X, "X")
     r, c, ldw = _rows(W, "W")
     _same_dtype(X, W, "X and W")
     if (c if by_vocab else r) != H:
         raise ValueError(f"X is {T}x{H} but W is {r}x{c}" + (" (vocabulary first)" if by_vocab else ""))
+    return T, H, r if by_vocab else c, ldx, ldw
+
+
+def _head_sizes(X, W, target, by_vocab):
+    """(T, H, V, ldx, ldw) of matching X, W and targets."""
+    sizes = _head_operands(X, W, by_vocab)
+    T = sizes[0]
     if target.dtype != _torch().int32 or target.dim() != 1 or not target.is_contiguous():
         raise TypeError("target must be a contiguous int32 vector")
     if target.numel() != T:
         raise ValueError(f"{target.numel()} targets for {T} rows")
-    return T, H, r if by_vocab else c, ldx, ldw
+    return sizes
 
 
 def _row_floats(t, T, name):
@@ -872,18 +880,24 @@ def fp4lin_head_loss(X, W, target, loss, lse, ws, by_vocab=False, stream=None):
           _row_floats(lse, T, "lse"), ws.data_ptr(), _nbytes(ws), _queue(stream, device))
 
 
-def fp4lin_head_loss_backward(X, W, target, lse, dloss, dX, dW, ws, by_vocab=False, stream=None):
-    T, H, V, ldx, ldw = _head_sizes(X, W, target, by_vocab)
-    device = _gpu(("X", X), ("W", W), ("target", target), ("lse", lse), ("dloss", dloss), ("dX", dX),
-                  ("dW", dW), ("ws", ws))
+def _head_gradients(X, W, dX, dW):
+    """The row strides of gradients that fit X and W."""
     _same_dtype(X, dX, "X and dX")
     _same_dtype(X, dW, "X and dW")
     Tx, Hx, lddx = _rows(dX, "dX")
     r, c, lddw = _rows(dW, "dW")
-    if Tx != T or Hx != H:
-        raise ValueError(f"dX is {Tx}x{Hx}, not {T}x{H}")
+    if dX.shape != X.shape:
+        raise ValueError(f"dX is {Tx}x{Hx}, not {X.shape[0]}x{X.shape[1]}")
     if dW.shape != W.shape:
         raise ValueError(f"dW is {r}x{c}, W {W.shape[0]}x{W.shape[1]}")
+    return lddx, lddw
+
+
+def fp4lin_head_loss_backward(X, W, target, lse, dloss, dX, dW, ws, by_vocab=False, stream=None):
+    T, H, V, ldx, ldw = _head_sizes(X, W, target, by_vocab)
+    device = _gpu(("X", X), ("W", W), ("target", target), ("lse", lse), ("dloss", dloss), ("dX", dX),
+                  ("dW", dW), ("ws", ws))
+    lddx, lddw = _head_gradients(X, W, dX, dW)
     _call(device, "fp4lin_head_loss_backward", X.data_ptr(), W.data_ptr(), _code(X),
           int(bool(by_vocab)), target.data_ptr(), _row_floats(lse, T, "lse"),
           _row_floats(dloss, T, "dloss"), T, H, V, ldx, ldw, dX.data_ptr(), lddx, dW.data_ptr(),
@@ -932,6 +946,90 @@ def head_loss_backward(X, W, target, lse, dloss, by_vocab=False, stream=None):
         dX = torch.empty((sizes[0], sizes[1]), dtype=X.dtype, device=X.device)
         dW = torch.empty(tuple(W.shape), dtype=W.dtype, device=W.device)
         fp4lin_head_loss_backward(X, W, target, lse, dloss, dX, dW, ws, by_vocab)
+    return dX, dW
+
+
+# ---- head loss against a teacher's top logits --------------------------------------------
+def head_distill_workspace_bytes(dtype_code, by_vocab, T, H, V, k, ldx, ldw, backward=False) -> int:
+    f = lib().fp4lin_head_distill_backward_workspace_bytes if backward else \
+        lib().fp4lin_head_distill_workspace_bytes
+    return int(f(dtype_code, int(bool(by_vocab)), T, H, V, k, ldx, ldw))
+
+
+def _teacher(index, teacher, T):
+    """The addresses, the logits' type and the entries a row of a teacher's lists."""
+    if index.dtype != _torch().int32 or not index.is_contiguous() or not teacher.is_contiguous():
+        raise TypeError("index must be a contiguous int32 tensor, teacher a contiguous one")
+    if index.dim() != 2 or index.shape[0] != T:
+        raise ValueError(f"index must be ({T}, entries)")
+    if teacher.shape != index.shape:
+        raise ValueError(f"teacher is {tuple(teacher.shape)}, index {tuple(index.shape)}")
+    return index.data_ptr(), teacher.data_ptr(), _code(teacher), index.shape[1]
+
+
+def fp4lin_head_distill(X, W, index, teacher, loss, lse, ws, temperature=1.0, by_vocab=False, stream=None):
+    T, H, V, ldx, ldw = _head_operands(X, W, by_vocab)
+    device = _gpu(("X", X), ("W", W), ("index", index), ("teacher", teacher), ("loss", loss), ("lse", lse),
+                  ("ws", ws))
+    _call(device, "fp4lin_head_distill", X.data_ptr(), W.data_ptr(), _code(X), int(bool(by_vocab)),
+          *_teacher(index, teacher, T), float(temperature), T, H, V, ldx, ldw,
+          _row_floats(loss, T, "loss"), _row_floats(lse, T, "lse"), ws.data_ptr(), _nbytes(ws),
+          _queue(stream, device))
+
+
+def fp4lin_head_distill_backward(X, W, index, teacher, lse, dloss, dX, dW, ws, temperature=1.0, by_vocab=False,
+                                 stream=None):
+    T, H, V, ldx, ldw = _head_operands(X, W, by_vocab)
+    device = _gpu(("X", X), ("W", W), ("index", index), ("teacher", teacher), ("lse", lse), ("dloss", dloss),
+                  ("dX", dX), ("dW", dW), ("ws", ws))
+    lddx, lddw = _head_gradients(X, W, dX, dW)
+    _call(device, "fp4lin_head_distill_backward", X.data_ptr(), W.data_ptr(), _code(X),
+          int(bool(by_vocab)), *_teacher(index, teacher, T), float(temperature),
+          _row_floats(lse, T, "lse"), _row_floats(dloss, T, "dloss"), T, H, V, ldx, ldw, dX.data_ptr(),
+          lddx, dW.data_ptr(), lddw, ws.data_ptr(), _nbytes(ws), _queue(stream, device))
+
+
+def _distill_ws(X, sizes, k, by_vocab, backward, where):
+    torch = _torch()
+    T, H, V, ldx, ldw = sizes
+    n = head_distill_workspace_bytes(_code(X), by_vocab, T, H, V, k, ldx, ldw, backward)
+    if n == 0:
+        raise Fp4linError(_lib.ERR_SHAPE, where)
+    return torch.empty(n, dtype=torch.uint8, device=X.device)
+
+
+def head_distill(X, W, index, teacher, temperature=1.0, by_vocab=False, stream=None):
+    """The divergence of the rows' softmax over z = X W / temperature from a teacher's
+    softmax over the logits `teacher` (T, k) / temperature of the tokens `index` (T, k)
+    int32, without keeping z. X and W as in head_loss, teacher float32 or bfloat16.
+    Entries outside the vocabulary or of -infinity are left out. Returns (loss, lse),
+    float32 of T entries; a row without an entry has loss 0."""
+    torch = _torch()
+    _gpu(("X", X), ("W", W))
+    with _on(X, stream):
+        X, W = _aligned(X), _aligned(W)
+        sizes = _head_operands(X, W, by_vocab)
+        k = _teacher(index, teacher, sizes[0])[3]
+        ws = _distill_ws(X, sizes, k, by_vocab, False, "head_distill")
+        loss = torch.empty(sizes[0], dtype=torch.float32, device=X.device)
+        lse = torch.empty(sizes[0], dtype=torch.float32, device=X.device)
+        fp4lin_head_distill(X, W, index, teacher, loss, lse, ws, temperature, by_vocab)
+    return loss, lse
+
+
+def head_distill_backward(X, W, index, teacher, lse, dloss, temperature=1.0, by_vocab=False, stream=None):
+    """Gradients of sum(dloss * loss) of head_distill: (dX, dW), of X's and W's shape and
+    dtype. lse is head_distill's, dloss float32 of T entries."""
+    torch = _torch()
+    _gpu(("X", X), ("W", W))
+    with _on(X, stream):
+        X, W = _aligned(X), _aligned(W)
+        sizes = _head_operands(X, W, by_vocab)
+        k = _teacher(index, teacher, sizes[0])[3]
+        ws = _distill_ws(X, sizes, k, by_vocab, True, "head_distill_backward")
+        dX = torch.empty((sizes[0], sizes[1]), dtype=X.dtype, device=X.device)
+        dW = torch.empty(tuple(W.shape), dtype=W.dtype, device=W.device)
+        fp4lin_head_distill_backward(X, W, index, teacher, lse, dloss, dX, dW, ws, temperature, by_vocab)
     return dX, dW
 
 

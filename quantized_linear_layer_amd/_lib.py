@@ -107,6 +107,16 @@ SIGNATURES = {
     "fp4lin_head_loss_backward": (c_int, [c_ptr, c_ptr, c_int, c_int, c_ptr, c_ptr, c_ptr, c_i64,
                                           c_i64, c_i64, c_i64, c_i64, c_ptr, c_i64, c_ptr, c_i64,
                                           c_ptr, c_size, c_ptr]),
+    "fp4lin_head_distill_workspace_bytes": (c_size, [c_int, c_int, c_i64, c_i64, c_i64, c_i64, c_i64,
+                                                     c_i64]),
+    "fp4lin_head_distill_backward_workspace_bytes": (c_size, [c_int, c_int, c_i64, c_i64, c_i64,
+                                                              c_i64, c_i64, c_i64]),
+    "fp4lin_head_distill": (c_int, [c_ptr, c_ptr, c_int, c_int, c_ptr, c_ptr, c_int, c_i64, c_dbl,
+                                    c_i64, c_i64, c_i64, c_i64, c_i64, c_ptr, c_ptr, c_ptr, c_size,
+                                    c_ptr]),
+    "fp4lin_head_distill_backward": (c_int, [c_ptr, c_ptr, c_int, c_int, c_ptr, c_ptr, c_int, c_i64,
+                                             c_dbl, c_ptr, c_ptr, c_i64, c_i64, c_i64, c_i64, c_i64,
+                                             c_ptr, c_i64, c_ptr, c_i64, c_ptr, c_size, c_ptr]),
     "fp4lin_clip_workspace_bytes": (c_size, [c_i64, c_i64]),
     "fp4lin_grad_norm": (c_int, [ctypes.POINTER(Grad), c_i64, c_ptr, c_ptr, c_size, c_ptr]),
     "fp4lin_clip_grads": (c_int, [ctypes.POINTER(Grad), c_i64, c_dbl, c_ptr, c_ptr, c_size, c_ptr]),

@@ -960,12 +960,16 @@ namespace {
 
 struct HeadLayout {
   fp4lin::HeadPlan plan;
-  size_t x, w, part, tlogit, G, acc, top, total;
+  size_t x, w, part, tlogit, G, acc, top;
+  size_t entry, first, kept, sums;  // distillation
+  size_t total;
 };
 
-// Sizes and strides that both calls check, and where they keep what they keep.
+// Sizes and strides that the calls check, and where they keep what they keep. k: a
+// teacher's entries a row, 0 for one target a row.
 fp4lin_status head_layout(fp4lin_dtype dt, fp4lin_head_layout layout, int64_t T, int64_t H,
-                          int64_t V, int64_t ldx, int64_t ldw, bool backward, HeadLayout* out) {
+                          int64_t V, int64_t k, int64_t ldx, int64_t ldw, bool backward,
+                          HeadLayout* out) {
   if (bad_dtype(dt)) return FP4LIN_ERR_DTYPE;
   const bool by_vocab = layout == FP4LIN_HEAD_VOCAB_MAJOR;
   if (!by_vocab && layout != FP4LIN_HEAD_HIDDEN_MAJOR) return FP4LIN_ERR_SHAPE;
@@ -990,10 +994,16 @@ fp4lin_status head_layout(fp4lin_dtype dt, fp4lin_head_layout layout, int64_t T,
   if (backward) {
     o.G = take(size_t(T) * size_t(o.plan.ldg) * size_t(esz));
     o.acc = take(size_t(T) * size_t(o.plan.ldp) * size_t(o.plan.slices) * 4);
-    o.top = take(4);
+    o.top = take(8);
   } else {
     o.part = take(size_t(T) * size_t(o.plan.parts) * 8);
-    o.tlogit = take(size_t(T) * 4);
+    o.tlogit = take(size_t(T) * 4 * (k > 0 ? size_t(o.plan.parts) : 1));
+  }
+  if (k > 0) {
+    o.entry = take(size_t(T) * size_t(k) * 8);
+    o.first = take(size_t(T) * (size_t(V + 31) / 32 + 1) * 2);
+    o.kept = take(size_t(T) * 4);
+    o.sums = take(size_t(T) * 8);
   }
   o.total = off > 256 ? off : 256;
   *out = o;
@@ -1001,16 +1011,15 @@ fp4lin_status head_layout(fp4lin_dtype dt, fp4lin_head_layout layout, int64_t T,
 }
 
 fp4lin_status head_call(const void* X, const void* W, fp4lin_dtype dt, fp4lin_head_layout layout,
-                        const int32_t* target, int64_t T, int64_t H, int64_t V, int64_t ldx,
-                        int64_t ldw, void* ws, size_t ws_bytes, bool backward, HeadLayout* o,
-                        fp4lin::HeadCall* c) {
-  const fp4lin_status s = head_layout(dt, layout, T, H, V, ldx, ldw, backward, o);
+                        const int32_t* target, int64_t T, int64_t H, int64_t V, int64_t k,
+                        int64_t ldx, int64_t ldw, void* ws, size_t ws_bytes, bool backward,
+                        HeadLayout* o, fp4lin::HeadCall* c) {
+  const fp4lin_status s = head_layout(dt, layout, T, H, V, k, ldx, ldw, backward, o);
   if (s != FP4LIN_OK) return s;
   if (ws == nullptr) return FP4LIN_ERR_NULL;
   if (!aligned16(ws) || !aligned16(X) || !aligned16(W)) return FP4LIN_ERR_ALIGN;
   if (ws_bytes < o->total) return FP4LIN_ERR_WORKSPACE;
   char* const base = static_cast<char*>(ws);
-  *c = fp4lin::HeadCall{};
   c->X = X;
   c->W = W;
   c->T = T;
@@ -1027,6 +1036,33 @@ fp4lin_status head_call(const void* X, const void* W, fp4lin_dtype dt, fp4lin_he
   c->G = base + o->G;
   c->acc = reinterpret_cast<float*>(base + o->acc);
   c->top = reinterpret_cast<float*>(base + o->top);
+  if (k > 0) {
+    c->k = k;
+    c->teacher_entry = base + o->entry;
+    c->teacher_first = reinterpret_cast<uint16_t*>(base + o->first);
+    c->kept = reinterpret_cast<int32_t*>(base + o->kept);
+    c->teacher_sums = base + o->sums;
+    c->tdot = c->tlogit;
+    c->target = c->kept;
+  }
+  return FP4LIN_OK;
+}
+
+// A teacher's list: what the two calls that take one check besides.
+fp4lin_status teacher_call(const int32_t* index, const void* teacher, fp4lin_dtype tdt, int64_t k,
+                           double temperature, fp4lin::HeadCall* c) {
+  if (bad_dtype(tdt)) return FP4LIN_ERR_DTYPE;
+  if (k < 1 || k > 1024) return FP4LIN_ERR_SHAPE;
+  const float inv = float(1.0 / temperature);
+  if (!(temperature > 0.0) || !std::isfinite(temperature) || !std::isfinite(inv) || inv == 0.0f)
+    return FP4LIN_ERR_VALUE;
+  if (reinterpret_cast<uintptr_t>(index) % 4 != 0 ||
+      reinterpret_cast<uintptr_t>(teacher) % (tdt == FP4LIN_BF16 ? 2 : 4) != 0)
+    return FP4LIN_ERR_ALIGN;
+  c->index = index;
+  c->teacher = teacher;
+  c->teacher_bf16 = tdt == FP4LIN_BF16;
+  c->inv_temperature = inv;
   return FP4LIN_OK;
 }
 
@@ -1037,14 +1073,14 @@ extern "C" {
 size_t fp4lin_head_loss_workspace_bytes(fp4lin_dtype dt, fp4lin_head_layout layout, int64_t T,
                                         int64_t H, int64_t V, int64_t ldx, int64_t ldw) {
   HeadLayout o;
-  return head_layout(dt, layout, T, H, V, ldx, ldw, false, &o) == FP4LIN_OK ? o.total : 0;
+  return head_layout(dt, layout, T, H, V, 0, ldx, ldw, false, &o) == FP4LIN_OK ? o.total : 0;
 }
 
 size_t fp4lin_head_loss_backward_workspace_bytes(fp4lin_dtype dt, fp4lin_head_layout layout,
                                                  int64_t T, int64_t H, int64_t V, int64_t ldx,
                                                  int64_t ldw) {
   HeadLayout o;
-  return head_layout(dt, layout, T, H, V, ldx, ldw, true, &o) == FP4LIN_OK ? o.total : 0;
+  return head_layout(dt, layout, T, H, V, 0, ldx, ldw, true, &o) == FP4LIN_OK ? o.total : 0;
 }
 
 fp4lin_status fp4lin_head_loss(const void* X, const void* W, fp4lin_dtype dt,
@@ -1055,9 +1091,9 @@ fp4lin_status fp4lin_head_loss(const void* X, const void* W, fp4lin_dtype dt,
       (T != 0 && (X == nullptr || target == nullptr || loss == nullptr || lse == nullptr)))
     return FP4LIN_ERR_NULL;
   HeadLayout o;
-  fp4lin::HeadCall c;
+  fp4lin::HeadCall c{};
   const fp4lin_status s =
-      head_call(X, W, dt, layout, target, T, H, V, ldx, ldw, ws, ws_bytes, false, &o, &c);
+      head_call(X, W, dt, layout, target, T, H, V, 0, ldx, ldw, ws, ws_bytes, false, &o, &c);
   if (s != FP4LIN_OK || T == 0) return s;
   c.loss = loss;
   c.lse_out = lse;
@@ -1075,9 +1111,73 @@ fp4lin_status fp4lin_head_loss_backward(const void* X, const void* W, fp4lin_dty
                   dX == nullptr)))
     return FP4LIN_ERR_NULL;
   HeadLayout o;
-  fp4lin::HeadCall c;
+  fp4lin::HeadCall c{};
   const fp4lin_status s =
-      head_call(X, W, dt, layout, target, T, H, V, ldx, ldw, ws, ws_bytes, true, &o, &c);
+      head_call(X, W, dt, layout, target, T, H, V, 0, ldx, ldw, ws, ws_bytes, true, &o, &c);
+  if (s != FP4LIN_OK) return s;
+  if (lddx < H || lddw < (c.by_vocab ? H : V)) return FP4LIN_ERR_SHAPE;
+  c.lse = lse;
+  c.dloss = dloss;
+  c.dX = dX;
+  c.dW = dW;
+  c.lddx = lddx;
+  c.lddw = lddw;
+  return launch_status(fp4lin::launch_head_loss_backward(c, dt == FP4LIN_BF16, o.plan, stream));
+}
+
+size_t fp4lin_head_distill_workspace_bytes(fp4lin_dtype dt, fp4lin_head_layout layout, int64_t T,
+                                           int64_t H, int64_t V, int64_t k, int64_t ldx,
+                                           int64_t ldw) {
+  HeadLayout o;
+  if (k < 1 || k > 1024) return 0;
+  return head_layout(dt, layout, T, H, V, k, ldx, ldw, false, &o) == FP4LIN_OK ? o.total : 0;
+}
+
+size_t fp4lin_head_distill_backward_workspace_bytes(fp4lin_dtype dt, fp4lin_head_layout layout,
+                                                    int64_t T, int64_t H, int64_t V, int64_t k,
+                                                    int64_t ldx, int64_t ldw) {
+  HeadLayout o;
+  if (k < 1 || k > 1024) return 0;
+  return head_layout(dt, layout, T, H, V, k, ldx, ldw, true, &o) == FP4LIN_OK ? o.total : 0;
+}
+
+fp4lin_status fp4lin_head_distill(const void* X, const void* W, fp4lin_dtype dt,
+                                  fp4lin_head_layout layout, const int32_t* index,
+                                  const void* teacher, fp4lin_dtype tdt, int64_t k,
+                                  double temperature, int64_t T, int64_t H, int64_t V, int64_t ldx,
+                                  int64_t ldw, float* loss, float* lse, void* ws, size_t ws_bytes,
+                                  hipStream_t stream) {
+  if (W == nullptr || (T != 0 && (X == nullptr || index == nullptr || teacher == nullptr ||
+                                  loss == nullptr || lse == nullptr)))
+    return FP4LIN_ERR_NULL;
+  HeadLayout o;
+  fp4lin::HeadCall c{};
+  fp4lin_status s = teacher_call(index, teacher, tdt, k, temperature, &c);
+  if (s != FP4LIN_OK) return s;
+  s = head_call(X, W, dt, layout, nullptr, T, H, V, k, ldx, ldw, ws, ws_bytes, false, &o, &c);
+  if (s != FP4LIN_OK || T == 0) return s;
+  c.loss = loss;
+  c.lse_out = lse;
+  return launch_status(fp4lin::launch_head_loss(c, dt == FP4LIN_BF16, o.plan, stream));
+}
+
+fp4lin_status fp4lin_head_distill_backward(const void* X, const void* W, fp4lin_dtype dt,
+                                           fp4lin_head_layout layout, const int32_t* index,
+                                           const void* teacher, fp4lin_dtype tdt, int64_t k,
+                                           double temperature, const float* lse, const float* dloss,
+                                           int64_t T, int64_t H, int64_t V, int64_t ldx,
+                                           int64_t ldw, void* dX, int64_t lddx, void* dW,
+                                           int64_t lddw, void* ws, size_t ws_bytes,
+                                           hipStream_t stream) {
+  if (W == nullptr || dW == nullptr ||
+      (T != 0 && (X == nullptr || index == nullptr || teacher == nullptr || lse == nullptr ||
+                  dloss == nullptr || dX == nullptr)))
+    return FP4LIN_ERR_NULL;
+  HeadLayout o;
+  fp4lin::HeadCall c{};
+  fp4lin_status s = teacher_call(index, teacher, tdt, k, temperature, &c);
+  if (s != FP4LIN_OK) return s;
+  s = head_call(X, W, dt, layout, nullptr, T, H, V, k, ldx, ldw, ws, ws_bytes, true, &o, &c);
   if (s != FP4LIN_OK) return s;
   if (lddx < H || lddw < (c.by_vocab ? H : V)) return FP4LIN_ERR_SHAPE;
   c.lse = lse;

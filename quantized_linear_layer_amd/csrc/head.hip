@@ -29,6 +29,15 @@
 // arrays are added in a fixed order at the end. No atomics: results repeat bit
 // for bit.
 //
+// Distillation takes the same products. The logits are z = l / temperature, and in the
+// place of the one-hot target stands a distribution over the indices that a teacher
+// lists for the row, its softmax over them:
+//   loss_t = sum_j p_tj (log p_tj - z_(t, index_tj)) + lse_t
+//   G_tv   = (exp(z_tv - lse_t) - sum over index_tj = v of p_tj) * dloss_t / temperature
+// A kernel of its own turns each row's list into (column, p) pairs sorted by column
+// and into the place in that list where every 32 columns begin, so that a tile finds
+// the pairs of its rows and columns without searching (teacher.hpp).
+//
 // Operands whose rows do not start on 16 bytes or whose contiguous size is not a
 // multiple of 8 elements are first copied, padded with zeros. The backward always
 // takes a copy of X, in which the rows that are left out are zero: what they hold,
@@ -39,6 +48,7 @@
 #include "device_common.hpp"
 #include "gemm_core.hpp"
 #include "internal.hpp"
+#include "teacher.hpp"
 
 namespace fp4lin {
 
@@ -113,6 +123,10 @@ struct HeadArgs {
   const float* top;  // G's scale, see head_prepare_kernel
   T* G;
   int64_t ldg;
+  // distillation: target is then 0 for a row that has entries and -1 for one that
+  // is left out
+  TeacherList teacher;
+  float* tdot;  // [T][parts]: sum of p z over a group of columns
 };
 
 // One (m, s) a row and wave, and the targets' logits. Bound by the matrix core and
@@ -121,7 +135,7 @@ struct HeadArgs {
 // 1.42). The pair leaves instead of 256 columns of logits, so the tile's way out is
 // 8 bytes a row and wave. With 32 rows the kernel is a read of W: 43 us for 262 MB
 // (6.1 TB/s). float32 1001 x 515 by 5003: 64 us (81 TFLOP/s).
-template <class C, class T, int kBT>
+template <class C, class T, int kBT, bool kDistill>
 __global__ __launch_bounds__(C::kThreads, C::kMinBlocks) void head_lse_kernel(HeadArgs<T> p) {
   constexpr int FM = C::FM, FN = C::FN;
   __shared__ __attribute__((aligned(16))) uint8_t st0[C::kStageBytes];
@@ -140,23 +154,54 @@ __global__ __launch_bounds__(C::kThreads, C::kMinBlocks) void head_lse_kernel(He
   product_tile<C>(f, (p.H + kStepElems<T> - 1) / kStepElems<T>, st0, st1, st2, st3, st4);
 
   const int row0 = m0 + wm * FM * 32, col0 = n0 + wn * FN * 32;
-  // the rows of this wave whose target it holds: few, so they are looked up one
-  // by one among the accumulators
-  const int trow = row0 + lane;
-  const int tcol = lane < FM * 32 && trow < p.T_ ? p.target[trow] : -1;
-  uint64_t hits = __ballot(tcol >= col0 && tcol < col0 + FN * 32 && tcol < p.V);
-  while (hits != 0) {
-    const int l = __builtin_ctzll(hits);
-    hits &= hits - 1;
-    const int c = __builtin_amdgcn_readlane(tcol, l) - col0;
+  if constexpr (kDistill) {
+    const float inv = p.teacher.inv_temperature;
 #pragma unroll
     for (int fm = 0; fm < FM; ++fm)
 #pragma unroll
       for (int fn = 0; fn < FN; ++fn)
 #pragma unroll
-        for (int r = 0; r < 16; ++r)
-          if (fm * 32 + frag_row(r, lane) == l && fn * 32 + (lane & 31) == c)
-            p.tlogit[row0 + l] = f.acc[fm][fn][r];
+        for (int r = 0; r < 16; ++r) f.acc[fm][fn][r] *= inv;
+    using Blocks = TileBlocks<C>;
+    Blocks blocks(st0, st1, st2, wave, lane, m0, n0);
+    TeacherTile<C> entries(p.teacher, row0, col0, p.T_, lane);
+    float dot[FM];
+#pragma unroll
+    for (int fm = 0; fm < FM; ++fm) {
+      dot[fm] = 0.0f;
+#pragma unroll
+      for (int fp = 0; fp < FN; fp += Blocks::kPair) {
+        if (!entries.any(fm, fp)) continue;
+        blocks.write(fm, fp, [&](int i, int j, int r) { return f.acc[i][j][r]; });
+        __builtin_amdgcn_wave_barrier();
+        entries.each(fm, fp, [&](int at, float prob) {
+          dot[fm] = fmaf(prob, blocks.eb[(lane & 31) * Blocks::kER + at], dot[fm]);
+        });
+        __builtin_amdgcn_wave_barrier();
+      }
+      dot[fm] += __shfl_xor(dot[fm], 32, kWave);
+      const int row = row0 + fm * 32 + (lane & 31);
+      if (lane < 32 && row < p.T_) p.tdot[int64_t(row) * p.parts + tn * C::WN + wn] = dot[fm];
+    }
+  } else {
+    // the rows of this wave whose target it holds: few, so they are looked up one
+    // by one among the accumulators
+    const int trow = row0 + lane;
+    const int tcol = lane < FM * 32 && trow < p.T_ ? p.target[trow] : -1;
+    uint64_t hits = __ballot(tcol >= col0 && tcol < col0 + FN * 32 && tcol < p.V);
+    while (hits != 0) {
+      const int l = __builtin_ctzll(hits);
+      hits &= hits - 1;
+      const int c = __builtin_amdgcn_readlane(tcol, l) - col0;
+  #pragma unroll
+      for (int fm = 0; fm < FM; ++fm)
+  #pragma unroll
+        for (int fn = 0; fn < FN; ++fn)
+  #pragma unroll
+          for (int r = 0; r < 16; ++r)
+            if (fm * 32 + frag_row(r, lane) == l && fn * 32 + (lane & 31) == c)
+              p.tlogit[row0 + l] = f.acc[fm][fn][r];
+    }
   }
   // columns past the vocabulary count as -inf
 #pragma unroll
@@ -190,9 +235,11 @@ __global__ __launch_bounds__(C::kThreads, C::kMinBlocks) void head_lse_kernel(He
 // 1000 pairs: 7.6 us; one thread a row: 75) wait for few loads in a row.
 constexpr int kJoinRows = 4;
 
+template <bool kDistill>
 __global__ __launch_bounds__(kJoinRows * 64) void head_join_kernel(
     const float2* __restrict__ part, int P, int T, int V, const int32_t* __restrict__ target,
-    const float* __restrict__ tlogit, float* __restrict__ loss, float* __restrict__ lse) {
+    const float* __restrict__ tlogit, const float* __restrict__ tdot,
+    const float2* __restrict__ teacher_sums, float* __restrict__ loss, float* __restrict__ lse) {
   const int lane = threadIdx.x & 63;
   const int row = blockIdx.x * kJoinRows + (threadIdx.x >> 6);
   if (row >= T) return;
@@ -210,11 +257,24 @@ __global__ __launch_bounds__(kJoinRows * 64) void head_join_kernel(
     const float m2 = __shfl_xor(m, off, kWave), s2 = __shfl_xor(s, off, kWave);
     join(m2, s2);
   }
+  float dot = 0.0f;
+  if constexpr (kDistill) {
+    for (int j = lane; j < P; j += 64) dot += tdot[int64_t(row) * P + j];
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) dot += __shfl_xor(dot, off, kWave);
+  }
   if (lane != 0) return;
   const float l = m + logf(s);
   lse[row] = l;
   const int t = target[row];
-  loss[row] = t >= 0 && t < V ? l - tlogit[row] : 0.0f;
+  if constexpr (kDistill) {
+    // (sum p log p, sum p) of the rounded p: what their sum is off 1 by then meets
+    // log p - z + lse, not lse
+    const float2 sums = teacher_sums[row];
+    loss[row] = t >= 0 ? fmaf(l, sums.y, sums.x - dot) : 0.0f;
+  } else {
+    loss[row] = t >= 0 && t < V ? l - tlogit[row] : 0.0f;
+  }
 }
 
 // bfloat16 G is kept in pieces of 32 columns, the rows of a piece together: the
@@ -226,7 +286,7 @@ constexpr bool kGPieces = sizeof(T) == 2;
 // G of a piece of the vocabulary over the largest |dloss|, zeros in the columns
 // that pad it to a multiple of 32 (float32: 8). As head_lse_kernel bound by the
 // matrix core: 8192 x 4096 by 8192 columns in 471 us (1.17 PFLOP/s).
-template <class C, class T, int kBT>
+template <class C, class T, int kBT, bool kDistill>
 __global__ __launch_bounds__(C::kThreads, C::kMinBlocks) void head_grad_kernel(HeadArgs<T> p) {
   constexpr int FM = C::FM, FN = C::FN;
   __shared__ __attribute__((aligned(16))) uint8_t st0[C::kStageBytes];
@@ -260,25 +320,29 @@ __global__ __launch_bounds__(C::kThreads, C::kMinBlocks) void head_grad_kernel(H
       const bool out = t < 0 || t >= p.Vall;
       if (out) g[fm][r] = 0.0f;
 #pragma unroll
-      for (int fn = 0; fn < FN; ++fn)
+      for (int fn = 0; fn < FN; ++fn) {
+        if constexpr (kDistill) f.acc[fm][fn][r] *= p.teacher.inv_temperature;
         f.acc[fm][fn][r] = out ? 0.0f : exp_diff(f.acc[fm][fn][r], lse);
+      }
     }
-  // the one-hot part, as in head_lse_kernel
-  const int trow = row0 + lane;
-  const int tcol = lane < FM * 32 && trow < p.T_ ? p.target[trow] : -1;
-  uint64_t hits = __ballot(tcol >= p.v0 + col0 && tcol < p.v0 + col0 + FN * 32);
-  while (hits != 0) {
-    const int l = __builtin_ctzll(hits);
-    hits &= hits - 1;
-    const int c = __builtin_amdgcn_readlane(tcol, l) - p.v0 - col0;
-#pragma unroll
-    for (int fm = 0; fm < FM; ++fm)
-#pragma unroll
-      for (int fn = 0; fn < FN; ++fn)
-#pragma unroll
-        for (int r = 0; r < 16; ++r)
-          if (fm * 32 + frag_row(r, lane) == l && fn * 32 + (lane & 31) == c)
-            f.acc[fm][fn][r] -= 1.0f;
+  if constexpr (!kDistill) {
+    // the one-hot part, as in head_lse_kernel
+    const int trow = row0 + lane;
+    const int tcol = lane < FM * 32 && trow < p.T_ ? p.target[trow] : -1;
+    uint64_t hits = __ballot(tcol >= p.v0 + col0 && tcol < p.v0 + col0 + FN * 32);
+    while (hits != 0) {
+      const int l = __builtin_ctzll(hits);
+      hits &= hits - 1;
+      const int c = __builtin_amdgcn_readlane(tcol, l) - p.v0 - col0;
+  #pragma unroll
+      for (int fm = 0; fm < FM; ++fm)
+  #pragma unroll
+        for (int fn = 0; fn < FN; ++fn)
+  #pragma unroll
+          for (int r = 0; r < 16; ++r)
+            if (fm * 32 + frag_row(r, lane) == l && fn * 32 + (lane & 31) == c)
+              f.acc[fm][fn][r] -= 1.0f;
+    }
   }
   // columns past the piece: the zeros that pad G
 #pragma unroll
@@ -290,15 +354,39 @@ __global__ __launch_bounds__(C::kThreads, C::kMinBlocks) void head_grad_kernel(H
         for (int r = 0; r < 16; ++r) f.acc[fm][fn][r] = 0.0f;
     }
   const int cols = kGPieces<T> ? (p.V + 31) & ~31 : (p.V + 7) & ~7;
-  emit_tile<C, kOutVec<T>>(
-      st0, st1, st2, wave, lane, m0, n0,
-      [&](int fm, int fn, int r) { return f.acc[fm][fn][r] * g[fm][r]; },
-      [&](int gr, int gc, const float* v) {
-        if (gr >= p.T_) return;
-        T* const dst = kGPieces<T> ? p.G + (gc / 32 * int64_t(p.T_) + gr) * 32 + gc % 32
-                                   : p.G + int64_t(gr) * p.ldg + gc;
-        store_vec<false>(dst, v, cols - gc, true);
-      });
+  const auto value = [&](int fm, int fn, int r) { return f.acc[fm][fn][r] * g[fm][r]; };
+  const auto emit = [&](int gr, int gc, const float* v) {
+    if (gr >= p.T_) return;
+    T* const dst = kGPieces<T> ? p.G + (gc / 32 * int64_t(p.T_) + gr) * 32 + gc % 32
+                               : p.G + int64_t(gr) * p.ldg + gc;
+    store_vec<false>(dst, v, cols - gc, true);
+  };
+  if constexpr (kDistill) {
+    // the teacher's part is taken off in the block, by the lane that has the row: its
+    // entries one by one, so that one index listed twice is taken off twice
+    using Blocks = TileBlocks<C>;
+    Blocks blocks(st0, st1, st2, wave, lane, m0, n0);
+    TeacherTile<C> entries(p.teacher, row0, p.v0 + col0, p.T_, lane);
+#pragma unroll
+    for (int fm = 0; fm < FM; ++fm) {
+      const int row = row0 + fm * 32 + (lane & 31);
+      const float mine = p.dloss[row < p.T_ ? row : p.T_ - 1] / top;
+#pragma unroll
+      for (int fp = 0; fp < FN; fp += Blocks::kPair) {
+        blocks.write(fm, fp, value);
+        __builtin_amdgcn_wave_barrier();
+        entries.each(fm, fp, [&](int at, float prob) {
+          float& q = blocks.eb[(lane & 31) * Blocks::kER + at];
+          q = fmaf(-prob, mine, q);
+        });
+        __builtin_amdgcn_wave_barrier();
+        blocks.template read<kOutVec<T>>(fm, fp, emit);
+        __builtin_amdgcn_wave_barrier();
+      }
+    }
+  } else {
+    emit_tile<C, kOutVec<T>>(st0, st1, st2, wave, lane, m0, n0, value, emit);
+  }
 }
 
 // Elements from an operand's reduction element 0 to k0, a multiple of a K step.
@@ -443,7 +531,8 @@ struct PrepareArgs {
   const float* dloss;
   const int32_t* target;
   int T_, V;
-  float* top;
+  float over;  // of the second scale
+  float* top;  // [2]: the largest |dloss|, and that times `over`: the products' scale
 };
 
 // One thread per 8 elements of the copy.
@@ -528,7 +617,9 @@ __global__ __launch_bounds__(256) void head_prepare_kernel(PrepareArgs<T> p) {
   __syncthreads();
   if (threadIdx.x == 0) {
     m = fmaxf(fmaxf(sh[0], sh[1]), fmaxf(sh[2], sh[3]));
-    *p.top = m != 0.0f ? m : 1.0f;
+    m = m != 0.0f ? m : 1.0f;
+    p.top[0] = m;
+    p.top[1] = m * p.over;
   }
 }
 
@@ -667,6 +758,11 @@ HeadPlan head_plan(bool bf16, bool backward, int64_t T, int64_t H, int64_t V, bo
 
 namespace {
 
+TeacherList teacher_list(const HeadCall& c) {
+  return TeacherList{static_cast<const int2*>(c.teacher_entry), c.teacher_first, int(c.k),
+                     int(teacher_groups(c.V)) + 1, c.inv_temperature};
+}
+
 // X and W as the products take them, copied where they have to be; for the
 // backward the largest |dloss| besides. X: as the logits read it.
 template <class T>
@@ -694,6 +790,7 @@ hipError_t prepare(const HeadCall& c, const HeadPlan& h, bool backward, DenseOpe
   p.target = c.target;
   p.T_ = int(c.T);
   p.V = int(c.V);
+  p.over = c.distill() ? c.inv_temperature : 1.0f;
   p.top = c.top;
   const int blocks = p.x.blocks + p.w.blocks + (backward ? 1 : 0);
   if (blocks > 0) head_prepare_kernel<T><<<unsigned(blocks), 256, 0, stream>>>(p);
@@ -713,7 +810,7 @@ DenseOperand<T> weight_columns(const HeadCall& c, const HeadPlan& h, const T* W,
   return DenseOperand<T>{W + v0, h.ldw, 0, int(round8(n)), int(c.H)};
 }
 
-template <class T, bool kGrad>
+template <class T, bool kGrad, bool kDistill>
 hipError_t logits(Tile t, bool by_vocab, const HeadArgs<T>& a, hipStream_t stream) {
   const int64_t tiles = tiles_of(t, a.T_, a.V);
   if (tiles >= (int64_t(1) << 31)) return hipErrorInvalidValue;
@@ -722,14 +819,14 @@ hipError_t logits(Tile t, bool by_vocab, const HeadArgs<T>& a, hipStream_t strea
     const dim3 grid(unsigned(tiles), 1, 1);
     if constexpr (kGrad) {
       if (by_vocab)
-        head_grad_kernel<C, T, kAlong><<<grid, C::kThreads, 0, stream>>>(a);
+        head_grad_kernel<C, T, kAlong, kDistill><<<grid, C::kThreads, 0, stream>>>(a);
       else
-        head_grad_kernel<C, T, kAcross><<<grid, C::kThreads, 0, stream>>>(a);
+        head_grad_kernel<C, T, kAcross, kDistill><<<grid, C::kThreads, 0, stream>>>(a);
     } else {
       if (by_vocab)
-        head_lse_kernel<C, T, kAlong><<<grid, C::kThreads, 0, stream>>>(a);
+        head_lse_kernel<C, T, kAlong, kDistill><<<grid, C::kThreads, 0, stream>>>(a);
       else
-        head_lse_kernel<C, T, kAcross><<<grid, C::kThreads, 0, stream>>>(a);
+        head_lse_kernel<C, T, kAcross, kDistill><<<grid, C::kThreads, 0, stream>>>(a);
     }
     return hipGetLastError();
   });
@@ -761,10 +858,23 @@ hipError_t run_forward(const HeadCall& c, const HeadPlan& h, hipStream_t stream)
   a.part = static_cast<float2*>(c.part);
   a.parts = int(h.parts);
   a.tlogit = c.tlogit;
-  e = logits<T, false>(pick_tile(sizeof(T) == 2, c.T, c.V), c.by_vocab, a, stream);
+  const Tile t = pick_tile(sizeof(T) == 2, c.T, c.V);
+  const unsigned joins = unsigned(ceil_div(c.T, kJoinRows));
+  if (c.distill()) {
+    a.teacher = teacher_list(c);
+    a.tdot = c.tdot;
+    e = logits<T, false, true>(t, c.by_vocab, a, stream);
+    if (e != hipSuccess) return e;
+    head_join_kernel<true><<<joins, kJoinRows * 64, 0, stream>>>(
+        a.part, int(h.parts), int(c.T), int(c.V), c.target, nullptr, c.tdot,
+        static_cast<const float2*>(c.teacher_sums), c.loss, c.lse_out);
+    return hipGetLastError();
+  }
+  e = logits<T, false, false>(t, c.by_vocab, a, stream);
   if (e != hipSuccess) return e;
-  head_join_kernel<<<unsigned(ceil_div(c.T, kJoinRows)), kJoinRows * 64, 0, stream>>>(
-      a.part, int(h.parts), int(c.T), int(c.V), c.target, c.tlogit, c.loss, c.lse_out);
+  head_join_kernel<false><<<joins, kJoinRows * 64, 0, stream>>>(
+      a.part, int(h.parts), int(c.T), int(c.V), c.target, c.tlogit, nullptr, nullptr, c.loss,
+      c.lse_out);
   return hipGetLastError();
 }
 
@@ -797,7 +907,13 @@ hipError_t run_backward(const HeadCall& c, const HeadPlan& h, hipStream_t stream
       a.top = c.top;
       a.G = G;
       a.ldg = h.ldg;
-      e = logits<T, true>(pick_tile(kBf16, c.T, n), c.by_vocab, a, stream);
+      const Tile t = pick_tile(kBf16, c.T, n);
+      if (c.distill()) {
+        a.teacher = teacher_list(c);
+        e = logits<T, true, true>(t, c.by_vocab, a, stream);
+      } else {
+        e = logits<T, true, false>(t, c.by_vocab, a, stream);
+      }
       if (e != hipSuccess) return e;
 
       // dX: G (T x n) times W's piece transposed; the columns that fill n to n8 are
@@ -811,7 +927,7 @@ hipError_t run_backward(const HeadCall& c, const HeadPlan& h, hipStream_t stream
       const int64_t per = ceil_div(ceil_div(n, h.slices), 64) * 64;
       if (direct) {
         const ProductArgs<T, T> q{A, B, int(c.T), int(c.H), n8, static_cast<T*>(c.dX), c.lddx, 0, 1,
-                                  c.top};
+                                  c.top + 1};
         e = c.by_vocab ? product<T, kAlong, kAcross, T, false>(tx, q, 1, stream)
                        : product<T, kAlong, kAlong, T, false>(tx, q, 1, stream);
       } else {
@@ -832,25 +948,30 @@ hipError_t run_backward(const HeadCall& c, const HeadPlan& h, hipStream_t stream
         kGPieces<T> ? DenseOperand<T>{X.p, 0, c.T * 32, int(round32(c.H)), int(c.T)}
                     : DenseOperand<T>{X.p, X.ld, 0, int(round8(c.H)), int(c.T)};
     const ProductArgs<T, T> q{c.by_vocab ? Gt : Xt, c.by_vocab ? Xt : Gt, int(rows), int(cols),
-                              int(c.T), dW + v0 * (c.by_vocab ? c.lddw : 1), c.lddw, 0, 1, c.top};
+                              int(c.T), dW + v0 * (c.by_vocab ? c.lddw : 1), c.lddw, 0, 1,
+                              c.top + 1};
     e = product<T, kAcrossRows, kAcrossRows, T, false>(pick_tile(kBf16, rows, cols), q, 1, stream);
     if (e != hipSuccess) return e;
   }
   if (direct || c.T == 0) return hipSuccess;
   head_sum_kernel<T><<<copy_blocks(c.T * (h.ldp / 4)), 256, 0, stream>>>(
-      c.acc, int(h.slices), c.T * h.ldp, c.T, int(c.H), h.ldp, c.top, static_cast<T*>(c.dX),
-      c.lddx);
+      c.acc, int(h.slices), c.T * h.ldp, c.T, int(c.H), h.ldp, c.top + 1,
+      static_cast<T*>(c.dX), c.lddx);
   return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_head_loss(const HeadCall& c, bool bf16, const HeadPlan& h, hipStream_t stream) {
+  const hipError_t e = c.distill() ? launch_teacher(c, stream) : hipSuccess;
+  if (e != hipSuccess) return e;
   return bf16 ? run_forward<uint16_t>(c, h, stream) : run_forward<float>(c, h, stream);
 }
 
 hipError_t launch_head_loss_backward(const HeadCall& c, bool bf16, const HeadPlan& h,
                                      hipStream_t stream) {
+  const hipError_t e = c.distill() && c.T > 0 ? launch_teacher(c, stream) : hipSuccess;
+  if (e != hipSuccess) return e;
   return bf16 ? run_backward<uint16_t>(c, h, stream) : run_backward<float>(c, h, stream);
 }
 

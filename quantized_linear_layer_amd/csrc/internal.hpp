@@ -151,6 +151,18 @@ struct HeadCall {
   const float *lse, *dloss;
   void *dX, *dW;
   int64_t lddx, lddw;
+  // distillation (k > 0): a teacher's k entries a row; target is then `kept`
+  int64_t k;
+  const int32_t* index;
+  const void* teacher;
+  bool teacher_bf16;
+  float inv_temperature;
+  void *teacher_entry, *teacher_sums;
+  uint16_t* teacher_first;
+  int32_t* kept;
+  float* tdot;
+
+  bool distill() const { return k > 0; }
 };
 hipError_t launch_head_loss(const HeadCall& c, bool bf16, const HeadPlan& h, hipStream_t stream);
 hipError_t launch_head_loss_backward(const HeadCall& c, bool bf16, const HeadPlan& h,

@@ -1,0 +1,242 @@
+// A teacher's top logits, as the head's distillation takes them (head.hip).
+//
+// Each row lists k indices into the vocabulary with a logit u each;
+//   p_j = exp(u_j / temperature - M) / sum_i exp(u_i / temperature - M)
+// over those in the vocabulary (M the largest). Entries outside it, and those whose p
+// is 0 (u of -infinity, or far below M), are left out, so that what the student has at
+// their place is not asked; a row with no other entry is left out itself. Kept
+// per row, in the workspace:
+//   entry   the (column, p) pairs sorted by column, ties in the list's order
+//   first   for every 32 columns, how many pairs lie before them
+//   sums    (sum p log p, sum p) of the p as they are rounded
+#pragma once
+
+#include "device_common.hpp"
+#include "gemm_core.hpp"
+#include "internal.hpp"
+
+namespace fp4lin {
+
+struct TeacherList {
+  const int2* entry;      // [T][k]: column, bits of p
+  const uint16_t* first;  // [T][ld]
+  int k, ld;
+  float inv_temperature;
+};
+
+// The entries of a wave's rows and columns, block by block (TileBlocks): the lane has
+// row lane % 32 of the block, and with two fragments a block its half's 32 columns.
+// What all blocks begin with is read at once, before the first is visited: of most
+// (row, 32 columns) there is nothing or one entry.
+template <class C>
+struct TeacherTile {
+  using Blocks = TileBlocks<C>;
+  static constexpr int kPair = Blocks::kPair, kN = C::FN / kPair;
+
+  const int2* entry;
+  int col0, lane;
+  int begin[C::FM][kN], end[C::FM][kN];
+  int2 head[C::FM][kN];
+
+  // col0: of the wave in the vocabulary, a multiple of 32
+  __device__ __attribute__((always_inline)) inline TeacherTile(const TeacherList& t, int row0,
+                                                               int col0_, int rows, int lane_)
+      : entry(t.entry), col0(col0_), lane(lane_) {
+    const int half = lane >> 5;
+#pragma unroll
+    for (int fm = 0; fm < C::FM; ++fm) {
+      const int row = row0 + fm * 32 + (lane & 31);
+      const bool in = row < rows && half < kPair;
+#pragma unroll
+      for (int n = 0; n < kN; ++n) {
+        const int g = col0 / 32 + n * kPair + half;
+        begin[fm][n] = end[fm][n] = 0;
+        if (in && g + 1 < t.ld) {
+          const uint16_t* const f = t.first + int64_t(row) * t.ld + g;
+          begin[fm][n] = f[0];
+          end[fm][n] = f[1];
+        }
+      }
+    }
+#pragma unroll
+    for (int fm = 0; fm < C::FM; ++fm) {
+      const int64_t at = int64_t(row0 + fm * 32 + (lane & 31)) * t.k;
+#pragma unroll
+      for (int n = 0; n < kN; ++n)
+        if (begin[fm][n] < end[fm][n]) head[fm][n] = entry[at + begin[fm][n]];
+    }
+    row_at[0] = int64_t(row0 + (lane & 31)) * t.k;
+#pragma unroll
+    for (int fm = 1; fm < C::FM; ++fm) row_at[fm] = row_at[0] + int64_t(fm) * 32 * t.k;
+  }
+
+  __device__ __attribute__((always_inline)) inline bool any(int fm, int fp) const {
+    return __ballot(begin[fm][fp / kPair] < end[fm][fp / kPair]) != 0;
+  }
+
+  // f(column in the block, p) for the lane's entries, in their order
+  template <class F>
+  __device__ __attribute__((always_inline)) inline void each(int fm, int fp, const F& f) const {
+    const int n = fp / kPair, base = col0 + fp * 32;
+    int2 e = head[fm][n];
+    for (int i = begin[fm][n]; i < end[fm][n];) {
+      f(e.x - base, __int_as_float(e.y));
+      if (++i < end[fm][n]) e = entry[row_at[fm] + i];
+    }
+  }
+
+ private:
+  int64_t row_at[C::FM];
+};
+
+constexpr int kMaxTeacher = 1024;
+__host__ inline int64_t teacher_groups(int64_t V) { return (V + 31) / 32; }
+
+struct TeacherArgs {
+  const int32_t* index;
+  const void* logit;
+  bool bf16;
+  int T, k, V;
+  float inv_temperature;
+  int2* entry;
+  uint16_t* first;
+  int ld;
+  int32_t* kept;  // 0 or -1
+  float2* sums;
+};
+
+// kThreads a row. The order of a row's k entries is found by counting, for each, the
+// entries before it: k reads of shared memory that all lanes share.
+template <int kThreads>
+__global__ __launch_bounds__(256) void teacher_kernel(TeacherArgs p) {
+  constexpr int kRows = 256 / kThreads, kWaves = kThreads / 64;
+  constexpr int kList = kThreads == 64 ? 64 : kMaxTeacher;
+  constexpr int kPer = kList / kThreads;  // entries a thread, at most
+  __shared__ int32_t key_s[kRows][kList], sorted_s[kRows][kList];
+  __shared__ float red[kRows][kWaves];
+  const int t = threadIdx.x % kThreads, r = threadIdx.x / kThreads, lane = threadIdx.x & 63;
+  const int row = blockIdx.x * kRows + r;
+  const bool in = row < p.T;
+  int32_t* const key = key_s[r];
+  int32_t* const sorted = sorted_s[r];
+  // over the row's threads, on all of them, in one order
+  auto reduce = [&](float v, auto op) {
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) v = op(v, __shfl_xor(v, off, kWave));
+    if constexpr (kWaves > 1) {
+      __syncthreads();
+      if (lane == 0) red[r][t / 64] = v;
+      __syncthreads();
+      v = red[r][0];
+#pragma unroll
+      for (int w = 1; w < kWaves; ++w) v = op(v, red[r][w]);
+    }
+    return v;
+  };
+  auto add = [](float a, float b) { return a + b; };
+
+  constexpr int32_t kOut = 0x7fffffff;
+  float u[kPer];
+  int32_t col[kPer];
+  float top = -__builtin_huge_valf();
+  bool bad = false;  // a NaN among them
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int j = t + i * kThreads;
+    col[i] = kOut;
+    u[i] = -__builtin_huge_valf();
+    if (in && j < p.k) {
+      const int64_t at = int64_t(row) * p.k + j;
+      const int32_t c = p.index[at];
+      const float l = p.bf16 ? BF16In::widen(static_cast<const uint16_t*>(p.logit)[at])
+                             : static_cast<const float*>(p.logit)[at];
+      if (c >= 0 && c < p.V) {
+        col[i] = c;
+        u[i] = l * p.inv_temperature;
+        bad |= u[i] != u[i];
+        top = fmaxf(top, u[i]);
+      }
+    }
+  }
+  top = reduce(top, [](float a, float b) { return fmaxf(a, b); });
+  const bool nan = reduce(bad ? 1.0f : 0.0f, add) != 0.0f;
+  const bool some = nan || top != -__builtin_huge_valf();
+  float e[kPer], sum = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    e[i] = col[i] == kOut || u[i] == -__builtin_huge_valf() ? 0.0f : expf(u[i] - top);
+    sum += e[i];
+  }
+  sum = reduce(sum, add);
+  const float log_sum = logf(sum);
+  float plogp = 0.0f, total = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int j = t + i * kThreads;
+    const float prob = e[i] / sum;
+    if (!some || prob == 0.0f) col[i] = kOut;
+    if (col[i] != kOut) {
+      plogp = fmaf(prob, (u[i] - top) - log_sum, plogp);
+      total += prob;
+    }
+    e[i] = prob;
+    if (j < kList) key[j] = col[i];
+  }
+  plogp = reduce(plogp, add);
+  total = reduce(total, add);
+  if (t == 0 && in) {
+    p.kept[row] = some ? 0 : -1;
+    p.sums[row] = make_float2(plogp, total);
+  }
+  __syncthreads();
+
+  int place[kPer] = {};
+  for (int i = 0; i < p.k; ++i) {
+    const int32_t other = key[i];
+#pragma unroll
+    for (int q = 0; q < kPer; ++q)
+      place[q] += other < col[q] || (other == col[q] && i < t + q * kThreads);
+  }
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int j = t + i * kThreads;
+    if (!in || j >= p.k) continue;
+    sorted[place[i]] = col[i];
+    p.entry[int64_t(row) * p.k + place[i]] = make_int2(col[i], __float_as_int(e[i]));
+  }
+  __syncthreads();
+  if (!in) return;
+  for (int g = t; g < p.ld; g += kThreads) {
+    int lo = 0, hi = p.k;  // entries below column 32 g
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (sorted[mid] < 32 * int64_t(g))
+        lo = mid + 1;
+      else
+        hi = mid;
+    }
+    p.first[int64_t(row) * p.ld + g] = uint16_t(lo);
+  }
+}
+
+inline hipError_t launch_teacher(const HeadCall& c, hipStream_t stream) {
+  const TeacherArgs p{c.index,
+                      c.teacher,
+                      c.teacher_bf16,
+                      int(c.T),
+                      int(c.k),
+                      int(c.V),
+                      c.inv_temperature,
+                      static_cast<int2*>(c.teacher_entry),
+                      c.teacher_first,
+                      int(teacher_groups(c.V)) + 1,
+                      c.kept,
+                      static_cast<float2*>(c.teacher_sums)};
+  if (c.k <= 64)
+    teacher_kernel<64><<<unsigned((c.T + 3) / 4), 256, 0, stream>>>(p);
+  else
+    teacher_kernel<256><<<unsigned(c.T), 256, 0, stream>>>(p);
+  return hipGetLastError();
+}
+
+}  // namespace fp4lin

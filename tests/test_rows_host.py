@@ -191,3 +191,81 @@ def test_binding_refusals(library):
         with pytest.raises((ValueError, TypeError)):
             call()
         assert library.calls == [], i
+
+
+# ---- the head loss against a teacher's top logits --------------------------------------
+HID, VOC = _lib.HEAD_HIDDEN_MAJOR, _lib.HEAD_VOCAB_MAJOR
+
+
+def distill_ws(dt=1, layout=HID, T=64, H=64, V=512, k=8, ldx=64, ldw=512, backward=False):
+    f = L.fp4lin_head_distill_backward_workspace_bytes if backward else L.fp4lin_head_distill_workspace_bytes
+    return f(dt, layout, T, H, V, k, ldx, ldw)
+
+
+def distill(X=FAKE, W=FAKE, dt=1, layout=HID, index=FAKE, teacher=FAKE, tdt=0, k=8, temperature=1.0, T=4, H=64, V=512,
+            ldx=64, ldw=512, loss=FAKE, lse=FAKE, ws=FAKE, n=BIG):
+    return L.fp4lin_head_distill(X, W, dt, layout, index, teacher, tdt, k, temperature, T, H, V, ldx, ldw, loss, lse,
+                                 ws, n, None)
+
+
+def distill_back(X=FAKE, W=FAKE, dt=1, layout=HID, index=FAKE, teacher=FAKE, tdt=0, k=8, temperature=1.0, T=4, H=64,
+                 V=512, ldx=64, ldw=512, lse=FAKE, dloss=FAKE, dX=FAKE, lddx=64, dW=FAKE, lddw=512, ws=FAKE, n=BIG):
+    return L.fp4lin_head_distill_backward(X, W, dt, layout, index, teacher, tdt, k, temperature, lse, dloss, T, H, V,
+                                          ldx, ldw, dX, lddx, dW, lddw, ws, n, None)
+
+
+@pytest.mark.parametrize("call,pointers", [
+    (distill, ("X", "W", "index", "teacher", "loss", "lse", "ws")),
+    (distill_back, ("X", "W", "index", "teacher", "lse", "dloss", "dX", "dW", "ws"))])
+def test_distill_refusals(call, pointers):
+    for name in pointers:
+        assert call(**{name: None}) == _lib.ERR_NULL, name
+    assert call(dt=2) == _lib.ERR_DTYPE and call(tdt=2) == _lib.ERR_DTYPE
+    for bad in (dict(layout=5), dict(T=-1), dict(H=0), dict(V=0), dict(ldx=63), dict(ldw=511), dict(k=0), dict(k=1025)):
+        assert call(**bad) == _lib.ERR_SHAPE, bad
+    for bad in (0.0, -1.0, float("nan"), float("inf"), 1e-40, 1e46):
+        assert call(temperature=bad) == _lib.ERR_VALUE, bad
+    for name in ("X", "W", "ws", "index", "teacher"):
+        assert call(**{name: HALF}) == _lib.ERR_ALIGN, name
+    assert call(teacher=ODD, tdt=1) == _lib.ERR_ALIGN
+    assert call(n=distill_ws(T=4, backward=call is distill_back) - 1) == _lib.ERR_WORKSPACE
+    if call is distill_back:
+        assert call(lddx=63) == _lib.ERR_SHAPE and call(lddw=511) == _lib.ERR_SHAPE
+    else:
+        assert call(T=0, X=None, index=None, teacher=None, loss=None, lse=None) == _lib.OK
+
+
+@pytest.mark.parametrize("backward", [False, True])
+def test_distill_workspace(backward):
+    plain = L.fp4lin_head_loss_backward_workspace_bytes if backward else L.fp4lin_head_loss_workspace_bytes
+    # a teacher's pairs and where every 32 columns begin among them
+    assert distill_ws(backward=backward) >= plain(1, HID, 64, 64, 512, 64, 512) + 64 * (8 * 8 + 17 * 2)
+    assert distill_ws(T=0, backward=backward) >= 256
+    for bad in (dict(k=0), dict(k=1025), dict(T=-1), dict(V=0), dict(layout=2), dict(dt=3), dict(ldw=511)):
+        assert distill_ws(**bad, backward=backward) == 0, bad
+
+
+def test_distill_binding_refusals(library):
+    X, W, f, ws = torch.zeros((4, 8)), torch.zeros((8, 6)), torch.zeros(4), torch.zeros(64, dtype=torch.uint8)
+    i, u = ints(4, 3), torch.zeros((4, 3))
+    bad = [
+        lambda: qll.fp4lin_head_distill(X, W, i.long(), u, f, f, ws),
+        lambda: qll.fp4lin_head_distill(X, W, ints(3, 4).t(), u, f, f, ws),
+        lambda: qll.fp4lin_head_distill(X, W, ints(3, 3), torch.zeros((3, 3)), f, f, ws),
+        lambda: qll.fp4lin_head_distill(X, W, ints(4), torch.zeros(4), f, f, ws),
+        lambda: qll.fp4lin_head_distill(X, W, i, torch.zeros((4, 2)), f, f, ws),
+        lambda: qll.fp4lin_head_distill(X, W, i, u.double(), f, f, ws),
+        lambda: qll.fp4lin_head_distill(X, W, i, u, f[:3], f, ws),
+        lambda: qll.fp4lin_head_distill(X, W, i, u, f, f, ws, by_vocab=True),
+        lambda: qll.fp4lin_head_distill_backward(X, W, i, u, f, f.double(), X, W, ws),
+        lambda: qll.fp4lin_head_distill_backward(X, W, i, u, f, f, X[:3], W, ws),
+        lambda: qll.fp4lin_head_distill_backward(X, W, i, u, f, f, X, W.t(), ws),
+        lambda: qll.fp4lin_head_distill_backward(X, W, i, u, f, f, X.bfloat16(), W, ws),
+    ]
+    for n, call in enumerate(bad):
+        with pytest.raises((ValueError, TypeError)):
+            call()
+        assert library.calls == [], n
+    qll.fp4lin_head_distill(X, W, i, u, f, f, ws)
+    qll.fp4lin_head_distill_backward(X, W, i, u, f, f, X, W, ws)
+    assert library.gpus == [1, 1]
