@@ -791,7 +791,7 @@ fp4lin_status embed_layout(int64_t T, int64_t V, int64_t H, EmbedLayout* out) {
     return at;
   };
   EmbedLayout o{};
-  o.order = take(size_t(T) * 4);
+  o.order = take(size_t(T) * 8);
   o.ends = take(size_t(V) * 4);
   o.part = take(size_t(fp4lin::embed_pieces(T)) * 2 * (size_t(H + 7) / 8 * 8) * 4);
   o.total = off;
@@ -946,7 +946,7 @@ fp4lin_status fp4lin_embed_backward(const void* dX, fp4lin_dtype dt, const int32
   c.add = add != 0;
   c.dE = dE;
   c.ldde = ldde;
-  c.order = reinterpret_cast<int32_t*>(base + o.order);
+  c.order = base + o.order;
   c.ends = reinterpret_cast<int32_t*>(base + o.ends);
   c.part = reinterpret_cast<float*>(base + o.part);
   return launch_status(

@@ -50,52 +50,124 @@ __global__ __launch_bounds__(kRowThreads) void embed_kernel(EmbedArgs p, Divisor
   });
 }
 
-__global__ __launch_bounds__(kSortWaves * 64) void embed_sort_kernel(SortArgs p) { sort_body(p); }
-
 constexpr int kList = 32;
 
 struct EmbedBackArgs {
   const void* dX;
   int64_t lddx;
-  const int32_t *token, *order, *ends;  // order, ends: of the sort
   int32_t T, V;
   int64_t H;
   float scale;
   int add;
   void* dE;
   int64_t ldde;
-  float* part;    // [pieces][2][groups * 8]: of the first list of a piece, of the last
-  uint32_t rows;  // items of the table's rows
-  uint32_t cuts;  // items of the pieces
+  float* part;  // [pieces][2][groups * 8]: of the first list of a piece, of the last
 };
 
-__device__ inline int32_t list_begin(const EmbedBackArgs& p, int32_t v) { return v > 0 ? p.ends[v - 1] : 0; }
+// What the sort leaves: order[i] = (position, token), ends[v] = positions with a token <= v
+// in the vocabulary. Nothing that the kernels below write overlaps it.
+struct Sorted {
+  const int2* __restrict__ order;
+  const int32_t* __restrict__ ends;
 
-// sum[] += the rows of dX at the sorted positions begin .. end - 1
+  __device__ __attribute__((always_inline)) inline int32_t begin_of(int32_t v) const {
+    return v > 0 ? ends[v - 1] : 0;
+  }
+};
+
+// The sort, on the first workgroups, which wait for loads and for each other most of
+// the time; the others fill the table with zeros meanwhile.
+struct FillArgs {
+  void* dE;
+  int64_t ldde, H;
+  uint32_t items;  // 0: nothing to fill
+};
+
+template <class Out, bool kOnce>
+__global__ __launch_bounds__(kSortWaves * 64, 8) void embed_sort_kernel(SortArgs p, FillArgs f, Divisor groups,
+                                                                        uint32_t sorters) {
+  if (blockIdx.x < sorters) return sort_body<kOnce>(p);
+  const uint64_t step = uint64_t(gridDim.x - sorters) * (kSortWaves * 64);
+  for (uint64_t i = uint64_t(blockIdx.x - sorters) * (kSortWaves * 64) + threadIdx.x; i < f.items; i += step) {
+    const uint32_t v = groups(uint32_t(i));
+    const int64_t c = int64_t(uint32_t(i) - v * groups.d) * 8;
+    by_width(f.H - c, [&](auto w) {
+      put8<Out, decltype(w)::value>(static_cast<typename Out::T*>(f.dE) + int64_t(v) * f.ldde + c, f.H - c,
+                                    Vec8<Out>{});
+    });
+  }
+}
+
 template <class In, bool kWhole>
-__device__ inline void add_rows(const EmbedBackArgs& p, int32_t begin, int32_t end, int64_t c,
-                                int64_t valid, float (&sum)[8]) {
-  constexpr int U = 4;  // rows in flight
-  for (int32_t i = begin; i < end; i += U) {
-    Vec8<In> v[U];
+__device__ __attribute__((always_inline)) inline void read_row(const EmbedBackArgs& p, int32_t row, int64_t c,
+                                                               Vec8<In>& v) {
+  get8<In, kWhole>(static_cast<const typename In::T*>(p.dX) + int64_t(row) * p.lddx + c, p.H - c, v);
+}
+
+template <class In>
+__device__ __attribute__((always_inline)) inline void add_row(const Vec8<In>& v, float (&sum)[8]) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int32_t t = p.order[i + u < end ? i + u : end - 1];
-      get8<In, kWhole>(static_cast<const typename In::T*>(p.dX) + int64_t(t) * p.lddx + c, valid, v[u]);
+  for (int k = 0; k < 8; ++k) sum[k] += In::widen(v.v[k]);
+}
+
+// sum[] += the first n (below 8) of the rows t: four, two and one at a time, without a
+// condition on any load: one behind a branch is waited for before the next.
+template <class In, bool kWhole>
+__device__ __attribute__((always_inline)) inline void add_few(const EmbedBackArgs& p, const int32_t (&t)[8],
+                                                              int32_t n, int64_t c, float (&sum)[8]) {
+  if (n & 4) {
+    Vec8<In> v[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) read_row<In, kWhole>(p, t[u], c, v[u]);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) add_row<In>(v[u], sum);
+  }
+  if (n & 2) {
+    Vec8<In> v[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int32_t early = t[u], late = t[4 + u];
+      read_row<In, kWhole>(p, n & 4 ? late : early, c, v[u]);
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (i + u < end) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) sum[k] += In::widen(v[u].v[k]);
-      }
+    for (int u = 0; u < 2; ++u) add_row<In>(v[u], sum);
   }
+  if (n & 1) {
+    Vec8<In> v;
+    const int32_t t0 = t[0], t2 = t[2], t4 = t[4], t6 = t[6];
+    read_row<In, kWhole>(p, n & 4 ? (n & 2 ? t6 : t4) : (n & 2 ? t2 : t0), c, v);
+    add_row<In>(v, sum);
+  }
+}
+
+// sum[] += the rows of dX at the sorted positions begin .. end - 1, eight of them on
+// their way at a time. The next rows' positions are read while these are added.
+template <class In, bool kWhole>
+__device__ __attribute__((always_inline)) inline void add_rows(const EmbedBackArgs& p, const int2* order,
+                                                               int32_t begin, int32_t end, int64_t c,
+                                                               float (&sum)[8]) {
+  int32_t t[8];
+  auto look = [&](int32_t i) {
+#pragma unroll
+    for (int u = 0; u < 8; ++u) t[u] = order[i + u < end ? i + u : end - 1].x;
+  };
+  look(begin);
+  int32_t i = begin;
+  for (; i + 8 <= end; i += 8) {
+    Vec8<In> v[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) read_row<In, kWhole>(p, t[u], c, v[u]);
+    look(i + 8 < end ? i + 8 : end - 1);
+#pragma unroll
+    for (int u = 0; u < 8; ++u) add_row<In>(v[u], sum);
+  }
+  add_few<In, kWhole>(p, t, end - i, c, sum);
 }
 
 // scale * sum, or that on top of what is there, to row v
 template <class Out, bool kWhole>
-__device__ inline void put_row(const EmbedBackArgs& p, int32_t v, int64_t c, int64_t valid,
-                               float (&sum)[8]) {
+__device__ __attribute__((always_inline)) inline void put_row(const EmbedBackArgs& p, int32_t v, int64_t c,
+                                                              int64_t valid, float (&sum)[8]) {
   typename Out::T* const dst = static_cast<typename Out::T*>(p.dE) + int64_t(v) * p.ldde + c;
   if (p.add) {
     Vec8<Out> old;
@@ -109,81 +181,204 @@ __device__ inline void put_row(const EmbedBackArgs& p, int32_t v, int64_t c, int
   put8<Out, kWhole>(dst, valid, rounded<Out>(sum));
 }
 
-// The first workgroups take the pieces of long lists, the others the table's rows.
-template <class In, class Out>
-__global__ __launch_bounds__(kRowThreads) void embed_back_kernel(EmbedBackArgs p, Divisor groups,
-                                                                 uint32_t cut_blocks) {
-  if (blockIdx.x < cut_blocks) {
-    const uint32_t i = blockIdx.x * kRowThreads + threadIdx.x;
-    if (i >= p.cuts) return;
-    const uint32_t piece = groups(i);
-    const int64_t c = int64_t(i - piece * groups.d) * 8, valid = p.H - c;
-    const int32_t kept = p.ends[p.V - 1];
-    const int32_t a = int32_t(piece) * kList, b = kept - a < kList ? kept : a + kList;
-    if (a >= b) return;
-    float* const part = p.part + (int64_t(piece) * 2 * groups.d) * 8 + c;
-    auto sum_of = [&](int32_t begin, int32_t end, float* dst) {
-      float sum[8] = {};
-      by_width(valid, [&](auto whole) { add_rows<In, decltype(whole)::value>(p, begin, end, c, valid, sum); });
-#pragma unroll
-      for (int k = 0; k < 8; ++k) dst[k] = sum[k];
-    };
-    const int32_t v0 = p.token[p.order[a]], v1 = p.token[p.order[b - 1]];
-    const int32_t end0 = p.ends[v0], begin1 = list_begin(p, v1);
-    if (end0 - list_begin(p, v0) > kList) sum_of(a, end0 < b ? end0 : b, part);
-    if (v1 != v0 && p.ends[v1] - begin1 > kList) sum_of(begin1, b, part + int64_t(groups.d) * 8);
-    return;
+// The part of a piece that belongs to long lists: at most the first one, that came from
+// the piece before, and the last one.
+struct Piece {
+  int32_t begin[2], end[2];
+};
+__device__ __attribute__((always_inline)) inline Piece piece_at(const EmbedBackArgs& p, const Sorted& s,
+                                                                int32_t piece) {
+  Piece r{};
+  const int32_t kept = s.ends[p.V - 1];
+  const int32_t a = piece * kList, b = kept - a < kList ? kept : a + kList;
+  if (a >= b) return r;
+  const int32_t v0 = s.order[a].y, v1 = s.order[b - 1].y;
+  const int32_t end0 = s.ends[v0], begin1 = s.begin_of(v1);
+  if (end0 - s.begin_of(v0) > kList) {
+    r.begin[0] = a;
+    r.end[0] = end0 < b ? end0 : b;
   }
-  const uint64_t i = uint64_t(blockIdx.x - cut_blocks) * kRowThreads + threadIdx.x;
-  if (i >= p.rows) return;
-  const uint32_t v = groups(uint32_t(i));
-  const int64_t c = int64_t(uint32_t(i) - v * groups.d) * 8, valid = p.H - c;
-  const int32_t begin = list_begin(p, v), end = p.ends[v];
-  if (end - begin > kList || (p.add && begin == end)) return;
-  by_width(valid, [&](auto whole) {
-    float sum[8] = {};
-    add_rows<In, decltype(whole)::value>(p, begin, end, c, valid, sum);
-    put_row<Out, decltype(whole)::value>(p, v, c, valid, sum);
-  });
+  if (v1 != v0 && s.ends[v1] - begin1 > kList) {
+    r.begin[1] = begin1;
+    r.end[1] = b;
+  }
+  return r;
 }
 
-// The long list that begins in a piece, if one does: its pieces added in order.
-template <class Out>
-__global__ __launch_bounds__(kRowThreads) void embed_join_kernel(EmbedBackArgs p, Divisor groups) {
-  const uint64_t i = uint64_t(blockIdx.x) * kRowThreads + threadIdx.x;
-  if (i >= p.cuts) return;
-  const uint32_t piece = groups(uint32_t(i));
-  const int64_t c = int64_t(uint32_t(i) - piece * groups.d) * 8, valid = p.H - c;
-  const int32_t kept = p.ends[p.V - 1];
-  const int32_t a = int32_t(piece) * kList, b = kept - a < kList ? kept : a + kList;
-  if (a >= b) return;
-  const int32_t v = p.token[p.order[b - 1]];
-  const int32_t begin = list_begin(p, v), end = p.ends[v];
-  if (begin < a || end - begin <= kList) return;
-  const int64_t ld = int64_t(groups.d) * 8;
-  // a list that begins with a piece is its first one
-  const float* src = p.part + (int64_t(piece) * 2 + (begin > a ? 1 : 0)) * ld + c;
-  float sum[8];
+template <class In, bool kWhole>
+__device__ __attribute__((always_inline)) inline void sum_piece(const EmbedBackArgs& p, const Sorted& s,
+                                                                const Piece& r, uint32_t piece,
+                                                                uint32_t groups, int64_t c) {
+  for (int which = 0; which < 2; ++which) {
+    const int32_t begin = which == 0 ? r.begin[0] : r.begin[1], end = which == 0 ? r.end[0] : r.end[1];
+    if (begin >= end) continue;
+    float sum[8] = {};
+    add_rows<In, kWhole>(p, s.order, begin, end, c, sum);
+    float* const dst = p.part + (int64_t(piece) * 2 + which) * groups * 8 + c;
 #pragma unroll
-  for (int k = 0; k < 8; ++k) sum[k] = src[k];
+    for (int k = 0; k < 8; ++k) dst[k] = sum[k];
+  }
+}
+
+// The list that begins at sorted position i, if one does and it is not long. The first
+// eight positions are read before it is known how many of them belong to it.
+struct List {
+  int32_t v, n;  // n = 0: none
+  int32_t t[8];  // the first positions
+};
+__device__ __attribute__((always_inline)) inline List list_at(const EmbedBackArgs& p, const Sorted& s, int32_t i) {
+  List r{};
+  int2 o[8];
+#pragma unroll
+  for (int u = 0; u < 8; ++u) o[u] = s.order[i + u < p.T ? i + u : p.T - 1];
+  const int32_t before = i > 0 ? s.order[i - 1].y : -1;
+  r.v = o[0].y;  // p.V: this position is left out
+  if (r.v >= p.V || r.v == before) return r;
+  int32_t n = 0;
+#pragma unroll
+  for (int u = 0; u < 8; ++u) {
+    r.t[u] = o[u].x;
+    n += i + u < p.T && o[u].y == r.v;
+  }
+  if (n == 8) n = s.ends[r.v] - i;
+  r.n = n > kList ? 0 : n;
+  return r;
+}
+
+template <class In, class Out, bool kWhole>
+__device__ __attribute__((always_inline)) inline void sum_list(const EmbedBackArgs& p, const Sorted& s,
+                                                               const List& list, int32_t i, int64_t c) {
+  float sum[8] = {};
+  if (list.n < 8)
+    add_few<In, kWhole>(p, list.t, list.n, c, sum);
+  else
+    add_rows<In, kWhole>(p, s.order, i, i + list.n, c, sum);
+  put_row<Out, kWhole>(p, list.v, c, p.H - c, sum);
+}
+
+// kPer threads a piece of long lists (the first workgroups), or a sorted position, of
+// which those that begin a list have work: it is one for a whole wave, whose lanes then
+// branch together.
+template <class In, class Out, int kPer>
+__global__ __launch_bounds__(kRowThreads) void embed_back_kernel(EmbedBackArgs p,
+                                                                 const int2* __restrict__ order,
+                                                                 const int32_t* __restrict__ ends,
+                                                                 uint32_t groups, uint32_t cut_blocks) {
+  constexpr int kRows = kRowThreads / kPer;
+  const Sorted s{order, ends};
+  const int64_t c0 = int64_t(threadIdx.x % kPer) * 8;
+  const uint32_t in_block = __builtin_amdgcn_readfirstlane(threadIdx.x / kPer);
+  if (blockIdx.x < cut_blocks) {
+    const uint32_t piece = blockIdx.x * kRows + in_block;
+    const Piece r = piece_at(p, s, int32_t(piece));
+    for (int64_t c = c0; c < p.H; c += kPer * 8)
+      by_width(p.H - c, [&](auto w) { sum_piece<In, decltype(w)::value>(p, s, r, piece, groups, c); });
+    return;
+  }
+  const int32_t i = int32_t((blockIdx.x - cut_blocks) * kRows + in_block);
+  if (i >= p.T) return;
+  const List list = list_at(p, s, i);
+  if (list.n == 0) return;
+  for (int64_t c = c0; c < p.H; c += kPer * 8)
+    by_width(p.H - c, [&](auto w) { sum_list<In, Out, decltype(w)::value>(p, s, list, i, c); });
+}
+
+// The same for narrow rows, whose groups of eight follow one another.
+template <class In, class Out>
+__global__ __launch_bounds__(kRowThreads) void embed_back_narrow_kernel(EmbedBackArgs p,
+                                                                        const int2* __restrict__ order,
+                                                                        const int32_t* __restrict__ ends,
+                                                                        Divisor groups, uint32_t cut_blocks,
+                                                                        uint32_t cuts, uint32_t items) {
+  const Sorted s{order, ends};
+  const bool cut = blockIdx.x < cut_blocks;
+  const uint64_t j = uint64_t(blockIdx.x - (cut ? 0 : cut_blocks)) * kRowThreads + threadIdx.x;
+  if (j >= (cut ? cuts : items)) return;
+  const uint32_t i = groups(uint32_t(j));
+  const int64_t c = int64_t(uint32_t(j) - i * groups.d) * 8;
+  if (cut) {
+    const Piece r = piece_at(p, s, int32_t(i));
+    by_width(p.H - c, [&](auto w) { sum_piece<In, decltype(w)::value>(p, s, r, i, groups.d, c); });
+    return;
+  }
+  const List list = list_at(p, s, int32_t(i));
+  if (list.n == 0) return;
+  by_width(p.H - c, [&](auto w) { sum_list<In, Out, decltype(w)::value>(p, s, list, int32_t(i), c); });
+}
+
+// The long list that begins in a piece, if one does: its pieces added by eight waves, each
+// every eighth of them, and the waves' sums in order. Workgroup b takes piece
+// b / chunks and 512 columns.
+constexpr int kJoinWaves = 8;
+
+template <class Out>
+__global__ __launch_bounds__(kJoinWaves * 64) void embed_join_kernel(EmbedBackArgs p,
+                                                                     const int2* __restrict__ order,
+                                                                     const int32_t* __restrict__ ends,
+                                                                     uint32_t groups, uint32_t chunks) {
+  __shared__ float sh[kJoinWaves][8][64];
+  const Sorted s{order, ends};
+  const int32_t piece = int32_t(blockIdx.x / chunks);
+  const int32_t a = piece * kList, kept = s.ends[p.V - 1];
+  const int32_t b = kept - a < kList ? kept : a + kList;
+  if (a >= b) return;
+  const int32_t v = s.order[b - 1].y;
+  const int32_t begin = s.begin_of(v), end = s.ends[v];
+  if (begin < a || end - begin <= kList) return;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t group = (blockIdx.x - uint32_t(piece) * chunks) * 64 + lane;
+  const bool in = group < groups;
+  const int64_t c = int64_t(in ? group : 0) * 8, ld = int64_t(groups) * 8;
   const int32_t last = (end - 1) / kList;
-  constexpr int U = 8;  // pieces in flight
-  for (int32_t q = int32_t(piece) + 1; q <= last; q += U) {
+  // a list that begins inside a piece is its last one, one that begins with it its first
+  auto read = [&](int32_t q, float (&f)[8]) {
+    const float* const src = p.part + (int64_t(q) * 2 + (q == piece && begin > a ? 1 : 0)) * ld + c;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) f[k] = src[k];
+  };
+  float sum[8] = {};
+  constexpr int U = 4;  // pieces in flight
+  for (int32_t q = piece + wave; q <= last; q += U * kJoinWaves) {
     float f[U][8];
 #pragma unroll
+    for (int u = 0; u < U; ++u) read(q + u * kJoinWaves <= last ? q + u * kJoinWaves : last, f[u]);
+#pragma unroll
     for (int u = 0; u < U; ++u) {
-      src = p.part + int64_t(q + u <= last ? q + u : last) * 2 * ld + c;
+      const bool there = q + u * kJoinWaves <= last;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) f[u][k] = src[k];
+      for (int k = 0; k < 8; ++k) sum[k] += there ? f[u][k] : 0.0f;
     }
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (q + u <= last) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) sum[k] += f[u][k];
-      }
   }
-  by_width(valid, [&](auto whole) { put_row<Out, decltype(whole)::value>(p, v, c, valid, sum); });
+#pragma unroll
+  for (int k = 0; k < 8; ++k) sh[wave][k][lane] = sum[k];
+  __syncthreads();
+  if (wave != 0 || !in) return;
+#pragma unroll
+  for (int w = 1; w < kJoinWaves; ++w)
+#pragma unroll
+    for (int k = 0; k < 8; ++k) sum[k] += sh[w][k][lane];
+  by_width(p.H - c, [&](auto whole) { put_row<Out, decltype(whole)::value>(p, v, c, p.H - c, sum); });
+}
+
+unsigned blocks_of(uint64_t n, uint64_t a_block) { return unsigned((n + a_block - 1) / a_block); }
+
+template <class In, class Out>
+void back_rows(const EmbedBackArgs& p, const int2* order, const int32_t* ends, const Divisor& groups,
+               uint32_t pieces, hipStream_t stream) {
+  auto wide = [&](auto per_c) {
+    constexpr int kPer = decltype(per_c)::value, kRows = kRowThreads / kPer;
+    const unsigned cut = blocks_of(pieces, kRows);
+    embed_back_kernel<In, Out, kPer>
+        <<<cut + blocks_of(p.T, kRows), kRowThreads, 0, stream>>>(p, order, ends, groups.d, cut);
+  };
+  if (p.H > 1024) return wide(std::integral_constant<int, 256>{});
+  if (p.H > 512) return wide(std::integral_constant<int, 128>{});
+  if (p.H > 256) return wide(std::integral_constant<int, 64>{});
+  const uint32_t cuts = pieces * groups.d, items = uint32_t(p.T) * groups.d;
+  const unsigned cut = item_blocks(cuts);
+  embed_back_narrow_kernel<In, Out>
+      <<<cut + item_blocks(items), kRowThreads, 0, stream>>>(p, order, ends, groups, cut, cuts, items);
 }
 
 }  // namespace
@@ -206,22 +401,33 @@ int64_t embed_pieces(int64_t T) { return T > kList ? (T + kList - 1) / kList : 0
 hipError_t launch_embed_backward(const EmbedCall& c, bool dx_bf16, bool de_bf16, hipStream_t stream) {
   const Divisor groups(row_groups(c.H));
   const SortPlan s = sort_plan(c.V);
-  embed_sort_kernel<<<s.blocks, kSortWaves * 64, 0, stream>>>(
-      SortArgs{c.token, int32_t(c.T), int32_t(c.V), s.per, c.ends, c.order, nullptr});
+  const SortArgs q{c.token, int32_t(c.T), int32_t(c.V), s.per, c.ends, static_cast<int2*>(c.order), nullptr};
+  const FillArgs f{c.dE, c.ldde, c.H, c.add ? 0 : uint32_t(c.V) * groups.d};
   const uint32_t pieces = uint32_t(embed_pieces(c.T));
-  const EmbedBackArgs p{c.dX,          c.lddx,  c.token, c.order, c.ends, int32_t(c.T),
-                        int32_t(c.V),  c.H,     c.scale, c.add,   c.dE,   c.ldde,
-                        c.part,        uint32_t(c.V) * groups.d,  pieces * groups.d};
-  const unsigned cut_blocks = item_blocks(p.cuts), row_blocks = item_blocks(p.rows);
+  const EmbedBackArgs p{c.dX,    c.lddx, int32_t(c.T), int32_t(c.V), c.H,
+                        c.scale, c.add,  c.dE,         c.ldde,       c.part};
   return with_type(de_bf16, [&](auto out) {
     using Out = decltype(out);
-    const hipError_t e = with_type(dx_bf16, [&](auto in) {
-      embed_back_kernel<decltype(in), Out>
-          <<<cut_blocks + row_blocks, kRowThreads, 0, stream>>>(p, groups, cut_blocks);
-      return hipGetLastError();
-    });
-    if (e != hipSuccess || pieces == 0) return e;
-    embed_join_kernel<Out><<<cut_blocks, kRowThreads, 0, stream>>>(p, groups);
+    // up to four rounds of the workgroups that fit the GPU at once (two a CU)
+    const unsigned fill = blocks_of(f.items, kSortWaves * 64);
+    const unsigned fillers = fill < 2048 ? fill : 2048;
+    if (c.T <= kSortOnce)
+      embed_sort_kernel<Out, true>
+          <<<s.blocks + fillers, kSortWaves * 64, 0, stream>>>(q, f, groups, s.blocks);
+    else
+      embed_sort_kernel<Out, false>
+          <<<s.blocks + fillers, kSortWaves * 64, 0, stream>>>(q, f, groups, s.blocks);
+    if (c.T > 0) {
+      if (dx_bf16)
+        back_rows<BF16In, Out>(p, q.order, q.ends, groups, pieces, stream);
+      else
+        back_rows<F32In, Out>(p, q.order, q.ends, groups, pieces, stream);
+    }
+    if (pieces > 0) {
+      const uint32_t chunks = (groups.d + 63) / 64;
+      embed_join_kernel<Out>
+          <<<pieces * chunks, kJoinWaves * 64, 0, stream>>>(p, q.order, q.ends, groups.d, chunks);
+    }
     return hipGetLastError();
   });
 }

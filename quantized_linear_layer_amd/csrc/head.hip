@@ -150,10 +150,16 @@ __global__ __launch_bounds__(C::kThreads, C::kMinBlocks) void head_lse_kernel(He
   int tm, tn;
   tile_of(xcd_run(blockIdx.x, tiles_m * tiles_n), tiles_m, tiles_n, tm, tn);
   const int m0 = tm * C::BM, n0 = tn * C::BN;
+  const int row0 = m0 + wm * FM * 32, col0 = n0 + wn * FN * 32;
+  using Entries = std::conditional_t<kDistill, TeacherTile<C>, NoTeacher>;
+  // tiles of few rows have registers left: what the tile's end needs is read now
+  constexpr bool kEarly = C::BM == 64;
+  Entries entries;
+  if constexpr (kEarly) entries.read(p.teacher, row0, col0, p.T_, lane);
   DenseFeed<C, T, kAlong, kBT> f(p.X, p.W, m0, n0, wave, lane);
   product_tile<C>(f, (p.H + kStepElems<T> - 1) / kStepElems<T>, st0, st1, st2, st3, st4);
 
-  const int row0 = m0 + wm * FM * 32, col0 = n0 + wn * FN * 32;
+  if constexpr (!kEarly) entries.read(p.teacher, row0, col0, p.T_, lane);
   if constexpr (kDistill) {
     const float inv = p.teacher.inv_temperature;
 #pragma unroll
@@ -164,7 +170,6 @@ __global__ __launch_bounds__(C::kThreads, C::kMinBlocks) void head_lse_kernel(He
         for (int r = 0; r < 16; ++r) f.acc[fm][fn][r] *= inv;
     using Blocks = TileBlocks<C>;
     Blocks blocks(st0, st1, st2, wave, lane, m0, n0);
-    TeacherTile<C> entries(p.teacher, row0, col0, p.T_, lane);
     float dot[FM];
 #pragma unroll
     for (int fm = 0; fm < FM; ++fm) {
@@ -235,11 +240,9 @@ __global__ __launch_bounds__(C::kThreads, C::kMinBlocks) void head_lse_kernel(He
 // 1000 pairs: 7.6 us; one thread a row: 75) wait for few loads in a row.
 constexpr int kJoinRows = 4;
 
-template <bool kDistill>
 __global__ __launch_bounds__(kJoinRows * 64) void head_join_kernel(
     const float2* __restrict__ part, int P, int T, int V, const int32_t* __restrict__ target,
-    const float* __restrict__ tlogit, const float* __restrict__ tdot,
-    const float2* __restrict__ teacher_sums, float* __restrict__ loss, float* __restrict__ lse) {
+    const float* __restrict__ tlogit, float* __restrict__ loss, float* __restrict__ lse) {
   const int lane = threadIdx.x & 63;
   const int row = blockIdx.x * kJoinRows + (threadIdx.x >> 6);
   if (row >= T) return;
@@ -257,24 +260,87 @@ __global__ __launch_bounds__(kJoinRows * 64) void head_join_kernel(
     const float m2 = __shfl_xor(m, off, kWave), s2 = __shfl_xor(s, off, kWave);
     join(m2, s2);
   }
-  float dot = 0.0f;
-  if constexpr (kDistill) {
-    for (int j = lane; j < P; j += 64) dot += tdot[int64_t(row) * P + j];
-#pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) dot += __shfl_xor(dot, off, kWave);
-  }
   if (lane != 0) return;
   const float l = m + logf(s);
   lse[row] = l;
   const int t = target[row];
-  if constexpr (kDistill) {
-    // (sum p log p, sum p) of the rounded p: what their sum is off 1 by then meets
-    // log p - z + lse, not lse
-    const float2 sums = teacher_sums[row];
-    loss[row] = t >= 0 ? fmaf(l, sums.y, sums.x - dot) : 0.0f;
-  } else {
-    loss[row] = t >= 0 && t < V ? l - tlogit[row] : 0.0f;
+  loss[row] = t >= 0 && t < V ? l - tlogit[row] : 0.0f;
+}
+
+// The same for distillation, with each group's sum of p z; kWaves waves a row.
+template <int kWaves>
+__global__ __launch_bounds__(256) void distill_join_kernel(
+    const float2* __restrict__ part, const float* __restrict__ tdot, int P, int T,
+    const int32_t* __restrict__ kept, const float2* __restrict__ teacher_sums,
+    float* __restrict__ loss, float* __restrict__ lse) {
+  constexpr int kRows = 4 / kWaves, U = 4;
+  __shared__ float sh[3][4];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t row = int64_t(blockIdx.x) * kRows + wave / kWaves;
+  const bool in = row < T;
+  const float2* const mine = part + (in ? row : 0) * P;
+  const float* const dots = tdot + (in ? row : 0) * P;
+  constexpr float kNone = -__builtin_huge_valf();
+  // (a row of -infinity alone keeps 0 as what its exponentials are taken over)
+  auto over = [](float m) { return m == kNone ? 0.0f : m; };
+  float m = kNone, s = 0.0f, dot = 0.0f;
+  for (int j0 = (wave % kWaves) * 64 + lane; j0 < P; j0 += kWaves * 64 * U) {
+    float2 v[U];
+    float d[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int j = j0 + u * kWaves * 64;
+      v[u] = mine[j < P ? j : P - 1];
+      d[u] = dots[j < P ? j : P - 1];
+    }
+    float top = m;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (j0 + u * kWaves * 64 >= P) {
+        v[u] = make_float2(kNone, 0.0f);
+        d[u] = 0.0f;
+      }
+      top = fmaxf(top, v[u].x);
+      dot += d[u];
+    }
+    s *= exp_diff(m, over(top));
+#pragma unroll
+    for (int u = 0; u < U; ++u) s = fmaf(v[u].y, exp_diff(v[u].x, over(top)), s);
+    m = top;
   }
+  auto join = [&](float all) {  // s over the largest
+    s *= exp_diff(m, over(all));
+    m = all;
+  };
+  join(wave_max(m));
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) {
+    s += __shfl_xor(s, off, kWave);
+    dot += __shfl_xor(dot, off, kWave);
+  }
+  if constexpr (kWaves > 1) {
+    if (lane == 0) {
+      sh[0][wave] = m;
+      sh[1][wave] = s;
+      sh[2][wave] = dot;
+    }
+    __syncthreads();
+    const float all = fmaxf(fmaxf(sh[0][0], sh[0][1]), fmaxf(sh[0][2], sh[0][3]));
+    s = dot = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      s = fmaf(sh[1][w], exp_diff(sh[0][w], over(all)), s);
+      dot += sh[2][w];
+    }
+    m = all;
+  }
+  if (!in || lane != 0 || wave % kWaves != 0) return;
+  const float l = m + logf(s);
+  lse[row] = l;
+  // (sum p log p, sum p) of the rounded p: what their sum is off 1 by then meets
+  // log p - z + lse, not lse
+  const float2 sums = teacher_sums[row];
+  loss[row] = kept[row] >= 0 ? fmaf(l, sums.y, sums.x - dot) : 0.0f;
 }
 
 // bfloat16 G is kept in pieces of 32 columns, the rows of a piece together: the
@@ -366,7 +432,8 @@ __global__ __launch_bounds__(C::kThreads, C::kMinBlocks) void head_grad_kernel(H
     // entries one by one, so that one index listed twice is taken off twice
     using Blocks = TileBlocks<C>;
     Blocks blocks(st0, st1, st2, wave, lane, m0, n0);
-    TeacherTile<C> entries(p.teacher, row0, p.v0 + col0, p.T_, lane);
+    TeacherTile<C> entries;
+    entries.read(p.teacher, row0, p.v0 + col0, p.T_, lane);
 #pragma unroll
     for (int fm = 0; fm < FM; ++fm) {
       const int row = row0 + fm * 32 + (lane & 31);
@@ -859,22 +926,26 @@ hipError_t run_forward(const HeadCall& c, const HeadPlan& h, hipStream_t stream)
   a.parts = int(h.parts);
   a.tlogit = c.tlogit;
   const Tile t = pick_tile(sizeof(T) == 2, c.T, c.V);
-  const unsigned joins = unsigned(ceil_div(c.T, kJoinRows));
   if (c.distill()) {
     a.teacher = teacher_list(c);
     a.tdot = c.tdot;
     e = logits<T, false, true>(t, c.by_vocab, a, stream);
     if (e != hipSuccess) return e;
-    head_join_kernel<true><<<joins, kJoinRows * 64, 0, stream>>>(
-        a.part, int(h.parts), int(c.T), int(c.V), c.target, nullptr, c.tdot,
-        static_cast<const float2*>(c.teacher_sums), c.loss, c.lse_out);
-    return hipGetLastError();
+    const auto join = [&](auto waves) {
+      constexpr int kWaves = decltype(waves)::value;
+      distill_join_kernel<kWaves><<<unsigned(ceil_div(c.T, 4 / kWaves)), 256, 0, stream>>>(
+          a.part, c.tdot, int(h.parts), int(c.T), c.target, static_cast<const float2*>(c.teacher_sums),
+          c.loss, c.lse_out);
+      return hipGetLastError();
+    };
+    // four waves a row where one would read more than four pairs a lane
+    if (h.parts > 256) return join(std::integral_constant<int, 4>{});
+    return join(std::integral_constant<int, 1>{});
   }
   e = logits<T, false, false>(t, c.by_vocab, a, stream);
   if (e != hipSuccess) return e;
-  head_join_kernel<false><<<joins, kJoinRows * 64, 0, stream>>>(
-      a.part, int(h.parts), int(c.T), int(c.V), c.target, c.tlogit, nullptr, nullptr, c.loss,
-      c.lse_out);
+  head_join_kernel<<<unsigned(ceil_div(c.T, kJoinRows)), kJoinRows * 64, 0, stream>>>(
+      a.part, int(h.parts), int(c.T), int(c.V), c.target, c.tlogit, c.loss, c.lse_out);
   return hipGetLastError();
 }
 

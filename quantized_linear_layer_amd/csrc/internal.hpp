@@ -216,7 +216,8 @@ struct EmbedCall {
   bool add;
   void* dE;
   int64_t ldde;
-  int32_t *order, *ends;
+  void* order;  // T pairs of int32
+  int32_t* ends;
   float* part;
 };
 hipError_t launch_embed(const EmbedCall& c, bool table_bf16, bool out_bf16, hipStream_t stream);

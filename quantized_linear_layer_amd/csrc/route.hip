@@ -20,10 +20,83 @@ namespace fp4lin {
 
 namespace {
 
-__global__ __launch_bounds__(kSortWaves * 64) void route_sort_kernel(SortArgs p) { sort_body(p); }
+template <bool kOnce>
+__global__ __launch_bounds__(kSortWaves * 64) void route_sort_kernel(SortArgs p) {
+  sort_body<kOnce>(p);
+}
+
+// The same sort where each workgroup has one key (up to 255 experts), on more
+// workgroups than there are keys: workgroup (e, q) places the slots of expert e in part
+// q of the slots. Where these begin is the number of slots with a smaller expert
+// anywhere and with this one in the parts before, so one comparison a slot, 256 slots a
+// wave and step; only its own part is looked at slot by slot.
+constexpr int kOneKey = 255;
+
+__global__ __launch_bounds__(kSortWaves * 64) void route_place_kernel(SortArgs p, int parts,
+                                                                      int32_t part_len) {
+  __shared__ int32_t less[kSortWaves], here[kSortWaves], upto[kSortWaves];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int e = blockIdx.x / parts, q = blockIdx.x - e * parts;
+  const uint32_t E = uint32_t(p.keys);
+  const int64_t begin = int64_t(q) * part_len, n = p.n;
+  const int64_t past = begin + part_len < n ? begin + part_len : n;
+  // an expert out of range, negative ones too, is expert E
+  auto key_of = [&](uint32_t raw) { return raw < E ? raw : E; };
+
+  int32_t before = 0, all = 0;
+  for (int64_t i0 = int64_t(wave) * 256; i0 < n; i0 += kSortWaves * 256) {
+    const int64_t i = i0 + lane * 4;
+    uint32_t k[4];
+    if (i + 4 <= n) {
+      const Bytes16 b = *reinterpret_cast<const Bytes16*>(p.key + i);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) k[j] = key_of(b.w[j]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) k[j] = i + j < n ? key_of(uint32_t(p.key[i + j])) : E + 1;
+    }
+    const uint32_t limit = uint32_t(e) + (i0 < begin ? 1 : 0);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) before += __builtin_popcountll(__ballot(k[j] < limit));
+    if (q == 0) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) all += __builtin_popcountll(__ballot(k[j] <= uint32_t(e)));
+    }
+  }
+  // this wave's slots of the part: [first, end)
+  const int64_t seg = part_len / kSortWaves, first = begin + wave * seg;
+  const int64_t end = first + seg < past ? first + seg : past;
+  auto mine = [&](int64_t i0) {
+    const int64_t i = i0 + lane;
+    return __ballot(i < end && key_of(uint32_t(p.key[i < end ? i : end - 1])) == uint32_t(e));
+  };
+  int32_t own = 0;
+  for (int64_t i0 = first; i0 < end; i0 += 64) own += __builtin_popcountll(mine(i0));
+  if (lane == 0) {
+    less[wave] = before;
+    here[wave] = own;
+    upto[wave] = all;
+  }
+  __syncthreads();
+  int32_t at = 0, total = 0;
+#pragma unroll
+  for (int w = 0; w < kSortWaves; ++w) {
+    at += less[w] + (w < wave ? here[w] : 0);
+    total += upto[w];
+  }
+  if (q == 0 && threadIdx.x == 0 && uint32_t(e) < E) p.ends[e] = total;
+  for (int64_t i0 = first; i0 < end; i0 += 64) {
+    const uint64_t m = mine(i0);
+    if ((m >> lane) & 1)
+      p.place[i0 + lane] = at + int32_t(__builtin_amdgcn_mbcnt_hi(
+                                    uint32_t(m >> 32), __builtin_amdgcn_mbcnt_lo(uint32_t(m), 0)));
+    at += __builtin_popcountll(m);
+  }
+}
 
 // Rows that an expert has made: those below row_end's last entry, clamped.
-__device__ inline int32_t rows_made(const int32_t* row_end, int32_t E, int32_t M) {
+__device__ __attribute__((always_inline)) inline int32_t rows_made(const int32_t* row_end, int32_t E, int32_t M) {
   const int32_t n = row_end[E - 1];
   return n < 0 ? 0 : n < M ? n : M;
 }
@@ -123,8 +196,6 @@ struct CombineArgs {
   uint32_t items;
 };
 
-constexpr int kSlots = 4;  // of a token, their rows read together
-
 template <class In, class Out>
 __global__ __launch_bounds__(kRowThreads) void combine_kernel(CombineArgs p, Divisor groups) {
   const Item it = item_of(p.items, groups);
@@ -139,27 +210,28 @@ __global__ __launch_bounds__(kRowThreads) void combine_kernel(CombineArgs p, Div
     const int32_t made = rows_made(p.row_end, p.E, p.M);
     float sum[8] = {};
     const int64_t slot0 = int64_t(it.row) * p.k;
-    for (int32_t j0 = 0; j0 < p.k; j0 += kSlots) {
-      Vec8<In> v[kSlots];
-      float w[kSlots];
-      bool has[kSlots];
+    in_groups(p.k, [&](int32_t j, auto size) {
+      constexpr int N = decltype(size)::value;
+      Vec8<In> v[N];
+      float w[N];
+      bool has[N];
 #pragma unroll
-      for (int u = 0; u < kSlots; ++u) {
-        const int32_t j = j0 + u < p.k ? j0 + u : p.k - 1;
-        const int32_t r = p.slot_row[slot0 + j];
-        has[u] = j0 + u < p.k && r >= 0 && r < made;
-        w[u] = p.weight != nullptr ? p.weight[slot0 + j] : 1.0f;
-        if (has[u])
-          get8<In, kWhole>(static_cast<const typename In::T*>(p.Y) + int64_t(r) * p.ldy + it.c, valid,
-                           v[u]);
+      for (int u = 0; u < N; ++u) {
+        const int32_t r = p.slot_row[slot0 + j + u];
+        has[u] = r >= 0 && r < made;
+        // (row 0 in the place of one that is not there: read, not used)
+        get8<In, kWhole>(static_cast<const typename In::T*>(p.Y) + int64_t(has[u] ? r : 0) * p.ldy + it.c,
+                         valid, v[u]);
       }
 #pragma unroll
-      for (int u = 0; u < kSlots; ++u)
-        if (has[u]) {
+      for (int u = 0; u < N; ++u) w[u] = p.weight != nullptr ? p.weight[slot0 + j + u] : 1.0f;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) sum[i] = fmaf(w[u], In::widen(v[u].v[i]), sum[i]);
-        }
-    }
+      for (int u = 0; u < N; ++u) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          sum[i] = has[u] ? fmaf(w[u], In::widen(v[u].v[i]), sum[i]) : sum[i];
+      }
+    });
 #pragma unroll
     for (int i = 0; i < 8; ++i) sum[i] += Out::widen(res.v[i]);
     put8<Out, kWhole>(static_cast<typename Out::T*>(p.out) + int64_t(it.row) * p.ldo + it.c, valid,
@@ -181,27 +253,30 @@ struct CombineBackArgs {
   int64_t H;
 };
 
-// kPer threads a token. A row of dout is read once for kSlots slots.
-template <class In, class D, class Out, int kPer>
+// kPer threads a token; a row of dout is read once for each group of its slots. kDots:
+// the weights' gradients are wanted.
+template <class In, class D, class Out, int kPer, bool kDots>
 __global__ __launch_bounds__(kRowThreads) void combine_back_kernel(CombineBackArgs p) {
   constexpr int kTokens = kRowThreads / kPer, kParts = kPer > 64 ? kPer / 64 : 1;
-  __shared__ float part[kParts][kSlots];
+  __shared__ float part[2][kParts][4];
   const int t = threadIdx.x % kPer;
   const int64_t token = int64_t(blockIdx.x) * kTokens + threadIdx.x / kPer;
   const bool in = token < p.T;
   const int32_t made = rows_made(p.row_end, p.E, p.M);
   const typename D::T* const d = static_cast<const typename D::T*>(p.dout) + (in ? token : 0) * p.lddo;
   const int64_t slot0 = (in ? token : 0) * p.k;
-  const bool dots = p.dweight != nullptr;
-  for (int32_t j0 = 0; j0 < p.k; j0 += kSlots) {
-    int32_t r[kSlots];
-    float w[kSlots], dot[kSlots] = {};
+  int turn = 0;
+  in_groups(p.k, [&](int32_t j, auto size) {
+    constexpr int N = decltype(size)::value;
+    int32_t r[N];
+    float w[N], dot[N] = {};
+    bool has[N];  // an expert has made the row
 #pragma unroll
-    for (int u = 0; u < kSlots; ++u) {
-      const int32_t j = j0 + u < p.k ? j0 + u : p.k - 1;
-      r[u] = p.slot_row[slot0 + j];
-      if (!in || j0 + u >= p.k || r[u] >= p.M) r[u] = -1;
-      w[u] = p.weight != nullptr ? p.weight[slot0 + j] : 1.0f;
+    for (int u = 0; u < N; ++u) {
+      r[u] = p.slot_row[slot0 + j + u];
+      if (!in || r[u] >= p.M) r[u] = -1;
+      has[u] = r[u] >= 0 && r[u] < made;
+      w[u] = has[u] ? (p.weight != nullptr ? p.weight[slot0 + j + u] : 1.0f) : 0.0f;
     }
     for (int64_t c = int64_t(t) * 8; c < p.H; c += int64_t(kPer) * 8) {
       const int64_t valid = p.H - c;
@@ -209,56 +284,58 @@ __global__ __launch_bounds__(kRowThreads) void combine_back_kernel(CombineBackAr
         constexpr bool kWhole = decltype(whole)::value;
         Vec8<D> g;
         get8<D, kWhole>(d + c, valid, g);
-        Vec8<In> y[kSlots];
+        Vec8<In> y[N];
+        if constexpr (kDots) {
+          // (row 0 in the place of one that is not there: read, not used)
 #pragma unroll
-        for (int u = 0; u < kSlots; ++u)
-          if (dots && r[u] >= 0 && r[u] < made)
-            get8<In, kWhole>(static_cast<const typename In::T*>(p.Y) + int64_t(r[u]) * p.ldy + c, valid,
-                             y[u]);
+          for (int u = 0; u < N; ++u)
+            get8<In, kWhole>(static_cast<const typename In::T*>(p.Y) + int64_t(has[u] ? r[u] : 0) * p.ldy + c,
+                             valid, y[u]);
+        }
 #pragma unroll
-        for (int u = 0; u < kSlots; ++u) {
-          if (r[u] < 0) continue;
-          float o[8] = {};
-          if (r[u] < made) {
+        for (int u = 0; u < N; ++u) {
+          float o[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float gi = D::widen(g.v[i]);
-              o[i] = w[u] * gi;
-              if (dots) dot[u] = fmaf(gi, In::widen(y[u].v[i]), dot[u]);
-            }
+          for (int i = 0; i < 8; ++i) {
+            const float gi = D::widen(g.v[i]);
+            o[i] = has[u] ? w[u] * gi : 0.0f;
+            if constexpr (kDots) dot[u] = has[u] ? fmaf(gi, In::widen(y[u].v[i]), dot[u]) : 0.0f;
           }
-          put8<Out, kWhole>(static_cast<typename Out::T*>(p.dY) + int64_t(r[u]) * p.lddy + c, valid,
-                            rounded<Out>(o));
+          if (r[u] >= 0)
+            put8<Out, kWhole>(static_cast<typename Out::T*>(p.dY) + int64_t(r[u]) * p.lddy + c, valid,
+                              rounded<Out>(o));
         }
       });
     }
-    if (!dots) continue;
+    if constexpr (kDots) {
 #pragma unroll
-    for (int u = 0; u < kSlots; ++u) {
+      for (int u = 0; u < N; ++u) {
 #pragma unroll
-      for (int off = (kPer < 64 ? kPer : 64) / 2; off >= 1; off >>= 1)
-        dot[u] += __shfl_xor(dot[u], off, kWave);
-    }
-    if constexpr (kParts > 1) {
-      __syncthreads();
-      if ((threadIdx.x & 63) == 0) {
-#pragma unroll
-        for (int u = 0; u < kSlots; ++u) part[threadIdx.x >> 6][u] = dot[u];
+        for (int off = (kPer < 64 ? kPer : 64) / 2; off >= 1; off >>= 1)
+          dot[u] += __shfl_xor(dot[u], off, kWave);
       }
-      __syncthreads();
+      if constexpr (kParts > 1) {
+        // (in two places in turns, so that one barrier a group is enough)
+        float(&mine)[kParts][4] = part[turn];
+        turn ^= 1;
+        if ((threadIdx.x & 63) == 0) {
 #pragma unroll
-      for (int u = 0; u < kSlots; ++u) {
-        dot[u] = part[0][u];
+          for (int u = 0; u < N; ++u) mine[threadIdx.x >> 6][u] = dot[u];
+        }
+        __syncthreads();
 #pragma unroll
-        for (int q = 1; q < kParts; ++q) dot[u] += part[q][u];
+        for (int u = 0; u < N; ++u) {
+          dot[u] = mine[0][u];
+#pragma unroll
+          for (int q = 1; q < kParts; ++q) dot[u] += mine[q][u];
+        }
+      }
+      if (t == 0 && in) {
+#pragma unroll
+        for (int u = 0; u < N; ++u) p.dweight[slot0 + j + u] = dot[u];
       }
     }
-    if (t == 0 && in) {
-#pragma unroll
-      for (int u = 0; u < kSlots; ++u)
-        if (j0 + u < p.k) p.dweight[slot0 + j0 + u] = dot[u];
-    }
-  }
+  });
 }
 
 template <class In>
@@ -272,8 +349,18 @@ hipError_t run_dispatch(const RouteCall& c, hipStream_t stream) {
     return hipGetLastError();
   }
   const SortPlan s = sort_plan(c.E);
-  route_sort_kernel<<<s.blocks, kSortWaves * 64, 0, stream>>>(
-      SortArgs{c.expert, int32_t(M), int32_t(c.E), s.per, c.row_end_out, nullptr, c.slot_row_out});
+  const SortArgs q{c.expert, int32_t(M), int32_t(c.E), s.per, c.row_end_out, nullptr, c.slot_row_out};
+  if (c.E <= kOneKey) {
+    // parts of whole 64 slots a wave, about two workgroups a CU in all
+    const int64_t step = kSortWaves * 64, most = M > 0 ? (M + step - 1) / step : 1;
+    const int64_t want = 512 / (c.E + 1) > 1 ? 512 / (c.E + 1) : 1;
+    const int64_t len = (most + (want < most ? want : most) - 1) / (want < most ? want : most) * step;
+    const int parts = int(M > 0 ? (M + len - 1) / len : 1);
+    route_place_kernel<<<unsigned((c.E + 1) * parts), kSortWaves * 64, 0, stream>>>(q, parts, int32_t(len));
+  } else if (M <= kSortOnce)
+    route_sort_kernel<true><<<s.blocks, kSortWaves * 64, 0, stream>>>(q);
+  else
+    route_sort_kernel<false><<<s.blocks, kSortWaves * 64, 0, stream>>>(q);
   if (M > 0) {
     const Divisor groups(row_groups(c.H));
     p.items = uint32_t(c.T) * groups.d;
@@ -307,20 +394,22 @@ hipError_t launch_experts_combine_backward(const RouteCall& c, bool y_bf16, bool
   const CombineBackArgs p{c.dout,  c.lddo,    c.Y,          c.ldy,        c.slot_row,   c.row_end,
                           c.weight, c.dY,     c.lddy,       c.dweight,    int32_t(c.T), int32_t(c.k),
                           int32_t(c.E), int32_t(c.T * c.k), c.H};
-  return with_type(y_bf16, [&](auto in) {
-    return with_type(dout_bf16, [&](auto d) {
-      return with_type(dy_bf16, [&](auto out) {
-        auto go = [&](auto per_c) {
-          constexpr int kPer = decltype(per_c)::value;
-          const unsigned blocks = unsigned((c.T + kRowThreads / kPer - 1) / (kRowThreads / kPer));
-          combine_back_kernel<decltype(in), decltype(d), decltype(out), kPer>
-              <<<blocks, kRowThreads, 0, stream>>>(p);
-          return hipGetLastError();
-        };
-        if (c.H <= 128) return go(std::integral_constant<int, 16>{});
-        if (c.H <= 512) return go(std::integral_constant<int, 64>{});
-        return go(std::integral_constant<int, 256>{});
-      });
+  return with_type(dout_bf16, [&](auto d) {
+    return with_type(dy_bf16, [&](auto out) {
+      auto go = [&](auto in, auto dots, auto per_c) {
+        constexpr int kPer = decltype(per_c)::value;
+        const unsigned blocks = unsigned((c.T + kRowThreads / kPer - 1) / (kRowThreads / kPer));
+        combine_back_kernel<decltype(in), decltype(d), decltype(out), kPer, decltype(dots)::value>
+            <<<blocks, kRowThreads, 0, stream>>>(p);
+        return hipGetLastError();
+      };
+      auto by_columns = [&](auto in, auto dots) {
+        if (c.H <= 128) return go(in, dots, std::integral_constant<int, 16>{});
+        if (c.H <= 512) return go(in, dots, std::integral_constant<int, 64>{});
+        return go(in, dots, std::integral_constant<int, 256>{});
+      };
+      if (c.dweight == nullptr) return by_columns(F32In{}, std::false_type{});
+      return with_type(y_bf16, [&](auto in) { return by_columns(in, std::true_type{}); });
     });
   });
 }

@@ -22,7 +22,7 @@ struct __attribute__((packed, aligned(2))) Bytes16 {
 // kWhole: all eight are there. Otherwise the first `valid` of them (zeros are read
 // past them).
 template <class In, bool kWhole>
-__device__ inline void get8(const typename In::T* __restrict__ p, int64_t valid, Vec8<In>& v) {
+__device__ __attribute__((always_inline)) inline void get8(const typename In::T* __restrict__ p, int64_t valid, Vec8<In>& v) {
   if constexpr (kWhole) {
     constexpr int kPieces = In::kBytes / 2;
     Bytes16 b[kPieces];
@@ -36,7 +36,7 @@ __device__ inline void get8(const typename In::T* __restrict__ p, int64_t valid,
 }
 
 template <class In, bool kWhole>
-__device__ inline void put8(typename In::T* __restrict__ p, int64_t valid, const Vec8<In>& v) {
+__device__ __attribute__((always_inline)) inline void put8(typename In::T* __restrict__ p, int64_t valid, const Vec8<In>& v) {
   if constexpr (kWhole) {
     constexpr int kPieces = In::kBytes / 2;
     Bytes16 b[kPieces];
@@ -53,16 +53,27 @@ __device__ inline void put8(typename In::T* __restrict__ p, int64_t valid, const
 // f(whole) once for a group of `valid` columns: one branch for everything that is
 // read and written there, so that no load waits behind another's branch.
 template <class F>
-__device__ inline void by_width(int64_t valid, const F& f) {
+__device__ __attribute__((always_inline)) inline void by_width(int64_t valid, const F& f) {
   if (valid >= 8)
     f(std::true_type{});
   else
     f(std::false_type{});
 }
 
+// n in groups of 4, 2 and 1, group(offset, size) in order. Each group's loads can then
+// be issued together without a condition on any of them: a load behind a branch is waited
+// for before the next one.
+template <class F>
+__device__ __attribute__((always_inline)) inline void in_groups(int32_t n, const F& group) {
+  int32_t i = 0;
+  for (; i + 4 <= n; i += 4) group(i, std::integral_constant<int, 4>{});
+  if (n & 2) group(i, std::integral_constant<int, 2>{});
+  if (n & 1) group(n - 1, std::integral_constant<int, 1>{});
+}
+
 // fp32 values to the stored type: float as they are, bfloat16 rounded to nearest even.
 template <class In>
-__device__ inline Vec8<In> rounded(const float (&f)[8]) {
+__device__ __attribute__((always_inline)) inline Vec8<In> rounded(const float (&f)[8]) {
   Vec8<In> v;
   if constexpr (In::kBytes == 2) {
     const uint32_t u[4] = {bf16_pair(f[0], f[1]), bf16_pair(f[2], f[3]), bf16_pair(f[4], f[5]),
@@ -87,7 +98,7 @@ struct Divisor {
     s1 = l < 1 ? l : 1;
     s2 = l > 1 ? l - 1 : 0;
   }
-  __device__ inline uint32_t operator()(uint32_t n) const {
+  __device__ __attribute__((always_inline)) inline uint32_t operator()(uint32_t n) const {
     const uint32_t t = __umulhi(m, n);
     return (t + ((n - t) >> s1)) >> s2;
   }
@@ -100,7 +111,7 @@ struct Item {
   int64_t c;
   bool in;
 };
-__device__ inline Item item_of(uint32_t items, const Divisor& groups) {
+__device__ __attribute__((always_inline)) inline Item item_of(uint32_t items, const Divisor& groups) {
   const uint64_t i = uint64_t(blockIdx.x) * blockDim.x + threadIdx.x;
   const uint32_t row = groups(uint32_t(i));
   return Item{row, int64_t(uint32_t(i) - row * groups.d) * 8, i < items};
@@ -124,22 +135,27 @@ __host__ inline unsigned item_blocks(uint64_t items) {
 // and reads all elements, counting those below its keys and its own ones, so that
 // it knows where its keys begin without hearing from the others. Its 16 waves take
 // consecutive parts of the elements; counts by key and wave, scanned in that
-// order, are where each wave places its elements in a second reading. Lanes of a
-// wave with one key find each other by ballots over the key's bits, so the time
-// does not depend on how the keys are distributed. No atomics that return: the
-// order is that of the elements.
+// order, are where each wave's elements of a key begin. Lanes of a wave with one key
+// find each other by ballots over the key's bits, so the time does not depend on how
+// the keys are distributed. No atomics that return: the order is that of the
+// elements.
 //   ends[k]   number of elements with a key <= k, for k < keys
-//   order     elements by key (not needed: NULL)
+//   order     (element, key) by key (not needed: NULL)
 //   place     where each element came to be (not needed: NULL)
 // ---------------------------------------------------------------------------
 struct SortArgs {
   const int32_t* key;
   int32_t n, keys, per;
-  int32_t *ends, *order, *place;
+  int32_t* ends;
+  int2* order;
+  int32_t* place;
 };
 
 constexpr int kSortWaves = 16;
 constexpr int kSortKeys = 512;  // most keys a workgroup
+// Elements a lane reads at a time; up to kSortOnce elements are read once.
+constexpr int kSortRegs = 16;
+constexpr int64_t kSortOnce = int64_t(kSortRegs) * kSortWaves * 64;
 
 struct SortPlan {
   int32_t per;
@@ -154,92 +170,114 @@ __host__ inline SortPlan sort_plan(int64_t keys) {
   return SortPlan{int32_t(per), unsigned((all + per - 1) / per)};
 }
 
-// (in a header that several sources include, each with a kernel of its own)
-__device__ inline void sort_body(const SortArgs& p) {
-  constexpr int U = 8;  // loads in flight a lane
+// (in a header that several sources include, each with kernels of its own) kOnce: n is
+// at most kSortOnce; else the elements are read again to be placed.
+template <bool kOnce>
+__device__ __attribute__((always_inline)) inline void sort_body(const SortArgs& p) {
+  constexpr int U = kOnce ? kSortRegs : 8;
   __shared__ int32_t cnt[kSortWaves][kSortKeys];
-  __shared__ int32_t sums[kSortWaves];
-  __shared__ int32_t below_all;
+  __shared__ int32_t sums[kSortWaves], below_s[kSortWaves];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int32_t lo = blockIdx.x * p.per;
   const int32_t left = p.keys + 1 - lo;
   const int32_t mine = left < p.per ? left : p.per;
-  for (int i = threadIdx.x; i < kSortWaves * mine; i += kSortWaves * 64)
-    cnt[i / mine][i % mine] = 0;
-  if (threadIdx.x == 0) below_all = 0;
-  __syncthreads();
+  const int bits = mine > 1 ? 32 - __builtin_clz(mine - 1) : 0;
 
-  const int64_t seg = (int64_t(p.n) + kSortWaves * 64 - 1) / (kSortWaves * 64) * 64;
-  const int64_t first = wave * seg, past = first + seg < p.n ? first + seg : p.n;
-  // key of element i relative to lo; one that is not there counts as above
-  auto load = [&](int64_t i0, int32_t (&k)[U]) {
+  // (positions stay below 2^30 + 2^16)
+  const int32_t seg = (p.n + kSortWaves * 64 - 1) / (kSortWaves * 64) * 64;
+  const int32_t first = wave * seg, past = first + seg < p.n ? first + seg : p.n;
+  // keys from element i0 on, relative to lo; one that is not there counts as above
+  int32_t key[U];
+  auto load = [&](int32_t i0) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int64_t i = i0 + u * 64 + lane;
-      const int32_t raw = i < past ? p.key[i] : 0;
-      k[u] = i >= past ? p.keys + 1 : (raw >= 0 && raw < p.keys) ? raw : p.keys;
+      const int32_t i = i0 + u * 64 + lane;
+      const uint32_t raw = uint32_t(p.key[i < p.n ? i : p.n - 1]), keys = uint32_t(p.keys);
+      key[u] = (i >= past ? p.keys + 1 : int32_t(raw < keys ? raw : keys)) - lo;
     }
   };
-  int32_t below = 0;
-  for (int64_t i0 = first; i0 < past; i0 += U * 64) {
-    int32_t k[U];
-    load(i0, k);
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      below += k[u] < lo;
-      if (k[u] >= lo && k[u] - lo < mine) atomicAdd(&cnt[wave][k[u] - lo], 1);
+  auto count = [&](int32_t r, int32_t& below) {
+    below += __builtin_popcountll(__ballot(r < 0));
+    const bool in = uint32_t(r) < uint32_t(mine);
+    const uint64_t any = __ballot(in);
+    if (any == 0) return;
+    // often one key: counted at once, not lane after lane
+    const int32_t one = __builtin_amdgcn_readlane(r, __builtin_ctzll(any));
+    if (__ballot(r == one) == any) {
+      if (lane == 0) cnt[wave][one] += __builtin_popcountll(any);
+    } else if (in) {
+      atomicAdd(&cnt[wave][r], 1);
     }
+  };
+  auto place = [&](int32_t i, int32_t r) {
+    const bool in = uint32_t(r) < uint32_t(mine);
+    const uint64_t any = __ballot(in);
+    if (any == 0) return;
+    uint32_t low = uint32_t(any), high = uint32_t(any >> 32);  // lanes with the same key
+    for (int b = 0; b < bits; ++b) {
+      const int32_t bit = (r << (31 - b)) >> 31;
+      const uint64_t set = __ballot(bit != 0);
+      low &= ~(uint32_t(set) ^ uint32_t(bit));
+      high &= ~(uint32_t(set >> 32) ^ uint32_t(bit));
+    }
+    if (!in) return;
+    const int32_t before = int32_t(__builtin_amdgcn_mbcnt_hi(high, __builtin_amdgcn_mbcnt_lo(low, 0)));
+    const int32_t at = cnt[wave][r] + before;
+    // the last of them moves the start on, for all have read it
+    if (before + 1 == __builtin_popcount(low) + __builtin_popcount(high)) cnt[wave][r] = at + 1;
+    if (p.order != nullptr) p.order[at] = make_int2(i, lo + r);
+    if (p.place != nullptr) p.place[i] = at;
+  };
+
+  for (int r = lane; r < mine; r += 64) cnt[wave][r] = 0;
+  int32_t below = 0;
+  for (int32_t i0 = first; i0 < past; i0 += U * 64) {
+    load(i0);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (i0 + u * 64 < past) count(key[u], below);
+    if constexpr (kOnce) break;
   }
-  below = int32_t(wave_sum_u32(uint32_t(below)));
-  if (lane == 0) atomicAdd(&below_all, below);
+  if (lane == 0) below_s[wave] = below;
   __syncthreads();
 
   // counts to starts: thread k takes key lo + k of every wave
   const int k = threadIdx.x;
-  uint32_t total = 0;
-  if (k < mine)
-    for (int w = 0; w < kSortWaves; ++w) total += uint32_t(cnt[w][k]);
-  uint32_t in_wave;
-  const uint32_t ahead = wave_exclusive_scan(total, in_wave);
-  if (lane == 0) sums[wave] = int32_t(in_wave);
-  __syncthreads();
-  uint32_t start = uint32_t(below_all) + ahead;
-  for (int w = 0; w < wave; ++w) start += uint32_t(sums[w]);
+  uint32_t total = 0, c[kSortWaves] = {};
+  if (k < mine) {
+#pragma unroll
+    for (int w = 0; w < kSortWaves; ++w) {
+      c[w] = uint32_t(cnt[w][k]);
+      total += c[w];
+    }
+  }
+  uint32_t start = 0, in_wave = total;
+  if (mine > 1) {
+    start = wave_exclusive_scan(total, in_wave);
+    if (lane == 0) sums[wave] = int32_t(in_wave);
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kSortWaves; ++w) start += w < wave ? uint32_t(sums[w]) : 0u;
+  }
+#pragma unroll
+  for (int w = 0; w < kSortWaves; ++w) start += uint32_t(below_s[w]);
   if (k < mine) {
     if (lo + k < p.keys) p.ends[lo + k] = int32_t(start + total);
+#pragma unroll
     for (int w = 0; w < kSortWaves; ++w) {
-      const uint32_t c = uint32_t(cnt[w][k]);
       cnt[w][k] = int32_t(start);
-      start += c;
+      start += c[w];
     }
   }
   __syncthreads();
 
-  const int bits = mine > 1 ? 32 - __builtin_clz(mine - 1) : 0;
-  for (int64_t i0 = first; i0 < past; i0 += U * 64) {
-    int32_t key[U];
-    load(i0, key);
+  for (int32_t i0 = first; i0 < past; i0 += U * 64) {
+    if constexpr (!kOnce) load(i0);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int32_t r = key[u] - lo;
-      const bool in = r >= 0 && r < mine;
-      uint64_t same = __ballot(in);
-      if (same == 0) continue;
-      for (int b = 0; b < bits; ++b) {
-        const uint64_t set = __ballot((r >> b) & 1);
-        same &= (r >> b) & 1 ? set : ~set;
-      }
-      if (in) {
-        const int32_t base = cnt[wave][r];
-        const int32_t at = base + __builtin_popcountll(same & ((uint64_t(1) << lane) - 1));
-        const int64_t i = i0 + u * 64 + lane;
-        if (p.order != nullptr) p.order[at] = int32_t(i);
-        if (p.place != nullptr) p.place[i] = at;
-        // the last of them moves the start on, for all have read it
-        if ((same >> lane) == 1) cnt[wave][r] = at + 1;
-      }
-    }
+    for (int u = 0; u < U; ++u)
+      if (i0 + u * 64 < past) place(i0 + u * 64 + lane, key[u]);
+    if constexpr (kOnce) break;
   }
 }
 

@@ -14,6 +14,7 @@
 #include "device_common.hpp"
 #include "gemm_core.hpp"
 #include "internal.hpp"
+#include "rows.hpp"
 
 namespace fp4lin {
 
@@ -39,9 +40,11 @@ struct TeacherTile {
   int2 head[C::FM][kN];
 
   // col0: of the wave in the vocabulary, a multiple of 32
-  __device__ __attribute__((always_inline)) inline TeacherTile(const TeacherList& t, int row0,
-                                                               int col0_, int rows, int lane_)
-      : entry(t.entry), col0(col0_), lane(lane_) {
+  __device__ __attribute__((always_inline)) inline void read(const TeacherList& t, int row0, int col0_,
+                                                             int rows, int lane_) {
+    entry = t.entry;
+    col0 = col0_;
+    lane = lane_;
     const int half = lane >> 5;
 #pragma unroll
     for (int fm = 0; fm < C::FM; ++fm) {
@@ -89,6 +92,11 @@ struct TeacherTile {
   int64_t row_at[C::FM];
 };
 
+// In its place where there is no teacher.
+struct NoTeacher {
+  __device__ inline void read(const TeacherList&, int, int, int, int) {}
+};
+
 constexpr int kMaxTeacher = 1024;
 __host__ inline int64_t teacher_groups(int64_t V) { return (V + 31) / 32; }
 
@@ -106,19 +114,23 @@ struct TeacherArgs {
 };
 
 // kThreads a row. The order of a row's k entries is found by counting, for each, the
-// entries before it: k reads of shared memory that all lanes share.
+// entries before it: k reads of shared memory that all lanes share. `first` is the sum
+// of the counts of entries by 32 columns, kSpan of those a thread and step.
 template <int kThreads>
 __global__ __launch_bounds__(256) void teacher_kernel(TeacherArgs p) {
   constexpr int kRows = 256 / kThreads, kWaves = kThreads / 64;
   constexpr int kList = kThreads == 64 ? 64 : kMaxTeacher;
   constexpr int kPer = kList / kThreads;  // entries a thread, at most
-  __shared__ int32_t key_s[kRows][kList], sorted_s[kRows][kList];
+  constexpr int kSpan = 16, kStep = kThreads * kSpan;
+  __shared__ int32_t key_s[kRows][kList];
+  __shared__ __attribute__((aligned(16))) uint32_t count_s[kRows][kStep];
   __shared__ float red[kRows][kWaves];
+  __shared__ uint32_t ahead_s[kRows][kWaves];
   const int t = threadIdx.x % kThreads, r = threadIdx.x / kThreads, lane = threadIdx.x & 63;
   const int row = blockIdx.x * kRows + r;
   const bool in = row < p.T;
   int32_t* const key = key_s[r];
-  int32_t* const sorted = sorted_s[r];
+  uint32_t* const count = count_s[r];
   // over the row's threads, on all of them, in one order
   auto reduce = [&](float v, auto op) {
 #pragma unroll
@@ -200,22 +212,61 @@ __global__ __launch_bounds__(256) void teacher_kernel(TeacherArgs p) {
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int j = t + i * kThreads;
-    if (!in || j >= p.k) continue;
-    sorted[place[i]] = col[i];
-    p.entry[int64_t(row) * p.k + place[i]] = make_int2(col[i], __float_as_int(e[i]));
+    if (in && j < p.k)
+      p.entry[int64_t(row) * p.k + place[i]] = make_int2(col[i], __float_as_int(e[i]));
   }
-  __syncthreads();
-  if (!in) return;
-  for (int g = t; g < p.ld; g += kThreads) {
-    int lo = 0, hi = p.k;  // entries below column 32 g
-    while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      if (sorted[mid] < 32 * int64_t(g))
-        lo = mid + 1;
-      else
-        hi = mid;
+  uint32_t before = 0;  // entries below the step
+  for (int g0 = 0; g0 < p.ld; g0 += kStep) {
+    __syncthreads();  // the step before is read
+    uint4* const mine = reinterpret_cast<uint4*>(count + t * kSpan);
+#pragma unroll
+    for (int q = 0; q < kSpan / 4; ++q) mine[q] = make_uint4(0, 0, 0, 0);
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      // an entry lies before the groups from the one after its own on
+      const int g = col[i] == kOut ? -1 : col[i] / 32 + 1 - g0;
+      if (g >= 0 && g < kStep) atomicAdd(&count[g], 1u);
     }
-    p.first[int64_t(row) * p.ld + g] = uint16_t(lo);
+    __syncthreads();
+    uint32_t n[kSpan], sum = 0;
+#pragma unroll
+    for (int q = 0; q < kSpan / 4; ++q) {
+      const uint4 v = mine[q];
+      n[4 * q] = sum += v.x;
+      n[4 * q + 1] = sum += v.y;
+      n[4 * q + 2] = sum += v.z;
+      n[4 * q + 3] = sum += v.w;
+    }
+    uint32_t total;
+    uint32_t ahead = wave_exclusive_scan(sum, total);
+    if constexpr (kWaves > 1) {
+      if (lane == 0) ahead_s[r][t / 64] = total;
+      __syncthreads();
+      total = 0;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) {
+        ahead += w < t / 64 ? ahead_s[r][w] : 0;
+        total += ahead_s[r][w];
+      }
+    }
+    ahead += before;
+    before += total;
+    if (!in) continue;
+    const int g = g0 + t * kSpan;
+    uint16_t* const dst = p.first + int64_t(row) * p.ld + g;
+    if (g + kSpan <= p.ld) {
+      Bytes16 b[kSpan / 8];
+#pragma unroll
+      for (int q = 0; q < kSpan / 2; ++q)
+        b[q / 4].w[q % 4] = (ahead + n[2 * q]) | (ahead + n[2 * q + 1]) << 16;
+#pragma unroll
+      for (int q = 0; q < kSpan / 8; ++q) reinterpret_cast<Bytes16*>(dst)[q] = b[q];
+    } else {
+#pragma unroll
+      for (int q = 0; q < kSpan; ++q)
+        if (g + q < p.ld) dst[q] = uint16_t(ahead + n[q]);
+    }
   }
 }
 
