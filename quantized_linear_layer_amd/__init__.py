@@ -728,20 +728,22 @@ def fp4lin_experts_combine_backward(dout, Y, slot_row, row_end, dY, weight=None,
           dY.data_ptr(), _code(dY), lddy, dw, _queue(stream, device))
 
 
+# (The helpers look at their inputs and call the C entry themselves: what they have made
+# needs no second look.)
 def experts_dispatch(X, expert, experts, stream=None):
     """The rows of X (T, H) sorted by expert, as the products above take them. expert
     (T, k) or (T,) int32: each token's experts; one outside [0, experts) carries
     nothing. Returns (Xs (T * k, H), row_end (experts,), slot_row of expert's shape):
     slot_row is each slot's row, the rows from row_end[-1] on are zeros. The gradient
     of X is experts_combine(dXs, slot_row, row_end)."""
-    torch = _torch()
-    T, H, _ = _rows(X, "X")
+    T, H, ldx = _rows(X, "X")
     T, k = _slots(expert, "expert", T)
+    device = _gpu(("X", X), ("expert", expert))
     with _on(X, stream):
-        Xs = torch.empty((T * k, H), dtype=X.dtype, device=X.device)
-        row_end = torch.empty(experts, dtype=torch.int32, device=X.device)
-        slot_row = torch.empty_like(expert)
-        fp4lin_experts_dispatch(X, expert, Xs, row_end, slot_row)
+        Xs, row_end, slot_row = X.new_empty((T * k, H)), expert.new_empty((experts,)), expert.new_empty(expert.shape)
+        _check(lib().fp4lin_experts_dispatch(X.data_ptr(), _code(X), expert.data_ptr(), T, k, experts, H, ldx,
+                                             Xs.data_ptr(), H, row_end.data_ptr(), slot_row.data_ptr(),
+                                             _queue(None, device)), "experts_dispatch")
     return Xs, row_end, slot_row
 
 
@@ -750,13 +752,22 @@ def experts_combine(Y, slot_row, row_end, weight=None, residual=None, out_dtype=
     slot_row's shape) times their rows of Y (T * k, H). slot_row and row_end are
     experts_dispatch's; slots that carry nothing have no part. out_dtype: the
     residual's, else Y's by default."""
-    torch = _torch()
     T, k = _slots(slot_row, "slot_row")
-    H = _rows(Y, "Y")[1]
+    M, H, ldy = _rows(Y, "Y")
+    _need(M == T * k, f"Y has {M} rows, not {T * k}")
+    some = [(n, t) for n, t in (("weight", weight), ("residual", residual)) if t is not None]
+    device = _gpu(("Y", Y), ("slot_row", slot_row), ("row_end", row_end), *some)
+    ldr, res, dtype = 0, None, out_dtype or Y.dtype
+    if residual is not None:
+        ldr, res, dtype = _matrix_of(residual, T, H, "residual"), residual.data_ptr(), residual.dtype
+        if out_dtype not in (None, dtype):
+            raise TypeError(f"residual is {dtype}, the output {out_dtype}")
+    E = row_end.numel()
     with _on(Y, stream):
-        dtype = out_dtype or (Y if residual is None else residual).dtype
-        out = torch.empty((T, H), dtype=dtype, device=Y.device)
-        fp4lin_experts_combine(Y, slot_row, row_end, out, weight, residual)
+        out = Y.new_empty((T, H), dtype=dtype)
+        _check(lib().fp4lin_experts_combine(Y.data_ptr(), _code(Y), slot_row.data_ptr(), _row_end(row_end, E),
+                                            _weight(weight, T, k), res, T, k, E, H, ldy, ldr, out.data_ptr(),
+                                            _code(out), H, _queue(None, device)), "experts_combine")
     return out
 
 
@@ -764,14 +775,23 @@ def experts_combine_backward(dout, Y, slot_row, row_end, weight=None, out_dtype=
     """Gradients of experts_combine from that of its output, dout (T, H): (dY (T * k, H)
     of out_dtype, dout's by default, dweight float32 of slot_row's shape). Without weight
     Y may be None, and dweight is None. The residual's gradient is dout."""
-    torch = _torch()
-    T, H, _ = _rows(dout, "dout")
+    T, H, lddo = _rows(dout, "dout")
     T, k = _slots(slot_row, "slot_row", T)
+    some = [] if weight is None else [("Y", Y), ("weight", weight)]
+    device = _gpu(("dout", dout), ("slot_row", slot_row), ("row_end", row_end), *some)
+    y, ydt, ldy, w, dw, dweight = None, F32, 0, None, None, None
+    if weight is not None:
+        y, ydt, ldy, w = Y.data_ptr(), _code(Y), _matrix_of(Y, T * k, H, "Y"), _weight(weight, T, k)
+    E = row_end.numel()
     with _on(dout, stream):
-        dY = torch.empty((T * k, H), dtype=out_dtype or dout.dtype, device=dout.device)
-        dweight = None if weight is None else torch.empty(slot_row.shape, dtype=torch.float32,
-                                                          device=dout.device)
-        fp4lin_experts_combine_backward(dout, Y, slot_row, row_end, dY, weight, dweight)
+        dY = dout.new_empty((T * k, H), dtype=out_dtype)
+        if weight is not None:
+            dweight = weight.new_empty(slot_row.shape)
+            dw = dweight.data_ptr()
+        _check(lib().fp4lin_experts_combine_backward(dout.data_ptr(), _code(dout), y, ydt, slot_row.data_ptr(),
+                                                     _row_end(row_end, E), w, T, k, E, H, lddo, ldy, dY.data_ptr(),
+                                                     _code(dY), H, dw, _queue(None, device)),
+               "experts_combine_backward")
     return dY, dweight
 
 
@@ -806,12 +826,15 @@ def fp4lin_embed_backward(dX, token, dE, ws, scale=1.0, add=False, stream=None):
 def embed(table, token, scale=1.0, out_dtype=None, stream=None):
     """out (*token.shape, H) = scale times the rows of table (V, H) that token (int32)
     names, zeros for a token outside [0, V). out_dtype: the table's by default."""
-    torch = _torch()
-    H = _rows(table, "table")[1]
+    V, H, ldt = _rows(table, "table")
+    shape = token.shape
+    T = token.numel()
+    device = _gpu(("table", table), ("token", token))
     with _on(table, stream):
-        out = torch.empty((token.numel(), H), dtype=out_dtype or table.dtype, device=table.device)
-        fp4lin_embed(table, token, out, scale)
-    return out if token.dim() == 1 else out.view(*token.shape, H)
+        out = table.new_empty((*shape, H), dtype=out_dtype)
+        _check(lib().fp4lin_embed(table.data_ptr(), _code(table), _tokens(token, T), T, V, H, ldt, scale,
+                                  out.data_ptr(), _code(out), H, _queue(None, device)), "embed")
+    return out
 
 
 def embed_backward(dX, token, vocab, scale=1.0, out_dtype=None, add_to=None, stream=None):
@@ -820,19 +843,24 @@ def embed_backward(dX, token, vocab, scale=1.0, out_dtype=None, add_to=None, str
     float32 and in the order of the positions. add_to: a gradient of the table (the
     head's, where the two share it) that the result is added to in place and that is
     returned; its rows without a position stay as they are."""
-    torch = _torch()
+    T = token.numel()
+    device = _gpu(("dX", dX), ("token", token), *(() if add_to is None else (("add_to", add_to),)))
     with _on(dX, stream):
         if dX.dim() != 2:
-            dX = dX.reshape(token.numel(), dX.shape[-1])
-        T, H, _ = _rows(dX, "dX")
+            dX = dX.reshape(T, dX.shape[-1])
+        rows, H, lddx = _rows(dX, "dX")
+        _need(rows == T, f"dX has {rows} rows for {T} tokens")
         n = lib().fp4lin_embed_backward_workspace_bytes(T, vocab, H)
         if n == 0:
             raise Fp4linError(_lib.ERR_SHAPE, "embed_backward")
-        ws = torch.empty(n, dtype=torch.uint8, device=dX.device)
-        dE = torch.empty((vocab, H), dtype=out_dtype or dX.dtype, device=dX.device) if add_to is None \
-            else add_to
-        _need(dE.shape[0] == vocab, f"add_to has {dE.shape[0]} rows, not {vocab}")
-        fp4lin_embed_backward(dX, token, dE, ws, scale, add_to is not None)
+        ws = token.new_empty((n + 3) // 4)
+        if add_to is None:
+            dE, ldde = dX.new_empty((vocab, H), dtype=out_dtype), H
+        else:
+            dE, ldde = add_to, _matrix_of(add_to, vocab, H, "add_to")
+        _check(lib().fp4lin_embed_backward(dX.data_ptr(), _code(dX), _tokens(token, T), T, vocab, H, lddx, scale,
+                                           add_to is not None, dE.data_ptr(), _code(dE), ldde, ws.data_ptr(), n,
+                                           _queue(None, device)), "embed_backward")
     return dE
 
 

@@ -25,12 +25,12 @@ __global__ __launch_bounds__(kSortWaves * 64) void route_sort_kernel(SortArgs p)
   sort_body<kOnce>(p);
 }
 
-// The same sort where each workgroup has one key (up to 255 experts), on more
+// The same sort where each workgroup has one key (up to 511 experts), on more
 // workgroups than there are keys: workgroup (e, q) places the slots of expert e in part
 // q of the slots. Where these begin is the number of slots with a smaller expert
 // anywhere and with this one in the parts before, so one comparison a slot, 256 slots a
 // wave and step; only its own part is looked at slot by slot.
-constexpr int kOneKey = 255;
+constexpr int kOneKey = 511;
 
 __global__ __launch_bounds__(kSortWaves * 64) void route_place_kernel(SortArgs p, int parts,
                                                                       int32_t part_len) {
@@ -64,15 +64,27 @@ __global__ __launch_bounds__(kSortWaves * 64) void route_place_kernel(SortArgs p
       for (int j = 0; j < 4; ++j) all += __builtin_popcountll(__ballot(k[j] <= uint32_t(e)));
     }
   }
-  // this wave's slots of the part: [first, end)
+  // this wave's slots of the part: [first, end), four times 64 of them at a time
+  constexpr int U = 4;
   const int64_t seg = part_len / kSortWaves, first = begin + wave * seg;
   const int64_t end = first + seg < past ? first + seg : past;
-  auto mine = [&](int64_t i0) {
-    const int64_t i = i0 + lane;
-    return __ballot(i < end && key_of(uint32_t(p.key[i < end ? i : end - 1])) == uint32_t(e));
+  auto mine = [&](int64_t i0, uint64_t (&m)[U]) {
+    uint32_t k[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t i = i0 + u * 64 + lane;
+      k[u] = key_of(uint32_t(p.key[i < end ? i : end - 1]));
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) m[u] = __ballot(i0 + u * 64 + lane < end && k[u] == uint32_t(e));
   };
   int32_t own = 0;
-  for (int64_t i0 = first; i0 < end; i0 += 64) own += __builtin_popcountll(mine(i0));
+  for (int64_t i0 = first; i0 < end; i0 += U * 64) {
+    uint64_t m[U];
+    mine(i0, m);
+#pragma unroll
+    for (int u = 0; u < U; ++u) own += __builtin_popcountll(m[u]);
+  }
   if (lane == 0) {
     less[wave] = before;
     here[wave] = own;
@@ -86,12 +98,17 @@ __global__ __launch_bounds__(kSortWaves * 64) void route_place_kernel(SortArgs p
     total += upto[w];
   }
   if (q == 0 && threadIdx.x == 0 && uint32_t(e) < E) p.ends[e] = total;
-  for (int64_t i0 = first; i0 < end; i0 += 64) {
-    const uint64_t m = mine(i0);
-    if ((m >> lane) & 1)
-      p.place[i0 + lane] = at + int32_t(__builtin_amdgcn_mbcnt_hi(
-                                    uint32_t(m >> 32), __builtin_amdgcn_mbcnt_lo(uint32_t(m), 0)));
-    at += __builtin_popcountll(m);
+  for (int64_t i0 = first; i0 < end; i0 += U * 64) {
+    uint64_t m[U];
+    mine(i0, m);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if ((m[u] >> lane) & 1)
+        p.place[i0 + u * 64 + lane] =
+            at + int32_t(__builtin_amdgcn_mbcnt_hi(uint32_t(m[u] >> 32),
+                                                   __builtin_amdgcn_mbcnt_lo(uint32_t(m[u]), 0)));
+      at += __builtin_popcountll(m[u]);
+    }
   }
 }
 
@@ -126,8 +143,8 @@ __global__ __launch_bounds__(kRowThreads) void dispatch_kernel(DispatchArgs p, D
     const int32_t* const rows = p.slot_row + int64_t(it.row) * p.k;
     for (int32_t j = 0; j < p.k; ++j) {
       const int32_t r = rows[j];
-      put8<In, kWhole>(static_cast<typename In::T*>(p.Xs) + int64_t(r) * p.ldxs + it.c, valid,
-                       r < made ? v : Vec8<In>{});
+      put8<In, kWhole, true>(static_cast<typename In::T*>(p.Xs) + int64_t(r) * p.ldxs + it.c, valid,
+                             r < made ? v : Vec8<In>{});
     }
   });
 }
@@ -258,7 +275,7 @@ struct CombineBackArgs {
 template <class In, class D, class Out, int kPer, bool kDots>
 __global__ __launch_bounds__(kRowThreads) void combine_back_kernel(CombineBackArgs p) {
   constexpr int kTokens = kRowThreads / kPer, kParts = kPer > 64 ? kPer / 64 : 1;
-  __shared__ float part[2][kParts][4];
+  __shared__ float part[2][kRowThreads / 64][4];  // of each wave
   const int t = threadIdx.x % kPer;
   const int64_t token = int64_t(blockIdx.x) * kTokens + threadIdx.x / kPer;
   const bool in = token < p.T;
@@ -302,8 +319,8 @@ __global__ __launch_bounds__(kRowThreads) void combine_back_kernel(CombineBackAr
             if constexpr (kDots) dot[u] = has[u] ? fmaf(gi, In::widen(y[u].v[i]), dot[u]) : 0.0f;
           }
           if (r[u] >= 0)
-            put8<Out, kWhole>(static_cast<typename Out::T*>(p.dY) + int64_t(r[u]) * p.lddy + c, valid,
-                              rounded<Out>(o));
+            put8<Out, kWhole, true>(static_cast<typename Out::T*>(p.dY) + int64_t(r[u]) * p.lddy + c, valid,
+                                    rounded<Out>(o));
         }
       });
     }
@@ -316,18 +333,19 @@ __global__ __launch_bounds__(kRowThreads) void combine_back_kernel(CombineBackAr
       }
       if constexpr (kParts > 1) {
         // (in two places in turns, so that one barrier a group is enough)
-        float(&mine)[kParts][4] = part[turn];
+        float(&mine)[kRowThreads / 64][4] = part[turn];
         turn ^= 1;
         if ((threadIdx.x & 63) == 0) {
 #pragma unroll
           for (int u = 0; u < N; ++u) mine[threadIdx.x >> 6][u] = dot[u];
         }
         __syncthreads();
+        const int first = threadIdx.x / kPer * kParts;  // wave of the token
 #pragma unroll
         for (int u = 0; u < N; ++u) {
-          dot[u] = mine[0][u];
+          dot[u] = mine[first][u];
 #pragma unroll
-          for (int q = 1; q < kParts; ++q) dot[u] += mine[q][u];
+          for (int q = 1; q < kParts; ++q) dot[u] += mine[first + q][u];
         }
       }
       if (t == 0 && in) {
@@ -406,6 +424,7 @@ hipError_t launch_experts_combine_backward(const RouteCall& c, bool y_bf16, bool
       auto by_columns = [&](auto in, auto dots) {
         if (c.H <= 128) return go(in, dots, std::integral_constant<int, 16>{});
         if (c.H <= 512) return go(in, dots, std::integral_constant<int, 64>{});
+        if (c.H <= 1024) return go(in, dots, std::integral_constant<int, 128>{});
         return go(in, dots, std::integral_constant<int, 256>{});
       };
       if (c.dweight == nullptr) return by_columns(F32In{}, std::false_type{});

@@ -35,14 +35,22 @@ __device__ __attribute__((always_inline)) inline void get8(const typename In::T*
   }
 }
 
-template <class In, bool kWhole>
-__device__ __attribute__((always_inline)) inline void put8(typename In::T* __restrict__ p, int64_t valid, const Vec8<In>& v) {
+// kStream: non-temporal, for rows that are written to places all over an output.
+template <class In, bool kWhole, bool kStream = false>
+__device__ __attribute__((always_inline)) inline void put8(typename In::T* __restrict__ p, int64_t valid,
+                                                           const Vec8<In>& v) {
   if constexpr (kWhole) {
     constexpr int kPieces = In::kBytes / 2;
-    Bytes16 b[kPieces];
+    typedef unsigned int u32x4 __attribute__((ext_vector_type(4), aligned(2)));
+    u32x4 b[kPieces];
     __builtin_memcpy(b, &v, sizeof(v));
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i) reinterpret_cast<Bytes16*>(p)[i] = b[i];
+    for (int i = 0; i < kPieces; ++i) {
+      if constexpr (kStream)
+        __builtin_nontemporal_store(b[i], reinterpret_cast<u32x4*>(p) + i);
+      else
+        reinterpret_cast<u32x4*>(p)[i] = b[i];
+    }
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
