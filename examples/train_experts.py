@@ -3,13 +3,14 @@
     python examples/train_experts.py [--steps 60]
 
     x = Emb[token]                                   bfloat16
-    e, p = the router's best expert of a token and its softmax weight
-    h = relu(Up_e x),  y = x + p * Down_e h          experts' products, FP4
+    e, p = the router's two best experts of a token and their softmax weights
+    h_e = relu(Up_e x),  y = x + sum p_e * Down_e h_e    experts' products, FP4
     loss = cross entropy of y Head against the next token, without the logits
 
-The backward is written out with the same calls (dgrad and wgrad of the experts,
-the head loss's gradients), the gradients are clipped by their global norm and
-the weights updated by Adam in float32. The text is a fixed permutation of the
+Dispatch takes the tokens' rows to their experts, combine brings them back. The
+backward is written out with the same calls (dgrad and wgrad of the experts, the
+gradients of combine, dispatch, the head loss and the embedding), the gradients are
+clipped by their global norm and the weights updated by Adam in float32. The text is a fixed permutation of the
 vocabulary: each token has one successor, so the loss can fall to zero.
 """
 import argparse
@@ -42,38 +43,33 @@ class Model:
         """(mean loss, gradients by name) of one batch of tokens and next tokens."""
         w = {k: v.bfloat16() for k, v in self.w.items()}
         experts = w["up"].shape[0]
-        x = w["emb"][tokens.long()]
+        x = ql.embed(w["emb"], tokens)
         prob = (x.float() @ self.w["router"]).softmax(1)
-        weight, expert = prob.max(1)
+        weight, expert = prob.topk(2, dim=1)
         # the rows by expert; the ends of the experts' rows stay on the GPU
-        order = torch.argsort(expert, stable=True)
-        row_end = torch.bincount(expert, minlength=experts).cumsum(0).to(torch.int32)
-        xs, gate = x[order], weight[order, None]
+        xs, row_end, slot_row = ql.experts_dispatch(x, expert.to(torch.int32), experts)
 
         u = ql.experts_forward_mx(xs, w["up"], row_end)
         h = u.relu().bfloat16()
         d = ql.experts_forward_mx(h, w["down"], row_end)
-        ys = (xs.float() + gate * d).bfloat16()
-        target = targets[order]
-        loss, lse = ql.head_loss(ys, w["head"], target)
+        y = ql.experts_combine(d, slot_row, row_end, weight, x)
+        loss, lse = ql.head_loss(y, w["head"], targets)
 
-        counted = (target >= 0).sum()
+        counted = (targets >= 0).sum()
         dloss = torch.full_like(loss, 1.0) / counted
-        dy, dhead = ql.head_loss_backward(ys, w["head"], target, lse, dloss)
-        dd = (gate * dy.float()).bfloat16()
+        dy, dhead = ql.head_loss_backward(y, w["head"], targets, lse, dloss)
+        dd, dweight = ql.experts_combine_backward(dy, d, slot_row, row_end, weight)
         ddown = ql.experts_wgrad_mx(h, dd, row_end)
         dh = ql.experts_dgrad_mx(dd, w["down"], row_end)
         du = torch.where(u > 0, dh, 0.0).bfloat16()
         dup = ql.experts_wgrad_mx(xs, du, row_end)
-        dx = dy.float() + ql.experts_dgrad_mx(du, w["up"], row_end)
-        # the router through the weight of the chosen expert
-        dweight = (dy.float() * d).sum(1, keepdim=True)
-        onehot = torch.nn.functional.one_hot(expert[order], experts)
-        dlogits = dweight * gate * (onehot - prob[order])
-        dx += dlogits @ self.w["router"].t()
-        demb = torch.zeros_like(self.w["emb"]).index_add_(0, tokens.long()[order], dx)
-        grads = dict(emb=demb, router=xs.float().t() @ dlogits, up=dup, down=ddown,
-                     head=dhead.float())
+        dxs = ql.experts_dgrad_mx(du, w["up"], row_end)
+        # the router through the weights of the chosen experts
+        dprob = torch.zeros_like(prob).scatter_(1, expert, dweight)
+        dlogits = prob * (dprob - (dprob * prob).sum(1, keepdim=True))
+        dx = dy.float() + ql.experts_combine(dxs, slot_row, row_end) + dlogits @ self.w["router"].t()
+        demb = ql.embed_backward(dx, tokens, w["emb"].shape[0])
+        grads = dict(emb=demb, router=x.float().t() @ dlogits, up=dup, down=ddown, head=dhead.float())
         return loss.sum() / counted, grads
 
     def step(self, tokens, targets, rate=3e-3, max_norm=1.0):

@@ -81,7 +81,6 @@ struct FillArgs {
   void* dE;
   int64_t ldde, H;
   uint32_t items;  // 0: nothing to fill
-  int stream;
 };
 
 template <class Out, bool kOnce>
@@ -95,10 +94,7 @@ __global__ __launch_bounds__(kSortWaves * 64, 8) void embed_sort_kernel(SortArgs
     by_width(f.H - c, [&](auto w) {
       constexpr bool kWhole = decltype(w)::value;
       typename Out::T* const dst = static_cast<typename Out::T*>(f.dE) + int64_t(v) * f.ldde + c;
-      if (f.stream)
-        put8<Out, kWhole, true>(dst, f.H - c, Vec8<Out>{});
-      else
-        put8<Out, kWhole>(dst, f.H - c, Vec8<Out>{});
+      put8<Out, kWhole>(dst, f.H - c, Vec8<Out>{});
     });
   }
 }
@@ -407,10 +403,7 @@ hipError_t launch_embed_backward(const EmbedCall& c, bool dx_bf16, bool de_bf16,
   const Divisor groups(row_groups(c.H));
   const SortPlan s = sort_plan(c.V);
   const SortArgs q{c.token, int32_t(c.T), int32_t(c.V), s.per, c.ends, static_cast<int2*>(c.order), nullptr};
-  // a table that outgrows the last-level cache is filled past it, so that the rows of dX
-  // stay there (8192 x 4096 into 32000 rows of bfloat16: 75.2 us; 79.0 through the cache)
-  const bool stream_fill = c.V * c.H * (de_bf16 ? 2 : 4) > kStreamBytes;
-  const FillArgs f{c.dE, c.ldde, c.H, c.add ? 0 : uint32_t(c.V) * groups.d, stream_fill};
+  const FillArgs f{c.dE, c.ldde, c.H, c.add ? 0 : uint32_t(c.V) * groups.d};
   const uint32_t pieces = uint32_t(embed_pieces(c.T));
   const EmbedBackArgs p{c.dX,    c.lddx, int32_t(c.T), int32_t(c.V), c.H,
                         c.scale, c.add,  c.dE,         c.ldde,       c.part};
