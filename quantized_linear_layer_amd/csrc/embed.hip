@@ -30,6 +30,8 @@ struct EmbedArgs {
   uint32_t items;
 };
 
+// Bound by memory: 8192 rows of 4096 in bfloat16 17.5 us (134 MB, part of it in the
+// last-level cache); 64 rows 2.6 us, which is latency.
 template <class In, class Out>
 __global__ __launch_bounds__(kRowThreads) void embed_kernel(EmbedArgs p, Divisor groups) {
   const Item it = item_of(p.items, groups);
@@ -50,7 +52,10 @@ __global__ __launch_bounds__(kRowThreads) void embed_kernel(EmbedArgs p, Divisor
   });
 }
 
-constexpr int kList = 32;
+// Calls with 16 / 32 / 64, us: 8192 positions of a text into 32000 rows of 4096 78.0 / 78.7 /
+// 83.9, 4096 into rows of 1024 21.5 / 22.1 / 23.8, 1001 into 5003 rows of 515 14.5 / 18.1 /
+// 20.5; 8192 positions all over the vocabulary 74.0 / 71.9 / 70.5.
+constexpr int kList = 16;
 
 struct EmbedBackArgs {
   const void* dX;
@@ -76,17 +81,19 @@ struct Sorted {
 };
 
 // The sort, on the first workgroups, which wait for loads and for each other most of
-// the time; the others fill the table with zeros meanwhile.
+// the time; the others fill the table with zeros meanwhile: 8192 positions and 32000 rows
+// of 4096 in bfloat16 37 us, the sort alone 8.6 and the zeros alone 33 (262 MB: 7.9 TB/s, as
+// most of it stays in the last-level cache).
 struct FillArgs {
   void* dE;
   int64_t ldde, H;
   uint32_t items;  // 0: nothing to fill
 };
 
-template <class Out, bool kOnce>
+template <class Out>
 __global__ __launch_bounds__(kSortWaves * 64, 8) void embed_sort_kernel(SortArgs p, FillArgs f, Divisor groups,
                                                                         uint32_t sorters) {
-  if (blockIdx.x < sorters) return sort_body<kOnce>(p);
+  if (blockIdx.x < sorters) return sort_body(p);
   const uint64_t step = uint64_t(gridDim.x - sorters) * (kSortWaves * 64);
   for (uint64_t i = uint64_t(blockIdx.x - sorters) * (kSortWaves * 64) + threadIdx.x; i < f.items; i += step) {
     const uint32_t v = groups(uint32_t(i));
@@ -259,7 +266,11 @@ __device__ __attribute__((always_inline)) inline void sum_list(const EmbedBackAr
 
 // kPer threads a piece of long lists (the first workgroups), or a sorted position, of
 // which those that begin a list have work: it is one for a whole wave, whose lanes then
-// branch together.
+// branch together (with a thread's own position for each eight columns, 8192 positions and
+// rows of 4096 take 90 instead of 78 us, 1024 wide 23.3 instead of 22.4, 64 wide 18.2 instead
+// of 15.1). Bound by memory and by the chain of loads of a list: positions, rows, 31 us for
+// 8192 positions all over 32000 rows of 4096 (134 MB), 35 of a text. Going by positions and
+// not by the table's rows took the call from 106 to 78 us.
 template <class In, class Out, int kPer>
 __global__ __launch_bounds__(kRowThreads) void embed_back_kernel(EmbedBackArgs p,
                                                                  const int2* __restrict__ order,
@@ -282,29 +293,6 @@ __global__ __launch_bounds__(kRowThreads) void embed_back_kernel(EmbedBackArgs p
   if (list.n == 0) return;
   for (int64_t c = c0; c < p.H; c += kPer * 8)
     by_width(p.H - c, [&](auto w) { sum_list<In, Out, decltype(w)::value>(p, s, list, i, c); });
-}
-
-// The same for narrow rows, whose groups of eight follow one another.
-template <class In, class Out>
-__global__ __launch_bounds__(kRowThreads) void embed_back_narrow_kernel(EmbedBackArgs p,
-                                                                        const int2* __restrict__ order,
-                                                                        const int32_t* __restrict__ ends,
-                                                                        Divisor groups, uint32_t cut_blocks,
-                                                                        uint32_t cuts, uint32_t items) {
-  const Sorted s{order, ends};
-  const bool cut = blockIdx.x < cut_blocks;
-  const uint64_t j = uint64_t(blockIdx.x - (cut ? 0 : cut_blocks)) * kRowThreads + threadIdx.x;
-  if (j >= (cut ? cuts : items)) return;
-  const uint32_t i = groups(uint32_t(j));
-  const int64_t c = int64_t(uint32_t(j) - i * groups.d) * 8;
-  if (cut) {
-    const Piece r = piece_at(p, s, int32_t(i));
-    by_width(p.H - c, [&](auto w) { sum_piece<In, decltype(w)::value>(p, s, r, i, groups.d, c); });
-    return;
-  }
-  const List list = list_at(p, s, int32_t(i));
-  if (list.n == 0) return;
-  by_width(p.H - c, [&](auto w) { sum_list<In, Out, decltype(w)::value>(p, s, list, int32_t(i), c); });
 }
 
 // The long list that begins in a piece, if one does: its pieces added by eight waves, each
@@ -373,13 +361,12 @@ void back_rows(const EmbedBackArgs& p, const int2* order, const int32_t* ends, c
     embed_back_kernel<In, Out, kPer>
         <<<cut + blocks_of(p.T, kRows), kRowThreads, 0, stream>>>(p, order, ends, groups.d, cut);
   };
-  if (p.H > 1024) return wide(std::integral_constant<int, 256>{});
-  if (p.H > 512) return wide(std::integral_constant<int, 128>{});
-  if (p.H > 256) return wide(std::integral_constant<int, 64>{});
-  const uint32_t cuts = pieces * groups.d, items = uint32_t(p.T) * groups.d;
-  const unsigned cut = item_blocks(cuts);
-  embed_back_narrow_kernel<In, Out>
-      <<<cut + item_blocks(items), kRowThreads, 0, stream>>>(p, order, ends, groups, cut, cuts, items);
+  // 64 / 128 / 256 threads, us: 4096 positions into 32000 rows 512 wide 18.3 / 18.8 / 20.1,
+  // 1024 wide 24.9 / 22.4 / 23.8, 8192 positions 2048 wide 41.2 / 36.8 / 37.4, 4096 wide
+  // 99 / 83 / 78
+  if (p.H <= 512) return wide(std::integral_constant<int, 64>{});
+  if (p.H <= 2048) return wide(std::integral_constant<int, 128>{});
+  wide(std::integral_constant<int, 256>{});
 }
 
 }  // namespace
@@ -412,12 +399,7 @@ hipError_t launch_embed_backward(const EmbedCall& c, bool dx_bf16, bool de_bf16,
     // up to four rounds of the workgroups that fit the GPU at once (two a CU)
     const unsigned fill = blocks_of(f.items, kSortWaves * 64);
     const unsigned fillers = fill < 2048 ? fill : 2048;
-    if (c.T <= kSortOnce)
-      embed_sort_kernel<Out, true>
-          <<<s.blocks + fillers, kSortWaves * 64, 0, stream>>>(q, f, groups, s.blocks);
-    else
-      embed_sort_kernel<Out, false>
-          <<<s.blocks + fillers, kSortWaves * 64, 0, stream>>>(q, f, groups, s.blocks);
+    embed_sort_kernel<Out><<<s.blocks + fillers, kSortWaves * 64, 0, stream>>>(q, f, groups, s.blocks);
     if (c.T > 0) {
       if (dx_bf16)
         back_rows<BF16In, Out>(p, q.order, q.ends, groups, pieces, stream);

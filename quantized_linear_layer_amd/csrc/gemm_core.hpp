@@ -479,86 +479,59 @@ __device__ __attribute__((always_inline)) inline void gemm_pipeline_turns(F& f, 
   raw_barrier();
 }
 
-// The wave-private LDS blocks that a finished tile passes through (the stage buffers
+// A finished tile leaves through a wave-private LDS block (the stage buffers
 // are free after the pipeline): two 32x32 fragments at a time (one where the
-// stages are small), in rows of kER floats.
-template <class C>
-struct TileBlocks {
-  static constexpr int FM = C::FM, FN = C::FN, kWaves = C::kThreads / kWave;
-  static constexpr int kPair =
-      FN % 2 == 0 && 3 * (C::kStageBytes / (32 * 72 * 4)) >= kWaves ? 2 : 1;
-  // row of a 32 x (32 * kPair) chunk (floats), padded where there is room
-  static constexpr int kER = 32 * kPair + (3 * (C::kStageBytes / (32 * 40 * 4)) >= kWaves ? 8 : 0);
-  // each stage buffer holds the blocks of kEpiPer waves
-  static constexpr int kEpiPer = C::kStageBytes / (32 * kER * 4);
-  static_assert(kEpiPer >= 1 && 3 * kEpiPer >= kWaves, "epilogue blocks fit the stages");
-
-  float* eb;
-  int lane, row0, col0;  // the wave's first row and column
-
-  __device__ __attribute__((always_inline)) inline TileBlocks(uint8_t* st0, uint8_t* st1,
-                                                              uint8_t* st2, int wave, int lane_,
-                                                              int m0, int n0)
-      : lane(lane_), row0(m0 + wave / C::WN * (FM * 32)), col0(n0 + wave % C::WN * (FN * 32)) {
-    uint8_t* const ebs = wave < kEpiPer ? st0 : (wave < 2 * kEpiPer ? st1 : st2);
-    eb = reinterpret_cast<float*>(ebs) + (wave % kEpiPer) * (32 * kER);
-  }
-
-  // The block of fragments (fm, fp .. fp + kPair - 1). value(fm, fn, r) is element r
-  // of fragment (fm, fn): lanes 0..31 hold 32 consecutive columns of one row and
-  // lanes 32..63 the same columns four rows down.
-  template <class Value>
-  __device__ __attribute__((always_inline)) inline void write(int fm, int fp, const Value& value) {
-    const int col_l = lane & 31;
-#pragma unroll
-    for (int h = 0; h < kPair; ++h)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        const int rl = 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
-        eb[rl * kER + h * 32 + col_l] = value(fm, fp + h, r);
-      }
-  }
-
-  // The block that write has left, as rows: emit(row, col, v) takes kVec consecutive
-  // elements of one row, row and col in the matrix that m0 and n0 index, not yet
-  // tested against its size.
-  template <int kVec, class Emit>
-  __device__ __attribute__((always_inline)) inline void read(int fm, int fp, const Emit& emit) {
-    constexpr int kLanes = 32 * kPair / kVec;  // lanes a row
-    constexpr int kRows = kWave / kLanes;      // rows a sweep
-    const int row_base = row0 + fm * 32;
-    const int col_base = col0 + fp * 32;
-#pragma unroll
-    for (int it = 0; it < 32 / kRows; ++it) {
-      const int rl = it * kRows + lane / kLanes;
-      const int cl = (lane % kLanes) * kVec;
-      float v[kVec];
-#pragma unroll
-      for (int i = 0; i < kVec; i += 4) {
-        const float4 q = *reinterpret_cast<const float4*>(eb + rl * kER + cl + i);
-        v[i] = q.x;
-        v[i + 1] = q.y;
-        v[i + 2] = q.z;
-        v[i + 3] = q.w;
-      }
-      emit(row_base + rl, col_base + cl, v);
-    }
-  }
-};
-
-// A finished tile leaves through those blocks, one after the other.
+// stages are small) are written in the MFMA layout and read back as rows.
+// value(fm, fn, r) is element r of fragment (fm, fn): lanes 0..31 hold 32
+// consecutive columns of one row and lanes 32..63 the same columns four rows
+// down. emit(row, col, v) takes kVec consecutive elements of one row, row and
+// col in the matrix that m0 and n0 index, not yet tested against its size.
 template <class C, int kVec, class Value, class Emit>
 __device__ __attribute__((always_inline)) inline void emit_tile(uint8_t* st0, uint8_t* st1,
                                                                 uint8_t* st2, int wave, int lane,
                                                                 int m0, int n0, const Value& value,
                                                                 const Emit& emit) {
-  TileBlocks<C> blocks(st0, st1, st2, wave, lane, m0, n0);
+  constexpr int FM = C::FM, FN = C::FN, kWaves = C::kThreads / kWave;
+  constexpr int kPair = FN % 2 == 0 && 3 * (C::kStageBytes / (32 * 72 * 4)) >= kWaves ? 2 : 1;
+  // row of a 32 x (32 * kPair) chunk (floats), padded where there is room
+  constexpr int kER = 32 * kPair + (3 * (C::kStageBytes / (32 * 40 * 4)) >= kWaves ? 8 : 0);
+  const int wm = wave / C::WN, wn = wave % C::WN;
+  const int col_l = lane & 31;
+  // each stage buffer holds the blocks of kEpiPer waves
+  constexpr int kEpiPer = C::kStageBytes / (32 * kER * 4);
+  static_assert(kEpiPer >= 1 && 3 * kEpiPer >= kWaves, "epilogue blocks fit the stages");
+  uint8_t* const ebs = wave < kEpiPer ? st0 : (wave < 2 * kEpiPer ? st1 : st2);
+  float* eb = reinterpret_cast<float*>(ebs) + (wave % kEpiPer) * (32 * kER);
+  constexpr int kLanes = 32 * kPair / kVec;  // lanes a row
+  constexpr int kRows = kWave / kLanes;      // rows a sweep
 #pragma unroll
-  for (int fm = 0; fm < C::FM; ++fm)
+  for (int fm = 0; fm < FM; ++fm)
 #pragma unroll
-    for (int fp = 0; fp < C::FN; fp += TileBlocks<C>::kPair) {
-      blocks.write(fm, fp, value);
-      blocks.template read<kVec>(fm, fp, emit);
+    for (int fp = 0; fp < FN; fp += kPair) {
+#pragma unroll
+      for (int h = 0; h < kPair; ++h)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          const int rl = 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
+          eb[rl * kER + h * 32 + col_l] = value(fm, fp + h, r);
+        }
+      const int row_base = m0 + wm * (FM * 32) + fm * 32;
+      const int col_base = n0 + wn * (FN * 32) + fp * 32;
+#pragma unroll
+      for (int it = 0; it < 32 / kRows; ++it) {
+        const int rl = it * kRows + lane / kLanes;
+        const int cl = (lane % kLanes) * kVec;
+        float v[kVec];
+#pragma unroll
+        for (int i = 0; i < kVec; i += 4) {
+          const float4 q = *reinterpret_cast<const float4*>(eb + rl * kER + cl + i);
+          v[i] = q.x;
+          v[i + 1] = q.y;
+          v[i + 2] = q.z;
+          v[i + 3] = q.w;
+        }
+        emit(row_base + rl, col_base + cl, v);
+      }
     }
 }
 

@@ -36,7 +36,12 @@
 //   G_tv   = (exp(z_tv - lse_t) - sum over index_tj = v of p_tj) * dloss_t / temperature
 // A kernel of its own turns each row's list into (column, p) pairs sorted by column
 // and into the place in that list where every 32 columns begin, so that a tile finds
-// the pairs of its rows and columns without searching (teacher.hpp).
+// the pairs of its rows and columns without searching (teacher.hpp). A tile's logits pass
+// through shared memory for that, on their way out (G) or where a block has a pair; it
+// costs no time that shows: loss and gradients of 4096 x 2048 by 32000 with 64 pairs a
+// row 1851 us, with one target 1848.
+// Rounding G costs more of the gradients' accuracy than with a target, where one large
+// entry carries most of a row: 0.0023 of their norm in all (0.0017 is their own rounding).
 //
 // Operands whose rows do not start on 16 bytes or whose contiguous size is not a
 // multiple of 8 elements are first copied, padded with zeros. The backward always
@@ -150,16 +155,10 @@ __global__ __launch_bounds__(C::kThreads, C::kMinBlocks) void head_lse_kernel(He
   int tm, tn;
   tile_of(xcd_run(blockIdx.x, tiles_m * tiles_n), tiles_m, tiles_n, tm, tn);
   const int m0 = tm * C::BM, n0 = tn * C::BN;
-  const int row0 = m0 + wm * FM * 32, col0 = n0 + wn * FN * 32;
-  using Entries = std::conditional_t<kDistill, TeacherTile<C>, NoTeacher>;
-  // tiles of few rows have registers left: what the tile's end needs is read now
-  constexpr bool kEarly = C::BM == 64;
-  Entries entries;
-  if constexpr (kEarly) entries.read(p.teacher, row0, col0, p.T_, lane);
   DenseFeed<C, T, kAlong, kBT> f(p.X, p.W, m0, n0, wave, lane);
   product_tile<C>(f, (p.H + kStepElems<T> - 1) / kStepElems<T>, st0, st1, st2, st3, st4);
 
-  if constexpr (!kEarly) entries.read(p.teacher, row0, col0, p.T_, lane);
+  const int row0 = m0 + wm * FM * 32, col0 = n0 + wn * FN * 32;
   if constexpr (kDistill) {
     const float inv = p.teacher.inv_temperature;
 #pragma unroll
@@ -170,6 +169,7 @@ __global__ __launch_bounds__(C::kThreads, C::kMinBlocks) void head_lse_kernel(He
         for (int r = 0; r < 16; ++r) f.acc[fm][fn][r] *= inv;
     using Blocks = TileBlocks<C>;
     Blocks blocks(st0, st1, st2, wave, lane, m0, n0);
+    TeacherTile<C> entries(p.teacher, row0, col0, p.T_, lane);
     float dot[FM];
 #pragma unroll
     for (int fm = 0; fm < FM; ++fm) {
@@ -198,11 +198,11 @@ __global__ __launch_bounds__(C::kThreads, C::kMinBlocks) void head_lse_kernel(He
       const int l = __builtin_ctzll(hits);
       hits &= hits - 1;
       const int c = __builtin_amdgcn_readlane(tcol, l) - col0;
-  #pragma unroll
+#pragma unroll
       for (int fm = 0; fm < FM; ++fm)
-  #pragma unroll
+#pragma unroll
         for (int fn = 0; fn < FN; ++fn)
-  #pragma unroll
+#pragma unroll
           for (int r = 0; r < 16; ++r)
             if (fm * 32 + frag_row(r, lane) == l && fn * 32 + (lane & 31) == c)
               p.tlogit[row0 + l] = f.acc[fm][fn][r];
@@ -267,36 +267,35 @@ __global__ __launch_bounds__(kJoinRows * 64) void head_join_kernel(
   loss[row] = t >= 0 && t < V ? l - tlogit[row] : 0.0f;
 }
 
-// The same for distillation, with each group's sum of p z; kWaves waves a row.
-template <int kWaves>
-__global__ __launch_bounds__(256) void distill_join_kernel(
+// The same for distillation, with each group's sum of p z: four pairs of a row on their
+// way to each lane (32 rows, 1000 pairs: 4.9 us; one after the other 12).
+__global__ __launch_bounds__(kJoinRows * 64) void distill_join_kernel(
     const float2* __restrict__ part, const float* __restrict__ tdot, int P, int T,
     const int32_t* __restrict__ kept, const float2* __restrict__ teacher_sums,
     float* __restrict__ loss, float* __restrict__ lse) {
-  constexpr int kRows = 4 / kWaves, U = 4;
-  __shared__ float sh[3][4];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t row = int64_t(blockIdx.x) * kRows + wave / kWaves;
-  const bool in = row < T;
-  const float2* const mine = part + (in ? row : 0) * P;
-  const float* const dots = tdot + (in ? row : 0) * P;
+  constexpr int U = 4;
   constexpr float kNone = -__builtin_huge_valf();
-  // (a row of -infinity alone keeps 0 as what its exponentials are taken over)
+  const int lane = threadIdx.x & 63;
+  const int row = blockIdx.x * kJoinRows + (threadIdx.x >> 6);
+  if (row >= T) return;
+  const float2* const mine = part + int64_t(row) * P;
+  const float* const dots = tdot + int64_t(row) * P;
+  // (where all are -infinity the exponentials are taken over 0)
   auto over = [](float m) { return m == kNone ? 0.0f : m; };
   float m = kNone, s = 0.0f, dot = 0.0f;
-  for (int j0 = (wave % kWaves) * 64 + lane; j0 < P; j0 += kWaves * 64 * U) {
+  for (int j0 = lane; j0 < P; j0 += 64 * U) {
     float2 v[U];
     float d[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int j = j0 + u * kWaves * 64;
-      v[u] = mine[j < P ? j : P - 1];
-      d[u] = dots[j < P ? j : P - 1];
+      const int j = j0 + u * 64 < P ? j0 + u * 64 : P - 1;
+      v[u] = mine[j];
+      d[u] = dots[j];
     }
     float top = m;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (j0 + u * kWaves * 64 >= P) {
+      if (j0 + u * 64 >= P) {
         v[u] = make_float2(kNone, 0.0f);
         d[u] = 0.0f;
       }
@@ -308,34 +307,15 @@ __global__ __launch_bounds__(256) void distill_join_kernel(
     for (int u = 0; u < U; ++u) s = fmaf(v[u].y, exp_diff(v[u].x, over(top)), s);
     m = top;
   }
-  auto join = [&](float all) {  // s over the largest
-    s *= exp_diff(m, over(all));
-    m = all;
-  };
-  join(wave_max(m));
+  const float all = wave_max(m);
+  s *= exp_diff(m, over(all));
 #pragma unroll
   for (int off = 32; off >= 1; off >>= 1) {
     s += __shfl_xor(s, off, kWave);
     dot += __shfl_xor(dot, off, kWave);
   }
-  if constexpr (kWaves > 1) {
-    if (lane == 0) {
-      sh[0][wave] = m;
-      sh[1][wave] = s;
-      sh[2][wave] = dot;
-    }
-    __syncthreads();
-    const float all = fmaxf(fmaxf(sh[0][0], sh[0][1]), fmaxf(sh[0][2], sh[0][3]));
-    s = dot = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
-      s = fmaf(sh[1][w], exp_diff(sh[0][w], over(all)), s);
-      dot += sh[2][w];
-    }
-    m = all;
-  }
-  if (!in || lane != 0 || wave % kWaves != 0) return;
-  const float l = m + logf(s);
+  if (lane != 0) return;
+  const float l = all + logf(s);
   lse[row] = l;
   // (sum p log p, sum p) of the rounded p: what their sum is off 1 by then meets
   // log p - z + lse, not lse
@@ -400,11 +380,11 @@ __global__ __launch_bounds__(C::kThreads, C::kMinBlocks) void head_grad_kernel(H
       const int l = __builtin_ctzll(hits);
       hits &= hits - 1;
       const int c = __builtin_amdgcn_readlane(tcol, l) - p.v0 - col0;
-  #pragma unroll
+#pragma unroll
       for (int fm = 0; fm < FM; ++fm)
-  #pragma unroll
+#pragma unroll
         for (int fn = 0; fn < FN; ++fn)
-  #pragma unroll
+#pragma unroll
           for (int r = 0; r < 16; ++r)
             if (fm * 32 + frag_row(r, lane) == l && fn * 32 + (lane & 31) == c)
               f.acc[fm][fn][r] -= 1.0f;
@@ -432,8 +412,7 @@ __global__ __launch_bounds__(C::kThreads, C::kMinBlocks) void head_grad_kernel(H
     // entries one by one, so that one index listed twice is taken off twice
     using Blocks = TileBlocks<C>;
     Blocks blocks(st0, st1, st2, wave, lane, m0, n0);
-    TeacherTile<C> entries;
-    entries.read(p.teacher, row0, p.v0 + col0, p.T_, lane);
+    TeacherTile<C> entries(p.teacher, row0, p.v0 + col0, p.T_, lane);
 #pragma unroll
     for (int fm = 0; fm < FM; ++fm) {
       const int row = row0 + fm * 32 + (lane & 31);
@@ -926,25 +905,20 @@ hipError_t run_forward(const HeadCall& c, const HeadPlan& h, hipStream_t stream)
   a.parts = int(h.parts);
   a.tlogit = c.tlogit;
   const Tile t = pick_tile(sizeof(T) == 2, c.T, c.V);
+  const unsigned joins = unsigned(ceil_div(c.T, kJoinRows));
   if (c.distill()) {
     a.teacher = teacher_list(c);
     a.tdot = c.tdot;
     e = logits<T, false, true>(t, c.by_vocab, a, stream);
     if (e != hipSuccess) return e;
-    const auto join = [&](auto waves) {
-      constexpr int kWaves = decltype(waves)::value;
-      distill_join_kernel<kWaves><<<unsigned(ceil_div(c.T, 4 / kWaves)), 256, 0, stream>>>(
-          a.part, c.tdot, int(h.parts), int(c.T), c.target, static_cast<const float2*>(c.teacher_sums),
-          c.loss, c.lse_out);
-      return hipGetLastError();
-    };
-    // four waves a row where one would read more than four pairs a lane
-    if (h.parts > 256) return join(std::integral_constant<int, 4>{});
-    return join(std::integral_constant<int, 1>{});
+    distill_join_kernel<<<joins, kJoinRows * 64, 0, stream>>>(
+        a.part, c.tdot, int(h.parts), int(c.T), c.target, static_cast<const float2*>(c.teacher_sums),
+        c.loss, c.lse_out);
+    return hipGetLastError();
   }
   e = logits<T, false, false>(t, c.by_vocab, a, stream);
   if (e != hipSuccess) return e;
-  head_join_kernel<<<unsigned(ceil_div(c.T, kJoinRows)), kJoinRows * 64, 0, stream>>>(
+  head_join_kernel<<<joins, kJoinRows * 64, 0, stream>>>(
       a.part, int(h.parts), int(c.T), int(c.V), c.target, c.tlogit, c.loss, c.lse_out);
   return hipGetLastError();
 }

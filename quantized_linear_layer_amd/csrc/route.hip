@@ -20,17 +20,17 @@ namespace fp4lin {
 
 namespace {
 
-template <bool kOnce>
-__global__ __launch_bounds__(kSortWaves * 64) void route_sort_kernel(SortArgs p) {
-  sort_body<kOnce>(p);
-}
+__global__ __launch_bounds__(kSortWaves * 64) void route_sort_kernel(SortArgs p) { sort_body(p); }
 
-// The same sort where each workgroup has one key (up to 511 experts), on more
+// The same sort where each workgroup has one key (up to 255 experts), on more
 // workgroups than there are keys: workgroup (e, q) places the slots of expert e in part
 // q of the slots. Where these begin is the number of slots with a smaller expert
 // anywhere and with this one in the parts before, so one comparison a slot, 256 slots a
-// wave and step; only its own part is looked at slot by slot.
-constexpr int kOneKey = 511;
+// wave and step; only its own part is looked at slot by slot. Bound by instruction issue
+// on the CUs it reaches: 16384 slots of 8 experts in 5.2 us. The dispatch of them 512 wide
+// with this kernel / route_sort_kernel, us: 8 experts 10.0 / 16.6, 64 11.5 / 15.6, 256
+// 15.8 / 15.9, 500 16.7 / 15.3.
+constexpr int kOneKey = 255;
 
 __global__ __launch_bounds__(kSortWaves * 64) void route_place_kernel(SortArgs p, int parts,
                                                                       int32_t part_len) {
@@ -130,6 +130,11 @@ struct DispatchArgs {
   uint32_t items;
 };
 
+// Bound by memory: 8192 tokens to 2 of 8 experts, 4096 wide in bfloat16, 30 us alone and 38
+// after other kernels of a layer (201 MB: 6.7 and 5.3 TB/s; a copy reaches 5.1). The rows
+// go past the caches: a layer's dispatch, 8192 / 4096 / 1024 tokens, takes 38 / 21 / 5.4 us,
+// through them 47 / 32 / 19, and the quantizer that reads the rows next 53 / 33 / 20 and 51 /
+// 33 / 18.
 template <class In>
 __global__ __launch_bounds__(kRowThreads) void dispatch_kernel(DispatchArgs p, Divisor groups) {
   const Item it = item_of(p.items, groups);
@@ -153,8 +158,9 @@ __global__ __launch_bounds__(kRowThreads) void dispatch_kernel(DispatchArgs p, D
 // has all keys in shared memory and finds the places of its own tokens' slots by
 // counting those that come before, 64 a step by ballot. Workgroup b takes token
 // b / parts and a part of its columns; the ends of the experts' rows are spread over
-// all waves.
-constexpr int kFewSlots = 1024;
+// all waves. Bound by latency: 2 slots 2.4 us, 128 2.7, 512 4.2 (8 experts, 4096 wide), in
+// two launches 5.2, 5.6 and 6.1; 1024 slots 6.6 against 6.8, of 64 experts 7.8 against 6.6.
+constexpr int kFewSlots = 512;
 
 template <class In>
 __global__ __launch_bounds__(kRowThreads) void dispatch_few_kernel(DispatchArgs p, int parts) {
@@ -213,6 +219,9 @@ struct CombineArgs {
   uint32_t items;
 };
 
+// Bound by memory: 8192 tokens, 2 float32 rows of 4096 each and a bfloat16 residual, 73 us
+// (403 MB: 5.5 TB/s); 64 tokens 2.8 us, which is latency. The sums stay in the caches for
+// who reads them next (past them: 70 us, a layer as a whole the same).
 template <class In, class Out>
 __global__ __launch_bounds__(kRowThreads) void combine_kernel(CombineArgs p, Divisor groups) {
   const Item it = item_of(p.items, groups);
@@ -271,7 +280,11 @@ struct CombineBackArgs {
 };
 
 // kPer threads a token; a row of dout is read once for each group of its slots. kDots:
-// the weights' gradients are wanted.
+// the weights' gradients are wanted. Bound by memory: 4096 tokens, 2 float32 rows of 2048
+// each, bfloat16 gradients, 20.6 us (118 MB: 5.7 TB/s; with the rows written through the
+// caches 22.5). Threads a token, us with 128 / 256: 2048 tokens x 6 slots 768 wide 12.8 /
+// 15.4, 8 slots 1024 wide 13.7 / 16.0, 4096 x 2 2048 wide 20.6 / 21.3, 64 x 2 4096 wide 5.5 /
+// 4.3, 8192 x 2 4096 wide 98 / 89. Narrower rows leave lanes idle with as many.
 template <class In, class D, class Out, int kPer, bool kDots>
 __global__ __launch_bounds__(kRowThreads) void combine_back_kernel(CombineBackArgs p) {
   constexpr int kTokens = kRowThreads / kPer, kParts = kPer > 64 ? kPer / 64 : 1;
@@ -375,10 +388,9 @@ hipError_t run_dispatch(const RouteCall& c, hipStream_t stream) {
     const int64_t len = (most + (want < most ? want : most) - 1) / (want < most ? want : most) * step;
     const int parts = int(M > 0 ? (M + len - 1) / len : 1);
     route_place_kernel<<<unsigned((c.E + 1) * parts), kSortWaves * 64, 0, stream>>>(q, parts, int32_t(len));
-  } else if (M <= kSortOnce)
-    route_sort_kernel<true><<<s.blocks, kSortWaves * 64, 0, stream>>>(q);
-  else
-    route_sort_kernel<false><<<s.blocks, kSortWaves * 64, 0, stream>>>(q);
+  } else {
+    route_sort_kernel<<<s.blocks, kSortWaves * 64, 0, stream>>>(q);
+  }
   if (M > 0) {
     const Divisor groups(row_groups(c.H));
     p.items = uint32_t(c.T) * groups.d;

@@ -161,9 +161,6 @@ struct SortArgs {
 
 constexpr int kSortWaves = 16;
 constexpr int kSortKeys = 512;  // most keys a workgroup
-// Elements a lane reads at a time; up to kSortOnce elements are read once.
-constexpr int kSortRegs = 16;
-constexpr int64_t kSortOnce = int64_t(kSortRegs) * kSortWaves * 64;
 
 struct SortPlan {
   int32_t per;
@@ -178,11 +175,9 @@ __host__ inline SortPlan sort_plan(int64_t keys) {
   return SortPlan{int32_t(per), unsigned((all + per - 1) / per)};
 }
 
-// (in a header that several sources include, each with kernels of its own) kOnce: n is
-// at most kSortOnce; else the elements are read again to be placed.
-template <bool kOnce>
+// (in a header that several sources include, each with a kernel of its own)
 __device__ __attribute__((always_inline)) inline void sort_body(const SortArgs& p) {
-  constexpr int U = kOnce ? kSortRegs : 8;
+  constexpr int U = 8;  // elements a lane has on their way
   __shared__ int32_t cnt[kSortWaves][kSortKeys];
   __shared__ int32_t sums[kSortWaves], below_s[kSortWaves];
   const int lane = threadIdx.x & 63;
@@ -213,7 +208,7 @@ __device__ __attribute__((always_inline)) inline void sort_body(const SortArgs& 
     // often one key: counted at once, not lane after lane
     const int32_t one = __builtin_amdgcn_readlane(r, __builtin_ctzll(any));
     if (__ballot(r == one) == any) {
-      if (lane == 0) cnt[wave][one] += __builtin_popcountll(any);
+      if (lane == 0) atomicAdd(&cnt[wave][one], __builtin_popcountll(any));
     } else if (in) {
       atomicAdd(&cnt[wave][r], 1);
     }
@@ -231,9 +226,11 @@ __device__ __attribute__((always_inline)) inline void sort_body(const SortArgs& 
     }
     if (!in) return;
     const int32_t before = int32_t(__builtin_amdgcn_mbcnt_hi(high, __builtin_amdgcn_mbcnt_lo(low, 0)));
-    const int32_t at = cnt[wave][r] + before;
+    // (atomic accesses: another lane may have written what this one reads again)
+    const int32_t at = __hip_atomic_load(&cnt[wave][r], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WAVEFRONT) + before;
     // the last of them moves the start on, for all have read it
-    if (before + 1 == __builtin_popcount(low) + __builtin_popcount(high)) cnt[wave][r] = at + 1;
+    if (before + 1 == __builtin_popcount(low) + __builtin_popcount(high))
+      __hip_atomic_store(&cnt[wave][r], at + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WAVEFRONT);
     if (p.order != nullptr) p.order[at] = make_int2(i, lo + r);
     if (p.place != nullptr) p.place[i] = at;
   };
@@ -245,7 +242,6 @@ __device__ __attribute__((always_inline)) inline void sort_body(const SortArgs& 
 #pragma unroll
     for (int u = 0; u < U; ++u)
       if (i0 + u * 64 < past) count(key[u], below);
-    if constexpr (kOnce) break;
   }
   if (lane == 0) below_s[wave] = below;
   __syncthreads();
@@ -281,11 +277,10 @@ __device__ __attribute__((always_inline)) inline void sort_body(const SortArgs& 
   __syncthreads();
 
   for (int32_t i0 = first; i0 < past; i0 += U * 64) {
-    if constexpr (!kOnce) load(i0);
+    load(i0);
 #pragma unroll
     for (int u = 0; u < U; ++u)
       if (i0 + u * 64 < past) place(i0 + u * 64 + lane, key[u]);
-    if constexpr (kOnce) break;
   }
 }
 

@@ -18,6 +18,73 @@
 
 namespace fp4lin {
 
+// The wave-private LDS blocks that emit_tile passes a finished tile through (the stage
+// buffers are free after the pipeline), for kernels that look into them on the way: two
+// 32x32 fragments at a time (one where the stages are small), in rows of kER floats.
+template <class C>
+struct TileBlocks {
+  static constexpr int FM = C::FM, FN = C::FN, kWaves = C::kThreads / kWave;
+  static constexpr int kPair =
+      FN % 2 == 0 && 3 * (C::kStageBytes / (32 * 72 * 4)) >= kWaves ? 2 : 1;
+  // row of a 32 x (32 * kPair) chunk (floats), padded where there is room
+  static constexpr int kER = 32 * kPair + (3 * (C::kStageBytes / (32 * 40 * 4)) >= kWaves ? 8 : 0);
+  // each stage buffer holds the blocks of kEpiPer waves
+  static constexpr int kEpiPer = C::kStageBytes / (32 * kER * 4);
+  static_assert(kEpiPer >= 1 && 3 * kEpiPer >= kWaves, "epilogue blocks fit the stages");
+
+  float* eb;
+  int lane, row0, col0;  // the wave's first row and column
+
+  __device__ __attribute__((always_inline)) inline TileBlocks(uint8_t* st0, uint8_t* st1,
+                                                              uint8_t* st2, int wave, int lane_,
+                                                              int m0, int n0)
+      : lane(lane_), row0(m0 + wave / C::WN * (FM * 32)), col0(n0 + wave % C::WN * (FN * 32)) {
+    uint8_t* const ebs = wave < kEpiPer ? st0 : (wave < 2 * kEpiPer ? st1 : st2);
+    eb = reinterpret_cast<float*>(ebs) + (wave % kEpiPer) * (32 * kER);
+  }
+
+  // The block of fragments (fm, fp .. fp + kPair - 1). value(fm, fn, r) is element r
+  // of fragment (fm, fn): lanes 0..31 hold 32 consecutive columns of one row and
+  // lanes 32..63 the same columns four rows down.
+  template <class Value>
+  __device__ __attribute__((always_inline)) inline void write(int fm, int fp, const Value& value) {
+    const int col_l = lane & 31;
+#pragma unroll
+    for (int h = 0; h < kPair; ++h)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const int rl = 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
+        eb[rl * kER + h * 32 + col_l] = value(fm, fp + h, r);
+      }
+  }
+
+  // The block that write has left, as rows: emit(row, col, v) takes kVec consecutive
+  // elements of one row, row and col in the matrix that m0 and n0 index, not yet
+  // tested against its size.
+  template <int kVec, class Emit>
+  __device__ __attribute__((always_inline)) inline void read(int fm, int fp, const Emit& emit) {
+    constexpr int kLanes = 32 * kPair / kVec;  // lanes a row
+    constexpr int kRows = kWave / kLanes;      // rows a sweep
+    const int row_base = row0 + fm * 32;
+    const int col_base = col0 + fp * 32;
+#pragma unroll
+    for (int it = 0; it < 32 / kRows; ++it) {
+      const int rl = it * kRows + lane / kLanes;
+      const int cl = (lane % kLanes) * kVec;
+      float v[kVec];
+#pragma unroll
+      for (int i = 0; i < kVec; i += 4) {
+        const float4 q = *reinterpret_cast<const float4*>(eb + rl * kER + cl + i);
+        v[i] = q.x;
+        v[i + 1] = q.y;
+        v[i + 2] = q.z;
+        v[i + 3] = q.w;
+      }
+      emit(row_base + rl, col_base + cl, v);
+    }
+  }
+};
+
 struct TeacherList {
   const int2* entry;      // [T][k]: column, bits of p
   const uint16_t* first;  // [T][ld]
@@ -40,11 +107,9 @@ struct TeacherTile {
   int2 head[C::FM][kN];
 
   // col0: of the wave in the vocabulary, a multiple of 32
-  __device__ __attribute__((always_inline)) inline void read(const TeacherList& t, int row0, int col0_,
-                                                             int rows, int lane_) {
-    entry = t.entry;
-    col0 = col0_;
-    lane = lane_;
+  __device__ __attribute__((always_inline)) inline TeacherTile(const TeacherList& t, int row0,
+                                                               int col0_, int rows, int lane_)
+      : entry(t.entry), col0(col0_), lane(lane_) {
     const int half = lane >> 5;
 #pragma unroll
     for (int fm = 0; fm < C::FM; ++fm) {
@@ -92,11 +157,6 @@ struct TeacherTile {
   int64_t row_at[C::FM];
 };
 
-// In its place where there is no teacher.
-struct NoTeacher {
-  __device__ inline void read(const TeacherList&, int, int, int, int) {}
-};
-
 constexpr int kMaxTeacher = 1024;
 __host__ inline int64_t teacher_groups(int64_t V) { return (V + 31) / 32; }
 
@@ -113,6 +173,8 @@ struct TeacherArgs {
   float2* sums;
 };
 
+// Bound by latency: 32 lists of 64 over 32000 columns 5.7 us, 4096 of them 10 (with every
+// place searched for in the sorted list 12.2 and 17).
 // kThreads a row. The order of a row's k entries is found by counting, for each, the
 // entries before it: k reads of shared memory that all lanes share. `first` is the sum
 // of the counts of entries by 32 columns, kSpan of those a thread and step.
