@@ -146,7 +146,9 @@ __host__ inline unsigned item_blocks(uint64_t items) {
 // order, are where each wave's elements of a key begin. Lanes of a wave with one key
 // find each other by ballots over the key's bits, so the time does not depend on how
 // the keys are distributed. No atomics that return: the order is that of the
-// elements.
+// elements. Bound by instruction issue and the latency of its few rounds of loads: 8192
+// elements and 32000 keys 8.6 us, 1000 elements 4.7, 30000 26 (every workgroup reads them
+// all, so that the time grows with the elements as what they move does).
 //   ends[k]   number of elements with a key <= k, for k < keys
 //   order     (element, key) by key (not needed: NULL)
 //   place     where each element came to be (not needed: NULL)
