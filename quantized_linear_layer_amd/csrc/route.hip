@@ -161,6 +161,9 @@ __global__ __launch_bounds__(kRowThreads) void dispatch_kernel(DispatchArgs p, D
 // all waves. Bound by latency: 2 slots 2.4 us, 128 2.7, 512 4.2 (8 experts, 4096 wide), in
 // two launches 5.2, 5.6 and 6.1; 1024 slots 6.6 against 6.8, of 64 experts 7.8 against 6.6.
 constexpr int kFewSlots = 512;
+// Steps of 64 slots that a wave may take for the ends of its share of the experts' rows: of
+// 1 token's 2 slots, 64 experts (16 steps) 3.7 us, 256 (64) 8.2, in two launches 5.2.
+constexpr int64_t kFewSteps = 16;
 
 template <class In>
 __global__ __launch_bounds__(kRowThreads) void dispatch_few_kernel(DispatchArgs p, int parts) {
@@ -374,8 +377,9 @@ hipError_t run_dispatch(const RouteCall& c, hipStream_t stream) {
   const int64_t M = c.T * c.k;
   DispatchArgs p{c.X,        c.ldx,       c.Xs,       c.ldxs, c.expert, c.slot_row_out, c.row_end_out,
                  int32_t(c.k), int32_t(c.E), int32_t(M), c.H,    0};
-  if (M <= kFewSlots && M > 0) {
-    const int64_t parts = (row_groups(c.H) + kRowThreads - 1) / kRowThreads;
+  const int64_t parts = (row_groups(c.H) + kRowThreads - 1) / kRowThreads;
+  const int64_t few_waves = c.T * parts * (kRowThreads / 64);
+  if (M > 0 && M <= kFewSlots && c.E * ((M + 63) / 64) <= kFewSteps * few_waves) {
     dispatch_few_kernel<In><<<unsigned(c.T * parts), kRowThreads, 0, stream>>>(p, int(parts));
     return hipGetLastError();
   }

@@ -159,6 +159,19 @@ def test_distill_large_tiles_and_pieces(ql, T):
         assert rel <= 2.0 ** -8, f"{name}: {rel}"
 
 
+@pytest.mark.parametrize("k", [40, 70])
+def test_large_vocabulary(ql, k):
+    """More groups of 32 columns than a list's threads count in one step (1024 and 4096)."""
+    T, H, V = 3, 16, 140001
+    X, W, index, teacher, dloss = inputs(T, H, V, k, wl.F32)
+    index[:, :4] = [V - 1, 0, 131071, 131072]
+    X64, W64 = X.f32.astype(np.float64), W.f32.astype(np.float64)
+    log(f"distill {T}x{H}x{V} {k}")
+    got = as64(run(ql, X, W, index, teacher, dloss, 1.0, True))
+    r = reference(X64, W64, index, teacher, dloss.astype(np.float64), 1.0)
+    check(got, X64, W64, r, wl.F32, 1.0)
+
+
 @pytest.mark.parametrize("dtype", [wl.F32, wl.BF16])
 def test_one_entry_is_a_target(ql, dtype):
     """A list of one entry has probability 1: the head loss of that target.

@@ -81,7 +81,8 @@ def to_gpu(a):
 SIZES = [(1, 1, 1, 1, 0.0), (1, 2, 8, 2048, 0.0), (3, 2, 4, 7, 0.5), (17, 4, 65, 64, 0.1), (64, 2, 8, 4096, 0.0),
          (128, 8, 16, 136, 0.0), (341, 3, 5, 515, 0.2), (342, 3, 5, 515, 0.2), (1001, 3, 5, 130, 0.1),
          (700, 5, 300, 33, 0.3), (200, 9, 7, 2056, 0.1), (50, 1, 3, 8193, 0.3), (2000, 1, 700, 24, 0.05),
-         (4096, 2, 600, 40, 1.0), (5000, 2, 1, 16, 0.0), (9, 70, 5, 12, 0.2)]
+         (4096, 2, 600, 40, 1.0), (5000, 2, 1, 16, 0.0), (9, 70, 5, 12, 0.2),
+         (1, 2, 256, 48, 0.0), (1, 2, 257, 48, 0.0), (2, 3, 65534, 24, 0.3), (170, 3, 2000, 9, 0.1), (171, 3, 255, 9, 0.0)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
