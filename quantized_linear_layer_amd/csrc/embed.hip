@@ -9,7 +9,8 @@
 // frequent tokens have long lists; a list of more than kList positions is cut where
 // the sorted positions pass a multiple of kList, each piece is summed by a thread of
 // its own into fp32, and a last launch adds a list's pieces in order. So no thread
-// adds more than kList rows, however the tokens are distributed.
+// adds more than kList rows, however the tokens are distributed. Few positions take one
+// launch, without the sort.
 #include "device_common.hpp"
 #include "internal.hpp"
 #include "rows.hpp"
@@ -350,6 +351,137 @@ __global__ __launch_bounds__(kJoinWaves * 64) void embed_join_kernel(EmbedBackAr
   by_width(p.H - c, [&](auto whole) { put_row<Out, decltype(whole)::value>(p, v, c, p.H - c, sum); });
 }
 
+// Few positions: all of it in one launch. Workgroup i < T has every token in shared
+// memory; if position i is the first one of its token, it lists the token's positions, in
+// order, and adds their rows: a thread eight columns, and where the columns leave threads
+// over, slices of a longer list, joined in order. The other workgroups fill rows that no
+// position names with zeros; they look for their own rows among the tokens.
+//
+// Bound by latency: tokens, rows, and of a long list its batches of eight. Calls, us, this
+// kernel / the sort and its lists: 64 and 192 positions of a text into 32000 rows of 1024
+// 13.3 / 15.5 and 14.4 / 16.7, on top of a gradient 7.7 / 12.3 and 7.6 / 12.1, into 5003 rows
+// of 515 8.3 / 13.2 and 9.4 / 13.3. At 384 it is 11.8 / 13.7 for the 515, 14.4 / 14.2 for
+// 32000 rows of 512, at 512 and more it is behind: a workgroup a position is too many.
+constexpr int kFewPositions = 256, kFewThreads = 1024;
+// Rows that one thread may come to add (all positions one token, the columns in sweeps).
+// 192 times one token, 2048 wide (48 rows a thread) 19.4 / 27.0, on top of a gradient 10.5 /
+// 12.4; 4096 wide (96) 56.9 / 43.0 and 17.6 / 13.6.
+constexpr int64_t kFewRows = 64;
+constexpr int kFillRows = 4096;  // most rows a filling workgroup
+
+struct EmbedFewArgs {
+  EmbedBackArgs b;
+  const int32_t* token;
+  uint32_t groups, slices;  // slices: of a list, kFewThreads / groups, at least 1
+  int fill_rows;            // rows a filling workgroup
+};
+
+template <class In, class Out>
+__global__ __launch_bounds__(kFewThreads) void embed_few_kernel(EmbedFewArgs p, Divisor groups) {
+  constexpr int kSteps = kFewPositions / 64, kWaves = kFewThreads / 64;
+  __shared__ int32_t key[kFewPositions], pos[kFewPositions];
+  __shared__ uint64_t same[kSteps];
+  __shared__ float sums[8][kFewThreads];
+  __shared__ uint8_t named[kFillRows];
+  const EmbedBackArgs& b = p.b;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+
+  if (blockIdx.x >= unsigned(b.T)) {
+    const int64_t v0 = int64_t(blockIdx.x - b.T) * p.fill_rows;
+    const int rows = int(b.V - v0 < p.fill_rows ? b.V - v0 : p.fill_rows);
+    for (int r = tid; r < rows; r += kFewThreads) named[r] = 0;
+    __syncthreads();
+    for (int i = tid; i < b.T; i += kFewThreads) {
+      const int64_t r = p.token[i] - v0;
+      if (r >= 0 && r < rows) named[r] = 1;
+    }
+    __syncthreads();
+    for (uint32_t i = tid; i < rows * p.groups; i += kFewThreads) {
+      const uint32_t r = groups(i);
+      if (named[r]) continue;
+      const int64_t c = int64_t(i - r * p.groups) * 8;
+      by_width(b.H - c, [&](auto w) {
+        put8<Out, decltype(w)::value>(static_cast<typename Out::T*>(b.dE) + (v0 + r) * b.ldde + c, b.H - c,
+                                      Vec8<Out>{});
+      });
+    }
+    return;
+  }
+
+  const int mine = blockIdx.x, steps = (b.T + 63) / 64;
+  for (int i = tid; i < steps * 64; i += kFewThreads) key[i] = i < b.T ? p.token[i] : -1;
+  __syncthreads();
+  const int32_t v = key[mine];
+  if (v < 0 || v >= b.V) return;
+  for (int s = wave; s < steps; s += kWaves) {
+    const uint64_t m = __ballot(key[s * 64 + lane] == v);
+    if (lane == 0) same[s] = m;
+  }
+  __syncthreads();
+  int n = 0;
+  bool first = true;
+  for (int s = 0; s < steps; ++s) {
+    const uint64_t m = same[s];
+    // positions of the token before this one
+    const uint64_t early = s < mine / 64 ? m : s == mine / 64 ? m & ((uint64_t(1) << (mine & 63)) - 1) : 0;
+    first = first && early == 0;
+    if (s % kWaves == wave && ((m >> lane) & 1))
+      pos[n + __builtin_popcountll(m & ((uint64_t(1) << lane) - 1))] = s * 64 + lane;
+    n += __builtin_popcountll(m);
+  }
+  if (!first) return;
+  __syncthreads();
+
+  const int slice = int(groups(uint32_t(tid))), per = n <= 8 ? n : (n + int(p.slices) - 1) / int(p.slices);
+  for (uint32_t g = p.slices > 1 ? uint32_t(tid) - slice * p.groups : uint32_t(tid);;) {
+    // (all threads come through the barriers below; those with nothing to do add nothing)
+    const bool in = g < p.groups && (p.slices == 1 || slice < int(p.slices));
+    // the last columns of rows that are no whole groups: read with the eight that end the row
+    const int64_t c = int64_t(in ? g : 0) * 8;
+    const int back = b.H >= 8 && c + 8 > b.H ? int(c + 8 - b.H) : 0;
+    const int begin = !in ? 0 : p.slices > 1 ? slice * per : 0, stop = begin + per < n ? begin + per : n;
+    const int end = in ? stop : 0;
+    float sum[8] = {};
+    by_width(b.H - (c - back), [&](auto w) {
+      constexpr bool kWhole = decltype(w)::value;
+      for (int i = begin; i < end; i += 8) {
+        int32_t t[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) t[u] = pos[i + u < end ? i + u : end - 1];
+        if (end - i >= 8) {
+          Vec8<In> x[8];
+#pragma unroll
+          for (int u = 0; u < 8; ++u) read_row<In, kWhole>(b, t[u], c - back, x[u]);
+#pragma unroll
+          for (int u = 0; u < 8; ++u) add_row<In>(x[u], sum);
+        } else {
+          add_few<In, kWhole>(b, t, end - i, c - back, sum);
+        }
+      }
+    });
+    if (p.slices > 1 && n > 8) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) sums[k][tid] = sum[k];
+      __syncthreads();
+      if (slice == 0)
+        for (uint32_t q = 1; q < p.slices; ++q) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) sum[k] += sums[k][q * p.groups + g];
+        }
+    }
+    for (int i = 0; i < back; ++i) {
+#pragma unroll
+      for (int k = 0; k < 7; ++k) sum[k] = sum[k + 1];
+    }
+    if (in && (p.slices == 1 || slice == 0))
+      by_width(b.H - c, [&](auto w) { put_row<Out, decltype(w)::value>(b, v, c, b.H - c, sum); });
+    if (p.slices > 1) return;
+    g += kFewThreads;
+    if (g - tid >= p.groups) return;
+  }
+}
+
 unsigned blocks_of(uint64_t n, uint64_t a_block) { return unsigned((n + a_block - 1) / a_block); }
 
 template <class In, class Out>
@@ -394,6 +526,21 @@ hipError_t launch_embed_backward(const EmbedCall& c, bool dx_bf16, bool de_bf16,
   const uint32_t pieces = uint32_t(embed_pieces(c.T));
   const EmbedBackArgs p{c.dX,    c.lddx, int32_t(c.T), int32_t(c.V), c.H,
                         c.scale, c.add,  c.dE,         c.ldde,       c.part};
+  const int64_t slices = kFewThreads / groups.d > 1 ? kFewThreads / groups.d : 1;
+  const int64_t sweeps = (groups.d + kFewThreads - 1) / kFewThreads;
+  if (c.T > 0 && c.T <= kFewPositions && (c.T + slices - 1) / slices * sweeps <= kFewRows) {
+    // about eight filling workgroups a CU
+    const int64_t rows = c.V / 2048 < 1 ? 1 : c.V / 2048 < kFillRows ? c.V / 2048 : kFillRows;
+    const EmbedFewArgs few{p, c.token, groups.d, uint32_t(slices), int(rows)};
+    const unsigned fill = c.add ? 0 : unsigned((c.V + rows - 1) / rows);
+    return with_type(dx_bf16, [&](auto in) {
+      return with_type(de_bf16, [&](auto out) {
+        embed_few_kernel<decltype(in), decltype(out)>
+            <<<unsigned(c.T) + fill, kFewThreads, 0, stream>>>(few, groups);
+        return hipGetLastError();
+      });
+    });
+  }
   return with_type(de_bf16, [&](auto out) {
     using Out = decltype(out);
     // up to four rounds of the workgroups that fit the GPU at once (two a CU)

@@ -89,7 +89,15 @@ def gradient(dX, tok, V, scale, base=None):
 # piece more; a vocabulary of one, of more than a workgroup's keys each, of less
 BACK = [(1, 1, 1, "uniform"), (1, 1000, 2048, "uniform"), (32, 3, 40, "same"), (33, 3, 40, "same"), (65, 1, 515, "same"),
         (1000, 77, 33, "uniform"), (1001, 5003, 515, "text"), (4096, 3000, 64, "text"), (8192, 2, 16, "uniform"),
-        (2000, 40000, 24, "low"), (3000, 300, 4104, "sorted"), (5000, 131100, 8, "uniform"), (1025, 257, 9, "text")]
+        (2000, 40000, 24, "low"), (3000, 300, 4104, "sorted"), (5000, 131100, 8, "uniform"), (1025, 257, 9, "text"),
+        # few positions, in one launch: at and past the most of them, and the most rows of one
+        # token that a thread may come to add; slices of a long list, sweeps over the columns,
+        # rows that end inside a group of eight; many rows to fill
+        (256, 50, 515, "same"), (257, 50, 515, "text"), (256, 50, 500, "same"), (256, 9, 2048, "same"),
+        (255, 9, 2049, "text"), (128, 9, 4096, "same"), (129, 9, 4096, "same"), (64, 9, 8192, "low"),
+        (32, 9, 8200, "same"), (33, 9, 8200, "same"), (256, 40000, 8, "uniform"), (200, 5000, 130, "low"),
+        (128, 70000, 264, "text"), (8, 3, 2048, "same"), (9, 3, 1000, "same"), (256, 1, 7, "same"),
+        (100, 2, 17, "low"), (1000, 50, 515, "same"), (384, 9, 2048, "same"), (1024, 40000, 8, "uniform")]
 
 
 @pytest.mark.parametrize("dtypes", ["bf16 bf16", "f32 f32", "bf16 f32", "f32 bf16"])
